@@ -384,6 +384,110 @@ TWQ_API twq_status twq_fold_transforms(const float* Q, const float* G, const uin
                                        twq_stream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside the shared layer. Row i of a batch may
+ * use one of `count` adapters of a layer (its request's fine-tuned A, B and factor s);
+ * the rows are grouped by adapter on the GPU once per batch (twq_group_rows), and each
+ * layer's adapter call reads that grouping. The pages have no counterpart: this is what
+ * a server or a trainer puts beside the frozen quantized layer.
+ *
+ *     h = x A^T                    (b x r, BF16)
+ *     y = base + s h B^T           base: the layer's Y, from any twq_*_linear call
+ *
+ * Rows whose id is outside [0, count) have no adapter: h = 0, y = base.
+ */
+
+/* Rows grouped by adapter (device pointers, caller-allocated; twq_row_groups_sizes). */
+typedef struct {
+  int64_t b, count;
+  int32_t* order;   /* b: row numbers sorted by id (stable), rows without adapter last */
+  int32_t* offsets; /* count + 1: group g is order[offsets[g]] .. order[offsets[g+1] - 1] */
+  int32_t* tiles;   /* row tiles of the kernels (internal format) */
+} twq_row_groups;
+
+/* Byte sizes of {order, offsets, tiles}. Host only. TWQ_ERR_INVALID_ARG on b < 0 or
+ * count < 1; TWQ_ERR_UNSUPPORTED beyond b <= 2^20, count <= 4096. */
+TWQ_API twq_status twq_row_groups_sizes(int64_t b, int64_t count, size_t bytes_out[3]);
+
+/*
+ * Groups the rows of a batch: a stable counting sort of the row numbers by id.
+ *   ids  b int32 (4-byte aligned), any values; outside [0, count): no adapter
+ *   g    b, count and the three output buffers (16-byte aligned)
+ * One launch, no host read-back. b == 0 writes the offsets (all 0) and empty tile lists.
+ */
+TWQ_API twq_status twq_group_rows(const int32_t* ids, const twq_row_groups* g, twq_stream_t stream);
+
+/* The adapters of one layer (device pointers). */
+typedef struct {
+  int64_t m, n, r, count;
+  const uint16_t* a;  /* count x r x m BF16 (each A: m contiguous) */
+  const uint16_t* b;  /* count x n x r BF16 (each B: r contiguous) */
+  const float* scale; /* count fp32: s of each adapter */
+} twq_adapters;
+
+/*
+ * The adapters of a batch's rows (forward pass), on BF16 X.
+ *   x     b x m BF16, row stride ldx elements (ldx >= m, ldx % 8 == 0)
+ *   g     from twq_group_rows with the same b and count
+ *   base  b x n BF16, or NULL (0); may be y itself
+ *   h     b x r BF16 (output; the backward pass reads it)
+ *   y     b x n BF16 (output, every row is written)
+ * h is summed in fp32 and rounded to BF16 once; s h B^T + base is summed in fp32 and
+ * rounded once. Rows are independent: an infinity or NaN in one row stays in that row.
+ * Shapes: m % 128 == 0, n % 128 == 0 (the layer's rule), both <= 2^20; r % 8 == 0,
+ *   8 <= r <= 128. b == 0 is a no-op.
+ * Errors: TWQ_ERR_INVALID_ARG on a null pointer, a bad shape, or g->b / g->count that do
+ *   not match; TWQ_ERR_UNSUPPORTED on r > 128 or beyond twq_row_groups_sizes' limits.
+ */
+TWQ_API twq_status twq_adapter_linear(const uint16_t* x, int64_t ldx, int64_t b,
+                                      const twq_adapters* ad, const twq_row_groups* g,
+                                      const uint16_t* base, uint16_t* h, uint16_t* y,
+                                      twq_stream_t stream);
+
+/*
+ * twq_adapter_linear on activation codes stored one per byte, the ones that the layer
+ * itself reads (twq_quantize_act_a8 or twq_quantize_act_i8): x[i, k] = xq8[i, k] *
+ * sx[i, k / 128]. Half of the bytes of BF16 X; a trainer that keeps the 8-bit codes and
+ * scales as its checkpoint of X uses them again in twq_adapter_backward_i8.
+ *   xq8  b x m int8;  sx  b x (m/128) fp32;  otherwise as twq_adapter_linear.
+ */
+TWQ_API twq_status twq_adapter_linear_i8(const int8_t* xq8, const float* sx, int64_t b,
+                                         const twq_adapters* ad, const twq_row_groups* g,
+                                         const uint16_t* base, uint16_t* h, uint16_t* y,
+                                         twq_stream_t stream);
+
+/*
+ * The adapters' backward pass.
+ *     dh = s dy B                  dx = dx_base + dh A
+ *     dA = sum over the adapter's rows of dh^T x
+ *     dB = sum over the adapter's rows of s dy^T h
+ *   dy       b x n BF16
+ *   x, ldx   the forward pass's X;  h  its h (b x r)
+ *   dx_base  b x m BF16 (the gradient through the frozen layer), or NULL (0); may be dx
+ *   dx       b x m BF16 (output; rows without adapter: dx_base)
+ *   da, db   count x r x m and count x n x r BF16 (outputs; adapters without rows: 0)
+ *   workspace  device buffer of twq_adapter_backward_workspace_bytes(b, m, n, r, count)
+ *       bytes, 16-byte aligned; calls that overlap on the GPU need one each
+ * Sums are held in fp32 and rounded once; their order depends only on the arguments'
+ * sizes and the grouping, so equal calls give equal bits. b == 0 writes da = db = 0.
+ * Shapes and errors as twq_adapter_linear; TWQ_ERR_INVALID_ARG on a short workspace.
+ */
+TWQ_API size_t twq_adapter_backward_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r,
+                                                    int64_t count);
+TWQ_API twq_status twq_adapter_backward(const uint16_t* dy, const uint16_t* x, int64_t ldx,
+                                        const uint16_t* h, int64_t b, const twq_adapters* ad,
+                                        const twq_row_groups* g, const uint16_t* dx_base,
+                                        uint16_t* dx, uint16_t* da, uint16_t* db, void* workspace,
+                                        size_t workspace_bytes, twq_stream_t stream);
+
+/* twq_adapter_backward with X from its 8-bit checkpoint (codes and scales). */
+TWQ_API twq_status twq_adapter_backward_i8(const uint16_t* dy, const int8_t* xq8, const float* sx,
+                                           const uint16_t* h, int64_t b, const twq_adapters* ad,
+                                           const twq_row_groups* g, const uint16_t* dx_base,
+                                           uint16_t* dx, uint16_t* da, uint16_t* db,
+                                           void* workspace, size_t workspace_bytes,
+                                           twq_stream_t stream);
+
+/*
  * Reads and clears the device-side status word (SYNCHRONIZES the device).
  * *code = 0 if no kernel's bounded wait has run out since the last call, else
  * a site code (which wait gave up). Returns TWQ_ERR_DEVICE if *code != 0.

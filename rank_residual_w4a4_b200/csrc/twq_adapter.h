@@ -1,0 +1,59 @@
+// Internal interface of the adapter operators (rows grouped by adapter, low-rank
+// adapters beside the layer, their gradients).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/twq.h"
+
+namespace twq {
+
+constexpr int64_t kMaxGroupRows = int64_t(1) << 20;
+constexpr int64_t kMaxGroups = 4096;
+
+// Upper bound of the number of tiles of `rows` rows: every group and the rows without
+// one can add a partial tile, but a tile holds at least one row.
+inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
+  const int64_t parts = b < count + 1 ? b : count + 1;
+  const int64_t cap = b / rows + parts;
+  return static_cast<int>(cap < b ? cap : b);
+}
+
+// tiles: {number of 16-row tiles, number of 128-row tiles, 0, 0}, then room for
+// row_tiles_cap(b, count, 16) entries of the first list and ..., 128) of the second;
+// an entry is {group or -1, first position in order, rows, 0}.
+struct RowGroupsView {
+  int b, count;
+  int32_t* order;
+  int32_t* offsets;
+  int4* tiles;
+};
+
+cudaError_t launch_group_rows(const int32_t* ids, const RowGroupsView& g, cudaStream_t st);
+
+struct AdapterCall {
+  RowGroupsView g;
+  int m, n, r;
+  const uint16_t* a;    // count x r x m
+  const uint16_t* bm;   // count x n x r
+  const float* scale;   // count
+  const uint16_t* x;    // BF16 X (row stride ldx), or null with codes
+  int64_t ldx;
+  const int8_t* xq8;    // 8-bit codes, b x m, or null
+  const float* sx;      // their scales, b x m/128
+  const uint16_t* base; // b x n (forward) or b x m (backward), or null
+  uint16_t* h;          // b x r: output of the forward pass, input of the backward pass
+  uint16_t* y;          // forward: b x n
+  const uint16_t* dy;   // backward: b x n
+  uint16_t* dx;         // b x m
+  uint16_t* da;         // count x r x m
+  uint16_t* db;         // count x n x r
+  void* workspace;
+};
+
+cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st);
+cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st);
+size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count);
+
+}  // namespace twq

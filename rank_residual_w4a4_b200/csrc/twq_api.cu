@@ -2,6 +2,7 @@
 // stream-ordered launches. No entry point allocates device memory.
 #include <string.h>
 
+#include "twq_adapter.h"
 #include "twq_internal.h"
 
 namespace {
@@ -352,6 +353,173 @@ twq_status twq_unfused_linear(const uint8_t* xq, const float* sx, int64_t b, con
   return s;
 }
 
+namespace {
+
+twq_status groups_ok(int64_t b, int64_t count) {
+  if (b < 0 || count < 1) return TWQ_ERR_INVALID_ARG;
+  if (b > twq::kMaxGroupRows || count > twq::kMaxGroups) return TWQ_ERR_UNSUPPORTED;
+  return TWQ_OK;
+}
+
+twq_status adapter_shape_ok(int64_t m, int64_t n, int64_t r) {
+  if (m <= 0 || n <= 0 || r <= 0 || m % 128 || n % 128 || r % 8) return TWQ_ERR_INVALID_ARG;
+  if (r > 128 || m > (int64_t(1) << 20) || n > (int64_t(1) << 20)) return TWQ_ERR_UNSUPPORTED;
+  return TWQ_OK;
+}
+
+// Everything of an adapter call that does not depend on how X is stored.
+twq_status check_adapters(int64_t b, const twq_adapters* ad, const twq_row_groups* g,
+                          twq::AdapterCall* c) {
+  if (!ad || !g) return TWQ_ERR_INVALID_ARG;
+  twq_status s = adapter_shape_ok(ad->m, ad->n, ad->r);
+  if (s == TWQ_OK) s = groups_ok(b, ad->count);
+  if (s != TWQ_OK) return s;
+  if (g->b != b || g->count != ad->count) return TWQ_ERR_INVALID_ARG;
+  if (!ad->a || !ad->b || !ad->scale) return TWQ_ERR_INVALID_ARG;
+  if (!g->order || !g->offsets || !g->tiles) return TWQ_ERR_INVALID_ARG;
+  if (!aligned16(ad->a) || !aligned16(ad->b) || !aligned16(ad->scale) || !aligned16(g->order) ||
+      !aligned16(g->offsets) || !aligned16(g->tiles))
+    return TWQ_ERR_MISALIGNED;
+  *c = twq::AdapterCall{};
+  c->g = twq::RowGroupsView{static_cast<int>(b), static_cast<int>(ad->count), g->order, g->offsets,
+                            reinterpret_cast<int4*>(g->tiles)};
+  c->m = static_cast<int>(ad->m);
+  c->n = static_cast<int>(ad->n);
+  c->r = static_cast<int>(ad->r);
+  c->a = ad->a;
+  c->bm = ad->b;
+  c->scale = ad->scale;
+  return TWQ_OK;
+}
+
+twq_status set_x(twq::AdapterCall* c, const uint16_t* x, int64_t ldx) {
+  if (!x || ldx < c->m) return TWQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8) return TWQ_ERR_MISALIGNED;
+  c->x = x;
+  c->ldx = ldx;
+  return TWQ_OK;
+}
+
+twq_status set_codes(twq::AdapterCall* c, const int8_t* xq8, const float* sx) {
+  if (!xq8 || !sx) return TWQ_ERR_INVALID_ARG;
+  if (!aligned16(xq8) || !aligned16(sx)) return TWQ_ERR_MISALIGNED;
+  c->xq8 = xq8;
+  c->sx = sx;
+  return TWQ_OK;
+}
+
+twq_status run_linear(twq::AdapterCall* c, const uint16_t* base, uint16_t* h, uint16_t* y,
+                      twq_stream_t stream) {
+  if (!h || !y) return TWQ_ERR_INVALID_ARG;
+  if (!aligned16(base) || !aligned16(h) || !aligned16(y)) return TWQ_ERR_MISALIGNED;
+  c->base = base;
+  c->h = h;
+  c->y = y;
+  return from_cuda(twq::launch_adapter_linear(*c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+twq_status run_backward(twq::AdapterCall* c, const uint16_t* dy, const uint16_t* h,
+                        const uint16_t* dx_base, uint16_t* dx, uint16_t* da, uint16_t* db,
+                        void* workspace, size_t workspace_bytes, twq_stream_t stream) {
+  if (c->g.b > 0) {
+    if (!dy || !h || !dx) return TWQ_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(dx) || !aligned16(dx_base))
+      return TWQ_ERR_MISALIGNED;
+  }
+  const size_t need =
+      twq_adapter_backward_workspace_bytes(c->g.b, c->m, c->n, c->r, c->g.count);
+  if (!da || !db || (need && !workspace)) return TWQ_ERR_INVALID_ARG;
+  if (!aligned16(da) || !aligned16(db) || !aligned16(workspace)) return TWQ_ERR_MISALIGNED;
+  if (workspace_bytes < need) return TWQ_ERR_INVALID_ARG;
+  c->dy = dy;
+  c->h = const_cast<uint16_t*>(h);  // read only in the backward pass
+  c->base = dx_base;
+  c->dx = dx;
+  c->da = da;
+  c->db = db;
+  c->workspace = workspace;
+  return from_cuda(twq::launch_adapter_backward(*c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+twq_status twq_row_groups_sizes(int64_t b, int64_t count, size_t bytes_out[3]) {
+  if (!bytes_out) return TWQ_ERR_INVALID_ARG;
+  const twq_status s = groups_ok(b, count);
+  if (s != TWQ_OK) return s;
+  bytes_out[0] = static_cast<size_t>(b) * 4;
+  bytes_out[1] = static_cast<size_t>(count + 1) * 4;
+  bytes_out[2] = 16 * (1 + static_cast<size_t>(twq::row_tiles_cap(b, count, 16)) +
+                       static_cast<size_t>(twq::row_tiles_cap(b, count, 128)));
+  return TWQ_OK;
+}
+
+twq_status twq_group_rows(const int32_t* ids, const twq_row_groups* g, twq_stream_t stream) {
+  if (!g) return TWQ_ERR_INVALID_ARG;
+  const twq_status s = groups_ok(g->b, g->count);
+  if (s != TWQ_OK) return s;
+  if (!g->offsets || !g->tiles || (g->b > 0 && (!ids || !g->order))) return TWQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ids) % 4 || !aligned16(g->order) || !aligned16(g->offsets) ||
+      !aligned16(g->tiles))
+    return TWQ_ERR_MISALIGNED;
+  const twq::RowGroupsView v{static_cast<int>(g->b), static_cast<int>(g->count), g->order,
+                             g->offsets, reinterpret_cast<int4*>(g->tiles)};
+  return from_cuda(twq::launch_group_rows(ids, v, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+twq_status twq_adapter_linear(const uint16_t* x, int64_t ldx, int64_t b, const twq_adapters* ad,
+                              const twq_row_groups* g, const uint16_t* base, uint16_t* h,
+                              uint16_t* y, twq_stream_t stream) {
+  twq::AdapterCall c;
+  twq_status s = check_adapters(b, ad, g, &c);
+  if (s != TWQ_OK || b == 0) return s;
+  s = set_x(&c, x, ldx);
+  return s != TWQ_OK ? s : run_linear(&c, base, h, y, stream);
+}
+
+twq_status twq_adapter_linear_i8(const int8_t* xq8, const float* sx, int64_t b,
+                                 const twq_adapters* ad, const twq_row_groups* g,
+                                 const uint16_t* base, uint16_t* h, uint16_t* y,
+                                 twq_stream_t stream) {
+  twq::AdapterCall c;
+  twq_status s = check_adapters(b, ad, g, &c);
+  if (s != TWQ_OK || b == 0) return s;
+  s = set_codes(&c, xq8, sx);
+  return s != TWQ_OK ? s : run_linear(&c, base, h, y, stream);
+}
+
+size_t twq_adapter_backward_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r,
+                                            int64_t count) {
+  if (groups_ok(b, count) != TWQ_OK || adapter_shape_ok(m, n, r) != TWQ_OK) return 0;
+  return twq::adapter_backward_workspace(b, m, n, r, count);
+}
+
+twq_status twq_adapter_backward(const uint16_t* dy, const uint16_t* x, int64_t ldx,
+                                const uint16_t* h, int64_t b, const twq_adapters* ad,
+                                const twq_row_groups* g, const uint16_t* dx_base, uint16_t* dx,
+                                uint16_t* da, uint16_t* db, void* workspace,
+                                size_t workspace_bytes, twq_stream_t stream) {
+  twq::AdapterCall c;
+  twq_status s = check_adapters(b, ad, g, &c);
+  if (s == TWQ_OK && b > 0) s = set_x(&c, x, ldx);
+  return s != TWQ_OK ? s
+                     : run_backward(&c, dy, h, dx_base, dx, da, db, workspace, workspace_bytes,
+                                    stream);
+}
+
+twq_status twq_adapter_backward_i8(const uint16_t* dy, const int8_t* xq8, const float* sx,
+                                   const uint16_t* h, int64_t b, const twq_adapters* ad,
+                                   const twq_row_groups* g, const uint16_t* dx_base, uint16_t* dx,
+                                   uint16_t* da, uint16_t* db, void* workspace,
+                                   size_t workspace_bytes, twq_stream_t stream) {
+  twq::AdapterCall c;
+  twq_status s = check_adapters(b, ad, g, &c);
+  if (s == TWQ_OK && b > 0) s = set_codes(&c, xq8, sx);
+  return s != TWQ_OK ? s
+                     : run_backward(&c, dy, h, dx_base, dx, da, db, workspace, workspace_bytes,
+                                    stream);
+}
+
 twq_status twq_device_status(int* code) {
   if (!code) return TWQ_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
@@ -397,6 +565,9 @@ int twq_launches_per_call(const char* ep) {
   if (!strcmp(ep, "twq_selftest_wait_timeout")) return 1;  // 1 for the batches twq_fused_linear_x takes
   if (!strcmp(ep, "twq_unfused_linear") || !strcmp(ep, "twq_unfused_linear_noalloc")) return 4;
   if (!strcmp(ep, "twq_fold_transforms")) return 5;
+  if (!strcmp(ep, "twq_group_rows")) return 1;
+  if (!strcmp(ep, "twq_adapter_linear") || !strcmp(ep, "twq_adapter_linear_i8")) return 2;
+  if (!strcmp(ep, "twq_adapter_backward") || !strcmp(ep, "twq_adapter_backward_i8")) return 4;
   return -1;
 }
 

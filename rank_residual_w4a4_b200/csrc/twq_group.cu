@@ -1,0 +1,179 @@
+// Rows of a batch grouped by adapter: a stable counting sort of the row numbers by id,
+// and the lists of row tiles (runs of at most 16 and at most 128 rows of one group) that
+// the adapter kernels walk. One block; nothing is read back by the host.
+#include "twq_adapter.h"
+
+namespace twq {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCountBytes = 160 * 1024;  // shared memory for the per-warp counts
+
+// Exclusive prefix sums over the block of three values per thread.
+__device__ __forceinline__ void block_scan3(int (&v)[3], int (&sum)[3], int (*ws)[kWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int in[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, v[k], off);
+      if (lane >= off) v[k] += o;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) ws[k][warp] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int t = ws[k][lane];  // kWarps == 32
+    const int mine = t;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, t, off);
+      if (lane >= off) t += o;
+    }
+    sum[k] = __shfl_sync(0xFFFFFFFFu, t, 31);
+    v[k] += __shfl_sync(0xFFFFFFFFu, t - mine, warp) - in[k];
+  }
+}
+
+// Largest key k in [0, n) with first[k] <= t (first is non-decreasing, first[0] == 0 <= t).
+__device__ __forceinline__ int find_key(const int* first, int n, int t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Keys are 0 .. count, key `count` collecting every row whose id is outside [0, count).
+// Warp w takes the rows [w * chunk, (w + 1) * chunk) in order: lanes with equal keys
+// find each other by a warp match, so a row's rank among its warp's rows of that key
+// needs no atomics and the order is the same on every run.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    group_rows_kernel(const int32_t* __restrict__ ids, int b, int count, int warps, int chunk,
+                      int32_t* __restrict__ order, int32_t* __restrict__ offsets,
+                      int4* __restrict__ tiles, int cap16) {
+  extern __shared__ int smem[];
+  __shared__ int ws[3][kWarps];
+  const int keys = count + 1;
+  int* start = smem;                // rows before the key
+  int* first16 = start + keys + 1;  // 16-row tiles before the key
+  int* first128 = first16 + keys + 1;
+  T* cnt = reinterpret_cast<T*>(first128 + keys + 1);  // warps x keys
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  for (int i = tid; i < warps * keys; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+
+  const int lo = min(b, warp * chunk), hi = warp < warps ? min(b, lo + chunk) : lo;
+  T* mine = cnt + (warp < warps ? warp : 0) * keys;
+  for (int i = lo; i < hi; i += 32) {
+    int key = -1;
+    if (i + lane < hi) {
+      const int id = __ldg(ids + i + lane);
+      key = (id < 0 || id >= count) ? count : id;
+    }
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    if (key >= 0 && lane == __ffs(same) - 1) mine[key] = mine[key] + __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+
+  // Per key: counts -> rows of the key in earlier warps; totals -> three prefix sums
+  // over the keys, each thread taking `per` consecutive ones.
+  const int per = (keys + kThreads - 1) / kThreads;
+  int v[3] = {0, 0, 0}, sum[3];
+  for (int j = 0; j < per; ++j) {
+    const int k = tid * per + j;
+    if (k >= keys) break;
+    int run = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int c = cnt[w * keys + k];
+      cnt[w * keys + k] = static_cast<T>(run);
+      run += c;
+    }
+    start[k] = run;
+    v[0] += run;
+    v[1] += (run + 15) >> 4;
+    v[2] += (run + 127) >> 7;
+  }
+  block_scan3(v, sum, ws);
+  for (int j = 0; j < per; ++j) {
+    const int k = tid * per + j;
+    if (k >= keys) break;
+    const int run = start[k];
+    start[k] = v[0];
+    first16[k] = v[1];
+    first128[k] = v[2];
+    offsets[k] = v[0];  // the last key's start is the end of group count - 1
+    v[0] += run;
+    v[1] += (run + 15) >> 4;
+    v[2] += (run + 127) >> 7;
+  }
+  if (tid == 0) {
+    start[keys] = sum[0];
+    tiles[0] = make_int4(sum[1], sum[2], 0, 0);
+  }
+  __syncthreads();
+
+  for (int i = lo; i < hi; i += 32) {
+    int key = -1;
+    if (i + lane < hi) {
+      const int id = __ldg(ids + i + lane);
+      key = (id < 0 || id >= count) ? count : id;
+    }
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    const int at = key >= 0 ? static_cast<int>(mine[key]) : 0;
+    __syncwarp();
+    if (key >= 0) {
+      order[start[key] + at + __popc(same & ((1u << lane) - 1u))] = i + lane;
+      if (lane == __ffs(same) - 1) mine[key] = static_cast<T>(at + __popc(same));
+    }
+    __syncwarp();
+  }
+
+  // Tile lists: {group (-1: rows without one), first position in `order`, rows, 0}
+  for (int t = tid; t < sum[1]; t += kThreads) {
+    const int k = find_key(first16, keys, t);
+    const int at = start[k] + (t - first16[k]) * 16;
+    tiles[1 + t] = make_int4(k < count ? k : -1, at, min(16, start[k + 1] - at), 0);
+  }
+  for (int t = tid; t < sum[2]; t += kThreads) {
+    const int k = find_key(first128, keys, t);
+    const int at = start[k] + (t - first128[k]) * 128;
+    tiles[1 + cap16 + t] = make_int4(k < count ? k : -1, at, min(128, start[k + 1] - at), 0);
+  }
+}
+
+template <typename T>
+cudaError_t launch(const int32_t* ids, int b, const RowGroupsView& g, cudaStream_t st) {
+  const int keys = g.count + 1;
+  int warps = kCountBytes / (keys * static_cast<int>(sizeof(T)));
+  if (warps > kWarps) warps = kWarps;
+  int chunk = (b + warps - 1) / warps;
+  chunk = (chunk + 31) / 32 * 32;
+  const int bytes = 3 * (keys + 1) * 4 + warps * keys * static_cast<int>(sizeof(T));
+  cudaError_t e = cudaFuncSetAttribute(group_rows_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  group_rows_kernel<T><<<1, kThreads, bytes, st>>>(
+      ids, b, g.count, warps, chunk, g.order, g.offsets, g.tiles, row_tiles_cap(b, g.count, 16));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_group_rows(const int32_t* ids, const RowGroupsView& g, cudaStream_t st) {
+  // 16-bit counts where no count can pass 65535: twice the warps for many groups.
+  return g.b <= 65535 ? launch<uint16_t>(ids, g.b, g, st) : launch<uint32_t>(ids, g.b, g, st);
+}
+
+}  // namespace twq

@@ -31,7 +31,10 @@ EXPORTS = ("twq_version", "twq_status_string", "twq_weights_sizes", "twq_act_siz
            "twq_fused_linear_x_host", "twq_quantize_act_a8", "twq_fused_linear_a8",
            "twq_fused_linear_x_a8", "twq_pack_l2_int4", "twq_fused_linear_s2q",
            "twq_linear_host", "twq_release_cache", "twq_selftest_wait_timeout",
-           "twq_quantize_act_i8", "twq_fused_linear_i8")
+           "twq_quantize_act_i8", "twq_fused_linear_i8", "twq_row_groups_sizes",
+           "twq_group_rows", "twq_adapter_linear", "twq_adapter_linear_i8",
+           "twq_adapter_backward_workspace_bytes", "twq_adapter_backward",
+           "twq_adapter_backward_i8")
 
 
 class TwqError(RuntimeError):
@@ -44,6 +47,17 @@ class _Weights(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("r", ctypes.c_int64),
                 ("rq", ctypes.c_void_p), ("sr", ctypes.c_void_p), ("l1q", ctypes.c_void_p),
                 ("sl1", ctypes.c_void_p), ("l2t", ctypes.c_void_p)]
+
+
+class _RowGroups(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("count", ctypes.c_int64), ("order", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("tiles", ctypes.c_void_p)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("r", ctypes.c_int64),
+                ("count", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -88,6 +102,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "twq_selftest_wait_timeout": ([P, P, I, P, P, I, P], ctypes.c_int),
         "twq_quantize_act_i8": ([P, I, I, I, P, P, P], ctypes.c_int),
         "twq_fused_linear_i8": ([P, P, I, P, P, P], ctypes.c_int),
+        "twq_row_groups_sizes": ([I, I, P], ctypes.c_int),
+        "twq_group_rows": ([P, P, P], ctypes.c_int),
+        "twq_adapter_linear": ([P, I, I, P, P, P, P, P, P], ctypes.c_int),
+        "twq_adapter_linear_i8": ([P, P, I, P, P, P, P, P, P], ctypes.c_int),
+        "twq_adapter_backward_workspace_bytes": ([I, I, I, I, I], S),
+        "twq_adapter_backward": ([P, P, I, P, I, P, P, P, P, P, P, P, S, P], ctypes.c_int),
+        "twq_adapter_backward_i8": ([P, P, P, P, I, P, P, P, P, P, P, P, S, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -488,6 +509,222 @@ def unfused_linear_noalloc(xq, sx, w: Weights, y=None, stream=None):
     for callers that may not allocate device memory. Calls that overlap on the GPU race
     on the shared scratch."""
     return _layer("twq_unfused_linear_noalloc", xq, sx, w, y, stream)
+
+
+class RowGroups:
+    """Rows of a batch grouped by adapter (group_rows): `order`, the b row numbers sorted
+    by id with the rows without adapter last, and `offsets` (count + 1), both int32;
+    group g is order[offsets[g]:offsets[g + 1]]."""
+
+    def __init__(self, b: int, count: int, device):
+        arr = (ctypes.c_size_t * 3)()
+        _check(load().twq_row_groups_sizes(b, count, arr), "twq_row_groups_sizes")
+        self.b, self.count = b, count
+        self._o = (arr[0] + 15) // 16 * 4   # offsets' first word; 16-byte aligned parts
+        self._t = self._o + (arr[1] + 15) // 16 * 4
+        self._buf = torch.empty(self._t + arr[2] // 4, dtype=torch.int32, device=device)
+        p = self._buf.data_ptr()
+        self._c = _RowGroups(b, count, p, p + 4 * self._o, p + 4 * self._t)
+        self._ref = ctypes.byref(self._c)
+
+    @property
+    def device(self):
+        return self._buf.device
+
+    @property
+    def order(self) -> torch.Tensor:
+        return self._buf[:self.b]
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self._buf[self._o:self._o + self.count + 1]
+
+
+def group_rows(ids: torch.Tensor, count: int, groups: RowGroups | None = None,
+               stream=None) -> RowGroups:
+    """Group the rows of a batch by adapter: ids (b int32), `count` adapters; a row whose
+    id is outside [0, count) has none. `groups`: a RowGroups of the same sizes to reuse
+    (its buffer is overwritten)."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise TypeError("ids must be a 1-D torch tensor")
+    p = _dev(ids, "ids", torch.int32)
+    with _on(ids.device):
+        if groups is None:
+            groups = RowGroups(ids.shape[0], count, ids.device)
+            _keep(stream, groups._buf)
+        elif (groups.b, groups.count) != (ids.shape[0], count) or groups.device != ids.device:
+            raise ValueError("groups must have the sizes and the device of this call")
+        _check(load().twq_group_rows(p or None, groups._ref, _stream(stream)), "twq_group_rows")
+    return groups
+
+
+class Adapters:
+    """The adapters of one layer: a (count x r x m BF16), b (count x n x r BF16) and scale
+    (count fp32), contiguous on one CUDA device. The tensors are read by every call, so
+    updates in place are seen."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor):
+        pa, pb = _dev(a, "a", torch.bfloat16), _dev(b, "b", torch.bfloat16)
+        ps = _dev(scale, "scale", torch.float32)
+        if a.dim() != 3 or b.dim() != 3 or scale.dim() != 1:
+            raise ValueError("a must be (count, r, m), b (count, n, r) and scale (count,)")
+        self.count, self.r, self.m = a.shape
+        self.n = b.shape[1]
+        if tuple(b.shape) != (self.count, self.n, self.r) or scale.shape[0] != self.count:
+            raise ValueError("a must be (count, r, m), b (count, n, r) and scale (count,)")
+        if a.device != b.device or a.device != scale.device:
+            raise ValueError("a, b and scale must be on one device")
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self._c = _Adapters(self.m, self.n, self.r, self.count, pa, pb, ps)
+        self._ref = ctypes.byref(self._c)
+
+
+class _on:
+    """Make `device` current for a call (kernels are launched on the current device)."""
+
+    __slots__ = ("_dev", "_prev")
+
+    def __init__(self, device):
+        self._dev = device.index
+
+    def __enter__(self):
+        self._prev = torch.cuda.current_device()
+        if self._prev != self._dev:
+            torch.cuda.set_device(self._dev)
+
+    def __exit__(self, *exc):
+        if self._prev != self._dev:
+            torch.cuda.set_device(self._prev)
+
+
+def _keep(stream, *tensors):
+    """Buffers allocated here for work on another stream stay reserved until it is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _mat(t, name, dtype, rows, cols, device) -> int:
+    """A contiguous rows x cols tensor on `device`: its address."""
+    p = _dev(t, name, dtype)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must be (%d, %d)" % (name, rows, cols))
+    if t.device != device:
+        raise ValueError("%s must be on the adapters' device" % name)
+    return p
+
+
+def _strided_x(x, b, ad):
+    """BF16 X (b x m, rows may be strided) -> its address and row stride."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a 2-D torch tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be on a CUDA device (the library has no CPU path)")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be torch.bfloat16, got %s" % x.dtype)
+    if x.shape[0] != b or x.shape[1] != ad.m or x.device != ad.device:
+        raise ValueError("x must be (%d, %d) on the adapters' device" % (b, ad.m))
+    if x.stride(1) != 1:
+        raise ValueError("x must have unit stride along m")
+    return x.data_ptr(), (x.stride(0) if b > 1 else ad.m)
+
+
+def _adapter_sizes(ad: Adapters, groups: RowGroups) -> int:
+    if groups.count != ad.count or groups.device != ad.device:
+        raise ValueError("groups must be of the adapters' count and device")
+    return groups.b
+
+
+def _adapter_linear(fn, args, ad, groups, base, y, h, stream):
+    b, dev = groups.b, ad.device
+    with _on(dev):
+        pb = None if base is None else _mat(base, "base", torch.bfloat16, b, ad.n, dev)
+        if y is None:
+            y = torch.empty((b, ad.n), dtype=torch.bfloat16, device=dev)
+            _keep(stream, y)
+        if h is None:
+            h = torch.empty((b, ad.r), dtype=torch.bfloat16, device=dev)
+            _keep(stream, h)
+        _check(getattr(load(), fn)(*args, b, ad._ref, groups._ref, pb,
+                                   _mat(h, "h", torch.bfloat16, b, ad.r, dev),
+                                   _mat(y, "y", torch.bfloat16, b, ad.n, dev), _stream(stream)), fn)
+    return y, h
+
+
+def adapter_linear(x: torch.Tensor, ad: Adapters, groups: RowGroups, base=None, y=None, h=None,
+                   stream=None):
+    """y = base + s (x A^T) B^T with each row's own adapter, and h = x A^T: (y, h), both
+    BF16. x is BF16 (b x m, rows may be strided); base is the layer's Y (may be y itself) or
+    None (0). A row without adapter has y = base and h = 0."""
+    return _adapter_linear("twq_adapter_linear", _strided_x(x, _adapter_sizes(ad, groups), ad), ad,
+                           groups, base, y, h, stream)
+
+
+def _codes(xq8, sx, b, ad):
+    return (_mat(xq8, "xq8", torch.int8, b, ad.m, ad.device),
+            _mat(sx, "sx", torch.float32, b, ad.m // 128, ad.device))
+
+
+def adapter_linear_i8(xq8: torch.Tensor, sx: torch.Tensor, ad: Adapters, groups: RowGroups,
+                      base=None, y=None, h=None, stream=None):
+    """adapter_linear on the layer's activation codes stored one per byte (from
+    quantize_act_a8 or quantize_act_i8) and their scales."""
+    return _adapter_linear("twq_adapter_linear_i8", _codes(xq8, sx, _adapter_sizes(ad, groups), ad),
+                           ad, groups, base, y, h, stream)
+
+
+def adapter_backward_workspace_bytes(b: int, m: int, n: int, r: int, count: int) -> int:
+    return int(load().twq_adapter_backward_workspace_bytes(b, m, n, r, count))
+
+
+def _adapter_backward(fn, dy, args, h, ad, groups, dx_base, dx, da, db, workspace, stream):
+    b, dev, bf = groups.b, ad.device, torch.bfloat16
+    with _on(dev):
+        pdy, ph = _mat(dy, "dy", bf, b, ad.n, dev), _mat(h, "h", bf, b, ad.r, dev)
+        pb = None if dx_base is None else _mat(dx_base, "dx_base", bf, b, ad.m, dev)
+        if dx is None:
+            dx = torch.empty((b, ad.m), dtype=bf, device=dev)
+            _keep(stream, dx)
+        if da is None:
+            da = torch.empty_like(ad.a)
+            _keep(stream, da)
+        if db is None:
+            db = torch.empty_like(ad.b)
+            _keep(stream, db)
+        for t, like, name in ((da, ad.a, "da"), (db, ad.b, "db")):
+            if t.shape != like.shape or t.device != dev:
+                raise ValueError("%s must have the shape and device of the adapters' weights" % name)
+        if workspace is None:
+            workspace = torch.empty(
+                max(adapter_backward_workspace_bytes(b, ad.m, ad.n, ad.r, ad.count), 16),
+                dtype=torch.uint8, device=dev)
+            _keep(stream, workspace)
+        elif workspace.device != dev:
+            raise ValueError("workspace must be on the adapters' device")
+        _check(getattr(load(), fn)(pdy, *args, ph, b, ad._ref, groups._ref, pb,
+                                   _mat(dx, "dx", bf, b, ad.m, dev), _dev(da, "da", bf),
+                                   _dev(db, "db", bf), _dev(workspace, "workspace", torch.uint8),
+                                   workspace.numel(), _stream(stream)), fn)
+    return dx, da, db
+
+
+def adapter_backward(dy, x, h, ad: Adapters, groups: RowGroups, dx_base=None, dx=None, da=None,
+                     db=None, workspace=None, stream=None):
+    """The adapters' gradients from dy (b x n), the forward pass's x and h: (dx, da, db),
+    BF16, with dx = dx_base + dh A (dx_base: the gradient through the frozen layer, may be
+    dx itself, or None) and da, db shaped like the adapters' a, b (adapters without rows: 0)."""
+    return _adapter_backward("twq_adapter_backward", dy,
+                             _strided_x(x, _adapter_sizes(ad, groups), ad), h, ad, groups, dx_base,
+                             dx, da, db, workspace, stream)
+
+
+def adapter_backward_i8(dy, xq8, sx, h, ad: Adapters, groups: RowGroups, dx_base=None, dx=None,
+                        da=None, db=None, workspace=None, stream=None):
+    """adapter_backward with X from its 8-bit checkpoint (codes and scales)."""
+    return _adapter_backward("twq_adapter_backward_i8", dy,
+                             _codes(xq8, sx, _adapter_sizes(ad, groups), ad), h, ad, groups,
+                             dx_base, dx, da, db, workspace, stream)
+
 
 
 def device_status() -> int:

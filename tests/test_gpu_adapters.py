@@ -1,0 +1,334 @@
+"""The adapter operators on the GPU against their definition in 64 bits (adapter_ref.py):
+rows grouped by adapter, adapters beside the layer on BF16 X and on codes, and their
+gradients; then the ways a program calls them (strided X, in place, another stream,
+captured and replayed, beside the layer itself)."""
+import pytest
+import torch
+
+import adapter_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def twq(device):
+    from rank_residual_w4a4_b200 import _build, twq as binding
+    _build.build()
+    binding.load()
+    return binding
+
+
+def make_ids(b, count, kind, gen):
+    if kind == "none":
+        return torch.full((b,), -1, dtype=torch.int32)
+    if kind == "one":
+        return torch.full((b,), count - 1, dtype=torch.int32)
+    ids = torch.randint(-1, count, (b,), generator=gen, dtype=torch.int32)
+    if kind == "runs":
+        ids = ids.sort().values
+    if kind == "wild":  # ids far outside the range mean no adapter
+        ids[::3] = count
+        ids[1::5] = 2 ** 31 - 1
+        ids[2::7] = -2 ** 31
+    return ids
+
+
+@pytest.mark.parametrize("b,count,kind", [
+    (0, 3, "mixed"), (1, 1, "one"), (1, 5, "none"), (31, 2, "mixed"), (33, 40, "wild"),
+    (1000, 1, "one"), (1023, 7, "runs"), (4097, 1024, "mixed"), (5000, 4096, "mixed"),
+    (16384, 64, "runs"), (65535, 33, "mixed"), (65536, 2, "one"), (70001, 4096, "wild"),
+])
+def test_group_rows(twq, device, b, count, kind):
+    gen = torch.Generator().manual_seed(b + count)
+    ids = make_ids(b, count, kind, gen)
+    g = twq.group_rows(ids.to(device), count)
+    key = torch.where((ids < 0) | (ids >= count), count, ids).long()
+    order = torch.sort(key, stable=True).indices.int()
+    hist = torch.bincount(key, minlength=count + 1)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), hist.cumsum(0)])[:count + 1].int()
+    assert torch.equal(g.order.cpu(), order)
+    assert torch.equal(g.offsets.cpu(), offsets)
+    # the same buffers again, with other ids
+    ids2 = ids.flip(0).contiguous()
+    g2 = twq.group_rows(ids2.to(device), count, groups=g)
+    assert g2 is g
+    key2 = key.flip(0)
+    assert torch.equal(g.order.cpu(), torch.sort(key2, stable=True).indices.int())
+
+
+class Case:
+    def __init__(self, twq, device, b, m, n, r, count, kind, codes, seed=0):
+        gen = torch.Generator().manual_seed(seed + b + 7 * r)
+        self.codes, self.b = codes, b
+
+        def normal(*shape, std=1.0):
+            return (torch.randn(shape, generator=gen) * std).to(torch.bfloat16).to(device)
+
+        self.ids = make_ids(b, count, kind, gen)
+        x = normal(b, m)
+        x[:, ::100] *= 30
+        self.x, self.dy, self.h = x, normal(b, n, std=0.01), normal(b, r)
+        self.base, self.dx_base = normal(b, n, std=3.0), normal(b, m, std=0.01)
+        self.ad = twq.Adapters(normal(count, r, m, std=m ** -0.5), normal(count, n, r, std=0.05),
+                               (torch.rand(count, generator=gen) * 4 - 2).to(device))
+        self.groups = twq.group_rows(self.ids.to(device), count)
+        if codes:
+            self.xargs = twq.quantize_act_a8(x) if b else (
+                torch.empty((0, m), dtype=torch.int8, device=device),
+                torch.empty((0, m // 128), dtype=torch.float32, device=device))
+            self.x64 = ref.x_of_codes(*self.xargs)
+            self.linear, self.backward = twq.adapter_linear_i8, twq.adapter_backward_i8
+        else:
+            self.xargs, self.x64 = (x,), x.double()
+            self.linear, self.backward = twq.adapter_linear, twq.adapter_backward
+
+    def ref_linear(self, base):
+        ad = self.ad
+        return ref.linear(self.x64, ad.a, ad.b, ad.scale, self.ids.to(ad.device),
+                          None if base is None else base.double(), self.codes)
+
+    def ref_backward(self, dx_base):
+        ad = self.ad
+        return ref.backward(self.dy.double(), self.x64, self.h.double(), ad.a, ad.b, ad.scale,
+                            self.ids.to(ad.device), None if dx_base is None else dx_base.double(),
+                            self.codes)
+
+    def check_linear(self, base, got):
+        for g, w, e, name in zip(got, *self.ref_linear(base), ("y", "h")):
+            ref.check(g, w, e, name)
+
+    def check_backward(self, dx_base, got):
+        for g, w, e, name in zip(got, *self.ref_backward(dx_base), ("dx", "da", "db")):
+            ref.check(g, w, e, name)
+
+
+# b, m, n, r, count, kind: one row to many, around the tile sizes, ranks that are no
+# multiple of 16 or 32, no adapter at all, adapters without rows, uneven shapes
+SHAPES = [
+    (1, 128, 128, 8, 1, "one"), (1, 4096, 256, 16, 8, "one"), (2, 256, 128, 8, 3, "none"),
+    (15, 512, 384, 24, 4, "mixed"), (16, 512, 512, 16, 1, "one"), (17, 640, 256, 40, 2, "one"),
+    (64, 1024, 1152, 56, 64, "mixed"), (127, 256, 640, 128, 2, "runs"),
+    (128, 384, 256, 64, 1, "one"), (129, 384, 256, 120, 1, "one"), (300, 1152, 896, 32, 5, "wild"),
+    (333, 128, 128, 96, 3, "mixed"), (1000, 512, 768, 72, 17, "mixed"),
+    (1500, 256, 1024, 16, 300, "mixed"), (2500, 768, 512, 128, 2, "runs"),
+    (5000, 256, 256, 48, 1, "one"), (700, 4096, 128, 112, 1, "runs"),
+]
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("b,m,n,r,count,kind", SHAPES)
+def test_linear(twq, device, b, m, n, r, count, kind, codes):
+    c = Case(twq, device, b, m, n, r, count, kind, codes)
+    c.check_linear(c.base, c.linear(*c.xargs, c.ad, c.groups, base=c.base))
+    c.check_linear(None, c.linear(*c.xargs, c.ad, c.groups))
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("b,m,n,r,count,kind", SHAPES)
+def test_backward(twq, device, b, m, n, r, count, kind, codes):
+    c = Case(twq, device, b, m, n, r, count, kind, codes)
+    first = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    c.check_backward(c.dx_base, first)
+    c.check_backward(None, c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups))
+    again = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    assert all(torch.equal(p, q) for p, q in zip(first, again))  # equal calls, equal bits
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+def test_no_rows(twq, device, codes):
+    c = Case(twq, device, 0, 256, 128, 16, 2, "mixed", codes)
+    y, h = c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+    assert y.shape == (0, 128) and h.shape == (0, 16)
+    dx, da, db = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups)
+    assert dx.shape == (0, 256) and not da.any() and not db.any()
+
+
+@pytest.mark.parametrize("b", [5, 40, 300, 2000])
+def test_rows_without_adapter_and_bad_values_stay_apart(twq, device, b):
+    """Rows without adapter are base bit for bit, whatever their X holds; an infinity or
+    NaN in a row with an adapter reaches that row's y and no other."""
+    c = Case(twq, device, b, 512, 256, 16, 3, "mixed", False)
+    c.ids[0], c.ids[1], c.ids[b - 1] = -1, 1, 7
+    c.groups = twq.group_rows(c.ids.to(device), 3)
+    y0, h0 = twq.adapter_linear(c.x, c.ad, c.groups, base=c.base)
+    bad = c.x.clone()
+    bad[0], bad[b - 1] = float("nan"), float("inf")
+    bad[1, 3] = float("nan")
+    y, h = twq.adapter_linear(bad, c.ad, c.groups, base=c.base)
+    out = (c.ids < 0) | (c.ids >= 3)
+    assert torch.equal(y[out.to(device)], c.base[out.to(device)]) and not h[out.to(device)].any()
+    assert y[1].isnan().all() and h[1].isnan().all()
+    keep = torch.ones(b, dtype=torch.bool, device=device)
+    keep[1] = False
+    assert torch.equal(y[keep], y0[keep]) and torch.equal(h[keep], h0[keep])
+    # gradients: a row without adapter takes no part
+    dy = c.dy.clone()
+    want = twq.adapter_backward(dy, c.x, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    bad = c.x.clone()
+    bad[0] = float("nan")
+    dy[0] = float("inf")
+    hb = c.h.clone()
+    hb[0] = float("nan")
+    got = twq.adapter_backward(dy, bad, hb, c.ad, c.groups, dx_base=c.dx_base)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("b", [3, 200, 900])
+def test_rows_are_independent_of_the_batch(twq, device, b):
+    """A row's y does not depend on the order of the ids of the others."""
+    c = Case(twq, device, b, 384, 256, 24, 4, "mixed", False)
+    y, h = twq.adapter_linear(c.x, c.ad, c.groups, base=c.base)
+    p = torch.randperm(b, generator=torch.Generator().manual_seed(1)).to(device)
+    g = twq.group_rows(c.ids.to(device)[p].contiguous(), 4)
+    yp, hp = twq.adapter_linear(c.x[p].contiguous(), c.ad, g, base=c.base[p].contiguous())
+    assert torch.equal(yp, y[p]) and torch.equal(hp, h[p])
+
+
+@pytest.mark.parametrize("b", [1, 9, 257])
+def test_strided_x_and_in_place(twq, device, b):
+    c = Case(twq, device, b, 256, 384, 16, 2, "mixed", False)
+    wide = torch.full((b, 256 + 72), float("nan"), dtype=torch.bfloat16, device=device)
+    wide[:, 64:320] = c.x
+    xs = wide[:, 64:320]
+    y, h = twq.adapter_linear(c.x, c.ad, c.groups, base=c.base)
+    ys, hs = twq.adapter_linear(xs, c.ad, c.groups, base=c.base)
+    assert torch.equal(y, ys) and torch.equal(h, hs)
+    inplace = c.base.clone()
+    yi, _ = twq.adapter_linear(xs, c.ad, c.groups, base=inplace, y=inplace)
+    assert yi.data_ptr() == inplace.data_ptr() and torch.equal(y, inplace)
+    want = twq.adapter_backward(c.dy, c.x, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    dx = c.dx_base.clone()
+    got = twq.adapter_backward(c.dy, xs, c.h, c.ad, c.groups, dx_base=dx, dx=dx)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("b", [24, 700])
+def test_stays_inside_its_buffers(twq, device, b):
+    """Words around every output and the workspace keep their values."""
+    c = Case(twq, device, b, 256, 384, 24, 3, "mixed", False)
+
+    def guarded(*shape):
+        n = 1
+        for s in shape:
+            n *= s
+        buf = torch.full((n + 512,), 7.0, dtype=torch.bfloat16, device=device)
+        return buf, buf[256:256 + n].view(shape)
+
+    nbytes = twq.adapter_backward_workspace_bytes(b, 256, 384, 24, 3)
+    wsb = torch.full((nbytes + 512,), 9, dtype=torch.uint8, device=device)
+    outs = [guarded(b, 384), guarded(b, 24), guarded(b, 256), guarded(3, 24, 256), guarded(3, 384, 24)]
+    (_, y), (_, h), (_, dx), (_, da), (_, db) = outs
+    twq.adapter_linear(c.x, c.ad, c.groups, base=c.base, y=y, h=h)
+    twq.adapter_backward(c.dy, c.x, c.h, c.ad, c.groups, dx=dx, da=da, db=db,
+                         workspace=wsb[256:256 + nbytes])
+    for buf, _ in outs:
+        assert bool((buf[:256] == 7).all()) and bool((buf[-256:] == 7).all())
+    assert bool((wsb[:256] == 9).all()) and bool((wsb[-256:] == 9).all())
+
+
+@pytest.mark.parametrize("b", [8, 600])
+def test_other_stream_and_graph(twq, device, b):
+    c = Case(twq, device, b, 512, 256, 16, 3, "mixed", False)
+    want = twq.adapter_linear(c.x, c.ad, c.groups, base=c.base)
+    wantb = twq.adapter_backward(c.dy, c.x, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = twq.adapter_linear(c.x, c.ad, c.groups, base=c.base, stream=s)
+    gotb = twq.adapter_backward(c.dy, c.x, c.h, c.ad, c.groups, dx_base=c.dx_base, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(p, q) for p, q in zip(got + gotb, want + wantb))
+    # captured once with the grouping inside, replayed for other ids and other values
+    ids = c.ids.to(device)
+    x, base, dy = c.x.clone(), c.base.clone(), c.dy.clone()
+    g = twq.group_rows(ids, 3)
+    ws = torch.empty(twq.adapter_backward_workspace_bytes(b, 512, 256, 16, 3), dtype=torch.uint8,
+                     device=device)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        twq.group_rows(ids, 3, groups=g)
+        y, h = twq.adapter_linear(x, c.ad, g, base=base)
+        grads = twq.adapter_backward(dy, x, h, c.ad, g, workspace=ws)
+    for seed in (5, 6):
+        d = Case(twq, device, b, 512, 256, 16, 3, "mixed", False, seed=seed)
+        ids.copy_(d.ids), x.copy_(d.x), base.copy_(d.base), dy.copy_(d.dy)
+        graph.replay()
+        g2 = twq.group_rows(d.ids.to(device), 3)
+        y2, h2 = twq.adapter_linear(d.x, c.ad, g2, base=d.base)
+        grads2 = twq.adapter_backward(d.dy, d.x, h2, c.ad, g2)
+        assert torch.equal(y, y2) and torch.equal(h, h2)
+        assert all(torch.equal(p, q) for p, q in zip(grads, grads2))
+
+
+def test_two_streams_at_once(twq, device):
+    cases = [Case(twq, device, 900, 512, 512, 32, 3, "mixed", False, seed=s) for s in (1, 2)]
+    want = [c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+            + c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [None, None]
+    for _ in range(5):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                got[i] = (c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+                          + c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(g, w))
+
+
+@pytest.mark.parametrize("b", [12, 260])
+def test_beside_the_layer(twq, device, b):
+    """A W4A8 layer with adapters, forward and backward, as a program runs it: the layer's
+    codes are quantized once and serve the layer, the adapters and, kept, the gradients."""
+    c = Case(twq, device, b, 512, 256, 16, 3, "mixed", True)
+    gen = torch.Generator().manual_seed(3)
+    bf = torch.bfloat16
+    w = twq.pack_weights((torch.randn(512, 256, generator=gen) * 0.02).to(bf).to(device),
+                         (torch.randn(512, 32, generator=gen) * 0.05).to(bf).to(device),
+                         (torch.randn(32, 256, generator=gen) * 0.05).to(bf).to(device))
+    xq8, sx = twq.quantize_act_a8(c.x)
+    layer = twq.fused_linear_a8(xq8, sx, w)
+    base = layer.clone()
+    y, h = twq.adapter_linear_i8(xq8, sx, c.ad, c.groups, base=layer, y=layer)
+    c.check_linear(base, (y, h))
+    c.h = h
+    c.check_backward(c.dx_base, twq.adapter_backward_i8(c.dy, xq8, sx, h, c.ad, c.groups,
+                                                        dx_base=c.dx_base))
+    # the 4-bit codes one per byte go the same way
+    q4, s4 = twq.quantize_act_i8(c.x)
+    c.x64 = ref.x_of_codes(q4, s4)
+    c.check_linear(None, twq.adapter_linear_i8(q4, s4, c.ad, c.groups))
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("b", [20, 200])
+def test_gradients_against_differences(twq, device, b):
+    """y is linear in x, in A and in B, each for itself, so a difference of two forward
+    passes over a step D is <dy, y(v + D) - y(v)> = <gradient, D> but for roundings:
+    those of y (u |y| / sqrt(3) at most, independent) and h behind it (u |h| / sqrt(3)
+    through B) in either pass, and of the gradient itself. Six standard deviations."""
+    c = Case(twq, device, b, 256, 256, 16, 2, "one", False)
+    ad, bf = c.ad, torch.bfloat16
+    y0, h0 = twq.adapter_linear(c.x, ad, c.groups)
+    dx, da, db = twq.adapter_backward(c.dy, c.x, h0, ad, c.groups)
+    gen = torch.Generator().manual_seed(9)
+    for grad, name in ((dx, "x"), (da, "a"), (db, "b")):
+        at = {"x": c.x, "a": ad.a, "b": ad.b}
+        v = at[name]
+        moved = (v.float() + torch.randn(v.shape, generator=gen).to(device) * v.float().std()).to(bf)
+        at[name] = moved
+        ad1 = twq.Adapters(at["a"], at["b"], ad.scale)
+        y1, h1 = twq.adapter_linear(at["x"], ad1, c.groups)
+        step = moved.double() - v.double()
+        left = (c.dy.double() * (y1.double() - y0.double())).sum().item()
+        right = (grad.double() * step).sum().item()
+        s = ad.scale.double()[-1].abs()
+        through = (c.dy.double() @ at["b"][-1].double()) * s
+        var = sum(((c.dy.double() * y.double()) ** 2).sum() + ((through * h.double()) ** 2).sum()
+                  for y, h in ((y0, h0), (y1, h1))) + 2 * ((grad.double() * step) ** 2).sum()
+        dev = ref.U / 3 ** 0.5 * var.sqrt().item()
+        assert abs(left - right) <= 6 * dev, (name, left, right, dev)
