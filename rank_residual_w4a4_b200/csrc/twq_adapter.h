@@ -22,13 +22,19 @@ inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
 
 // tiles: {number of 16-row tiles, number of 128-row tiles, 0, 0}, then room for
 // row_tiles_cap(b, count, 16) entries of the first list and ..., 128) of the second;
-// an entry is {group or -1, first position in order, rows, 0}.
+// an entry is {group or -1, first position in order, rows, 0}. After the entries: for each
+// group, then for the rows without one, the 128-row tiles before it (count + 1 integers).
 struct RowGroupsView {
   int b, count;
   int32_t* order;
   int32_t* offsets;
   int4* tiles;
 };
+
+inline int32_t* first128_of(const RowGroupsView& g) {
+  return reinterpret_cast<int32_t*>(g.tiles + 1 + row_tiles_cap(g.b, g.count, 16) +
+                                    row_tiles_cap(g.b, g.count, 128));
+}
 
 cudaError_t launch_group_rows(const int32_t* ids, const RowGroupsView& g, cudaStream_t st);
 
@@ -54,6 +60,7 @@ struct AdapterCall {
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st);
 cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st);
+cudaError_t read_and_clear_adapter_status(int* code);
 size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count);
 
 }  // namespace twq

@@ -1,0 +1,1144 @@
+// Low-rank adapters of many requests beside the shared layer, on the 5th-generation
+// tensor cores: the three products that the forward and the backward pass consist of,
+// each over tiles of at most 128 rows of one adapter (the rows grouped by adapter,
+// twq_group.cu), gathered by row number.
+//
+//   shrink   H = Z W^T       rows x r    forward Z = X, W = A;  backward Z = dY, W = B^T
+//   expand   Y = base + s H W^T          forward W = B, H = h;  backward W = A^T, H = dh
+//   outer    D_g = sum over rows Z^T H   dB from dY and h;      dA from X and dh
+//
+// All three are bound by HBM: 2 r operations for each element of X, Y or their gradients
+// that is read or written, against some 250 per byte that the tensor cores could do. So
+// each streams its large operand once through shared memory (or, expand, registers) and
+// leaves the products to tcgen05.mma with fp32 accumulators in tensor memory.
+// Rows are fetched by 16-byte cp.async into the 128-byte-swizzle layout, because a tile's
+// rows stand anywhere in the batch; rows beyond the tile and ranks beyond r are filled
+// with zeros, so nothing of another row or adapter takes part in a product.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "sm100_ptx.cuh"
+#include "twq_adapter.h"
+
+namespace twq {
+
+__device__ int g_adapter_status;
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a wait that lasts 2 s is a failure
+constexpr int kSms = 148;
+
+// Site codes of the bounded waits.
+enum : int { kSiteEmpty = 61, kSiteFull, kSiteAccEmpty, kSiteDone, kSiteHEmpty, kSiteDrain, kSiteEnd };
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       int site) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      atomicCAS(&g_adapter_status, 0, site);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+// Bounded wait; false once the block is giving up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                     int site) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, site);
+}
+
+// The same for a whole warp: one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int site) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort_flag, site));
+}
+// Waits for MMAs in flight, which complete by themselves, on every way out of a kernel (their
+// issuer may take kWaitLimitNs to give up its own wait, so twice that).
+__device__ __forceinline__ void wait_mmas(uint64_t* bar) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, 0)) {
+    if (global_timer_ns() - t0 > 2 * kWaitLimitNs) {
+      atomicCAS(&g_adapter_status, 0, kSiteEnd);
+      break;
+    }
+  }
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+// At most `pending` (0 .. 5) groups of this thread in flight.
+__device__ __forceinline__ void cp_wait_n(int pending) {
+  switch (pending) {
+    case 0: cp_wait<0>(); break;
+    case 1: cp_wait<1>(); break;
+    case 2: cp_wait<2>(); break;
+    case 3: cp_wait<3>(); break;
+    case 4: cp_wait<4>(); break;
+    default: cp_wait<5>(); break;
+  }
+}
+
+// Offset of 16-byte chunk c of row `row` in a tile of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(int row, int c) {
+  return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// Operand whose contiguous dimension is M or N ("MN-major"): memory rows are the reduction
+// index, 128 bytes (64 elements) each; 64-element column blocks lie `block_bytes` apart.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+constexpr uint32_t kAMajorMn = 1u << 15, kBMajorMn = 1u << 16;
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// 4 int8 codes -> their values times s, rounded to BF16. The code plus 128 becomes the low
+// mantissa byte of 2^23, so the subtraction is exact and only the product is rounded. BF16
+// is the type that the activation had; an fp32 operand would halve the MMA rate.
+__device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
+  const uint32_t u = w ^ 0x80808080u;
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | i)) - 8388736.0f) * s;
+  return make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+}
+__device__ __forceinline__ void dequant16(uint4 q, float s, uint4& a, uint4& b) {
+  const uint2 p0 = dequant4(q.x, s), p1 = dequant4(q.y, s), p2 = dequant4(q.z, s),
+              p3 = dequant4(q.w, s);
+  a = make_uint4(p0.x, p0.y, p1.x, p1.y);
+  b = make_uint4(p2.x, p2.y, p3.x, p3.y);
+}
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ float4 ld_peer16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// ------------------------------------------------------------------ shrink
+struct ShrinkArgs {
+  const int4* tiles;
+  const int32_t* order;
+  int cap16;
+  const uint16_t* z;  // BF16 rows (stride ldz), or codes
+  int64_t ldz;
+  const int8_t* q;
+  const float* sq;
+  const uint16_t* w;  // count x r x k, or (kTrans) count x k x r
+  const float* scale; // or null: 1
+  uint16_t* out;      // b x r
+  int k, r, rp;       // rp: r rounded up to 16
+  int stages, stage_bytes;
+};
+
+constexpr int kShrinkThreads = 288;  // 8 loading warps, then epilogue; 1 MMA warp
+constexpr int kShrinkMaxStages = 6;
+constexpr int kAhead = 3;  // codes: stages of loads held in registers
+
+// One row tile per cluster, whose blocks split the reduction over k and add their parts
+// through distributed shared memory in rank order.
+template <bool kCodes, bool kTrans>
+__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t s_full[kShrinkMaxStages], s_empty[kShrinkMaxStages], s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (static_cast<int>(blockIdx.y) >= p.tiles[0].y) return;
+  const int4 t = p.tiles[1 + p.cap16 + blockIdx.y];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int splits = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
+  if (t.x < 0) {  // rows without adapter
+    for (int i = rank * kShrinkThreads + tid; i < t.z * (p.r / 8); i += splits * kShrinkThreads) {
+      const int64_t row = p.order[t.y + i / (p.r / 8)];
+      *reinterpret_cast<uint4*>(p.out + row * p.r + i % (p.r / 8) * 8) = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  uint8_t* smem = align1k(smem_raw);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t tmem_cols = p.rp <= 32 ? 32 : (p.rp <= 64 ? 64 : 128);
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s_full[i], 8);
+      mbar_init(&s_empty[i], 1);
+    }
+    mbar_init(&s_done, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int kb = p.k / 64;
+  const int k0 = static_cast<int>(static_cast<int64_t>(rank) * kb / splits);
+  const int steps = static_cast<int>(static_cast<int64_t>(rank + 1) * kb / splits) - k0;
+
+  if (warp < 8) {
+    // Thread: rows tid / 8 + 32 j, chunk tid % 8 (BF16); rows tid / 4 + 64 j, 16 codes (codes).
+    constexpr int kRows = kCodes ? 2 : 4;
+    const int r0 = kCodes ? tid >> 2 : tid >> 3;
+    const int ch = kCodes ? tid & 3 : tid & 7;
+    int64_t row[kRows];
+    bool ok[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = r0 + j * (128 / kRows);
+      ok[j] = i < t.z;
+      row[j] = ok[j] ? p.order[t.y + i] : 0;
+    }
+    uint4 raw[kAhead][2];
+    float sc[kAhead][2];
+    auto fetch = [&](int step, uint4 (&v)[2], float (&s)[2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        s[j] = 0.0f;
+        if (ok[j] && step < steps) {
+          const int col = (k0 + step) * 64;
+          v[j] = __ldg(reinterpret_cast<const uint4*>(p.q + row[j] * p.k + col + ch * 16));
+          s[j] = __ldg(p.sq + row[j] * (p.k >> 7) + (col >> 7));
+        }
+      }
+    };
+    if constexpr (kCodes) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) fetch(a, raw[a], sc[a]);
+    }
+    const int lag = p.stages - 1;
+    const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.r * p.k;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool alive = true;
+    for (int base = 0; base < steps && alive; base += kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int step = base + a;
+        if (step >= steps) break;
+        if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
+          alive = false;
+          break;
+        }
+        const uint32_t zs = sbase + slot * p.stage_bytes, wsm = zs + 16384;
+        const int col = (k0 + step) * 64;
+        if constexpr (kTrans) {  // 64 rows of W (r contiguous): 64-column blocks of 8 KB
+          const int blocks8 = (p.rp + 63) / 64 * 8;
+          for (int i = tid; i < 64 * blocks8; i += 256) {
+            const int kr = i / blocks8, c = i % blocks8;
+            cp16(wsm + (c >> 3) * 8192 + sw128(kr, c & 7),
+                 wg + static_cast<int64_t>(col + kr) * p.r + (c * 8 < p.r ? c * 8 : 0), c * 8 < p.r);
+          }
+        } else {
+          for (int i = tid; i < p.rp * 8; i += 256) {
+            const int c = i >> 3;
+            cp16(wsm + sw128(c, i & 7),
+                 wg + static_cast<int64_t>(c < p.r ? c : 0) * p.k + col + (i & 7) * 8, c < p.r);
+          }
+        }
+        if constexpr (kCodes) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint4 lo, hi;
+            dequant16(raw[a][j], sc[a][j], lo, hi);
+            const int i = r0 + j * 64;
+            sts16(zs + sw128(i, 2 * ch), lo);
+            sts16(zs + sw128(i, 2 * ch + 1), hi);
+          }
+          fetch(step + kAhead, raw[a], sc[a]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kRows; ++j)
+            cp16(zs + sw128(r0 + j * 32, ch), p.z + row[j] * p.ldz + col + ch * 8, ok[j]);
+        }
+        cp_commit();
+        if (step >= lag) {  // the stage issued `lag` steps ago has landed
+          cp_wait_n(lag);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_full[(step - lag) % p.stages]);
+        }
+        if (++slot == p.stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    cp_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (alive && lane == 0)
+      for (int s = max(0, steps - lag); s < steps; ++s) mbar_arrive(&s_full[s % p.stages]);
+  } else if (lane == 0) {
+    const uint32_t idesc = idesc_bf16(p.rp) | (kTrans ? kBMajorMn : 0u);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int step = 0; step < steps; ++step) {
+      if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) break;
+      tc_fence_after();
+      const uint32_t zs = sbase + slot * p.stage_bytes, wsm = zs + 16384;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_bf16(tmem, smem_desc_sw128(zs + k * 32),
+                 kTrans ? smem_desc_mn(wsm + k * 2048, 8192) : smem_desc_sw128(wsm + k * 32), idesc,
+                 step > 0 || k > 0);
+      mma_commit(&s_empty[slot]);
+      if (++slot == p.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    mma_commit(&s_done);
+  }
+  __syncwarp();
+
+  // Parts to shared memory (the stages are free once every MMA has completed), then each
+  // block of the cluster adds a share of the rows over the blocks.
+  float* part = reinterpret_cast<float*>(smem);
+  const int pitch = p.rp + 4;
+  wait_mmas(&s_done);
+  __syncwarp();
+  if (warp < 8) {
+    tc_fence_after();
+    const int i = (warp & 3) * 32 + lane;
+    for (int c = (warp >> 2) * 8; c < p.rp; c += 16) {
+      uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (steps > 0) {
+        tmem_ld8(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c, v);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int u = 0; u < 8; u += 4)
+        *reinterpret_cast<uint4*>(part + i * pitch + c + u) =
+            make_uint4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, tmem_cols);
+  cluster_sync_startup();
+  const int lo = rank * 128 / splits, hi = min(t.z, (rank + 1) * 128 / splits);
+  const int quads = p.r / 4;
+  const float f = p.scale ? p.scale[t.x] : 1.0f;
+  for (int i = tid; i < (hi - lo) * quads; i += kShrinkThreads) {
+    const int rr = lo + i / quads, c = i % quads * 4;
+    const uint32_t at = smem_u32(part + rr * pitch + c);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < splits; ++s) {
+      const float4 o = ld_peer16(map_peer(at, s));
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    const int64_t orow = p.order[t.y + rr];
+    *reinterpret_cast<uint2*>(p.out + orow * p.r + c) =
+        make_uint2(pack2(v.x * f, v.y * f), pack2(v.z * f, v.w * f));
+  }
+  cluster_sync_startup();  // peers may still be reading this block's part
+}
+
+// ------------------------------------------------------------------ expand
+struct ExpandArgs {
+  const int4* tiles;
+  const int32_t* order;
+  int cap16;
+  const uint16_t* h;  // b x r
+  const uint16_t* w;  // count x n x r, or (kTrans) count x r x n
+  const float* scale; // or null: 1
+  const uint16_t* base;
+  uint16_t* y;
+  int n, r, rp;
+  int stage_bytes;
+};
+
+constexpr int kExpandThreads = 352;  // 8 epilogue warps, 1 MMA warp, 2 warps that load W
+constexpr int kExpandSlots = 4;      // W stages and accumulators of 64 columns
+
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// base and y may be one buffer: plain loads and stores, kept in program order.
+__device__ __forceinline__ uint4 ld_stream(const void* ptr) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(ptr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_stream(void* ptr, uint4 v) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// Pairs (columns 8 j + 2 t, + 1) of lane t of a quad, j = 0 .. 3, become the eight
+// columns 8 t .. 8 t + 7: a 4 x 4 transpose of pairs over the quad's lanes.
+__device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = (t & bit) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float give = up ? v[2 * j + e] : v[2 * (j | bit) + e];
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, give, bit);
+        if (up)
+          v[2 * j + e] = got;
+        else
+          v[2 * (j | bit) + e] = got;
+      }
+    }
+  }
+}
+
+// Row tile blockIdx.y, columns in units of 64 split over the grid's x. The accumulator is
+// read in the 16x256b form, where a quad of lanes holds 32 columns of a row in pairs; W's
+// rows are stored permuted (or, kTrans, the pairs are transposed over the quad), so that
+// each lane owns 8 consecutive columns and a quad reads and writes 64 bytes of a row.
+template <bool kTrans>
+__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t s_full[kExpandSlots], s_done[kExpandSlots], s_free[kExpandSlots], s_end;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  if (static_cast<int>(blockIdx.y) >= p.tiles[0].y) return;
+  const int4 t = p.tiles[1 + p.cap16 + blockIdx.y];
+  const int units = p.n / 64;
+  const int u0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * units / gridDim.x);
+  const int count = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * units / gridDim.x) - u0;
+  if (t.x < 0) {  // rows without adapter: base itself
+    if (p.base == p.y) return;
+    for (int i = tid; i < t.z * count * 8; i += kExpandThreads) {
+      const int64_t at = static_cast<int64_t>(p.order[t.y + i / (count * 8)]) * p.n + u0 * 64 +
+                         i % (count * 8) * 8;
+      st_stream(p.y + at, p.base ? ld_stream(p.base + at) : make_uint4(0, 0, 0, 0));
+    }
+    return;
+  }
+  uint8_t* smem = align1k(smem_raw);
+  const uint32_t sh = smem_u32(smem);
+  const int kt = (p.rp + 63) / 64;  // 64-wide tiles of the reduction
+  const uint32_t sw = sh + kt * 16384;
+  if (tid == 0) {
+    for (int i = 0; i < kExpandSlots; ++i) {
+      mbar_init(&s_full[i], 2);
+      mbar_init(&s_done[i], 1);
+      mbar_init(&s_free[i], 8);
+    }
+    mbar_init(&s_end, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, 64 * kExpandSlots);
+    tmem_relinquish();
+  }
+  {  // H: 128 rows x rp
+    const int chunks = p.rp / 8;
+    for (int i = tid; i < 128 * chunks; i += kExpandThreads) {
+      const int rr = i / chunks, c = i % chunks;
+      const bool ok = rr < t.z && c * 8 < p.r;
+      const int64_t row = ok ? p.order[t.y + rr] : 0;
+      cp16(sh + (c >> 3) * 16384 + sw128(rr, c & 7), p.h + row * p.r + (ok ? c * 8 : 0), ok);
+    }
+    cp_commit();
+    cp_wait<0>();
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp < 8) {
+    const int t4 = lane & 3;
+    int64_t at[4];  // this lane's 8 columns of unit 0 in its four rows
+    bool ok[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rr = (warp & 3) * 32 + i * 8 + (lane >> 2);
+      ok[i] = rr < t.z;
+      at[i] = (ok[i] ? static_cast<int64_t>(p.order[t.y + rr]) : 0) * p.n + u0 * 64 + (warp >> 2) * 32 +
+              t4 * 8;
+    }
+    const float f = p.scale ? p.scale[t.x] : 1.0f;
+    uint4 b0[4], b1[4];
+    auto fetch = [&](int u, uint4 (&b)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        b[i] = make_uint4(0, 0, 0, 0);
+        if (p.base && ok[i] && u < count) b[i] = ld_stream(p.base + at[i] + u * 64);
+      }
+    };
+    auto finish = [&](int u, uint4 (&b)[4]) -> bool {
+      const int slot = u % kExpandSlots;
+      if (!warp_wait(&s_done[slot], (u / kExpandSlots) & 1, &s_abort, kSiteDone)) return false;
+      tc_fence_after();
+      uint32_t v[2][16];
+      const uint32_t ta =
+          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + (warp >> 2) * 32;
+      tmem_ld_16x256b_x4(ta, v[0]);
+      tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[slot]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // rows lane / 4 + 8 i
+        float a[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
+        if constexpr (kTrans) quad_transpose(a, t4);
+        const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
+        if (ok[i]) st_stream(p.y + at[i] + u * 64, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      return true;
+    };
+    fetch(0, b0);
+    for (int u = 0; u < count; u += 2) {
+      fetch(u + 1, b1);
+      if (!finish(u, b0)) break;
+      if (u + 1 >= count) break;
+      fetch(u + 2, b0);
+      if (!finish(u + 1, b1)) break;
+    }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(64) | (kTrans ? kBMajorMn : 0u);
+      for (int u = 0; u < count; ++u) {
+        const int slot = u % kExpandSlots;
+        const uint32_t ph = (u / kExpandSlots) & 1;
+        if (!wait(&s_full[slot], ph, &s_abort, kSiteFull)) break;
+        if (u >= kExpandSlots && !wait(&s_free[slot], ph ^ 1u, &s_abort, kSiteAccEmpty)) break;
+        tc_fence_after();
+        const uint32_t ws = sw + slot * p.stage_bytes;
+        for (int k = 0; k < p.rp / 16; ++k)
+          mma_bf16(tmem + slot * 64, smem_desc_sw128(sh + (k >> 2) * 16384 + (k & 3) * 32),
+                   kTrans ? smem_desc_mn(ws + k * 2048, 0)
+                          : smem_desc_sw128(ws + (k >> 2) * 8192 + (k & 3) * 32),
+                   idesc, k > 0);
+        mma_commit(&s_done[slot]);
+      }
+      mma_commit(&s_end);
+      wait_mmas(&s_end);
+    }
+  } else {
+    const int l = tid - 288;
+    const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.n * p.r;
+    const int chunks = p.rp / 8;
+    for (int u = 0; u <= count; ++u) {
+      if (u < count) {
+        const int slot = u % kExpandSlots;
+        // the MMAs that read this stage are done when their accumulator is
+        if (u >= kExpandSlots &&
+            !warp_wait(&s_done[slot], ((u / kExpandSlots) & 1) ^ 1u, &s_abort, kSiteEmpty))
+          break;
+        const uint32_t ws = sw + slot * p.stage_bytes;
+        const int col = (u0 + u) * 64;
+        if constexpr (kTrans) {
+          for (int i = l; i < p.rp * 8; i += 64) {
+            const int k = i >> 3;
+            cp16(ws + sw128(k, i & 7),
+                 wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + col + (i & 7) * 8, k < p.r);
+          }
+        } else {
+          for (int i = l; i < 64 * chunks; i += 64) {
+            const int nr = i / chunks, c = i % chunks;
+            // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
+            const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
+            const bool ok = c * 8 < p.r;
+            cp16(ws + (c >> 3) * 8192 + sw128(q, c & 7),
+                 wg + static_cast<int64_t>(col + nr) * p.r + (ok ? c * 8 : 0), ok);
+          }
+        }
+        cp_commit();
+      }
+      if (u > 0) {
+        if (u < count)
+          cp_wait<1>();
+        else
+          cp_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_full[(u - 1) % kExpandSlots]);
+      }
+    }
+    cp_wait<0>();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, 64 * kExpandSlots);
+}
+
+// ------------------------------------------------------------------- outer
+struct OuterArgs {
+  const int4* tiles;
+  const int32_t* order;
+  const int32_t* first128;  // tiles of 128 rows before each group; [count]: all with adapter
+  int cap16, count;
+  const uint16_t* z;
+  int64_t ldz;
+  const int8_t* q;
+  const float* sq;
+  const uint16_t* h;  // b x r
+  const float* scale; // or null: 1
+  uint16_t* out;      // count x k x r, or (kByRank) count x r x k
+  float* part;        // 2 gridDim.y slots shaped like one group's output
+  int k, r, rp;
+  int stages, htiles; // Z stages, H tiles in shared memory
+  uint32_t tmem_cols;
+};
+
+constexpr int kOuterThreads = 416;  // 8 loading warps, 1 MMA warp, 4 drain warps (9 .. 12)
+constexpr int kOuterStages = 4;  // at most
+
+__host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles) {
+  return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
+}
+
+// A slice of Z's 128-column blocks (blockIdx.x), the row tiles of chunk blockIdx.y. Tiles of one
+// group form a run, summed in tensor memory (lane = column of Z, column = rank). A run that
+// is its whole group is rounded into `out`; one that the chunk's ends cut leaves its fp32
+// sums in the chunk's slot (0: the run starts the chunk, else 1) for the finish kernel.
+template <bool kCodes, bool kByRank>
+__global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t s_full[kOuterStages], s_empty[kOuterStages], s_hempty[kOuterStages], s_run,
+      s_free, s_end;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  const int total = p.first128[p.count];
+  const int begin = chunk_begin(blockIdx.y, gridDim.y, total);
+  const int end = chunk_begin(blockIdx.y + 1, gridDim.y, total);
+  const int blk0 = blockIdx.x * (p.k / 128) / gridDim.x;
+  const int nb = (blockIdx.x + 1) * (p.k / 128) / gridDim.x - blk0;
+  const int stages = p.stages;
+  if (begin == end) return;
+  uint8_t* smem = align1k(smem_raw);
+  const uint32_t sz = smem_u32(smem);
+  const int hblocks = (p.rp + 63) / 64;
+  const uint32_t sh = sz + stages * 32768;  // p.htiles H tiles of hblocks x 16 KB
+  const int4* tiles = p.tiles + 1 + p.cap16;
+  if (tid == 0) {
+    for (int i = 0; i < kOuterStages; ++i) {
+      mbar_init(&s_full[i], 8);
+      mbar_init(&s_empty[i], 1);
+      mbar_init(&s_hempty[i], 1);
+    }
+    mbar_init(&s_end, 1);
+    mbar_init(&s_run, 1);
+    mbar_init(&s_free, 4);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int steps = (end - begin) * nb;
+
+  if (warp < 8) {
+    const int r0 = tid >> 3, ch = tid & 7;  // rows r0 + 32 j, chunk ch (or 16 codes)
+    // position of the loads: step -> (tile, block), the tile's rows
+    int ltile = begin, lblk = 0;
+    int64_t row[4];
+    bool ok[4];
+    auto load_rows = [&]() {
+      const int4 t = ltile < end ? tiles[ltile] : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ok[j] = r0 + 32 * j < t.z;
+        row[j] = ok[j] ? p.order[t.y + r0 + 32 * j] : 0;
+      }
+    };
+    load_rows();
+    uint4 raw[kAhead][4];
+    float sc[kAhead][4];
+    auto fetch = [&](uint4 (&v)[4], float (&s)[4]) {  // codes of the load position, then advance
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        s[j] = 0.0f;
+        if (ok[j]) {
+          v[j] = __ldg(reinterpret_cast<const uint4*>(p.q + row[j] * p.k + (blk0 + lblk) * 128 + ch * 16));
+          s[j] = __ldg(p.sq + row[j] * (p.k >> 7) + blk0 + lblk);
+        }
+      }
+      if (++lblk == nb) {
+        lblk = 0;
+        ++ltile;
+        load_rows();
+      }
+    };
+    if constexpr (kCodes) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) fetch(raw[a], sc[a]);
+    }
+    int tile = begin, blk = 0, slot = 0, hs = 0;
+    uint32_t phase = 0, hphase = 0;
+    bool alive = true;
+    const int lag = stages - 1;
+    for (int base = 0; base < steps && alive; base += kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int step = base + a;
+        if (step >= steps) break;
+        if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
+          alive = false;
+          break;
+        }
+        if (blk == 0) {  // the tile's H comes with its first block
+          if (tile - begin >= p.htiles &&
+              !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty)) {
+            alive = false;
+            break;
+          }
+          const int4 t = tiles[tile];
+          const int chunks = hblocks * 8;
+          for (int i = tid; i < 128 * chunks; i += 256) {
+            const int rr = i / chunks, c = i % chunks;
+            const bool in = rr < t.z && c * 8 < p.r;
+            const int64_t hr = in ? p.order[t.y + rr] : 0;
+            cp16(sh + (hs * hblocks + (c >> 3)) * 16384 + sw128(rr, c & 7),
+                 p.h + hr * p.r + (in ? c * 8 : 0), in);
+          }
+        }
+        const uint32_t zs = sz + slot * 32768;
+        if constexpr (kCodes) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 lo, hi;
+            dequant16(raw[a][j], sc[a][j], lo, hi);
+            const uint32_t half = zs + (ch >> 2) * 16384;
+            sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3)), lo);
+            sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3) + 1), hi);
+          }
+          fetch(raw[a], sc[a]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
+                   p.z + row[j] * p.ldz + (blk0 + blk) * 128 + half * 64 + ch * 8, ok[j]);
+        }
+        cp_commit();
+        if (++blk == nb) {
+          blk = 0;
+          ++tile;
+          if (++hs == p.htiles) {
+            hs = 0;
+            hphase ^= 1u;
+          }
+          if constexpr (!kCodes) {
+            ltile = tile;
+            load_rows();
+          }
+        }
+        if (step >= lag) {
+          cp_wait_n(lag);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_full[(step - lag) % stages]);
+        }
+        if (++slot == stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    cp_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (alive && lane == 0)
+      for (int s = max(0, steps - lag); s < steps; ++s) mbar_arrive(&s_full[s % stages]);
+  } else if (warp == 8) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(p.rp) | kAMajorMn | kBMajorMn;
+      int runs = 0, slot = 0, hs = 0;
+      uint32_t phase = 0;
+      bool alive = true;
+      bool fresh = true;
+      for (int tile = begin; tile < end && alive; ++tile) {
+        const uint32_t hb = sh + hs * hblocks * 16384;
+        for (int b = 0; b < nb; ++b) {
+          if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t zs = sz + slot * 32768;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 128 rows: 8 steps of 16
+            mma_bf16(tmem + b * p.rp, smem_desc_mn(zs + k * 2048, 16384),
+                     smem_desc_mn(hb + k * 2048, 16384), idesc, !fresh || k > 0);
+          mma_commit(&s_empty[slot]);
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!alive) break;
+        mma_commit(&s_hempty[hs]);
+        if (++hs == p.htiles) hs = 0;
+        fresh = tile + 1 < end && tiles[tile + 1].x != tiles[tile].x;
+        if (fresh || tile + 1 == end) {
+          mma_commit(&s_run);
+          if (fresh && !wait(&s_free, runs & 1, &s_abort, kSiteAccEmpty)) {
+            alive = false;
+            break;
+          }
+          ++runs;
+          tc_fence_after();
+        }
+      }
+      mma_commit(&s_end);
+      wait_mmas(&s_end);
+    }
+  } else {
+    const int sub = warp & 3;  // tensor-memory lanes of this warp
+    const int64_t size = static_cast<int64_t>(p.k) * p.r;
+    int runs = 0;
+    for (int tile = begin; tile < end;) {
+      const int g = tiles[tile].x;
+      const int first = tile;
+      const int gb = p.first128[g], ge = p.first128[g + 1];
+      const int stop = min(end, ge);
+      tile = stop;
+      if (!warp_wait(&s_run, runs & 1, &s_abort, kSiteDrain)) break;
+      ++runs;
+      tc_fence_after();
+      const bool whole = first == gb && stop == ge;
+      const float f = p.scale ? p.scale[g] : 1.0f;
+      float* part = p.part + (2 * blockIdx.y + (first == begin ? 0 : 1)) * size;
+      uint16_t* out = p.out + g * size;
+      for (int b = 0; b < nb; ++b) {
+        const int64_t j = (blk0 + b) * 128 + sub * 32 + lane;
+        for (int c = 0; c < p.r; c += 8) {
+          uint32_t v[8];
+          tmem_ld8(tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * p.rp + c, v);
+          tmem_wait_ld();
+          float o[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) o[u] = f * __uint_as_float(v[u]);
+          if (kByRank) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (whole) {
+                const uint32_t h2 = pack2(o[u], 0.0f);
+                out[(c + u) * static_cast<int64_t>(p.k) + j] = static_cast<uint16_t>(h2);
+              } else {
+                part[(c + u) * static_cast<int64_t>(p.k) + j] = o[u];
+              }
+            }
+          } else if (whole) {
+            *reinterpret_cast<uint4*>(out + j * p.r + c) =
+                make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+          } else {
+            *reinterpret_cast<float4*>(part + j * p.r + c) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(part + j * p.r + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, p.tmem_cols);
+}
+
+// The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
+// zeros for the groups without rows. 4 elements a thread.
+struct FinishArgs {
+  const int32_t* first128;
+  int count;
+  struct {
+    const float* part;
+    uint16_t* out;
+    int64_t size;  // elements of a group, a multiple of 1024
+    int chunks;
+  } side[2];
+};
+
+__global__ void __launch_bounds__(256) finish_kernel(const FinishArgs p) {
+  pdl_wait();
+  const auto& s = p.side[blockIdx.z];
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (at >= s.size) return;
+  const int g = blockIdx.y, total = p.first128[p.count];
+  const int gb = p.first128[g], ge = p.first128[g + 1];
+  uint16_t* out = s.out + g * s.size + at;
+  if (gb == ge) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+    return;
+  }
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  int c = static_cast<int>(static_cast<int64_t>(gb) * s.chunks / total);
+  while (chunk_begin(c + 1, s.chunks, total) <= gb) ++c;
+  if (chunk_begin(c + 1, s.chunks, total) >= ge) return;  // inside one chunk: already written
+  for (; c < s.chunks; ++c) {
+    const int cb = chunk_begin(c, s.chunks, total);
+    if (cb >= ge) break;
+    if (chunk_begin(c + 1, s.chunks, total) == cb) continue;  // an empty chunk
+    const float4 o = *reinterpret_cast<const float4*>(s.part + (2 * c + (gb > cb ? 1 : 0)) * s.size + at);
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
+// -------------------------------------------------------------------- host
+int tiles_estimate(const AdapterCall& c) {
+  // full tiles and half a partial one per adapter
+  return std::max(1, std::min(row_tiles_cap(c.g.b, c.g.count, 128), c.g.b / 128 + (c.g.count + 1) / 2));
+}
+
+template <typename Args>
+cudaError_t launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, bool pdl,
+                   const Args& args, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = 1;
+    at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+int round16(int r) { return (r + 15) / 16 * 16; }
+
+// trans: W is count x k x r (the backward pass's B).
+cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, int64_t ldz, int k,
+                          const uint16_t* w, const float* scale, uint16_t* out, cudaStream_t st) {
+  const bool codes = !trans && c.xq8;
+  const int rp = round16(c.r);
+  ShrinkArgs p{c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
+               codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, w, scale, out, k, c.r, rp, 0, 0};
+  p.stage_bytes = 16384 + (trans ? (rp + 63) / 64 * 8192 : rp * 128);
+  // two blocks per SM: about 108 KB each, of which the parts need 128 x (rp + 4) fp32
+  p.stages = std::max(2, std::min(kShrinkMaxStages, 108 * 1024 / p.stage_bytes));
+  const int smem = std::max(p.stages * p.stage_bytes, 128 * (rp + 4) * 4) + 1024;
+  // split the reduction until two blocks per SM are busy, 8 blocks of one cluster at most
+  int splits = 1;
+  while (splits < 8 && tiles_estimate(c) * splits * 2 <= 2 * kSms) splits *= 2;
+  const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
+  auto kernel = trans ? shrink_kernel<false, true>
+                      : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
+  return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
+}
+
+cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, const uint16_t* w, int n,
+                          const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
+  const int rp = round16(c.r);
+  ExpandArgs p{c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, w, scale, c.base, y,
+               n, c.r, rp, trans ? rp * 128 : (rp + 63) / 64 * 8192};
+  const int smem = (rp + 63) / 64 * 16384 + kExpandSlots * p.stage_bytes + 1024;
+  // column slices of at least 256 columns so that the last wave of blocks is nearly full
+  const int tiles = tiles_estimate(c);
+  int best = 1;
+  double best_eff = 0.0;
+  for (int s = 1; s <= std::max(1, n / 256); ++s) {
+    const double waves = double(tiles) * s / (2 * kSms);
+    const double eff = waves / std::max(1.0, double(int64_t(waves + 0.999999)));
+    if (eff > best_eff + 0.02) best = s, best_eff = eff;
+    if (waves > 4.0) break;
+  }
+  const dim3 grid(best, row_tiles_cap(c.g.b, c.g.count, 128));
+  return launch(trans ? expand_kernel<true> : expand_kernel<false>, grid, kExpandThreads, smem, 1, pdl,
+                p, st);
+}
+
+// Column blocks and row chunks of the outer kernel: one thread block per SM, the split that
+// moves the fewest bytes through the busiest block (Z, H again for every slice, parts).
+struct OuterPlan {
+  int slices, chunks, stages, htiles;
+  uint32_t cols;
+};
+OuterPlan outer_plan(int64_t b, int64_t count, int k, int r) {
+  const int rp = round16(r), blocks = k / 128;
+  const int tiles = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>(row_tiles_cap(b, count, 128), b / 128 + (count + 1) / 2)));
+  OuterPlan best{blocks, 1, 0, 0, 0};
+  int best_nb = 1;
+  double cost = 1e30;
+  for (int nb = 1; nb <= 512 / rp && nb <= blocks; ++nb) {
+    const int slices = (blocks + nb - 1) / nb;
+    const int chunks = std::max(1, std::min(tiles, kSms / slices));
+    const double waves = double((int64_t(slices) * chunks + kSms - 1) / kSms);
+    const double each = double((tiles + chunks - 1) / chunks) * (nb * 32768.0 + 256.0 * rp) +
+                        (chunks > 1 ? 2.0 * nb * 128 * rp * 4 : 0.0);
+    if (waves * each < cost) cost = waves * each, best_nb = nb, best = OuterPlan{slices, chunks, 0, 0, 0};
+  }
+  best.cols = 32;
+  while (static_cast<int>(best.cols) < best_nb * rp) best.cols *= 2;
+  // A tile's H is loaded with its first Z block. The loads run stages - 1 steps ahead of what
+  // they have handed over, so an H tile may be reused only htiles * nb >= nb + stages - 1
+  // steps later, or both sides would wait for each other (nb: the smallest slice's).
+  const int nb_min = blocks / best.slices, hbytes = (rp + 63) / 64 * 16384;
+  for (best.stages = kOuterStages;; --best.stages) {
+    best.htiles = std::max(2, 1 + (best.stages - 1 + nb_min - 1) / nb_min);
+    if (best.stages * 32768 + best.htiles * hbytes <= 224 * 1024) break;
+  }
+  return best;
+}
+
+template <bool kCodes, bool kByRank>
+cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint16_t* z, int64_t ldz,
+                         int k, const uint16_t* h, const float* scale, uint16_t* out, float* part,
+                         cudaStream_t st) {
+  const int rp = round16(c.r);
+  const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
+  OuterArgs p{c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
+              out, part, k, c.r, rp, plan.stages, plan.htiles, plan.cols};
+  const int smem = plan.stages * 32768 + plan.htiles * ((rp + 63) / 64) * 16384 + 1024;
+  return launch(outer_kernel<kCodes, kByRank>, dim3(plan.slices, plan.chunks), kOuterThreads, smem, 1,
+                false, p, st);
+}
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct BackwardSpace {
+  size_t dh, pa, pb, bytes;
+};
+BackwardSpace backward_space(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
+  BackwardSpace s;
+  s.dh = 0;
+  s.pa = up256(size_t(b) * r * 2);
+  s.pb = s.pa + up256(size_t(2) * outer_plan(b, count, int(m), int(r)).chunks * m * r * 4);
+  s.bytes = s.pb + up256(size_t(2) * outer_plan(b, count, int(n), int(r)).chunks * n * r * 4);
+  return s;
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_adapter_status(int* code) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_adapter_status, sizeof(int));
+  if (e != cudaSuccess || *code == 0) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_adapter_status, &zero, sizeof(int));
+}
+
+cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
+  cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
+  if (e != cudaSuccess) return e;
+  return launch_expand(c, false, c.h, c.bm, c.n, c.scale, c.y, true, st);
+}
+
+size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
+  return backward_space(b, m, n, r, count).bytes;
+}
+
+cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
+  const BackwardSpace s = backward_space(c.g.b, c.m, c.n, c.r, c.g.count);
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  uint16_t* dh = reinterpret_cast<uint16_t*>(ws + s.dh);
+  float* pa = reinterpret_cast<float*>(ws + s.pa);
+  float* pb = reinterpret_cast<float*>(ws + s.pb);
+  const OuterPlan oa = outer_plan(c.g.b, c.g.count, c.m, c.r);
+  const OuterPlan ob = outer_plan(c.g.b, c.g.count, c.n, c.r);
+  cudaError_t e = cudaSuccess;
+  if (c.g.b > 0) {
+    e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
+    if (e == cudaSuccess)
+      e = launch_outer<false, false>(c, ob, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, st);
+    if (e == cudaSuccess)
+      e = c.xq8 ? launch_outer<true, true>(c, oa, nullptr, 0, c.m, dh, nullptr, c.da, pa, st)
+                : launch_outer<false, true>(c, oa, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, st);
+    if (e == cudaSuccess) e = launch_expand(c, true, dh, c.a, c.m, nullptr, c.dx, false, st);
+    if (e != cudaSuccess) return e;
+  }
+  FinishArgs f{first128_of(c.g), c.g.count, {}};
+  f.side[0] = {pa, c.da, int64_t(c.m) * c.r, oa.chunks};
+  f.side[1] = {pb, c.db, int64_t(c.n) * c.r, ob.chunks};
+  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 1023) / 1024;
+  return launch(finish_kernel, dim3(static_cast<unsigned>(blocks), c.g.count, 2), 256, 0, 1, false, f, st);
+}
+
+}  // namespace twq

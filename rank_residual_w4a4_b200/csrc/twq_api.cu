@@ -450,7 +450,8 @@ twq_status twq_row_groups_sizes(int64_t b, int64_t count, size_t bytes_out[3]) {
   bytes_out[0] = static_cast<size_t>(b) * 4;
   bytes_out[1] = static_cast<size_t>(count + 1) * 4;
   bytes_out[2] = 16 * (1 + static_cast<size_t>(twq::row_tiles_cap(b, count, 16)) +
-                       static_cast<size_t>(twq::row_tiles_cap(b, count, 128)));
+                       static_cast<size_t>(twq::row_tiles_cap(b, count, 128))) +
+                 4 * static_cast<size_t>(count + 1);
   return TWQ_OK;
 }
 
@@ -524,12 +525,13 @@ twq_status twq_device_status(int* code) {
   if (!code) return TWQ_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return TWQ_ERR_CUDA;
-  int c1 = 0, c2 = 0, c3 = 0;
+  int c1 = 0, c2 = 0, c3 = 0, c4 = 0;
   e = twq::read_and_clear_device_status(&c1);
   if (e == cudaSuccess) e = twq::read_and_clear_decode_status(&c2);
   if (e == cudaSuccess) e = twq::read_and_clear_pair_status(&c3);
+  if (e == cudaSuccess) e = twq::read_and_clear_adapter_status(&c4);
   if (e != cudaSuccess) return TWQ_ERR_CUDA;
-  *code = c1 ? c1 : (c2 ? c2 : c3);
+  *code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : c4));
   return *code ? TWQ_ERR_DEVICE : TWQ_OK;
 }
 
@@ -567,7 +569,7 @@ int twq_launches_per_call(const char* ep) {
   if (!strcmp(ep, "twq_fold_transforms")) return 5;
   if (!strcmp(ep, "twq_group_rows")) return 1;
   if (!strcmp(ep, "twq_adapter_linear") || !strcmp(ep, "twq_adapter_linear_i8")) return 2;
-  if (!strcmp(ep, "twq_adapter_backward") || !strcmp(ep, "twq_adapter_backward_i8")) return 4;
+  if (!strcmp(ep, "twq_adapter_backward") || !strcmp(ep, "twq_adapter_backward_i8")) return 5;
   return -1;
 }
 

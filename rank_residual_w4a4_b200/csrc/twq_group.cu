@@ -60,7 +60,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     group_rows_kernel(const int32_t* __restrict__ ids, int b, int count, int warps, int chunk,
                       int32_t* __restrict__ order, int32_t* __restrict__ offsets,
-                      int4* __restrict__ tiles, int cap16) {
+                      int4* __restrict__ tiles, int32_t* __restrict__ tiles_before,
+                      int cap16) {
   extern __shared__ int smem[];
   __shared__ int ws[3][kWarps];
   const int keys = count + 1;
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     start[k] = v[0];
     first16[k] = v[1];
     first128[k] = v[2];
+    tiles_before[k] = v[2];
     offsets[k] = v[0];  // the last key's start is the end of group count - 1
     v[0] += run;
     v[1] += (run + 15) >> 4;
@@ -165,7 +167,8 @@ cudaError_t launch(const int32_t* ids, int b, const RowGroupsView& g, cudaStream
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   group_rows_kernel<T><<<1, kThreads, bytes, st>>>(
-      ids, b, g.count, warps, chunk, g.order, g.offsets, g.tiles, row_tiles_cap(b, g.count, 16));
+      ids, b, g.count, warps, chunk, g.order, g.offsets, g.tiles, first128_of(g),
+      row_tiles_cap(b, g.count, 16));
   return cudaGetLastError();
 }
 
