@@ -76,22 +76,14 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) 
                "r"(valid ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+// One arrival on `bar` (whose count includes it) once all cp.async of this thread so far have
+// landed. The thread goes on at once, so the depth of the loads is the number of stages, not
+// what the loading threads can wait for. The reader of the data fences the proxies.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
-// At most `pending` (0 .. 5) groups of this thread in flight.
-__device__ __forceinline__ void cp_wait_n(int pending) {
-  switch (pending) {
-    case 0: cp_wait<0>(); break;
-    case 1: cp_wait<1>(); break;
-    case 2: cp_wait<2>(); break;
-    case 3: cp_wait<3>(); break;
-    case 4: cp_wait<4>(); break;
-    default: cp_wait<5>(); break;
-  }
-}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Offset of 16-byte chunk c of row `row` in a tile of 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int row, int c) {
@@ -199,7 +191,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
   const uint32_t tmem_cols = p.rp <= 32 ? 32 : (p.rp <= 64 ? 64 : 128);
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s_full[i], 8);
+      mbar_init(&s_full[i], kCodes ? 264 : 256);
       mbar_init(&s_empty[i], 1);
     }
     mbar_init(&s_done, 1);
@@ -249,7 +241,6 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) fetch(a, raw[a], sc[a]);
     }
-    const int lag = p.stages - 1;
     const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.r * p.k;
     int slot = 0;
     uint32_t phase = 0;
@@ -294,12 +285,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
           for (int j = 0; j < kRows; ++j)
             cp16(zs + sw128(r0 + j * 32, ch), p.z + row[j] * p.ldz + col + ch * 8, ok[j]);
         }
-        cp_commit();
-        if (step >= lag) {  // the stage issued `lag` steps ago has landed
-          cp_wait_n(lag);
+        cp_arrive(&s_full[slot]);
+        if constexpr (kCodes) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[(step - lag) % p.stages]);
+          if (lane == 0) mbar_arrive(&s_full[slot]);
         }
         if (++slot == p.stages) {
           slot = 0;
@@ -307,17 +297,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
         }
       }
     }
-    cp_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (alive && lane == 0)
-      for (int s = max(0, steps - lag); s < steps; ++s) mbar_arrive(&s_full[s % p.stages]);
+    cp_wait_all();
   } else if (lane == 0) {
     const uint32_t idesc = idesc_bf16(p.rp) | (kTrans ? kBMajorMn : 0u);
     int slot = 0;
     uint32_t phase = 0;
     for (int step = 0; step < steps; ++step) {
       if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) break;
+      fence_proxy_async_smem();
       tc_fence_after();
       const uint32_t zs = sbase + slot * p.stage_bytes, wsm = zs + 16384;
 #pragma unroll
@@ -474,7 +461,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
   const uint32_t sw = sh + kt * 16384;
   if (tid == 0) {
     for (int i = 0; i < kExpandSlots; ++i) {
-      mbar_init(&s_full[i], 2);
+      mbar_init(&s_full[i], 64);
       mbar_init(&s_done[i], 1);
       mbar_init(&s_free[i], 8);
     }
@@ -494,8 +481,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
       const int64_t row = ok ? p.order[t.y + rr] : 0;
       cp16(sh + (c >> 3) * 16384 + sw128(rr, c & 7), p.h + row * p.r + (ok ? c * 8 : 0), ok);
     }
-    cp_commit();
-    cp_wait<0>();
+    cp_wait_all();
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -570,6 +556,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
         const uint32_t ph = (u / kExpandSlots) & 1;
         if (!wait(&s_full[slot], ph, &s_abort, kSiteFull)) break;
         if (u >= kExpandSlots && !wait(&s_free[slot], ph ^ 1u, &s_abort, kSiteAccEmpty)) break;
+        fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t ws = sw + slot * p.stage_bytes;
         for (int k = 0; k < p.rp / 16; ++k)
@@ -586,44 +573,33 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
     const int l = tid - 288;
     const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.n * p.r;
     const int chunks = p.rp / 8;
-    for (int u = 0; u <= count; ++u) {
-      if (u < count) {
-        const int slot = u % kExpandSlots;
-        // the MMAs that read this stage are done when their accumulator is
-        if (u >= kExpandSlots &&
-            !warp_wait(&s_done[slot], ((u / kExpandSlots) & 1) ^ 1u, &s_abort, kSiteEmpty))
-          break;
-        const uint32_t ws = sw + slot * p.stage_bytes;
-        const int col = (u0 + u) * 64;
-        if constexpr (kTrans) {
-          for (int i = l; i < p.rp * 8; i += 64) {
-            const int k = i >> 3;
-            cp16(ws + sw128(k, i & 7),
-                 wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + col + (i & 7) * 8, k < p.r);
-          }
-        } else {
-          for (int i = l; i < 64 * chunks; i += 64) {
-            const int nr = i / chunks, c = i % chunks;
-            // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
-            const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
-            const bool ok = c * 8 < p.r;
-            cp16(ws + (c >> 3) * 8192 + sw128(q, c & 7),
-                 wg + static_cast<int64_t>(col + nr) * p.r + (ok ? c * 8 : 0), ok);
-          }
+    for (int u = 0; u < count; ++u) {
+      const int slot = u % kExpandSlots;
+      // the MMAs that read this stage are done when their accumulator is
+      if (u >= kExpandSlots &&
+          !warp_wait(&s_done[slot], ((u / kExpandSlots) & 1) ^ 1u, &s_abort, kSiteEmpty))
+        break;
+      const uint32_t ws = sw + slot * p.stage_bytes;
+      const int col = (u0 + u) * 64;
+      if constexpr (kTrans) {
+        for (int i = l; i < p.rp * 8; i += 64) {
+          const int k = i >> 3;
+          cp16(ws + sw128(k, i & 7),
+               wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + col + (i & 7) * 8, k < p.r);
         }
-        cp_commit();
+      } else {
+        for (int i = l; i < 64 * chunks; i += 64) {
+          const int nr = i / chunks, c = i % chunks;
+          // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
+          const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
+          const bool ok = c * 8 < p.r;
+          cp16(ws + (c >> 3) * 8192 + sw128(q, c & 7),
+               wg + static_cast<int64_t>(col + nr) * p.r + (ok ? c * 8 : 0), ok);
+        }
       }
-      if (u > 0) {
-        if (u < count)
-          cp_wait<1>();
-        else
-          cp_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_full[(u - 1) % kExpandSlots]);
-      }
+      cp_arrive(&s_full[slot]);
     }
-    cp_wait<0>();
+    cp_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -684,7 +660,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
   const int4* tiles = p.tiles + 1 + p.cap16;
   if (tid == 0) {
     for (int i = 0; i < kOuterStages; ++i) {
-      mbar_init(&s_full[i], 8);
+      mbar_init(&s_full[i], kCodes ? 264 : 256);
       mbar_init(&s_empty[i], 1);
       mbar_init(&s_hempty[i], 1);
     }
@@ -744,7 +720,6 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
     int tile = begin, blk = 0, slot = 0, hs = 0;
     uint32_t phase = 0, hphase = 0;
     bool alive = true;
-    const int lag = stages - 1;
     for (int base = 0; base < steps && alive; base += kAhead) {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
@@ -789,7 +764,12 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
               cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
                    p.z + row[j] * p.ldz + (blk0 + blk) * 128 + half * 64 + ch * 8, ok[j]);
         }
-        cp_commit();
+        cp_arrive(&s_full[slot]);
+        if constexpr (kCodes) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_full[slot]);
+        }
         if (++blk == nb) {
           blk = 0;
           ++tile;
@@ -802,23 +782,13 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
             load_rows();
           }
         }
-        if (step >= lag) {
-          cp_wait_n(lag);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[(step - lag) % stages]);
-        }
         if (++slot == stages) {
           slot = 0;
           phase ^= 1u;
         }
       }
     }
-    cp_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (alive && lane == 0)
-      for (int s = max(0, steps - lag); s < steps; ++s) mbar_arrive(&s_full[s % stages]);
+    cp_wait_all();
   } else if (warp == 8) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(p.rp) | kAMajorMn | kBMajorMn;
@@ -833,6 +803,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
             alive = false;
             break;
           }
+          fence_proxy_async_smem();
           tc_fence_after();
           const uint32_t zs = sz + slot * 32768;
 #pragma unroll
@@ -1058,9 +1029,8 @@ OuterPlan outer_plan(int64_t b, int64_t count, int k, int r) {
   }
   best.cols = 32;
   while (static_cast<int>(best.cols) < best_nb * rp) best.cols *= 2;
-  // A tile's H is loaded with its first Z block. The loads run stages - 1 steps ahead of what
-  // they have handed over, so an H tile may be reused only htiles * nb >= nb + stages - 1
-  // steps later, or both sides would wait for each other (nb: the smallest slice's).
+  // A tile's H is loaded with its first Z block: as many H tiles as the Z stages reach ahead
+  // (nb_min: the blocks of the smallest slice).
   const int nb_min = blocks / best.slices, hbytes = (rp + 63) / 64 * 16384;
   for (best.stages = kOuterStages;; --best.stages) {
     best.htiles = std::max(2, 1 + (best.stages - 1 + nb_min - 1) / nb_min);
