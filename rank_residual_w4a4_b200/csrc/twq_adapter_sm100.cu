@@ -83,6 +83,16 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Offset of 16-byte chunk c of row `row` in a tile of 128-byte rows, 128-byte swizzle.
@@ -128,6 +138,19 @@ __device__ __forceinline__ void dequant16(uint4 q, float s, uint4& a, uint4& b) 
   b = make_uint4(p2.x, p2.y, p3.x, p3.y);
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds4(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -161,9 +184,12 @@ struct ShrinkArgs {
   int stages, stage_bytes;
 };
 
-constexpr int kShrinkThreads = 288;  // 8 loading warps, then epilogue; 1 MMA warp
+constexpr int kShrinkThreads = 352;  // 8 warps that load Z, then epilogue; 1 MMA warp; 2 load W
 constexpr int kShrinkMaxStages = 6;
-constexpr int kAhead = 3;  // codes: stages of loads held in registers
+// Codes are converted by the thread that loaded them: it keeps kAhead steps of its own codes
+// and scales in flight into a private part of shared memory, as it would in registers.
+constexpr int kAhead = 4;
+constexpr int kRawStep = 8192 + 2048;  // 128 x 64 codes; a scale for each 16
 
 // One row tile per cluster, whose blocks split the reduction over k and add their parts
 // through distributed shared memory in rank order.
@@ -191,7 +217,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
   const uint32_t tmem_cols = p.rp <= 32 ? 32 : (p.rp <= 64 ? 64 : 128);
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s_full[i], kCodes ? 264 : 256);
+      mbar_init(&s_full[i], kCodes ? 8 + 64 : 256 + 64);
       mbar_init(&s_empty[i], 1);
     }
     mbar_init(&s_done, 1);
@@ -223,78 +249,93 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
       ok[j] = i < t.z;
       row[j] = ok[j] ? p.order[t.y + i] : 0;
     }
-    uint4 raw[kAhead][2];
-    float sc[kAhead][2];
-    auto fetch = [&](int step, uint4 (&v)[2], float (&s)[2]) {
+    const uint32_t raw = sbase + p.stages * p.stage_bytes;
+    auto fetch = [&](int step) {
+      if (step < steps) {
+        const uint32_t at = raw + step % kAhead * kRawStep + tid * 16;
+        const uint32_t st = raw + step % kAhead * kRawStep + 8192 + tid * 4;
+        const int col = (k0 + step) * 64;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        v[j] = make_uint4(0, 0, 0, 0);
-        s[j] = 0.0f;
-        if (ok[j] && step < steps) {
-          const int col = (k0 + step) * 64;
-          v[j] = __ldg(reinterpret_cast<const uint4*>(p.q + row[j] * p.k + col + ch * 16));
-          s[j] = __ldg(p.sq + row[j] * (p.k >> 7) + (col >> 7));
+        for (int j = 0; j < 2; ++j) {
+          cp16(at + j * 4096, p.q + row[j] * p.k + col + ch * 16, ok[j]);
+          cp4(st + j * 1024, p.sq + row[j] * (p.k >> 7) + (col >> 7), ok[j]);
         }
       }
+      cp_commit();
     };
     if constexpr (kCodes) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) fetch(a, raw[a], sc[a]);
+      for (int a = 0; a < kAhead; ++a) fetch(a);
     }
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int step = 0; step < steps; ++step) {
+      uint4 v[2];
+      float sc[2];
+      if constexpr (kCodes) {
+        cp_wait<kAhead - 1>();
+        const uint32_t at = raw + step % kAhead * kRawStep + tid * 16;
+        const uint32_t st = raw + step % kAhead * kRawStep + 8192 + tid * 4;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          v[j] = lds16(at + j * 4096);
+          sc[j] = lds4(st + j * 1024);
+        }
+      }
+      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+      const uint32_t zs = sbase + slot * p.stage_bytes;
+      if constexpr (kCodes) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint4 lo, hi;
+          dequant16(v[j], sc[j], lo, hi);
+          const int i = r0 + j * 64;
+          sts16(zs + sw128(i, 2 * ch), lo);
+          sts16(zs + sw128(i, 2 * ch + 1), hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_full[slot]);
+        fetch(step + kAhead);
+      } else {
+        const int col = (k0 + step) * 64;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          cp16(zs + sw128(r0 + j * 32, ch), p.z + row[j] * p.ldz + col + ch * 8, ok[j]);
+        cp_arrive(&s_full[slot]);
+      }
+      if (++slot == p.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    cp_wait_all();
+  } else if (warp > 8) {
+    const int l = tid - 288;
     const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.r * p.k;
     int slot = 0;
     uint32_t phase = 0;
-    bool alive = true;
-    for (int base = 0; base < steps && alive; base += kAhead) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int step = base + a;
-        if (step >= steps) break;
-        if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
-          alive = false;
-          break;
+    for (int step = 0; step < steps; ++step) {
+      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+      const uint32_t ws = sbase + slot * p.stage_bytes + 16384;
+      const int col = (k0 + step) * 64;
+      if constexpr (kTrans) {  // 64 rows of W (r contiguous): 64-column blocks of 8 KB
+        const int chunks = p.rp / 8;
+        for (int i = l; i < 64 * chunks; i += 64) {
+          const int kr = i / chunks, c = i % chunks;
+          cp16(ws + (c >> 3) * 8192 + sw128(kr, c & 7),
+               wg + static_cast<int64_t>(col + kr) * p.r + (c * 8 < p.r ? c * 8 : 0), c * 8 < p.r);
         }
-        const uint32_t zs = sbase + slot * p.stage_bytes, wsm = zs + 16384;
-        const int col = (k0 + step) * 64;
-        if constexpr (kTrans) {  // 64 rows of W (r contiguous): 64-column blocks of 8 KB
-          const int blocks8 = (p.rp + 63) / 64 * 8;
-          for (int i = tid; i < 64 * blocks8; i += 256) {
-            const int kr = i / blocks8, c = i % blocks8;
-            cp16(wsm + (c >> 3) * 8192 + sw128(kr, c & 7),
-                 wg + static_cast<int64_t>(col + kr) * p.r + (c * 8 < p.r ? c * 8 : 0), c * 8 < p.r);
-          }
-        } else {
-          for (int i = tid; i < p.rp * 8; i += 256) {
-            const int c = i >> 3;
-            cp16(wsm + sw128(c, i & 7),
-                 wg + static_cast<int64_t>(c < p.r ? c : 0) * p.k + col + (i & 7) * 8, c < p.r);
-          }
+      } else {
+        for (int i = l; i < p.rp * 8; i += 64) {
+          const int c = i >> 3;
+          cp16(ws + sw128(c, i & 7),
+               wg + static_cast<int64_t>(c < p.r ? c : 0) * p.k + col + (i & 7) * 8, c < p.r);
         }
-        if constexpr (kCodes) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint4 lo, hi;
-            dequant16(raw[a][j], sc[a][j], lo, hi);
-            const int i = r0 + j * 64;
-            sts16(zs + sw128(i, 2 * ch), lo);
-            sts16(zs + sw128(i, 2 * ch + 1), hi);
-          }
-          fetch(step + kAhead, raw[a], sc[a]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kRows; ++j)
-            cp16(zs + sw128(r0 + j * 32, ch), p.z + row[j] * p.ldz + col + ch * 8, ok[j]);
-        }
-        cp_arrive(&s_full[slot]);
-        if constexpr (kCodes) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[slot]);
-        }
-        if (++slot == p.stages) {
-          slot = 0;
-          phase ^= 1u;
-        }
+      }
+      cp_arrive(&s_full[slot]);
+      if (++slot == p.stages) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
     cp_wait_all();
@@ -376,11 +417,11 @@ struct ExpandArgs {
   const uint16_t* base;
   uint16_t* y;
   int n, r, rp;
-  int stage_bytes;
+  int stage_bytes, slots, bslots;  // a W stage; W stages; base stages of 16 KB
 };
 
-constexpr int kExpandThreads = 352;  // 8 epilogue warps, 1 MMA warp, 2 warps that load W
-constexpr int kExpandSlots = 4;      // W stages and accumulators of 64 columns
+constexpr int kExpandThreads = 416;  // 8 epilogue warps, 1 MMA warp, 4 warps that load base and W
+constexpr int kExpandSlots = 4;      // at most: W stages with their accumulators; base stages
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
@@ -392,7 +433,6 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)
       : "r"(taddr)
       : "memory");
 }
-// base and y may be one buffer: plain loads and stores, kept in program order.
 __device__ __forceinline__ uint4 ld_stream(const void* ptr) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -405,6 +445,12 @@ __device__ __forceinline__ void st_stream(void* ptr, uint4 v) {
   asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
+}
+
+// Offset of 16-byte chunk c of row `row` of a base stage (128 rows x 128 bytes): the eight
+// lanes of a shared-memory phase read four chunks of two neighbouring rows.
+__device__ __forceinline__ uint32_t base_at(int row, int c) {
+  return static_cast<uint32_t>(row * 128 + ((c ^ ((row & 1) << 2) ^ ((row >> 1) & 3)) << 4));
 }
 
 // Pairs (columns 8 j + 2 t, + 1) of lane t of a quad, j = 0 .. 3, become the eight
@@ -432,11 +478,14 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
 // Row tile blockIdx.y, columns in units of 64 split over the grid's x. The accumulator is
 // read in the 16x256b form, where a quad of lanes holds 32 columns of a row in pairs; W's
 // rows are stored permuted (or, kTrans, the pairs are transposed over the quad), so that
-// each lane owns 8 consecutive columns and a quad reads and writes 64 bytes of a row.
+// each lane owns 8 consecutive columns and a quad writes 64 bytes of a row. base comes
+// through shared memory, several stages ahead; it may be y itself, since the lane that writes
+// an element is the only one that reads it, from the stage, before that.
 template <bool kTrans>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kExpandSlots], s_done[kExpandSlots], s_free[kExpandSlots], s_end;
+  __shared__ uint64_t s_full[kExpandSlots], s_done[kExpandSlots], s_free[kExpandSlots],
+      s_bfull[kExpandSlots], s_bfree[kExpandSlots], s_end;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -459,9 +508,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
   const uint32_t sh = smem_u32(smem);
   const int kt = (p.rp + 63) / 64;  // 64-wide tiles of the reduction
   const uint32_t sw = sh + kt * 16384;
+  const uint32_t sb = sw + p.slots * p.stage_bytes;
   if (tid == 0) {
     for (int i = 0; i < kExpandSlots; ++i) {
-      mbar_init(&s_full[i], 64);
+      mbar_init(&s_full[i], 128);
+      mbar_init(&s_bfull[i], 128);
+      mbar_init(&s_bfree[i], 8);
       mbar_init(&s_done[i], 1);
       mbar_init(&s_free[i], 8);
     }
@@ -501,17 +553,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
               t4 * 8;
     }
     const float f = p.scale ? p.scale[t.x] : 1.0f;
-    uint4 b0[4], b1[4];
-    auto fetch = [&](int u, uint4 (&b)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        b[i] = make_uint4(0, 0, 0, 0);
-        if (p.base && ok[i] && u < count) b[i] = ld_stream(p.base + at[i] + u * 64);
-      }
-    };
-    auto finish = [&](int u, uint4 (&b)[4]) -> bool {
-      const int slot = u % kExpandSlots;
-      if (!warp_wait(&s_done[slot], (u / kExpandSlots) & 1, &s_abort, kSiteDone)) return false;
+    int slot = 0, bs = 0;
+    uint32_t ph = 0, bph = 0;
+    for (int u = 0; u < count; ++u) {
+      if (!warp_wait(&s_done[slot], ph, &s_abort, kSiteDone)) break;
       tc_fence_after();
       uint32_t v[2][16];
       const uint32_t ta =
@@ -520,8 +565,19 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
       tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
       tmem_wait_ld();
       tc_fence_before();
+      uint4 b[4] = {};
+      if (p.base) {
+        if (!warp_wait(&s_bfull[bs], bph, &s_abort, kSiteFull)) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          b[i] = lds16(sb + bs * 16384 +
+                       base_at((warp & 3) * 32 + i * 8 + (lane >> 2), (warp >> 2) * 4 + t4));
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[slot]);
+      if (lane == 0) {
+        mbar_arrive(&s_free[slot]);
+        mbar_arrive(&s_bfree[bs]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // rows lane / 4 + 8 i
         float a[8];
@@ -538,24 +594,23 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
           o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
         if (ok[i]) st_stream(p.y + at[i] + u * 64, make_uint4(o[0], o[1], o[2], o[3]));
       }
-      return true;
-    };
-    fetch(0, b0);
-    for (int u = 0; u < count; u += 2) {
-      fetch(u + 1, b1);
-      if (!finish(u, b0)) break;
-      if (u + 1 >= count) break;
-      fetch(u + 2, b0);
-      if (!finish(u + 1, b1)) break;
+      if (++slot == p.slots) {
+        slot = 0;
+        ph ^= 1u;
+      }
+      if (++bs == p.bslots) {
+        bs = 0;
+        bph ^= 1u;
+      }
     }
   } else if (warp == 8) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(64) | (kTrans ? kBMajorMn : 0u);
+      int slot = 0;
+      uint32_t ph = 0;
       for (int u = 0; u < count; ++u) {
-        const int slot = u % kExpandSlots;
-        const uint32_t ph = (u / kExpandSlots) & 1;
         if (!wait(&s_full[slot], ph, &s_abort, kSiteFull)) break;
-        if (u >= kExpandSlots && !wait(&s_free[slot], ph ^ 1u, &s_abort, kSiteAccEmpty)) break;
+        if (u >= p.slots && !wait(&s_free[slot], ph ^ 1u, &s_abort, kSiteAccEmpty)) break;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t ws = sw + slot * p.stage_bytes;
@@ -565,6 +620,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
                           : smem_desc_sw128(ws + (k >> 2) * 8192 + (k & 3) * 32),
                    idesc, k > 0);
         mma_commit(&s_done[slot]);
+        if (++slot == p.slots) {
+          slot = 0;
+          ph ^= 1u;
+        }
       }
       mma_commit(&s_end);
       wait_mmas(&s_end);
@@ -573,22 +632,38 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
     const int l = tid - 288;
     const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.n * p.r;
     const int chunks = p.rp / 8;
+    const int br = l >> 3, bc = l & 7;  // base: rows br + 16 j, chunk bc
+    const uint16_t* bp[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      bp[j] = p.base + (br + 16 * j < t.z ? static_cast<int64_t>(p.order[t.y + br + 16 * j]) : 0) * p.n +
+              u0 * 64 + bc * 8;
+    int slot = 0, bs = 0;
+    uint32_t ph = 0, bph = 0;
     for (int u = 0; u < count; ++u) {
-      const int slot = u % kExpandSlots;
+      if (p.base) {
+        if (u >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, &s_abort, kSiteEmpty)) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          cp16(sb + bs * 16384 + base_at(br + 16 * j, bc), bp[j] + u * 64, br + 16 * j < t.z);
+        cp_arrive(&s_bfull[bs]);
+        if (++bs == p.bslots) {
+          bs = 0;
+          bph ^= 1u;
+        }
+      }
       // the MMAs that read this stage are done when their accumulator is
-      if (u >= kExpandSlots &&
-          !warp_wait(&s_done[slot], ((u / kExpandSlots) & 1) ^ 1u, &s_abort, kSiteEmpty))
-        break;
+      if (u >= p.slots && !warp_wait(&s_done[slot], ph ^ 1u, &s_abort, kSiteEmpty)) break;
       const uint32_t ws = sw + slot * p.stage_bytes;
       const int col = (u0 + u) * 64;
       if constexpr (kTrans) {
-        for (int i = l; i < p.rp * 8; i += 64) {
+        for (int i = l; i < p.rp * 8; i += 128) {
           const int k = i >> 3;
           cp16(ws + sw128(k, i & 7),
                wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + col + (i & 7) * 8, k < p.r);
         }
       } else {
-        for (int i = l; i < 64 * chunks; i += 64) {
+        for (int i = l; i < 64 * chunks; i += 128) {
           const int nr = i / chunks, c = i % chunks;
           // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
           const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
@@ -598,6 +673,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
         }
       }
       cp_arrive(&s_full[slot]);
+      if (++slot == p.slots) {
+        slot = 0;
+        ph ^= 1u;
+      }
     }
     cp_wait_all();
   }
@@ -621,13 +700,19 @@ struct OuterArgs {
   const float* scale; // or null: 1
   uint16_t* out;      // count x k x r, or (kByRank) count x r x k
   float* part;        // 2 gridDim.y slots shaped like one group's output
+  const uint16_t* w;  // kDual: count x k x r
+  float* dpart;       // kDual: gridDim.x x b x r, rows in the order of `order`
+  int64_t b;
   int k, r, rp;
   int stages, htiles; // Z stages, H tiles in shared memory
+  int dcol;           // kDual: first tensor-memory column of the two row accumulators
   uint32_t tmem_cols;
 };
 
-constexpr int kOuterThreads = 416;  // 8 loading warps, 1 MMA warp, 4 drain warps (9 .. 12)
-constexpr int kOuterStages = 4;  // at most
+constexpr int kOuterThreads = 480;  // 8 warps load Z; MMA warp; 4 drain warps (9 .. 12); 2 load H, W
+constexpr int kOuterStages = 4;     // at most
+constexpr int kOuterAhead = 3;      // as kAhead
+constexpr int kOuterRawStep = 16384 + 4096;
 
 __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles) {
   return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
@@ -637,13 +722,16 @@ __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles
 // group form a run, summed in tensor memory (lane = column of Z, column = rank). A run that
 // is its whole group is rounded into `out`; one that the chunk's ends cut leaves its fp32
 // sums in the chunk's slot (0: the run starts the chunk, else 1) for the finish kernel.
-template <bool kCodes, bool kByRank>
+// kDual (r <= 64): the same Z stage also serves the product over its columns, dh = Z W: a
+// tile's 128 x r sums over this slice go to `dpart`, and dY is read once for both gradients.
+template <bool kCodes, bool kByRank, bool kDual>
 __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kOuterStages], s_empty[kOuterStages], s_hempty[kOuterStages], s_run,
-      s_free, s_end;
+  __shared__ uint64_t s_full[kOuterStages], s_empty[kOuterStages], s_hfull[kOuterStages],
+      s_hempty[kOuterStages], s_dfull[2], s_dfree[2], s_run, s_free, s_end;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  constexpr int kStage = 32768 + (kDual ? 16384 : 0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   const int total = p.first128[p.count];
@@ -655,14 +743,20 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
   if (begin == end) return;
   uint8_t* smem = align1k(smem_raw);
   const uint32_t sz = smem_u32(smem);
-  const int hblocks = (p.rp + 63) / 64;
-  const uint32_t sh = sz + stages * 32768;  // p.htiles H tiles of hblocks x 16 KB
+  const int hbytes = (p.rp + 63) / 64 * 16384;
+  const uint32_t sh = sz + stages * kStage;        // p.htiles H tiles
+  const uint32_t sraw = sh + p.htiles * hbytes;    // kCodes: kOuterAhead steps
   const int4* tiles = p.tiles + 1 + p.cap16;
   if (tid == 0) {
     for (int i = 0; i < kOuterStages; ++i) {
-      mbar_init(&s_full[i], kCodes ? 264 : 256);
+      mbar_init(&s_full[i], (kCodes ? 8 : 256) + (kDual ? 64 : 0));
       mbar_init(&s_empty[i], 1);
+      mbar_init(&s_hfull[i], 64);
       mbar_init(&s_hempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_dfull[i], 1);
+      mbar_init(&s_dfree[i], 4);
     }
     mbar_init(&s_end, 1);
     mbar_init(&s_run, 1);
@@ -695,109 +789,93 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       }
     };
     load_rows();
-    uint4 raw[kAhead][4];
-    float sc[kAhead][4];
-    auto fetch = [&](uint4 (&v)[4], float (&s)[4]) {  // codes of the load position, then advance
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = make_uint4(0, 0, 0, 0);
-        s[j] = 0.0f;
-        if (ok[j]) {
-          v[j] = __ldg(reinterpret_cast<const uint4*>(p.q + row[j] * p.k + (blk0 + lblk) * 128 + ch * 16));
-          s[j] = __ldg(p.sq + row[j] * (p.k >> 7) + blk0 + lblk);
-        }
-      }
+    auto advance = [&]() {
       if (++lblk == nb) {
         lblk = 0;
         ++ltile;
         load_rows();
       }
     };
+    int rs = 0;  // raw slot of the next fetch, the one that the current step has just read
+    auto fetch = [&]() {
+      if (ltile < end) {
+        const uint32_t at = sraw + rs * kOuterRawStep + tid * 16;
+        const uint32_t st = sraw + rs * kOuterRawStep + 16384 + tid * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          cp16(at + j * 4096, p.q + row[j] * p.k + (blk0 + lblk) * 128 + ch * 16, ok[j]);
+          cp4(st + j * 1024, p.sq + row[j] * (p.k >> 7) + blk0 + lblk, ok[j]);
+        }
+        advance();
+      }
+      cp_commit();
+      if (++rs == kOuterAhead) rs = 0;
+    };
     if constexpr (kCodes) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) fetch(raw[a], sc[a]);
+      for (int a = 0; a < kOuterAhead; ++a) fetch();
     }
-    int tile = begin, blk = 0, slot = 0, hs = 0;
-    uint32_t phase = 0, hphase = 0;
-    bool alive = true;
-    for (int base = 0; base < steps && alive; base += kAhead) {
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int step = 0; step < steps; ++step) {
+      uint4 v[4];
+      float sc[4];
+      if constexpr (kCodes) {
+        cp_wait<kOuterAhead - 1>();
+        const uint32_t at = sraw + rs * kOuterRawStep + tid * 16;
+        const uint32_t st = sraw + rs * kOuterRawStep + 16384 + tid * 4;
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int step = base + a;
-        if (step >= steps) break;
-        if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
-          alive = false;
-          break;
+        for (int j = 0; j < 4; ++j) {
+          v[j] = lds16(at + j * 4096);
+          sc[j] = lds4(st + j * 1024);
         }
-        if (blk == 0) {  // the tile's H comes with its first block
-          if (tile - begin >= p.htiles &&
-              !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty)) {
-            alive = false;
-            break;
-          }
-          const int4 t = tiles[tile];
-          const int chunks = hblocks * 8;
-          for (int i = tid; i < 128 * chunks; i += 256) {
-            const int rr = i / chunks, c = i % chunks;
-            const bool in = rr < t.z && c * 8 < p.r;
-            const int64_t hr = in ? p.order[t.y + rr] : 0;
-            cp16(sh + (hs * hblocks + (c >> 3)) * 16384 + sw128(rr, c & 7),
-                 p.h + hr * p.r + (in ? c * 8 : 0), in);
-          }
+      }
+      if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+      const uint32_t zs = sz + slot * kStage;
+      if constexpr (kCodes) {
+        const uint32_t half = zs + (ch >> 2) * 16384;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 lo, hi;
+          dequant16(v[j], sc[j], lo, hi);
+          sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3)), lo);
+          sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3) + 1), hi);
         }
-        const uint32_t zs = sz + slot * 32768;
-        if constexpr (kCodes) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_full[slot]);
+        fetch();
+      } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 lo, hi;
-            dequant16(raw[a][j], sc[a][j], lo, hi);
-            const uint32_t half = zs + (ch >> 2) * 16384;
-            sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3)), lo);
-            sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3) + 1), hi);
-          }
-          fetch(raw[a], sc[a]);
-        } else {
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
-                   p.z + row[j] * p.ldz + (blk0 + blk) * 128 + half * 64 + ch * 8, ok[j]);
-        }
+          for (int half = 0; half < 2; ++half)
+            cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
+                 p.z + row[j] * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8, ok[j]);
         cp_arrive(&s_full[slot]);
-        if constexpr (kCodes) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[slot]);
-        }
-        if (++blk == nb) {
-          blk = 0;
-          ++tile;
-          if (++hs == p.htiles) {
-            hs = 0;
-            hphase ^= 1u;
-          }
-          if constexpr (!kCodes) {
-            ltile = tile;
-            load_rows();
-          }
-        }
-        if (++slot == stages) {
-          slot = 0;
-          phase ^= 1u;
-        }
+        advance();
+      }
+      if (++slot == stages) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
     cp_wait_all();
   } else if (warp == 8) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(p.rp) | kAMajorMn | kBMajorMn;
+      const uint32_t didesc = idesc_bf16(p.rp) | kBMajorMn;
       int runs = 0, slot = 0, hs = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, hphase = 0;
       bool alive = true;
       bool fresh = true;
       for (int tile = begin; tile < end && alive; ++tile) {
-        const uint32_t hb = sh + hs * hblocks * 16384;
+        const uint32_t hb = sh + hs * hbytes;
+        const int nth = tile - begin;
+        const uint32_t dacc = tmem + p.dcol + (nth & 1) * p.rp;
+        alive = wait(&s_hfull[hs], hphase, &s_abort, kSiteFull) &&
+                (!kDual || nth < 2 ||
+                 wait(&s_dfree[nth & 1], ((nth >> 1) & 1) ^ 1u, &s_abort, kSiteAccEmpty));
+        if (!alive) break;
         for (int b = 0; b < nb; ++b) {
           if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) {
             alive = false;
@@ -805,11 +883,17 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
           }
           fence_proxy_async_smem();
           tc_fence_after();
-          const uint32_t zs = sz + slot * 32768;
+          const uint32_t zs = sz + slot * kStage;
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 128 rows: 8 steps of 16
             mma_bf16(tmem + b * p.rp, smem_desc_mn(zs + k * 2048, 16384),
                      smem_desc_mn(hb + k * 2048, 16384), idesc, !fresh || k > 0);
+          if constexpr (kDual) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // 128 columns
+              mma_bf16(dacc, smem_desc_sw128(zs + (k >> 2) * 16384 + (k & 3) * 32),
+                       smem_desc_mn(zs + 32768 + k * 2048, 0), didesc, b > 0 || k > 0);
+          }
           mma_commit(&s_empty[slot]);
           if (++slot == stages) {
             slot = 0;
@@ -818,7 +902,11 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
         }
         if (!alive) break;
         mma_commit(&s_hempty[hs]);
-        if (++hs == p.htiles) hs = 0;
+        if (kDual) mma_commit(&s_dfull[nth & 1]);
+        if (++hs == p.htiles) {
+          hs = 0;
+          hphase ^= 1u;
+        }
         fresh = tile + 1 < end && tiles[tile + 1].x != tiles[tile].x;
         if (fresh || tile + 1 == end) {
           mma_commit(&s_run);
@@ -833,28 +921,59 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       mma_commit(&s_end);
       wait_mmas(&s_end);
     }
-  } else {
+  } else if (warp < 13) {
     const int sub = warp & 3;  // tensor-memory lanes of this warp
+    const uint32_t lanes = static_cast<uint32_t>(sub * 32) << 16;
     const int64_t size = static_cast<int64_t>(p.k) * p.r;
     int runs = 0;
-    for (int tile = begin; tile < end;) {
+    bool alive = true;
+    for (int tile = begin; tile < end && alive;) {
       const int g = tiles[tile].x;
       const int first = tile;
       const int gb = p.first128[g], ge = p.first128[g + 1];
       const int stop = min(end, ge);
+      const float f = p.scale ? p.scale[g] : 1.0f;
+      if constexpr (kDual) {
+        for (; tile < stop; ++tile) {
+          const int nth = tile - begin;
+          const int4 t = tiles[tile];
+          if (!warp_wait(&s_dfull[nth & 1], (nth >> 1) & 1, &s_abort, kSiteDrain)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const int i = sub * 32 + lane;
+          float* dst = p.dpart + (static_cast<int64_t>(blockIdx.x) * p.b + t.y + i) * p.r;
+          for (int c = 0; c < p.r; c += 8) {
+            uint32_t v[8];
+            tmem_ld8(tmem + lanes + p.dcol + (nth & 1) * p.rp + c, v);
+            tmem_wait_ld();
+            float o[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[u] = f * __uint_as_float(v[u]);
+            if (i < t.z) {
+              *reinterpret_cast<float4*>(dst + c) = make_float4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<float4*>(dst + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_dfree[nth & 1]);
+        }
+        if (!alive) break;
+      }
       tile = stop;
       if (!warp_wait(&s_run, runs & 1, &s_abort, kSiteDrain)) break;
       ++runs;
       tc_fence_after();
       const bool whole = first == gb && stop == ge;
-      const float f = p.scale ? p.scale[g] : 1.0f;
       float* part = p.part + (2 * blockIdx.y + (first == begin ? 0 : 1)) * size;
       uint16_t* out = p.out + g * size;
       for (int b = 0; b < nb; ++b) {
         const int64_t j = (blk0 + b) * 128 + sub * 32 + lane;
         for (int c = 0; c < p.r; c += 8) {
           uint32_t v[8];
-          tmem_ld8(tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * p.rp + c, v);
+          tmem_ld8(tmem + lanes + b * p.rp + c, v);
           tmem_wait_ld();
           float o[8];
 #pragma unroll
@@ -882,6 +1001,49 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free);
     }
+  } else {
+    const int l = tid - 416, chunks = p.rp / 8;
+    int slot = 0, hs = 0, step = 0;
+    uint32_t phase = 0, hphase = 0;
+    bool alive = true;
+    for (int tile = begin; tile < end && alive; ++tile) {
+      if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
+        break;
+      const int4 t = tiles[tile];
+      for (int i = l; i < 128 * chunks; i += 64) {
+        const int rr = i / chunks, c = i % chunks;
+        const bool in = rr < t.z && c * 8 < p.r;
+        const int64_t hr = in ? p.order[t.y + rr] : 0;
+        cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(rr, c & 7), p.h + hr * p.r + (in ? c * 8 : 0),
+             in);
+      }
+      cp_arrive(&s_hfull[hs]);
+      if (++hs == p.htiles) {
+        hs = 0;
+        hphase ^= 1u;
+      }
+      if constexpr (kDual) {
+        const uint16_t* wg = p.w + (static_cast<int64_t>(t.x) * p.k + blk0 * 128) * p.r;
+        for (int b = 0; b < nb; ++b, ++step) {
+          if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
+            alive = false;
+            break;
+          }
+          const uint32_t ws = sz + slot * kStage + 32768;
+          for (int i = l; i < 128 * chunks; i += 64) {
+            const int kr = i / chunks, c = i % chunks;
+            const bool in = c * 8 < p.r;
+            cp16(ws + sw128(kr, c), wg + static_cast<int64_t>(b * 128 + kr) * p.r + (in ? c * 8 : 0), in);
+          }
+          cp_arrive(&s_full[slot]);
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    cp_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -889,8 +1051,31 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
   if (warp == 8) tmem_dealloc(tmem, p.tmem_cols);
 }
 
+// dh (b x r) from the slices' parts, added in slice order. 4 elements a thread.
+struct ReduceArgs {
+  const float* dpart;  // slices x b x r, rows in the order of `order`
+  const int32_t *order, *offsets;
+  uint16_t* dh;
+  int64_t b;
+  int count, r, slices;
+};
+
+__global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int64_t pos = at / p.r;
+  if (pos >= p.offsets[p.count]) return;
+  const int64_t row = p.order[pos];
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < p.slices; ++s) {
+    const float4 o = __ldg(reinterpret_cast<const float4*>(p.dpart + s * p.b * p.r + at));
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  *reinterpret_cast<uint2*>(p.dh + row * p.r + at % p.r) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
 // The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
-// zeros for the groups without rows. 4 elements a thread.
+// zeros for the groups without rows. 16 elements a thread, four loads at a time.
 struct FinishArgs {
   const int32_t* first128;
   int count;
@@ -905,27 +1090,34 @@ struct FinishArgs {
 __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs p) {
   pdl_wait();
   const auto& s = p.side[blockIdx.z];
-  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4096 + threadIdx.x * 4;
   if (at >= s.size) return;
+  const int n = static_cast<int>(min(static_cast<int64_t>(4), (s.size - at + 1023) / 1024));
   const int g = blockIdx.y, total = p.first128[p.count];
   const int gb = p.first128[g], ge = p.first128[g + 1];
   uint16_t* out = s.out + g * s.size + at;
-  if (gb == ge) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
-    return;
+  float4 v[4] = {};
+  if (gb < ge) {
+    int c = static_cast<int>(static_cast<int64_t>(gb) * s.chunks / total);
+    while (chunk_begin(c + 1, s.chunks, total) <= gb) ++c;
+    if (chunk_begin(c + 1, s.chunks, total) >= ge) return;  // inside one chunk: already written
+    for (; c < s.chunks; ++c) {
+      const int cb = chunk_begin(c, s.chunks, total);
+      if (cb >= ge) break;
+      if (chunk_begin(c + 1, s.chunks, total) == cb) continue;  // an empty chunk
+      const float* part = s.part + (2 * c + (gb > cb ? 1 : 0)) * s.size + at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= n) break;
+        const float4 o = __ldg(reinterpret_cast<const float4*>(part + i * 1024));
+        v[i].x += o.x, v[i].y += o.y, v[i].z += o.z, v[i].w += o.w;
+      }
+    }
   }
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  int c = static_cast<int>(static_cast<int64_t>(gb) * s.chunks / total);
-  while (chunk_begin(c + 1, s.chunks, total) <= gb) ++c;
-  if (chunk_begin(c + 1, s.chunks, total) >= ge) return;  // inside one chunk: already written
-  for (; c < s.chunks; ++c) {
-    const int cb = chunk_begin(c, s.chunks, total);
-    if (cb >= ge) break;
-    if (chunk_begin(c + 1, s.chunks, total) == cb) continue;  // an empty chunk
-    const float4 o = *reinterpret_cast<const float4*>(s.part + (2 * c + (gb > cb ? 1 : 0)) * s.size + at);
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-  }
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n)
+      *reinterpret_cast<uint2*>(out + i * 1024) = make_uint2(pack2(v[i].x, v[i].y), pack2(v[i].z, v[i].w));
 }
 
 // -------------------------------------------------------------------- host
@@ -973,9 +1165,10 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   ShrinkArgs p{c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
                codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, w, scale, out, k, c.r, rp, 0, 0};
   p.stage_bytes = 16384 + (trans ? (rp + 63) / 64 * 8192 : rp * 128);
-  // two blocks per SM: about 108 KB each, of which the parts need 128 x (rp + 4) fp32
-  p.stages = std::max(2, std::min(kShrinkMaxStages, 108 * 1024 / p.stage_bytes));
-  const int smem = std::max(p.stages * p.stage_bytes, 128 * (rp + 4) * 4) + 1024;
+  // two blocks per SM: about 110 KB each, of which the parts need 128 x (rp + 4) fp32
+  const int raw = codes ? kAhead * kRawStep : 0;
+  p.stages = std::max(2, std::min(kShrinkMaxStages, (110 * 1024 - raw) / p.stage_bytes));
+  const int smem = std::max(p.stages * p.stage_bytes + raw, 128 * (rp + 4) * 4) + 1024;
   // split the reduction until two blocks per SM are busy, 8 blocks of one cluster at most
   int splits = 1;
   while (splits < 8 && tiles_estimate(c) * splits * 2 <= 2 * kSms) splits *= 2;
@@ -989,8 +1182,12 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, c
                           const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r);
   ExpandArgs p{c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, w, scale, c.base, y,
-               n, c.r, rp, trans ? rp * 128 : (rp + 63) / 64 * 8192};
-  const int smem = (rp + 63) / 64 * 16384 + kExpandSlots * p.stage_bytes + 1024;
+               n, c.r, rp, trans ? rp * 128 : (rp + 63) / 64 * 8192, 0, 0};
+  // two blocks per SM: H, 3 W stages (2 beyond rank 64), base stages in what is left of 110 KB
+  const int hbytes = (rp + 63) / 64 * 16384;
+  p.slots = rp > 64 ? 2 : 3;
+  p.bslots = std::min(kExpandSlots, (110 * 1024 - hbytes - p.slots * p.stage_bytes) / 16384);
+  const int smem = hbytes + p.slots * p.stage_bytes + p.bslots * 16384 + 1024;
   // column slices of at least 256 columns so that the last wave of blocks is nearly full
   const int tiles = tiles_estimate(c);
   int best = 1;
@@ -1009,60 +1206,75 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, c
 // Column blocks and row chunks of the outer kernel: one thread block per SM, the split that
 // moves the fewest bytes through the busiest block (Z, H again for every slice, parts).
 struct OuterPlan {
-  int slices, chunks, stages, htiles;
+  int slices, chunks, stages, htiles, dcol;
   uint32_t cols;
 };
-OuterPlan outer_plan(int64_t b, int64_t count, int k, int r) {
+OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool dual) {
   const int rp = round16(r), blocks = k / 128;
   const int tiles = static_cast<int>(
       std::max<int64_t>(1, std::min<int64_t>(row_tiles_cap(b, count, 128), b / 128 + (count + 1) / 2)));
-  OuterPlan best{blocks, 1, 0, 0, 0};
-  int best_nb = 1;
+  OuterPlan best{};
   double cost = 1e30;
-  for (int nb = 1; nb <= 512 / rp && nb <= blocks; ++nb) {
+  for (int nb = 1; nb <= 512 / rp - (dual ? 2 : 0) && nb <= blocks; ++nb) {
     const int slices = (blocks + nb - 1) / nb;
     const int chunks = std::max(1, std::min(tiles, kSms / slices));
     const double waves = double((int64_t(slices) * chunks + kSms - 1) / kSms);
-    const double each = double((tiles + chunks - 1) / chunks) * (nb * 32768.0 + 256.0 * rp) +
+    const double each = double((tiles + chunks - 1) / chunks) *
+                            (nb * 32768.0 + 256.0 * rp + (dual ? 512.0 * rp : 0.0)) +
                         (chunks > 1 ? 2.0 * nb * 128 * rp * 4 : 0.0);
-    if (waves * each < cost) cost = waves * each, best_nb = nb, best = OuterPlan{slices, chunks, 0, 0, 0};
+    const double all = waves * each + (dual ? double(slices) * tiles * 512 * rp / kSms : 0.0);
+    if (all < cost) {
+      cost = all;
+      best.slices = slices;
+      best.chunks = chunks;
+      best.dcol = nb * rp;
+    }
   }
+  const int used = best.dcol + (dual ? 2 * rp : 0);
   best.cols = 32;
-  while (static_cast<int>(best.cols) < best_nb * rp) best.cols *= 2;
-  // A tile's H is loaded with its first Z block: as many H tiles as the Z stages reach ahead
-  // (nb_min: the blocks of the smallest slice).
+  while (static_cast<int>(best.cols) < used) best.cols *= 2;
+  // As many H tiles as the Z stages reach ahead (nb_min: the blocks of the smallest slice).
   const int nb_min = blocks / best.slices, hbytes = (rp + 63) / 64 * 16384;
+  const int stage = 32768 + (dual ? 16384 : 0), raw = codes ? kOuterAhead * kOuterRawStep : 0;
   for (best.stages = kOuterStages;; --best.stages) {
     best.htiles = std::max(2, 1 + (best.stages - 1 + nb_min - 1) / nb_min);
-    if (best.stages * 32768 + best.htiles * hbytes <= 224 * 1024) break;
+    if (best.stages * stage + best.htiles * hbytes + raw <= 224 * 1024) break;
   }
   return best;
 }
 
-template <bool kCodes, bool kByRank>
+template <bool kCodes, bool kByRank, bool kDual>
 cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint16_t* z, int64_t ldz,
                          int k, const uint16_t* h, const float* scale, uint16_t* out, float* part,
-                         cudaStream_t st) {
+                         float* dpart, cudaStream_t st) {
   const int rp = round16(c.r);
   const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
   OuterArgs p{c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
-              out, part, k, c.r, rp, plan.stages, plan.htiles, plan.cols};
-  const int smem = plan.stages * 32768 + plan.htiles * ((rp + 63) / 64) * 16384 + 1024;
-  return launch(outer_kernel<kCodes, kByRank>, dim3(plan.slices, plan.chunks), kOuterThreads, smem, 1,
-                false, p, st);
+              out, part, c.bm, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols};
+  const int smem = plan.stages * (32768 + (kDual ? 16384 : 0)) +
+                   plan.htiles * ((rp + 63) / 64) * 16384 + (kCodes ? kOuterAhead * kOuterRawStep : 0) +
+                   1024;
+  return launch(outer_kernel<kCodes, kByRank, kDual>, dim3(plan.slices, plan.chunks), kOuterThreads, smem,
+                1, false, p, st);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-struct BackwardSpace {
-  size_t dh, pa, pb, bytes;
+struct BackwardPlan {
+  bool dual;  // dh and dB from one pass over dY: up to rank 64, where the row parts are small
+  OuterPlan a, b;
+  size_t dh, pa, pb, pd, bytes;  // workspace offsets
 };
-BackwardSpace backward_space(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
-  BackwardSpace s;
+BackwardPlan backward_plan(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count, bool codes) {
+  BackwardPlan s;
+  s.dual = r <= 64;
+  s.a = outer_plan(b, count, int(m), int(r), codes, false);
+  s.b = outer_plan(b, count, int(n), int(r), false, s.dual);
   s.dh = 0;
   s.pa = up256(size_t(b) * r * 2);
-  s.pb = s.pa + up256(size_t(2) * outer_plan(b, count, int(m), int(r)).chunks * m * r * 4);
-  s.bytes = s.pb + up256(size_t(2) * outer_plan(b, count, int(n), int(r)).chunks * n * r * 4);
+  s.pb = s.pa + up256(size_t(2) * s.a.chunks * m * r * 4);
+  s.pd = s.pb + up256(size_t(2) * s.b.chunks * n * r * 4);
+  s.bytes = s.pd + (s.dual ? up256(size_t(s.b.slices) * b * r * 4) : 0);
   return s;
 }
 
@@ -1082,32 +1294,40 @@ cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
 }
 
 size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
-  return backward_space(b, m, n, r, count).bytes;
+  // the plans differ only in what shared memory holds, not in slices and chunks
+  return backward_plan(b, m, n, r, count, false).bytes;
 }
 
 cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
-  const BackwardSpace s = backward_space(c.g.b, c.m, c.n, c.r, c.g.count);
+  const BackwardPlan s = backward_plan(c.g.b, c.m, c.n, c.r, c.g.count, c.xq8 != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   uint16_t* dh = reinterpret_cast<uint16_t*>(ws + s.dh);
   float* pa = reinterpret_cast<float*>(ws + s.pa);
   float* pb = reinterpret_cast<float*>(ws + s.pb);
-  const OuterPlan oa = outer_plan(c.g.b, c.g.count, c.m, c.r);
-  const OuterPlan ob = outer_plan(c.g.b, c.g.count, c.n, c.r);
+  float* pd = reinterpret_cast<float*>(ws + s.pd);
   cudaError_t e = cudaSuccess;
   if (c.g.b > 0) {
-    e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
+    if (s.dual) {
+      e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, st);
+      if (e != cudaSuccess) return e;
+      const ReduceArgs ra{pd, c.g.order, c.g.offsets, dh, c.g.b, c.g.count, c.r, s.b.slices};
+      const int64_t blocks = (int64_t(c.g.b) * c.r + 1023) / 1024;
+      e = launch(reduce_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, false, ra, st);
+    } else {
+      e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
+      if (e == cudaSuccess)
+        e = launch_outer<false, false, false>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, nullptr, st);
+    }
     if (e == cudaSuccess)
-      e = launch_outer<false, false>(c, ob, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, st);
-    if (e == cudaSuccess)
-      e = c.xq8 ? launch_outer<true, true>(c, oa, nullptr, 0, c.m, dh, nullptr, c.da, pa, st)
-                : launch_outer<false, true>(c, oa, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, st);
+      e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, st)
+                : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, st);
     if (e == cudaSuccess) e = launch_expand(c, true, dh, c.a, c.m, nullptr, c.dx, false, st);
     if (e != cudaSuccess) return e;
   }
   FinishArgs f{first128_of(c.g), c.g.count, {}};
-  f.side[0] = {pa, c.da, int64_t(c.m) * c.r, oa.chunks};
-  f.side[1] = {pb, c.db, int64_t(c.n) * c.r, ob.chunks};
-  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 1023) / 1024;
+  f.side[0] = {pa, c.da, int64_t(c.m) * c.r, s.a.chunks};
+  f.side[1] = {pb, c.db, int64_t(c.n) * c.r, s.b.chunks};
+  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 4095) / 4096;
   return launch(finish_kernel, dim3(static_cast<unsigned>(blocks), c.g.count, 2), 256, 0, 1, false, f, st);
 }
 
