@@ -481,15 +481,16 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
 // each lane owns 8 consecutive columns and a quad writes 64 bytes of a row. base comes
 // through shared memory, several stages ahead; it may be y itself, since the lane that writes
 // an element is the only one that reads it, from the stage, before that.
+// Launched so that it may start before the kernel that writes H has ended: until then it reads
+// only what that kernel does not write (the grouping, W, base) and writes nothing.
 template <bool kTrans>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandArgs p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kExpandSlots], s_done[kExpandSlots], s_free[kExpandSlots],
-      s_bfull[kExpandSlots], s_bfree[kExpandSlots], s_end;
+      s_bfull[kExpandSlots], s_bfree[kExpandSlots], s_hfull, s_end;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
   if (static_cast<int>(blockIdx.y) >= p.tiles[0].y) return;
   const int4 t = p.tiles[1 + p.cap16 + blockIdx.y];
   const int units = p.n / 64;
@@ -497,6 +498,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
   const int count = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * units / gridDim.x) - u0;
   if (t.x < 0) {  // rows without adapter: base itself
     if (p.base == p.y) return;
+    pdl_wait();
     for (int i = tid; i < t.z * count * 8; i += kExpandThreads) {
       const int64_t at = static_cast<int64_t>(p.order[t.y + i / (count * 8)]) * p.n + u0 * 64 +
                          i % (count * 8) * 8;
@@ -517,6 +519,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
       mbar_init(&s_done[i], 1);
       mbar_init(&s_free[i], 8);
     }
+    mbar_init(&s_hfull, 256);
     mbar_init(&s_end, 1);
     s_abort = 0;
     fence_barrier_init();
@@ -524,17 +527,6 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
   if (warp == 8) {
     tmem_alloc(&s_tmem, 64 * kExpandSlots);
     tmem_relinquish();
-  }
-  {  // H: 128 rows x rp
-    const int chunks = p.rp / 8;
-    for (int i = tid; i < 128 * chunks; i += kExpandThreads) {
-      const int rr = i / chunks, c = i % chunks;
-      const bool ok = rr < t.z && c * 8 < p.r;
-      const int64_t row = ok ? p.order[t.y + rr] : 0;
-      cp16(sh + (c >> 3) * 16384 + sw128(rr, c & 7), p.h + row * p.r + (ok ? c * 8 : 0), ok);
-    }
-    cp_wait_all();
-    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -553,6 +545,23 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
               t4 * 8;
     }
     const float f = p.scale ? p.scale[t.x] : 1.0f;
+    {  // H: rows tid / 8 + 32 j, chunks tid % 8, + 8
+      int64_t hrow[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int rr = (tid >> 3) + 32 * j;
+        hrow[j] = rr < t.z ? p.order[t.y + rr] : -1;
+      }
+      pdl_wait();
+      for (int c = tid & 7; c * 8 < p.rp; c += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = hrow[j] >= 0 && c * 8 < p.r;
+          cp16(sh + (c >> 3) * 16384 + sw128((tid >> 3) + 32 * j, tid & 7),
+               p.h + (in ? hrow[j] * p.r + c * 8 : 0), in);
+        }
+      cp_arrive(&s_hfull);
+    }
     int slot = 0, bs = 0;
     uint32_t ph = 0, bph = 0;
     for (int u = 0; u < count; ++u) {
@@ -609,6 +618,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
       int slot = 0;
       uint32_t ph = 0;
       for (int u = 0; u < count; ++u) {
+        if (u == 0 && !wait(&s_hfull, 0, &s_abort, kSiteFull)) break;
         if (!wait(&s_full[slot], ph, &s_abort, kSiteFull)) break;
         if (u >= p.slots && !wait(&s_free[slot], ph ^ 1u, &s_abort, kSiteAccEmpty)) break;
         fence_proxy_async_smem();
@@ -735,12 +745,13 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   const int total = p.first128[p.count];
-  const int begin = chunk_begin(blockIdx.y, gridDim.y, total);
-  const int end = chunk_begin(blockIdx.y + 1, gridDim.y, total);
+  const int chunks = min(static_cast<int>(gridDim.y), total);  // none of them empty
+  if (static_cast<int>(blockIdx.y) >= chunks) return;
+  const int begin = chunk_begin(blockIdx.y, chunks, total);
+  const int end = chunk_begin(blockIdx.y + 1, chunks, total);
   const int blk0 = blockIdx.x * (p.k / 128) / gridDim.x;
   const int nb = (blockIdx.x + 1) * (p.k / 128) / gridDim.x - blk0;
   const int stages = p.stages;
-  if (begin == end) return;
   uint8_t* smem = align1k(smem_raw);
   const uint32_t sz = smem_u32(smem);
   const int hbytes = (p.rp + 63) / 64 * 16384;
@@ -1002,22 +1013,31 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       if (lane == 0) mbar_arrive(&s_free);
     }
   } else {
-    const int l = tid - 416, chunks = p.rp / 8;
+    const int l = tid - 416, rchunks = p.rp / 8;
+    const int hr = l >> 3, hc = l & 7;  // H: rows hr + 8 j, chunks hc, hc + 8
     int slot = 0, hs = 0, step = 0;
     uint32_t phase = 0, hphase = 0;
     bool alive = true;
+    int rows[16];  // of the next tile, -1 beyond its end
+    auto load_rows = [&](int tile) {
+      const int4 t = tile < end ? tiles[tile] : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) rows[j] = hr + 8 * j < t.z ? p.order[t.y + hr + 8 * j] : -1;
+    };
+    load_rows(begin);
     for (int tile = begin; tile < end && alive; ++tile) {
       if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
         break;
       const int4 t = tiles[tile];
-      for (int i = l; i < 128 * chunks; i += 64) {
-        const int rr = i / chunks, c = i % chunks;
-        const bool in = rr < t.z && c * 8 < p.r;
-        const int64_t hr = in ? p.order[t.y + rr] : 0;
-        cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(rr, c & 7), p.h + hr * p.r + (in ? c * 8 : 0),
-             in);
-      }
+      for (int c = hc; c < rchunks; c += 8)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const bool in = rows[j] >= 0 && c * 8 < p.r;
+          cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(hr + 8 * j, hc),
+               p.h + (in ? static_cast<int64_t>(rows[j]) * p.r + c * 8 : 0), in);
+        }
       cp_arrive(&s_hfull[hs]);
+      load_rows(tile + 1);
       if (++hs == p.htiles) {
         hs = 0;
         hphase ^= 1u;
@@ -1030,10 +1050,11 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
             break;
           }
           const uint32_t ws = sz + slot * kStage + 32768;
-          for (int i = l; i < 128 * chunks; i += 64) {
-            const int kr = i / chunks, c = i % chunks;
-            const bool in = c * 8 < p.r;
-            cp16(ws + sw128(kr, c), wg + static_cast<int64_t>(b * 128 + kr) * p.r + (in ? c * 8 : 0), in);
+          if (hc < rchunks) {
+            const bool in = hc * 8 < p.r;
+            const uint16_t* src = wg + static_cast<int64_t>(b * 128 + hr) * p.r + (in ? hc * 8 : 0);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) cp16(ws + sw128(hr + 8 * j, hc), src + j * 8 * p.r, in);
           }
           cp_arrive(&s_full[slot]);
           if (++slot == stages) {
@@ -1075,7 +1096,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
 }
 
 // The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
-// zeros for the groups without rows. 16 elements a thread, four loads at a time.
+// zeros for the groups without rows. 4 elements a thread.
 struct FinishArgs {
   const int32_t* first128;
   int count;
@@ -1087,37 +1108,36 @@ struct FinishArgs {
   } side[2];
 };
 
+// Largest c with chunk_begin(c) <= tile.
+__device__ __forceinline__ int chunk_of(int tile, int chunks, int tiles) {
+  int c = static_cast<int>(static_cast<int64_t>(tile) * chunks / tiles);
+  while (chunk_begin(c + 1, chunks, tiles) <= tile) ++c;
+  return c;
+}
+
 __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs p) {
-  pdl_wait();
-  const auto& s = p.side[blockIdx.z];
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4096 + threadIdx.x * 4;
-  if (at >= s.size) return;
-  const int n = static_cast<int>(min(static_cast<int64_t>(4), (s.size - at + 1023) / 1024));
+  const float* part = blockIdx.z ? p.side[1].part : p.side[0].part;
+  uint16_t* dst = blockIdx.z ? p.side[1].out : p.side[0].out;
+  const int64_t size = blockIdx.z ? p.side[1].size : p.side[0].size;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x * 4;
+  if (at >= size) return;
   const int g = blockIdx.y, total = p.first128[p.count];
   const int gb = p.first128[g], ge = p.first128[g + 1];
-  uint16_t* out = s.out + g * s.size + at;
-  float4 v[4] = {};
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (gb < ge) {
-    int c = static_cast<int>(static_cast<int64_t>(gb) * s.chunks / total);
-    while (chunk_begin(c + 1, s.chunks, total) <= gb) ++c;
-    if (chunk_begin(c + 1, s.chunks, total) >= ge) return;  // inside one chunk: already written
-    for (; c < s.chunks; ++c) {
-      const int cb = chunk_begin(c, s.chunks, total);
-      if (cb >= ge) break;
-      if (chunk_begin(c + 1, s.chunks, total) == cb) continue;  // an empty chunk
-      const float* part = s.part + (2 * c + (gb > cb ? 1 : 0)) * s.size + at;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= n) break;
-        const float4 o = __ldg(reinterpret_cast<const float4*>(part + i * 1024));
-        v[i].x += o.x, v[i].y += o.y, v[i].z += o.z, v[i].w += o.w;
-      }
+    const int chunks = min(blockIdx.z ? p.side[1].chunks : p.side[0].chunks, total);
+    const int c0 = chunk_of(gb, chunks, total), c1 = chunk_of(ge - 1, chunks, total);
+    if (c0 == c1) return;  // inside one chunk: already written
+    // the group's run is a chunk's second one only where the group starts inside it
+    v = __ldg(reinterpret_cast<const float4*>(
+        part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size + at));
+#pragma unroll 8
+    for (int c = c0 + 1; c <= c1; ++c) {
+      const float4 o = __ldg(reinterpret_cast<const float4*>(part + 2 * c * size + at));
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n)
-      *reinterpret_cast<uint2*>(out + i * 1024) = make_uint2(pack2(v[i].x, v[i].y), pack2(v[i].z, v[i].w));
+  *reinterpret_cast<uint2*>(dst + g * size + at) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
 }
 
 // -------------------------------------------------------------------- host
@@ -1169,9 +1189,9 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   const int raw = codes ? kAhead * kRawStep : 0;
   p.stages = std::max(2, std::min(kShrinkMaxStages, (110 * 1024 - raw) / p.stage_bytes));
   const int smem = std::max(p.stages * p.stage_bytes + raw, 128 * (rp + 4) * 4) + 1024;
-  // split the reduction until two blocks per SM are busy, 8 blocks of one cluster at most
-  int splits = 1;
-  while (splits < 8 && tiles_estimate(c) * splits * 2 <= 2 * kSms) splits *= 2;
+  // Split the reduction over a cluster of up to 8 blocks while all clusters fit at once: two
+  // blocks per SM, of which about 1 in 7 stays empty since a cluster keeps within a GPC.
+  const int splits = std::max(1, std::min(8, 2 * kSms * 6 / 7 / tiles_estimate(c)));
   const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
@@ -1188,15 +1208,14 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, c
   p.slots = rp > 64 ? 2 : 3;
   p.bslots = std::min(kExpandSlots, (110 * 1024 - hbytes - p.slots * p.stage_bytes) / 16384);
   const int smem = hbytes + p.slots * p.stage_bytes + p.bslots * 16384 + 1024;
-  // column slices of at least 256 columns so that the last wave of blocks is nearly full
-  const int tiles = tiles_estimate(c);
+  // column slices: whole waves of two blocks per SM; starting a block costs about 4 units
+  const int tiles = tiles_estimate(c), units = n / 64;
   int best = 1;
-  double best_eff = 0.0;
-  for (int s = 1; s <= std::max(1, n / 256); ++s) {
-    const double waves = double(tiles) * s / (2 * kSms);
-    const double eff = waves / std::max(1.0, double(int64_t(waves + 0.999999)));
-    if (eff > best_eff + 0.02) best = s, best_eff = eff;
-    if (waves > 4.0) break;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= std::max(1, units / 4); ++s) {
+    const int64_t waves = (int64_t(tiles) * s + 2 * kSms - 1) / (2 * kSms);
+    const int64_t all = waves * (4 + (units + s - 1) / s);
+    if (all < cost) cost = all, best = s;
   }
   const dim3 grid(best, row_tiles_cap(c.g.b, c.g.count, 128));
   return launch(trans ? expand_kernel<true> : expand_kernel<false>, grid, kExpandThreads, smem, 1, pdl,
@@ -1327,7 +1346,7 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
   FinishArgs f{first128_of(c.g), c.g.count, {}};
   f.side[0] = {pa, c.da, int64_t(c.m) * c.r, s.a.chunks};
   f.side[1] = {pb, c.db, int64_t(c.n) * c.r, s.b.chunks};
-  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 4095) / 4096;
+  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 1023) / 1024;
   return launch(finish_kernel, dim3(static_cast<unsigned>(blocks), c.g.count, 2), 256, 0, 1, false, f, st);
 }
 
