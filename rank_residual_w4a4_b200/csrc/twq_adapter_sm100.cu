@@ -728,6 +728,48 @@ __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles
   return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
 }
 
+// The rows of a run of tiles that one thread loads (row `first` + step j of each tile; -1 beyond
+// the tile's end), known a tile ahead, and the tile itself two ahead, so that no load of Z or
+// H waits for a look-up.
+template <int kRows>
+struct RowsAhead {
+  const int4* tiles;
+  const int32_t* order;
+  int tile, end, first, step;
+  int row[kRows], next[kRows];
+  int group, next_group;
+  int4 after;
+
+  __device__ __forceinline__ int4 load_tile(int i) const {
+    return i < end ? __ldg(tiles + i) : make_int4(-1, 0, 0, 0);
+  }
+  __device__ __forceinline__ void look_up(const int4& t, int (&r)[kRows]) const {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = first + step * j;
+      r[j] = i < t.z ? __ldg(order + t.y + i) : -1;
+    }
+  }
+  __device__ __forceinline__ void start(const int4* tl, const int32_t* ord, int begin, int stop, int f,
+                                        int st) {
+    tiles = tl, order = ord, tile = begin, end = stop, first = f, step = st;
+    const int4 t0 = load_tile(begin), t1 = load_tile(begin + 1);
+    after = load_tile(begin + 2);
+    look_up(t0, row);
+    look_up(t1, next);
+    group = t0.x, next_group = t1.x;
+  }
+  __device__ __forceinline__ void advance() {
+    ++tile;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) row[j] = next[j];
+    group = next_group;
+    look_up(after, next);
+    next_group = after.x;
+    after = load_tile(tile + 2);
+  }
+};
+
 // A slice of Z's 128-column blocks (blockIdx.x), the row tiles of chunk blockIdx.y. Tiles of one
 // group form a run, summed in tensor memory (lane = column of Z, column = rank). A run that
 // is its whole group is rounded into `out`; one that the chunk's ends cut leaves its fp32
@@ -787,35 +829,25 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
 
   if (warp < 8) {
     const int r0 = tid >> 3, ch = tid & 7;  // rows r0 + 32 j, chunk ch (or 16 codes)
-    // position of the loads: step -> (tile, block), the tile's rows
-    int ltile = begin, lblk = 0;
-    int64_t row[4];
-    bool ok[4];
-    auto load_rows = [&]() {
-      const int4 t = ltile < end ? tiles[ltile] : make_int4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ok[j] = r0 + 32 * j < t.z;
-        row[j] = ok[j] ? p.order[t.y + r0 + 32 * j] : 0;
-      }
-    };
-    load_rows();
+    RowsAhead<4> ra;  // position of the loads: its tile, and the block in it
+    ra.start(tiles, p.order, begin, end, r0, 32);
+    int lblk = 0;
     auto advance = [&]() {
       if (++lblk == nb) {
         lblk = 0;
-        ++ltile;
-        load_rows();
+        ra.advance();
       }
     };
     int rs = 0;  // raw slot of the next fetch, the one that the current step has just read
     auto fetch = [&]() {
-      if (ltile < end) {
+      if (ra.tile < end) {
         const uint32_t at = sraw + rs * kOuterRawStep + tid * 16;
         const uint32_t st = sraw + rs * kOuterRawStep + 16384 + tid * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          cp16(at + j * 4096, p.q + row[j] * p.k + (blk0 + lblk) * 128 + ch * 16, ok[j]);
-          cp4(st + j * 1024, p.sq + row[j] * (p.k >> 7) + blk0 + lblk, ok[j]);
+          const int64_t row = max(ra.row[j], 0);
+          cp16(at + j * 4096, p.q + row * p.k + (blk0 + lblk) * 128 + ch * 16, ra.row[j] >= 0);
+          cp4(st + j * 1024, p.sq + row * (p.k >> 7) + blk0 + lblk, ra.row[j] >= 0);
         }
         advance();
       }
@@ -861,7 +893,8 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
-                 p.z + row[j] * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8, ok[j]);
+                 p.z + max(ra.row[j], 0) * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8,
+                 ra.row[j] >= 0);
         cp_arrive(&s_full[slot]);
         advance();
       }
@@ -879,6 +912,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       uint32_t phase = 0, hphase = 0;
       bool alive = true;
       bool fresh = true;
+      int run_end = min(end, p.first128[tiles[begin].x + 1]);
       for (int tile = begin; tile < end && alive; ++tile) {
         const uint32_t hb = sh + hs * hbytes;
         const int nth = tile - begin;
@@ -918,12 +952,12 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
           hs = 0;
           hphase ^= 1u;
         }
-        fresh = tile + 1 < end && tiles[tile + 1].x != tiles[tile].x;
-        if (fresh || tile + 1 == end) {
+        fresh = tile + 1 == run_end;
+        if (fresh) {
           mma_commit(&s_run);
-          if (fresh && !wait(&s_free, runs & 1, &s_abort, kSiteAccEmpty)) {
-            alive = false;
-            break;
+          if (run_end < end) {
+            run_end = min(end, p.first128[tiles[run_end].x + 1]);
+            alive = wait(&s_free, runs & 1, &s_abort, kSiteAccEmpty);
           }
           ++runs;
           tc_fence_after();
@@ -1018,32 +1052,27 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
     int slot = 0, hs = 0, step = 0;
     uint32_t phase = 0, hphase = 0;
     bool alive = true;
-    int rows[16];  // of the next tile, -1 beyond its end
-    auto load_rows = [&](int tile) {
-      const int4 t = tile < end ? tiles[tile] : make_int4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) rows[j] = hr + 8 * j < t.z ? p.order[t.y + hr + 8 * j] : -1;
-    };
-    load_rows(begin);
+    RowsAhead<16> ra;
+    ra.start(tiles, p.order, begin, end, hr, 8);
     for (int tile = begin; tile < end && alive; ++tile) {
       if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
         break;
-      const int4 t = tiles[tile];
       for (int c = hc; c < rchunks; c += 8)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const bool in = rows[j] >= 0 && c * 8 < p.r;
+          const bool in = ra.row[j] >= 0 && c * 8 < p.r;
           cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(hr + 8 * j, hc),
-               p.h + (in ? static_cast<int64_t>(rows[j]) * p.r + c * 8 : 0), in);
+               p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
         }
       cp_arrive(&s_hfull[hs]);
-      load_rows(tile + 1);
       if (++hs == p.htiles) {
         hs = 0;
         hphase ^= 1u;
       }
+      const int group = ra.group;
+      ra.advance();
       if constexpr (kDual) {
-        const uint16_t* wg = p.w + (static_cast<int64_t>(t.x) * p.k + blk0 * 128) * p.r;
+        const uint16_t* wg = p.w + (static_cast<int64_t>(group) * p.k + blk0 * 128) * p.r;
         for (int b = 0; b < nb; ++b, ++step) {
           if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
             alive = false;
