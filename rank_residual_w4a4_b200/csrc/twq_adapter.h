@@ -22,8 +22,9 @@ inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
 
 // tiles: {number of 16-row tiles, number of 128-row tiles, 0, 0}, then room for
 // row_tiles_cap(b, count, 16) entries of the first list and ..., 128) of the second;
-// an entry is {group or -1, first position in order, rows, 0}. After the entries: for each
-// group, then for the rows without one, the 128-row tiles before it (count + 1 integers).
+// an entry is {group or -1, first position in order, rows, first row where the rows follow one
+// another in the batch, else -1}. After the entries: for each group, then for the rows without
+// one, the 128-row tiles before it (count + 1 integers).
 struct RowGroupsView {
   int b, count;
   int32_t* order;

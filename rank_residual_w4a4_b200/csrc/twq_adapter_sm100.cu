@@ -11,12 +11,15 @@
 // that is read or written, against some 250 per byte that the tensor cores could do. So
 // each streams its large operand once through shared memory (or, expand, registers) and
 // leaves the products to tcgen05.mma with fp32 accumulators in tensor memory.
-// Rows are fetched by 16-byte cp.async into the 128-byte-swizzle layout, because a tile's
-// rows stand anywhere in the batch; rows beyond the tile and ranks beyond r are filled
-// with zeros, so nothing of another row or adapter takes part in a product.
+// A tile whose rows follow one another in the batch (a request's prompt) comes by TMA; rows that
+// stand anywhere by 16-byte cp.async, into the same 128-byte-swizzle layout. Measured on 8192 rows
+// of 25600: TMA tiles 6.0 TB/s, TMA row gathers (4 rows an instruction) 3.8, cp.async 4.8.
+// Where rows of a tile are summed, its missing rows are zeros, and ranks beyond r always are,
+// so nothing of another row or adapter takes part in a product.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "sm100_ptx.cuh"
 #include "twq_adapter.h"
@@ -78,10 +81,26 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) 
 }
 // One arrival on `bar` (whose count includes it) once all cp.async of this thread so far have
 // landed. The thread goes on at once, so the depth of the loads is the number of stages, not
-// what the loading threads can wait for. The reader of the data fences the proxies.
+// what the loading threads can wait for. The reader of the data fences the proxies. Each
+// arrival takes the barrier about 2 cycles (320 of them: 0.35 us a stage, of the 0.7 us that
+// a 32 KB stage takes from HBM), so few threads load, with many copies each.
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+// More arrivals of one thread, for a barrier that counts the threads of the other way to load.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(count)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                         int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
@@ -168,8 +187,55 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// The rows of a run of tiles that one thread loads (row `first` + step j of each tile; -1 beyond
+// the tile's end), known a tile ahead, and the tile itself two ahead, so that no load of Z or
+// H waits for a look-up.
+template <int kRows>
+struct RowsAhead {
+  const int4* tiles;
+  const int32_t* order;
+  int tile, end, first, step;
+  int row[kRows], next[kRows];
+  int group, next_group;
+  int run, next_run;    // first row of a tile whose rows follow one another, else -1
+  int count, next_count;
+  int4 after;
+
+  __device__ __forceinline__ int4 load_tile(int i) const {
+    return i < end ? __ldg(tiles + i) : make_int4(-1, 0, 0, -1);
+  }
+  __device__ __forceinline__ void look_up(const int4& t, int (&r)[kRows]) const {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = first + step * j;
+      r[j] = i < t.z ? __ldg(order + t.y + i) : -1;
+    }
+  }
+  __device__ __forceinline__ void start(const int4* tl, const int32_t* ord, int begin, int stop, int f,
+                                        int st) {
+    tiles = tl, order = ord, tile = begin, end = stop, first = f, step = st;
+    const int4 t0 = load_tile(begin), t1 = load_tile(begin + 1);
+    after = load_tile(begin + 2);
+    look_up(t0, row);
+    look_up(t1, next);
+    group = t0.x, next_group = t1.x;
+    run = t0.w, next_run = t1.w;
+    count = t0.z, next_count = t1.z;
+  }
+  __device__ __forceinline__ void advance() {
+    ++tile;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) row[j] = next[j];
+    group = next_group, run = next_run, count = next_count;
+    look_up(after, next);
+    next_group = after.x, next_run = after.w, next_count = after.z;
+    after = load_tile(tile + 2);
+  }
+};
+
 // ------------------------------------------------------------------ shrink
 struct ShrinkArgs {
+  CUtensorMap map;  // Z: 128 rows x 64 columns
   const int4* tiles;
   const int32_t* order;
   int cap16;
@@ -184,7 +250,7 @@ struct ShrinkArgs {
   int stages, stage_bytes;
 };
 
-constexpr int kShrinkThreads = 352;  // 8 warps that load Z, then epilogue; 1 MMA warp; 2 load W
+constexpr int kShrinkThreads = 352;  // 8 warps load Z, then epilogue; MMA warp; 2 load W
 constexpr int kShrinkMaxStages = 6;
 // Codes are converted by the thread that loaded them: it keeps kAhead steps of its own codes
 // and scales in flight into a private part of shared memory, as it would in registers.
@@ -194,7 +260,7 @@ constexpr int kRawStep = 8192 + 2048;  // 128 x 64 codes; a scale for each 16
 // One row tile per cluster, whose blocks split the reduction over k and add their parts
 // through distributed shared memory in rank order.
 template <bool kCodes, bool kTrans>
-__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkArgs p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_constant__ ShrinkArgs p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kShrinkMaxStages], s_empty[kShrinkMaxStages], s_done;
   __shared__ uint32_t s_tmem;
@@ -215,9 +281,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
   uint8_t* smem = align1k(smem_raw);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t tmem_cols = p.rp <= 32 ? 32 : (p.rp <= 64 ? 64 : 128);
+  // rows beyond a partial tile's end then belong to others; their sums are not stored
+  const bool tma = !kCodes && t.w >= 0;
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s_full[i], kCodes ? 8 + 64 : 256 + 64);
+      mbar_init(&s_full[i], (kCodes ? 8 : tma ? 1 : 256) + 64);
       mbar_init(&s_empty[i], 1);
     }
     mbar_init(&s_done, 1);
@@ -236,7 +304,21 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
   const int k0 = static_cast<int>(static_cast<int64_t>(rank) * kb / splits);
   const int steps = static_cast<int>(static_cast<int64_t>(rank + 1) * kb / splits) - k0;
 
-  if (warp < 8) {
+  if (warp < 8 && tma) {
+    if (tid == 0) {
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int step = 0; step < steps; ++step) {
+        if (step >= p.stages && !wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+        mbar_arrive_expect_tx(&s_full[slot], 16384);
+        tma_load(sbase + slot * p.stage_bytes, &p.map, &s_full[slot], (k0 + step) * 64, t.w);
+        if (++slot == p.stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp < 8) {
     // Thread: rows tid / 8 + 32 j, chunk tid % 8 (BF16); rows tid / 4 + 64 j, 16 codes (codes).
     constexpr int kRows = kCodes ? 2 : 4;
     const int r0 = kCodes ? tid >> 2 : tid >> 3;
@@ -247,7 +329,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
     for (int j = 0; j < kRows; ++j) {
       const int i = r0 + j * (128 / kRows);
       ok[j] = i < t.z;
-      row[j] = ok[j] ? p.order[t.y + i] : 0;
+      row[j] = ok[j] ? __ldg(p.order + t.y + i) : 0;
     }
     const uint32_t raw = sbase + p.stages * p.stage_bytes;
     auto fetch = [&](int step) {
@@ -339,7 +421,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
       }
     }
     cp_wait_all();
-  } else if (lane == 0) {
+  } else if (warp == 8 && lane == 0) {
     const uint32_t idesc = idesc_bf16(p.rp) | (kTrans ? kBMajorMn : 0u);
     int slot = 0;
     uint32_t phase = 0;
@@ -408,6 +490,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const ShrinkA
 
 // ------------------------------------------------------------------ expand
 struct ExpandArgs {
+  CUtensorMap map;  // base: 128 rows x 64 columns
   const int4* tiles;
   const int32_t* order;
   int cap16;
@@ -416,12 +499,16 @@ struct ExpandArgs {
   const float* scale; // or null: 1
   const uint16_t* base;
   uint16_t* y;
+  const int32_t *first128, *offsets;
+  int b, count;
   int n, r, rp;
-  int stage_bytes, slots, bslots;  // a W stage; W stages; base stages of 16 KB
+  int stage_bytes, hslots, bslots;  // a W stage; H tiles; base stages of 16 KB
 };
 
-constexpr int kExpandThreads = 416;  // 8 epilogue warps, 1 MMA warp, 4 warps that load base and W
-constexpr int kExpandSlots = 4;      // at most: W stages with their accumulators; base stages
+constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H and base, 1 loads W
+constexpr int kExpandSlots = 4;      // W stages, and accumulators of 64 columns
+constexpr int kBaseSlots = 4;        // base stages, at most
+constexpr int kExpandBars = 256;     // bytes of barriers in front of the tiles' space
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
@@ -447,12 +534,6 @@ __device__ __forceinline__ void st_stream(void* ptr, uint4 v) {
                : "memory");
 }
 
-// Offset of 16-byte chunk c of row `row` of a base stage (128 rows x 128 bytes): the eight
-// lanes of a shared-memory phase read four chunks of two neighbouring rows.
-__device__ __forceinline__ uint32_t base_at(int row, int c) {
-  return static_cast<uint32_t>(row * 128 + ((c ^ ((row & 1) << 2) ^ ((row >> 1) & 3)) << 4));
-}
-
 // Pairs (columns 8 j + 2 t, + 1) of lane t of a quad, j = 0 .. 3, become the eight
 // columns 8 t .. 8 t + 7: a 4 x 4 transpose of pairs over the quad's lanes.
 __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
@@ -475,229 +556,280 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
   }
 }
 
-// Row tile blockIdx.y, columns in units of 64 split over the grid's x. The accumulator is
-// read in the 16x256b form, where a quad of lanes holds 32 columns of a row in pairs; W's
-// rows are stored permuted (or, kTrans, the pairs are transposed over the quad), so that
-// each lane owns 8 consecutive columns and a quad writes 64 bytes of a row. base comes
-// through shared memory, several stages ahead; it may be y itself, since the lane that writes
-// an element is the only one that reads it, from the stage, before that.
+// The units (64 columns of a row tile) of all tiles with an adapter, one tile's after
+// another's, in equal shares for the grid's blocks. The accumulator is read in the 16x256b form,
+// where a quad of lanes holds 32 columns of a row in pairs; W's rows are stored permuted (or,
+// kTrans, the pairs are transposed over the quad), so that each lane owns 8 consecutive columns
+// and a quad writes 64 bytes of a row. base comes through shared memory, several stages ahead;
+// it may be y itself, since the lane that writes an element is the only one that reads it, from
+// the stage, before that.
 // Launched so that it may start before the kernel that writes H has ended: until then it reads
 // only what that kernel does not write (the grouping, W, base) and writes nothing.
 template <bool kTrans>
-__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandArgs p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kExpandSlots], s_done[kExpandSlots], s_free[kExpandSlots],
-      s_bfull[kExpandSlots], s_bfree[kExpandSlots], s_hfull, s_end;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (static_cast<int>(blockIdx.y) >= p.tiles[0].y) return;
-  const int4 t = p.tiles[1 + p.cap16 + blockIdx.y];
-  const int units = p.n / 64;
-  const int u0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * units / gridDim.x);
-  const int count = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * units / gridDim.x) - u0;
-  if (t.x < 0) {  // rows without adapter: base itself
-    if (p.base == p.y) return;
-    pdl_wait();
-    for (int i = tid; i < t.z * count * 8; i += kExpandThreads) {
-      const int64_t at = static_cast<int64_t>(p.order[t.y + i / (count * 8)]) * p.n + u0 * 64 +
-                         i % (count * 8) * 8;
-      st_stream(p.y + at, p.base ? ld_stream(p.base + at) : make_uint4(0, 0, 0, 0));
-    }
-    return;
-  }
-  uint8_t* smem = align1k(smem_raw);
-  const uint32_t sh = smem_u32(smem);
+__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem[];  // no other shared memory: two blocks fill an SM
   const int kt = (p.rp + 63) / 64;  // 64-wide tiles of the reduction
-  const uint32_t sw = sh + kt * 16384;
-  const uint32_t sb = sw + p.slots * p.stage_bytes;
-  if (tid == 0) {
-    for (int i = 0; i < kExpandSlots; ++i) {
-      mbar_init(&s_full[i], 128);
-      mbar_init(&s_bfull[i], 128);
-      mbar_init(&s_bfree[i], 8);
-      mbar_init(&s_done[i], 1);
-      mbar_init(&s_free[i], 8);
-    }
-    mbar_init(&s_hfull, 256);
-    mbar_init(&s_end, 1);
-    s_abort = 0;
-    fence_barrier_init();
-  }
-  if (warp == 8) {
-    tmem_alloc(&s_tmem, 64 * kExpandSlots);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t sh = smem_u32(smem);
+  const uint32_t sw = sh + p.hslots * kt * 16384;
+  const uint32_t sb = sw + kExpandSlots * p.stage_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (sb - sh) + p.bslots * 16384);
+  uint64_t* s_full = bars;                          // W stage
+  uint64_t* s_done = s_full + kExpandSlots;         // accumulator (and its W stage read)
+  uint64_t* s_free = s_done + kExpandSlots;
+  uint64_t* s_bfull = s_free + kExpandSlots;
+  uint64_t* s_bfree = s_bfull + kBaseSlots;
+  uint64_t* s_hfull = s_bfree + kBaseSlots;
+  uint64_t* s_hfree = s_hfull + 2;
+  uint64_t* s_end = s_hfree + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_end + 1);
+  int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = p.n / 64;
+  const int64_t total = static_cast<int64_t>(p.first128[p.count]) * units;
+  const int64_t from = blockIdx.x * total / gridDim.x;
+  const int work = static_cast<int>((blockIdx.x + 1) * total / gridDim.x - from);
+  const int4* tiles = p.tiles + 1 + p.cap16;
+  const int tile0 = static_cast<int>(from / units), unit0 = static_cast<int>(from - int64_t(tile0) * units);
+  const int tile_end = tile0 + (unit0 + work + units - 1) / units;
 
-  if (warp < 8) {
-    const int t4 = lane & 3;
-    int64_t at[4];  // this lane's 8 columns of unit 0 in its four rows
-    bool ok[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rr = (warp & 3) * 32 + i * 8 + (lane >> 2);
-      ok[i] = rr < t.z;
-      at[i] = (ok[i] ? static_cast<int64_t>(p.order[t.y + rr]) : 0) * p.n + u0 * 64 + (warp >> 2) * 32 +
-              t4 * 8;
+  if (work > 0) {
+    if (tid == 0) {
+      for (int i = 0; i < kExpandSlots; ++i) {
+        mbar_init(&s_full[i], 32);
+        mbar_init(&s_done[i], 1);
+        mbar_init(&s_free[i], 8);
+      }
+      for (int i = 0; i < kBaseSlots; ++i) {
+        mbar_init(&s_bfull[i], 64);
+        mbar_init(&s_bfree[i], 8);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_hfull[i], 64);
+        mbar_init(&s_hfree[i], 1);
+      }
+      mbar_init(s_end, 1);
+      *s_abort = 0;
+      fence_barrier_init();
     }
-    const float f = p.scale ? p.scale[t.x] : 1.0f;
-    {  // H: rows tid / 8 + 32 j, chunks tid % 8, + 8
-      int64_t hrow[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rr = (tid >> 3) + 32 * j;
-        hrow[j] = rr < t.z ? p.order[t.y + rr] : -1;
-      }
-      pdl_wait();
-      for (int c = tid & 7; c * 8 < p.rp; c += 8)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = hrow[j] >= 0 && c * 8 < p.r;
-          cp16(sh + (c >> 3) * 16384 + sw128((tid >> 3) + 32 * j, tid & 7),
-               p.h + (in ? hrow[j] * p.r + c * 8 : 0), in);
-        }
-      cp_arrive(&s_hfull);
+    if (warp == 8) {
+      tmem_alloc(s_tmem, 64 * kExpandSlots);
+      tmem_relinquish();
     }
-    int slot = 0, bs = 0;
-    uint32_t ph = 0, bph = 0;
-    for (int u = 0; u < count; ++u) {
-      if (!warp_wait(&s_done[slot], ph, &s_abort, kSiteDone)) break;
-      tc_fence_after();
-      uint32_t v[2][16];
-      const uint32_t ta =
-          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + (warp >> 2) * 32;
-      tmem_ld_16x256b_x4(ta, v[0]);
-      tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      uint4 b[4] = {};
-      if (p.base) {
-        if (!warp_wait(&s_bfull[bs], bph, &s_abort, kSiteFull)) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b[i] = lds16(sb + bs * 16384 +
-                       base_at((warp & 3) * 32 + i * 8 + (lane >> 2), (warp >> 2) * 4 + t4));
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s_free[slot]);
-        mbar_arrive(&s_bfree[bs]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // rows lane / 4 + 8 i
-        float a[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
-        if constexpr (kTrans) quad_transpose(a, t4);
-        const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
-        if (ok[i]) st_stream(p.y + at[i] + u * 64, make_uint4(o[0], o[1], o[2], o[3]));
-      }
-      if (++slot == p.slots) {
-        slot = 0;
-        ph ^= 1u;
-      }
-      if (++bs == p.bslots) {
-        bs = 0;
-        bph ^= 1u;
-      }
-    }
-  } else if (warp == 8) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(64) | (kTrans ? kBMajorMn : 0u);
-      int slot = 0;
-      uint32_t ph = 0;
-      for (int u = 0; u < count; ++u) {
-        if (u == 0 && !wait(&s_hfull, 0, &s_abort, kSiteFull)) break;
-        if (!wait(&s_full[slot], ph, &s_abort, kSiteFull)) break;
-        if (u >= p.slots && !wait(&s_free[slot], ph ^ 1u, &s_abort, kSiteAccEmpty)) break;
-        fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+
+    if (warp < 8) {
+      const int t4 = lane & 3;
+      RowsAhead<4> ra;  // rows lane / 4 + 8 i of this warp's 32
+      ra.start(tiles, p.order, tile0, tile_end, (warp & 3) * 32 + (lane >> 2), 8);
+      float f = p.scale ? p.scale[ra.group] : 1.0f;
+      int slot = 0, bs = 0, u = unit0;
+      uint32_t ph = 0, bph = 0;
+      for (int i0 = 0; i0 < work; ++i0) {
+        if (!warp_wait(&s_done[slot], ph, s_abort, kSiteDone)) break;
         tc_fence_after();
-        const uint32_t ws = sw + slot * p.stage_bytes;
-        for (int k = 0; k < p.rp / 16; ++k)
-          mma_bf16(tmem + slot * 64, smem_desc_sw128(sh + (k >> 2) * 16384 + (k & 3) * 32),
-                   kTrans ? smem_desc_mn(ws + k * 2048, 0)
-                          : smem_desc_sw128(ws + (k >> 2) * 8192 + (k & 3) * 32),
-                   idesc, k > 0);
-        mma_commit(&s_done[slot]);
-        if (++slot == p.slots) {
+        uint32_t v[2][16];
+        const uint32_t ta =
+            tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + (warp >> 2) * 32;
+        tmem_ld_16x256b_x4(ta, v[0]);
+        tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
+        tmem_wait_ld();
+        tc_fence_before();
+        uint4 b[4] = {};
+        if (p.base) {
+          if (!warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull)) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            b[i] = lds16(sb + bs * 16384 +
+                         sw128((warp & 3) * 32 + i * 8 + (lane >> 2), (warp >> 2) * 4 + t4));
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_free[slot]);
+          mbar_arrive(&s_bfree[bs]);
+        }
+        const int col = u * 64 + (warp >> 2) * 32 + t4 * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
+          if constexpr (kTrans) quad_transpose(a, t4);
+          const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
+          if (ra.row[i] >= 0)
+            st_stream(p.y + static_cast<int64_t>(ra.row[i]) * p.n + col,
+                      make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        if (++u == units) {
+          u = 0;
+          ra.advance();
+          if (p.scale && ra.group >= 0) f = p.scale[ra.group];
+        }
+        if (++slot == kExpandSlots) {
           slot = 0;
           ph ^= 1u;
         }
-      }
-      mma_commit(&s_end);
-      wait_mmas(&s_end);
-    }
-  } else {
-    const int l = tid - 288;
-    const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.n * p.r;
-    const int chunks = p.rp / 8;
-    const int br = l >> 3, bc = l & 7;  // base: rows br + 16 j, chunk bc
-    const uint16_t* bp[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      bp[j] = p.base + (br + 16 * j < t.z ? static_cast<int64_t>(p.order[t.y + br + 16 * j]) : 0) * p.n +
-              u0 * 64 + bc * 8;
-    int slot = 0, bs = 0;
-    uint32_t ph = 0, bph = 0;
-    for (int u = 0; u < count; ++u) {
-      if (p.base) {
-        if (u >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, &s_abort, kSiteEmpty)) break;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          cp16(sb + bs * 16384 + base_at(br + 16 * j, bc), bp[j] + u * 64, br + 16 * j < t.z);
-        cp_arrive(&s_bfull[bs]);
         if (++bs == p.bslots) {
           bs = 0;
           bph ^= 1u;
         }
       }
-      // the MMAs that read this stage are done when their accumulator is
-      if (u >= p.slots && !warp_wait(&s_done[slot], ph ^ 1u, &s_abort, kSiteEmpty)) break;
-      const uint32_t ws = sw + slot * p.stage_bytes;
-      const int col = (u0 + u) * 64;
-      if constexpr (kTrans) {
-        for (int i = l; i < p.rp * 8; i += 128) {
-          const int k = i >> 3;
-          cp16(ws + sw128(k, i & 7),
-               wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + col + (i & 7) * 8, k < p.r);
+    } else if (warp == 8) {
+      if (lane == 0) {
+        const uint32_t idesc = idesc_bf16(64) | (kTrans ? kBMajorMn : 0u);
+        int slot = 0, hs = 0, u = unit0;
+        uint32_t ph = 0, hph = 0;
+        for (int i = 0; i < work; ++i) {
+          if ((i == 0 || u == 0) && !wait(&s_hfull[hs], hph, s_abort, kSiteFull)) break;
+          if (!wait(&s_full[slot], ph, s_abort, kSiteFull)) break;
+          if (i >= kExpandSlots && !wait(&s_free[slot], ph ^ 1u, s_abort, kSiteAccEmpty)) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t ws = sw + slot * p.stage_bytes, hb = sh + hs * kt * 16384;
+          for (int k = 0; k < p.rp / 16; ++k)
+            mma_bf16(tmem + slot * 64, smem_desc_sw128(hb + (k >> 2) * 16384 + (k & 3) * 32),
+                     kTrans ? smem_desc_mn(ws + k * 2048, 0)
+                            : smem_desc_sw128(ws + (k >> 2) * 8192 + (k & 3) * 32),
+                     idesc, k > 0);
+          mma_commit(&s_done[slot]);
+          if (++u == units) {
+            u = 0;
+            mma_commit(&s_hfree[hs]);
+            if (++hs == p.hslots) {
+              hs = 0;
+              hph ^= 1u;
+            }
+          }
+          if (++slot == kExpandSlots) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        }
+        mma_commit(s_end);
+        wait_mmas(s_end);
+      }
+    } else {
+      const int chunks = p.rp / 8;
+      int u = unit0;
+      if (warp < 11) {
+        const int r0 = (tid - 288) >> 3, ch = tid & 7;  // rows r0 + 8 j, chunk ch
+        RowsAhead<16> ra;
+        ra.start(tiles, p.order, tile0, tile_end, r0, 8);
+        int hs = 0, seen = 0, bs = 0;
+        uint32_t hph = 0, bph = 0;
+        pdl_wait();
+        for (int i = 0; i < work; ++i) {
+          if (i == 0 || u == 0) {
+            if (seen++ >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_abort, kSiteHEmpty)) break;
+            for (int c = ch; c < chunks; c += 8)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const bool in = ra.row[j] >= 0 && c * 8 < p.r;
+                cp16(sh + (hs * kt + (c >> 3)) * 16384 + sw128(r0 + 8 * j, ch),
+                     p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+              }
+            cp_arrive(&s_hfull[hs]);
+            if (++hs == p.hslots) {
+              hs = 0;
+              hph ^= 1u;
+            }
+          }
+          if (p.base) {
+            if (i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_abort, kSiteEmpty)) break;
+            if (ra.run >= 0) {  // rows beyond a partial tile's end are read and not used
+              if (tid == 288) {
+                mbar_arrive_expect_tx(&s_bfull[bs], 16384);
+                tma_load(sb + bs * 16384, &p.map, &s_bfull[bs], u * 64, ra.run);
+                mbar_arrive_n(&s_bfull[bs], 63);
+              }
+            } else {
+              const uint16_t* src = p.base + u * 64 + ch * 8;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                cp16(sb + bs * 16384 + sw128(r0 + 8 * j, ch),
+                     src + static_cast<int64_t>(max(ra.row[j], 0)) * p.n, ra.row[j] >= 0);
+              cp_arrive(&s_bfull[bs]);
+            }
+            if (++bs == p.bslots) {
+              bs = 0;
+              bph ^= 1u;
+            }
+          }
+          if (++u == units) {
+            u = 0;
+            ra.advance();
+          }
         }
       } else {
-        for (int i = l; i < 64 * chunks; i += 128) {
-          const int nr = i / chunks, c = i % chunks;
-          // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
-          const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
-          const bool ok = c * 8 < p.r;
-          cp16(ws + (c >> 3) * 8192 + sw128(q, c & 7),
-               wg + static_cast<int64_t>(col + nr) * p.r + (ok ? c * 8 : 0), ok);
+        const int r0 = lane >> 3, ch = lane & 7;
+        int tile = tile0, slot = 0, group = __ldg(&tiles[tile].x);
+        uint32_t ph = 0;
+        for (int i = 0; i < work; ++i) {
+          // the MMAs that read this stage are done when their accumulator is
+          if (i >= kExpandSlots && !warp_wait(&s_done[slot], ph ^ 1u, s_abort, kSiteEmpty)) break;
+          const uint16_t* wg = p.w + static_cast<int64_t>(group) * p.n * p.r;
+          const uint32_t ws = sw + slot * p.stage_bytes;
+          if constexpr (kTrans) {
+            for (int k = r0; k < p.rp; k += 4)
+              cp16(ws + sw128(k, ch), wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + u * 64 + ch * 8,
+                   k < p.r);
+          } else {
+            for (int c = ch; c < chunks; c += 8) {
+              const bool in = c * 8 < p.r;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int nr = r0 + 4 * j;
+                // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
+                const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
+                cp16(ws + (c >> 3) * 8192 + sw128(q, ch),
+                     wg + static_cast<int64_t>(u * 64 + nr) * p.r + (in ? c * 8 : 0), in);
+              }
+            }
+          }
+          cp_arrive(&s_full[slot]);
+          if (++slot == kExpandSlots) {
+            slot = 0;
+            ph ^= 1u;
+          }
+          if (++u == units && i + 1 < work) {
+            u = 0;
+            group = __ldg(&tiles[++tile].x);
+          }
         }
       }
-      cp_arrive(&s_full[slot]);
-      if (++slot == p.slots) {
-        slot = 0;
-        ph ^= 1u;
-      }
+      cp_wait_all();
     }
-    cp_wait_all();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 64 * kExpandSlots);
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 64 * kExpandSlots);
+
+  // Rows without adapter: base itself.
+  if (p.base == p.y) return;
+  pdl_wait();
+  const int bare = p.offsets[p.count];
+  const int64_t items = static_cast<int64_t>(p.b - bare) * (p.n / 8);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kExpandThreads + tid; i < items;
+       i += static_cast<int64_t>(gridDim.x) * kExpandThreads) {
+    const int64_t rr = i / (p.n / 8);
+    const int64_t at = static_cast<int64_t>(p.order[bare + rr]) * p.n + (i - rr * (p.n / 8)) * 8;
+    st_stream(p.y + at, p.base ? ld_stream(p.base + at) : make_uint4(0, 0, 0, 0));
+  }
 }
 
 // ------------------------------------------------------------------- outer
 struct OuterArgs {
+  CUtensorMap map;  // Z: 128 rows x 64 columns
   const int4* tiles;
   const int32_t* order;
   const int32_t* first128;  // tiles of 128 rows before each group; [count]: all with adapter
@@ -711,7 +843,7 @@ struct OuterArgs {
   uint16_t* out;      // count x k x r, or (kByRank) count x r x k
   float* part;        // 2 gridDim.y slots shaped like one group's output
   const uint16_t* w;  // kDual: count x k x r
-  float* dpart;       // kDual: gridDim.x x b x r, rows in the order of `order`
+  float* dpart;       // kDual: gridDim.x x b x r sums
   int64_t b;
   int k, r, rp;
   int stages, htiles; // Z stages, H tiles in shared memory
@@ -719,7 +851,7 @@ struct OuterArgs {
   uint32_t tmem_cols;
 };
 
-constexpr int kOuterThreads = 480;  // 8 warps load Z; MMA warp; 4 drain warps (9 .. 12); 2 load H, W
+constexpr int kOuterThreads = 480;  // 8 warps load Z; MMA warp; 4 drain; 2 load H, W
 constexpr int kOuterStages = 4;     // at most
 constexpr int kOuterAhead = 3;      // as kAhead
 constexpr int kOuterRawStep = 16384 + 4096;
@@ -728,56 +860,17 @@ __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles
   return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
 }
 
-// The rows of a run of tiles that one thread loads (row `first` + step j of each tile; -1 beyond
-// the tile's end), known a tile ahead, and the tile itself two ahead, so that no load of Z or
-// H waits for a look-up.
-template <int kRows>
-struct RowsAhead {
-  const int4* tiles;
-  const int32_t* order;
-  int tile, end, first, step;
-  int row[kRows], next[kRows];
-  int group, next_group;
-  int4 after;
-
-  __device__ __forceinline__ int4 load_tile(int i) const {
-    return i < end ? __ldg(tiles + i) : make_int4(-1, 0, 0, 0);
-  }
-  __device__ __forceinline__ void look_up(const int4& t, int (&r)[kRows]) const {
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int i = first + step * j;
-      r[j] = i < t.z ? __ldg(order + t.y + i) : -1;
-    }
-  }
-  __device__ __forceinline__ void start(const int4* tl, const int32_t* ord, int begin, int stop, int f,
-                                        int st) {
-    tiles = tl, order = ord, tile = begin, end = stop, first = f, step = st;
-    const int4 t0 = load_tile(begin), t1 = load_tile(begin + 1);
-    after = load_tile(begin + 2);
-    look_up(t0, row);
-    look_up(t1, next);
-    group = t0.x, next_group = t1.x;
-  }
-  __device__ __forceinline__ void advance() {
-    ++tile;
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) row[j] = next[j];
-    group = next_group;
-    look_up(after, next);
-    next_group = after.x;
-    after = load_tile(tile + 2);
-  }
-};
-
 // A slice of Z's 128-column blocks (blockIdx.x), the row tiles of chunk blockIdx.y. Tiles of one
 // group form a run, summed in tensor memory (lane = column of Z, column = rank). A run that
 // is its whole group is rounded into `out`; one that the chunk's ends cut leaves its fp32
-// sums in the chunk's slot (0: the run starts the chunk, else 1) for the finish kernel.
+// sums in the chunk's slot (0: the run starts the chunk, else 1) for the finish kernel, in the
+// order [block][rank / 4][column of the block][4], in which a warp writes 512 bytes at a time
+// (rows of the output would be 32 pieces in 32 lines: 6 us a run at 768 columns of rank 64).
 // kDual (r <= 64): the same Z stage also serves the product over its columns, dh = Z W: a
-// tile's 128 x r sums over this slice go to `dpart`, and dY is read once for both gradients.
+// tile's 128 x r sums over this slice go to `dpart` ([slice][rank / 4][position][4]), and dY is
+// read once for both gradients.
 template <bool kCodes, bool kByRank, bool kDual>
-__global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs p) {
+__global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_constant__ OuterArgs p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kOuterStages], s_empty[kOuterStages], s_hfull[kOuterStages],
       s_hempty[kOuterStages], s_dfull[2], s_dfree[2], s_run, s_free, s_end;
@@ -888,14 +981,23 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
         if (lane == 0) mbar_arrive(&s_full[slot]);
         fetch();
       } else {
+        if (ra.run >= 0 && ra.count == 128) {
+          if (tid == 0) {
+            mbar_arrive_expect_tx(&s_full[slot], 32768);
+            tma_load(zs, &p.map, &s_full[slot], (blk0 + lblk) * 128, ra.run);
+            tma_load(zs + 16384, &p.map, &s_full[slot], (blk0 + lblk) * 128 + 64, ra.run);
+            mbar_arrive_n(&s_full[slot], 255);
+          }
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
-                 p.z + max(ra.row[j], 0) * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8,
-                 ra.row[j] >= 0);
-        cp_arrive(&s_full[slot]);
+            for (int half = 0; half < 2; ++half)
+              cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
+                   p.z + max(ra.row[j], 0) * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8,
+                   ra.row[j] >= 0);
+          cp_arrive(&s_full[slot]);
+        }
         advance();
       }
       if (++slot == stages) {
@@ -966,7 +1068,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       mma_commit(&s_end);
       wait_mmas(&s_end);
     }
-  } else if (warp < 13) {
+  } else if (warp > 8 && warp < 13) {
     const int sub = warp & 3;  // tensor-memory lanes of this warp
     const uint32_t lanes = static_cast<uint32_t>(sub * 32) << 16;
     const int64_t size = static_cast<int64_t>(p.k) * p.r;
@@ -988,18 +1090,17 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
           }
           tc_fence_after();
           const int i = sub * 32 + lane;
-          float* dst = p.dpart + (static_cast<int64_t>(blockIdx.x) * p.b + t.y + i) * p.r;
-          for (int c = 0; c < p.r; c += 8) {
-            uint32_t v[8];
-            tmem_ld8(tmem + lanes + p.dcol + (nth & 1) * p.rp + c, v);
+          float* dst = p.dpart + (static_cast<int64_t>(blockIdx.x) * p.r * p.b + (t.y + i) * 4);
+          for (int c = 0; c < p.rp; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem + lanes + p.dcol + (nth & 1) * p.rp + c, v);
             tmem_wait_ld();
-            float o[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) o[u] = f * __uint_as_float(v[u]);
-            if (i < t.z) {
-              *reinterpret_cast<float4*>(dst + c) = make_float4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<float4*>(dst + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
-            }
+            for (int u = 0; u < 16; u += 4)
+              if (i < t.z && c + u < p.r)
+                *reinterpret_cast<float4*>(dst + (c + u) * p.b) =
+                    make_float4(f * __uint_as_float(v[u]), f * __uint_as_float(v[u + 1]),
+                                f * __uint_as_float(v[u + 2]), f * __uint_as_float(v[u + 3]));
           }
           tc_fence_before();
           __syncwarp();
@@ -1016,29 +1117,32 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       uint16_t* out = p.out + g * size;
       for (int b = 0; b < nb; ++b) {
         const int64_t j = (blk0 + b) * 128 + sub * 32 + lane;
-        for (int c = 0; c < p.r; c += 8) {
-          uint32_t v[8];
-          tmem_ld8(tmem + lanes + b * p.rp + c, v);
+        float* quads = part + static_cast<int64_t>(blk0 + b) * 128 * p.r + (sub * 32 + lane) * 4;
+        for (int c = 0; c < p.rp; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem + lanes + b * p.rp + c, v);
           tmem_wait_ld();
-          float o[8];
+          float o[16];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) o[u] = f * __uint_as_float(v[u]);
-          if (kByRank) {
+          for (int u = 0; u < 16; ++u) o[u] = f * __uint_as_float(v[u]);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              if (whole) {
-                const uint32_t h2 = pack2(o[u], 0.0f);
-                out[(c + u) * static_cast<int64_t>(p.k) + j] = static_cast<uint16_t>(h2);
-              } else {
-                part[(c + u) * static_cast<int64_t>(p.k) + j] = o[u];
-              }
+          for (int u = 0; u < 16; u += 8) {
+            if (c + u >= p.r) break;
+            if (!whole) {
+              *reinterpret_cast<float4*>(quads + (c + u) * 128) =
+                  make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]);
+              *reinterpret_cast<float4*>(quads + (c + u + 4) * 128) =
+                  make_float4(o[u + 4], o[u + 5], o[u + 6], o[u + 7]);
+            } else if (kByRank) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                out[(c + u + e) * static_cast<int64_t>(p.k) + j] =
+                    static_cast<uint16_t>(pack2(o[u + e], 0.0f));
+            } else {
+              *reinterpret_cast<uint4*>(out + j * p.r + c + u) =
+                  make_uint4(pack2(o[u], o[u + 1]), pack2(o[u + 2], o[u + 3]),
+                             pack2(o[u + 4], o[u + 5]), pack2(o[u + 6], o[u + 7]));
             }
-          } else if (whole) {
-            *reinterpret_cast<uint4*>(out + j * p.r + c) =
-                make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
-          } else {
-            *reinterpret_cast<float4*>(part + j * p.r + c) = make_float4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<float4*>(part + j * p.r + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
           }
         }
       }
@@ -1046,7 +1150,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free);
     }
-  } else {
+  } else if (warp >= 13) {
     const int l = tid - 416, rchunks = p.rp / 8;
     const int hr = l >> 3, hc = l & 7;  // H: rows hr + 8 j, chunks hc, hc + 8
     int slot = 0, hs = 0, step = 0;
@@ -1101,9 +1205,9 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const OuterArgs
   if (warp == 8) tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// dh (b x r) from the slices' parts, added in slice order. 4 elements a thread.
+// dh (b x r) from the slices' parts, added in slice order. A thread: 4 ranks of a position.
 struct ReduceArgs {
-  const float* dpart;  // slices x b x r, rows in the order of `order`
+  const float* dpart;  // slices x r / 4 x b x 4
   const int32_t *order, *offsets;
   uint16_t* dh;
   int64_t b;
@@ -1111,17 +1215,18 @@ struct ReduceArgs {
 };
 
 __global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
-  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  const int64_t pos = at / p.r;
+  const int64_t pos = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (pos >= p.offsets[p.count]) return;
   const int64_t row = p.order[pos];
+  const float* part = p.dpart + (blockIdx.y * p.b + pos) * 4;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
   for (int s = 0; s < p.slices; ++s) {
-    const float4 o = __ldg(reinterpret_cast<const float4*>(p.dpart + s * p.b * p.r + at));
+    const float4 o = __ldg(reinterpret_cast<const float4*>(part + s * p.b * p.r));
     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
   }
-  *reinterpret_cast<uint2*>(p.dh + row * p.r + at % p.r) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  *reinterpret_cast<uint2*>(p.dh + row * p.r + blockIdx.y * 4) =
+      make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
 }
 
 // The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
@@ -1134,7 +1239,8 @@ struct FinishArgs {
     uint16_t* out;
     int64_t size;  // elements of a group, a multiple of 1024
     int chunks;
-  } side[2];
+  } side[2];       // dA (count x r x k), dB (count x k x r)
+  int r;
 };
 
 // Largest c with chunk_begin(c) <= tile.
@@ -1166,7 +1272,21 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs p) {
       v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
   }
-  *reinterpret_cast<uint2*>(dst + g * size + at) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  // [block][rank / 4][column of the block][4] -> the output's place
+  const int64_t quad = at / 512, blk = quad / (p.r / 4);
+  const int c = static_cast<int>(quad - blk * (p.r / 4)) * 4;
+  const int64_t j = blk * 128 + (at >> 2) % 128;
+  uint16_t* out = dst + g * size;
+  if (blockIdx.z) {
+    *reinterpret_cast<uint2*>(out + j * p.r + c) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  } else {
+    const int64_t k = size / p.r;
+    const uint32_t lo = pack2(v.x, v.y), hi = pack2(v.z, v.w);
+    out[c * k + j] = static_cast<uint16_t>(lo);
+    out[(c + 1) * k + j] = static_cast<uint16_t>(lo >> 16);
+    out[(c + 2) * k + j] = static_cast<uint16_t>(hi);
+    out[(c + 3) * k + j] = static_cast<uint16_t>(hi >> 16);
+  }
 }
 
 // -------------------------------------------------------------------- host
@@ -1204,6 +1324,35 @@ cudaError_t launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int c
   return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// BF16 rows x cols, row stride `ld` elements, in boxes of 128 rows x 64 columns, 128-byte swizzle.
+cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, int64_t cols, int64_t ld) {
+  static std::atomic<EncodeTiledFn> known{nullptr};
+  EncodeTiledFn fn = known.load(std::memory_order_acquire);
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    fn = reinterpret_cast<EncodeTiledFn>(f);
+    known.store(fn, std::memory_order_release);
+  }
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 int round16(int r) { return (r + 15) / 16 * 16; }
 
 // trans: W is count x k x r (the backward pass's B).
@@ -1211,44 +1360,46 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
                           const uint16_t* w, const float* scale, uint16_t* out, cudaStream_t st) {
   const bool codes = !trans && c.xq8;
   const int rp = round16(c.r);
-  ShrinkArgs p{c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
+  ShrinkArgs p{{}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
                codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, w, scale, out, k, c.r, rp, 0, 0};
   p.stage_bytes = 16384 + (trans ? (rp + 63) / 64 * 8192 : rp * 128);
   // two blocks per SM: about 110 KB each, of which the parts need 128 x (rp + 4) fp32
   const int raw = codes ? kAhead * kRawStep : 0;
   p.stages = std::max(2, std::min(kShrinkMaxStages, (110 * 1024 - raw) / p.stage_bytes));
   const int smem = std::max(p.stages * p.stage_bytes + raw, 128 * (rp + 4) * 4) + 1024;
-  // Split the reduction over a cluster of up to 8 blocks while all clusters fit at once: two
-  // blocks per SM, of which about 1 in 7 stays empty since a cluster keeps within a GPC.
-  const int splits = std::max(1, std::min(8, 2 * kSms * 6 / 7 / tiles_estimate(c)));
-  const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
+  // Split the reduction over a cluster of up to 8 blocks, for about two blocks per SM (a few
+  // clusters that start late cost less than SMs that hold one block: 24 against 31 us for 67
+  // tiles in clusters of 4 and of 2).
+  const int splits = std::max(1, std::min(8, 290 / tiles_estimate(c)));
+  const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
+  if (!codes) {
+    const cudaError_t e = encode_rows(&p.map, z, c.g.b, k, ldz);
+    if (e != cudaSuccess) return e;
+  }
   return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
 }
 
 cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, const uint16_t* w, int n,
                           const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
-  const int rp = round16(c.r);
-  ExpandArgs p{c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, w, scale, c.base, y,
-               n, c.r, rp, trans ? rp * 128 : (rp + 63) / 64 * 8192, 0, 0};
-  // two blocks per SM: H, 3 W stages (2 beyond rank 64), base stages in what is left of 110 KB
-  const int hbytes = (rp + 63) / 64 * 16384;
-  p.slots = rp > 64 ? 2 : 3;
-  p.bslots = std::min(kExpandSlots, (110 * 1024 - hbytes - p.slots * p.stage_bytes) / 16384);
-  const int smem = hbytes + p.slots * p.stage_bytes + p.bslots * 16384 + 1024;
-  // column slices: whole waves of two blocks per SM; starting a block costs about 4 units
-  const int tiles = tiles_estimate(c), units = n / 64;
-  int best = 1;
-  int64_t cost = INT64_MAX;
-  for (int s = 1; s <= std::max(1, units / 4); ++s) {
-    const int64_t waves = (int64_t(tiles) * s + 2 * kSms - 1) / (2 * kSms);
-    const int64_t all = waves * (4 + (units + s - 1) / s);
-    if (all < cost) cost = all, best = s;
+  const int rp = round16(c.r), kt = (rp + 63) / 64;
+  ExpandArgs p{{}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, w, scale, c.base, y,
+               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, 0, 0, 0};
+  // two blocks per SM: 112 KB each, as much of it as is left for base (3 or 4 stages)
+  p.stage_bytes = trans ? rp * 128 : kt * 8192;
+  p.hslots = 1;
+  const int fixed = p.hslots * kt * 16384 + kExpandSlots * p.stage_bytes;
+  p.bslots = std::min(kBaseSlots, (112 * 1024 - fixed) / 16384);
+  const int smem = fixed + p.bslots * 16384 + kExpandBars;
+  if (c.base) {
+    const cudaError_t e = encode_rows(&p.map, c.base, c.g.b, n, n);
+    if (e != cudaSuccess) return e;
   }
-  const dim3 grid(best, row_tiles_cap(c.g.b, c.g.count, 128));
-  return launch(trans ? expand_kernel<true> : expand_kernel<false>, grid, kExpandThreads, smem, 1, pdl,
-                p, st);
+  const int64_t units = int64_t(row_tiles_cap(c.g.b, c.g.count, 128)) * (n / 64);
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(2 * kSms, units));
+  return launch(trans ? expand_kernel<true> : expand_kernel<false>, dim3(blocks), kExpandThreads, smem, 1,
+                pdl, p, st);
 }
 
 // Column blocks and row chunks of the outer kernel: one thread block per SM, the split that
@@ -1297,8 +1448,12 @@ cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint
                          float* dpart, cudaStream_t st) {
   const int rp = round16(c.r);
   const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
-  OuterArgs p{c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
+  OuterArgs p{{}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
               out, part, c.bm, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols};
+  if (!kCodes) {
+    const cudaError_t e = encode_rows(&p.map, z, c.g.b, k, ldz);
+    if (e != cudaSuccess) return e;
+  }
   const int smem = plan.stages * (32768 + (kDual ? 16384 : 0)) +
                    plan.htiles * ((rp + 63) / 64) * 16384 + (kCodes ? kOuterAhead * kOuterRawStep : 0) +
                    1024;
@@ -1359,8 +1514,7 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
       e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, st);
       if (e != cudaSuccess) return e;
       const ReduceArgs ra{pd, c.g.order, c.g.offsets, dh, c.g.b, c.g.count, c.r, s.b.slices};
-      const int64_t blocks = (int64_t(c.g.b) * c.r + 1023) / 1024;
-      e = launch(reduce_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, false, ra, st);
+      e = launch(reduce_kernel, dim3(static_cast<unsigned>((c.g.b + 255) / 256), c.r / 4), 256, 0, 1, false, ra, st);
     } else {
       e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
       if (e == cudaSuccess)
@@ -1372,7 +1526,7 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_expand(c, true, dh, c.a, c.m, nullptr, c.dx, false, st);
     if (e != cudaSuccess) return e;
   }
-  FinishArgs f{first128_of(c.g), c.g.count, {}};
+  FinishArgs f{first128_of(c.g), c.g.count, {}, c.r};
   f.side[0] = {pa, c.da, int64_t(c.m) * c.r, s.a.chunks};
   f.side[1] = {pb, c.db, int64_t(c.n) * c.r, s.b.chunks};
   const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 1023) / 1024;

@@ -59,7 +59,7 @@ __device__ __forceinline__ int find_key(const int* first, int n, int t) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     group_rows_kernel(const int32_t* __restrict__ ids, int b, int count, int warps, int chunk,
-                      int32_t* __restrict__ order, int32_t* __restrict__ offsets,
+                      int32_t* order, int32_t* __restrict__ offsets,
                       int4* __restrict__ tiles, int32_t* __restrict__ tiles_before,
                       int cap16) {
   extern __shared__ int smem[];
@@ -142,16 +142,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
 
-  // Tile lists: {group (-1: rows without one), first position in `order`, rows, 0}
+  // Tile lists. The rows of a group ascend, so they follow one another in the batch where the
+  // last one is as far from the first as there are rows.
+  __syncthreads();
+  auto make_tile = [&](int k, int at, int most) {
+    const int rows = min(most, start[k + 1] - at);
+    const int first = order[at], last = order[at + rows - 1];
+    return make_int4(k < count ? k : -1, at, rows, last - first == rows - 1 ? first : -1);
+  };
   for (int t = tid; t < sum[1]; t += kThreads) {
     const int k = find_key(first16, keys, t);
-    const int at = start[k] + (t - first16[k]) * 16;
-    tiles[1 + t] = make_int4(k < count ? k : -1, at, min(16, start[k + 1] - at), 0);
+    tiles[1 + t] = make_tile(k, start[k] + (t - first16[k]) * 16, 16);
   }
   for (int t = tid; t < sum[2]; t += kThreads) {
     const int k = find_key(first128, keys, t);
-    const int at = start[k] + (t - first128[k]) * 128;
-    tiles[1 + cap16 + t] = make_int4(k < count ? k : -1, at, min(128, start[k + 1] - at), 0);
+    tiles[1 + cap16 + t] = make_tile(k, start[k] + (t - first128[k]) * 128, 128);
   }
 }
 
