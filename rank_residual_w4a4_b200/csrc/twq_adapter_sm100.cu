@@ -597,11 +597,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       for (int i = 0; i < kExpandSlots; ++i) {
         mbar_init(&s_full[i], 32);
         mbar_init(&s_done[i], 1);
-        mbar_init(&s_free[i], 8);
+        mbar_init(&s_free[i], 4);
       }
       for (int i = 0; i < kBaseSlots; ++i) {
         mbar_init(&s_bfull[i], 64);
-        mbar_init(&s_bfree[i], 8);
+        mbar_init(&s_bfree[i], 4);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_hfull[i], 64);
@@ -621,65 +621,79 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     const uint32_t tmem = *s_tmem;
 
     if (warp < 8) {
+      // Warps 0 .. 3 take the even units of this block, 4 .. 7 the odd ones, each 32 rows of all 64
+      // columns: a warp's chain of waits and loads (about 2000 cycles) then spans two units.
       const int t4 = lane & 3;
       RowsAhead<4> ra;  // rows lane / 4 + 8 i of this warp's 32
       ra.start(tiles, p.order, tile0, tile_end, (warp & 3) * 32 + (lane >> 2), 8);
-      float f = p.scale ? p.scale[ra.group] : 1.0f;
-      int slot = 0, bs = 0, u = unit0;
+      int first = warp >> 2, u = unit0 + first;
+      if (u >= units) {
+        u -= units;
+        ra.advance();
+      }
+      float f = p.scale && ra.group >= 0 ? p.scale[ra.group] : 1.0f;
+      int slot = first, bs = first;
       uint32_t ph = 0, bph = 0;
-      for (int i0 = 0; i0 < work; ++i0) {
+      for (int i0 = first; i0 < work; i0 += 2) {
         if (!warp_wait(&s_done[slot], ph, s_abort, kSiteDone)) break;
+        if (p.base && !warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull)) break;
         tc_fence_after();
-        uint32_t v[2][16];
-        const uint32_t ta =
-            tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + (warp >> 2) * 32;
-        tmem_ld_16x256b_x4(ta, v[0]);
-        tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
-        tmem_wait_ld();
-        tc_fence_before();
-        uint4 b[4] = {};
-        if (p.base) {
-          if (!warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull)) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            b[i] = lds16(sb + bs * 16384 +
-                         sw128((warp & 3) * 32 + i * 8 + (lane >> 2), (warp >> 2) * 4 + t4));
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[2][16];
+          const uint32_t ta =
+              tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + half * 32;
+          tmem_ld_16x256b_x4(ta, v[0]);
+          tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
+          uint4 b[4] = {};
+          if (p.base) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              b[i] = lds16(sb + bs * 16384 + sw128((warp & 3) * 32 + i * 8 + (lane >> 2), half * 4 + t4));
+          }
+          tmem_wait_ld();
+          if (half == 1) {  // everything of this unit is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&s_free[slot]);
+              mbar_arrive(&s_bfree[bs]);
+            }
+          }
+          const int col = u * 64 + half * 32 + t4 * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
+            if constexpr (kTrans) quad_transpose(a, t4);
+            const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
+            if (ra.row[i] >= 0)
+              st_stream(p.y + static_cast<int64_t>(ra.row[i]) * p.n + col,
+                        make_uint4(o[0], o[1], o[2], o[3]));
+          }
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_free[slot]);
-          mbar_arrive(&s_bfree[bs]);
-        }
-        const int col = u * 64 + (warp >> 2) * 32 + t4 * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
-          if constexpr (kTrans) quad_transpose(a, t4);
-          const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
-          if (ra.row[i] >= 0)
-            st_stream(p.y + static_cast<int64_t>(ra.row[i]) * p.n + col,
-                      make_uint4(o[0], o[1], o[2], o[3]));
-        }
-        if (++u == units) {
-          u = 0;
+        u += 2;
+        if (u >= units) {
+          u -= units;
           ra.advance();
           if (p.scale && ra.group >= 0) f = p.scale[ra.group];
         }
-        if (++slot == kExpandSlots) {
-          slot = 0;
+        slot += 2;
+        if (slot >= kExpandSlots) {
+          slot -= kExpandSlots;
           ph ^= 1u;
         }
-        if (++bs == p.bslots) {
-          bs = 0;
+        bs += 2;
+        if (bs >= p.bslots) {
+          bs -= p.bslots;
           bph ^= 1u;
         }
       }
@@ -851,7 +865,7 @@ struct OuterArgs {
   uint32_t tmem_cols;
 };
 
-constexpr int kOuterThreads = 480;  // 8 warps load Z; MMA warp; 4 drain; 2 load H, W
+constexpr int kOuterThreads = 512;  // 8 warps load Z; MMA warp; 4 drain; 2 load H, W; MMA of dh
 constexpr int kOuterStages = 4;     // at most
 constexpr int kOuterAhead = 3;      // as kAhead
 constexpr int kOuterRawStep = 16384 + 4096;
@@ -896,7 +910,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < kOuterStages; ++i) {
       mbar_init(&s_full[i], (kCodes ? 8 : 256) + (kDual ? 64 : 0));
-      mbar_init(&s_empty[i], 1);
+      mbar_init(&s_empty[i], kDual ? 2 : 1);
       mbar_init(&s_hfull[i], 64);
       mbar_init(&s_hempty[i], 1);
     }
@@ -904,7 +918,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       mbar_init(&s_dfull[i], 1);
       mbar_init(&s_dfree[i], 4);
     }
-    mbar_init(&s_end, 1);
+    mbar_init(&s_end, kDual ? 2 : 1);
     mbar_init(&s_run, 1);
     mbar_init(&s_free, 4);
     s_abort = 0;
@@ -1009,7 +1023,6 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   } else if (warp == 8) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(p.rp) | kAMajorMn | kBMajorMn;
-      const uint32_t didesc = idesc_bf16(p.rp) | kBMajorMn;
       int runs = 0, slot = 0, hs = 0;
       uint32_t phase = 0, hphase = 0;
       bool alive = true;
@@ -1017,11 +1030,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       int run_end = min(end, p.first128[tiles[begin].x + 1]);
       for (int tile = begin; tile < end && alive; ++tile) {
         const uint32_t hb = sh + hs * hbytes;
-        const int nth = tile - begin;
-        const uint32_t dacc = tmem + p.dcol + (nth & 1) * p.rp;
-        alive = wait(&s_hfull[hs], hphase, &s_abort, kSiteFull) &&
-                (!kDual || nth < 2 ||
-                 wait(&s_dfree[nth & 1], ((nth >> 1) & 1) ^ 1u, &s_abort, kSiteAccEmpty));
+        alive = wait(&s_hfull[hs], hphase, &s_abort, kSiteFull);
         if (!alive) break;
         for (int b = 0; b < nb; ++b) {
           if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) {
@@ -1035,12 +1044,6 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
           for (int k = 0; k < 8; ++k)  // 128 rows: 8 steps of 16
             mma_bf16(tmem + b * p.rp, smem_desc_mn(zs + k * 2048, 16384),
                      smem_desc_mn(hb + k * 2048, 16384), idesc, !fresh || k > 0);
-          if constexpr (kDual) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)  // 128 columns
-              mma_bf16(dacc, smem_desc_sw128(zs + (k >> 2) * 16384 + (k & 3) * 32),
-                       smem_desc_mn(zs + 32768 + k * 2048, 0), didesc, b > 0 || k > 0);
-          }
           mma_commit(&s_empty[slot]);
           if (++slot == stages) {
             slot = 0;
@@ -1049,7 +1052,6 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
         }
         if (!alive) break;
         mma_commit(&s_hempty[hs]);
-        if (kDual) mma_commit(&s_dfull[nth & 1]);
         if (++hs == p.htiles) {
           hs = 0;
           hphase ^= 1u;
@@ -1064,6 +1066,40 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
           ++runs;
           tc_fence_after();
         }
+      }
+      mma_commit(&s_end);
+      wait_mmas(&s_end);
+    }
+  } else if (warp == 15) {
+    // An MMA of so few columns takes its issuer 60 to 100 cycles whatever its size, so the row
+    // sums have an issuer of their own.
+    if (kDual && lane == 0) {
+      const uint32_t didesc = idesc_bf16(p.rp) | kBMajorMn;
+      int slot = 0;
+      uint32_t phase = 0;
+      bool alive = true;
+      for (int nth = 0; nth < end - begin && alive; ++nth) {
+        const uint32_t dacc = tmem + p.dcol + (nth & 1) * p.rp;
+        if (nth >= 2 && !wait(&s_dfree[nth & 1], ((nth >> 1) & 1) ^ 1u, &s_abort, kSiteAccEmpty)) break;
+        for (int b = 0; b < nb; ++b) {
+          if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) {
+            alive = false;
+            break;
+          }
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t zs = sz + slot * kStage;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 128 columns
+            mma_bf16(dacc, smem_desc_sw128(zs + (k >> 2) * 16384 + (k & 3) * 32),
+                     smem_desc_mn(zs + 32768 + k * 2048, 0), didesc, b > 0 || k > 0);
+          mma_commit(&s_empty[slot]);
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        if (alive) mma_commit(&s_dfull[nth & 1]);
       }
       mma_commit(&s_end);
       wait_mmas(&s_end);
@@ -1150,7 +1186,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free);
     }
-  } else if (warp >= 13) {
+  } else if (warp > 12) {
     const int l = tid - 416, rchunks = p.rp / 8;
     const int hr = l >> 3, hc = l & 7;  // H: rows hr + 8 j, chunks hc, hc + 8
     int slot = 0, hs = 0, step = 0;
