@@ -187,22 +187,30 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// The rows of a run of tiles that one thread loads (row `first` + step j of each tile; -1 beyond
-// the tile's end), known a tile ahead, and the tile itself two ahead, so that no load of Z or
-// H waits for a look-up.
+// A block's work items, each a part of a row tile: item k is number first + stride k, in tile
+// number / parts.
+struct Items {
+  int first, stride, parts, count;
+  __device__ __forceinline__ int tile(int k) const { return (first + stride * k) / parts; }
+};
+
+// The rows of each item's tile that one thread loads (row `first` + step j of the tile; -1
+// beyond its end), known an item ahead, and the tile itself two ahead, so that no load of
+// Z, base or H waits for a look-up.
 template <int kRows>
 struct RowsAhead {
   const int4* tiles;
   const int32_t* order;
-  int tile, end, first, step;
+  Items items;
+  int at, first, step;
   int row[kRows], next[kRows];
   int group, next_group;
   int run, next_run;    // first row of a tile whose rows follow one another, else -1
   int count, next_count;
   int4 after;
 
-  __device__ __forceinline__ int4 load_tile(int i) const {
-    return i < end ? __ldg(tiles + i) : make_int4(-1, 0, 0, -1);
+  __device__ __forceinline__ int4 load_tile(int k) const {
+    return k < items.count ? __ldg(tiles + items.tile(k)) : make_int4(-1, 0, 0, -1);
   }
   __device__ __forceinline__ void look_up(const int4& t, int (&r)[kRows]) const {
 #pragma unroll
@@ -211,11 +219,10 @@ struct RowsAhead {
       r[j] = i < t.z ? __ldg(order + t.y + i) : -1;
     }
   }
-  __device__ __forceinline__ void start(const int4* tl, const int32_t* ord, int begin, int stop, int f,
-                                        int st) {
-    tiles = tl, order = ord, tile = begin, end = stop, first = f, step = st;
-    const int4 t0 = load_tile(begin), t1 = load_tile(begin + 1);
-    after = load_tile(begin + 2);
+  __device__ __forceinline__ void start(const int4* tl, const int32_t* ord, const Items& it, int f, int st) {
+    tiles = tl, order = ord, items = it, at = 0, first = f, step = st;
+    const int4 t0 = load_tile(0), t1 = load_tile(1);
+    after = load_tile(2);
     look_up(t0, row);
     look_up(t1, next);
     group = t0.x, next_group = t1.x;
@@ -223,13 +230,13 @@ struct RowsAhead {
     count = t0.z, next_count = t1.z;
   }
   __device__ __forceinline__ void advance() {
-    ++tile;
+    ++at;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) row[j] = next[j];
     group = next_group, run = next_run, count = next_count;
     look_up(after, next);
     next_group = after.x, next_run = after.w, next_count = after.z;
-    after = load_tile(tile + 2);
+    after = load_tile(at + 2);
   }
 };
 
@@ -300,9 +307,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int kb = p.k / 64;
-  const int k0 = static_cast<int>(static_cast<int64_t>(rank) * kb / splits);
-  const int steps = static_cast<int>(static_cast<int64_t>(rank + 1) * kb / splits) - k0;
+  // 64-column steps rank, rank + splits, ...: the cluster's blocks read neighbouring pieces of
+  // the rows at about the same time
+  const int steps = (p.k / 64 - rank + splits - 1) / splits;
 
   if (warp < 8 && tma) {
     if (tid == 0) {
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
       for (int step = 0; step < steps; ++step) {
         if (step >= p.stages && !wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
         mbar_arrive_expect_tx(&s_full[slot], 16384);
-        tma_load(sbase + slot * p.stage_bytes, &p.map, &s_full[slot], (k0 + step) * 64, t.w);
+        tma_load(sbase + slot * p.stage_bytes, &p.map, &s_full[slot], (rank + step * splits) * 64, t.w);
         if (++slot == p.stages) {
           slot = 0;
           phase ^= 1u;
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
       if (step < steps) {
         const uint32_t at = raw + step % kAhead * kRawStep + tid * 16;
         const uint32_t st = raw + step % kAhead * kRawStep + 8192 + tid * 4;
-        const int col = (k0 + step) * 64;
+        const int col = (rank + step * splits) * 64;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           cp16(at + j * 4096, p.q + row[j] * p.k + col + ch * 16, ok[j]);
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
         if (lane == 0) mbar_arrive(&s_full[slot]);
         fetch(step + kAhead);
       } else {
-        const int col = (k0 + step) * 64;
+        const int col = (rank + step * splits) * 64;
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
           cp16(zs + sw128(r0 + j * 32, ch), p.z + row[j] * p.ldz + col + ch * 8, ok[j]);
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
     for (int step = 0; step < steps; ++step) {
       if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
       const uint32_t ws = sbase + slot * p.stage_bytes + 16384;
-      const int col = (k0 + step) * 64;
+      const int col = (rank + step * splits) * 64;
       if constexpr (kTrans) {  // 64 rows of W (r contiguous): 64-column blocks of 8 KB
         const int chunks = p.rp / 8;
         for (int i = l; i < 64 * chunks; i += 64) {
@@ -502,12 +509,15 @@ struct ExpandArgs {
   const int32_t *first128, *offsets;
   int b, count;
   int n, r, rp;
-  int stage_bytes, hslots, bslots;  // a W stage; H tiles; base stages of 16 KB
+  int stage_bytes, slots, hslots, bslots;  // a W stage; W stages; H tiles; base stages of 16 KB
+  int segs;
 };
 
 constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H and base, 1 loads W
+// At most. The two halves of the epilogue warps take turns, so both numbers are even: a slot then
+// belongs to one half, and its barrier is never a whole turn ahead of a waiter.
 constexpr int kExpandSlots = 4;      // W stages, and accumulators of 64 columns
-constexpr int kBaseSlots = 4;        // base stages, at most
+constexpr int kBaseSlots = 4;        // base stages
 constexpr int kExpandBars = 256;     // bytes of barriers in front of the tiles' space
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
@@ -556,8 +566,10 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
   }
 }
 
-// The units (64 columns of a row tile) of all tiles with an adapter, one tile's after
-// another's, in equal shares for the grid's blocks. The accumulator is read in the 16x256b form,
+// Items: `segs` parts of each tile with an adapter, of about 8 units of 64 columns; the grid's
+// blocks take them in turn, so that at any time they work on neighbouring columns of a few row
+// tiles (a copy by blocks with a long part of a row tile each: 4.6 TB/s; with short ones in
+// turn: 5.8). The accumulator is read in the 16x256b form,
 // where a quad of lanes holds 32 columns of a row in pairs; W's rows are stored permuted (or,
 // kTrans, the pairs are transposed over the quad), so that each lane owns 8 consecutive columns
 // and a quad writes 64 bytes of a row. base comes through shared memory, several stages ahead;
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   const int kt = (p.rp + 63) / 64;  // 64-wide tiles of the reduction
   const uint32_t sh = smem_u32(smem);
   const uint32_t sw = sh + p.hslots * kt * 16384;
-  const uint32_t sb = sw + kExpandSlots * p.stage_bytes;
+  const uint32_t sb = sw + p.slots * p.stage_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (sb - sh) + p.bslots * 16384);
   uint64_t* s_full = bars;                          // W stage
   uint64_t* s_done = s_full + kExpandSlots;         // accumulator (and its W stage read)
@@ -585,14 +597,15 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int units = p.n / 64;
-  const int64_t total = static_cast<int64_t>(p.first128[p.count]) * units;
-  const int64_t from = blockIdx.x * total / gridDim.x;
-  const int work = static_cast<int>((blockIdx.x + 1) * total / gridDim.x - from);
+  const int total = p.first128[p.count] * p.segs;
+  Items items{static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), p.segs, 0};
+  items.count = (total - items.first + items.stride - 1) / items.stride;  // <= 0: none
   const int4* tiles = p.tiles + 1 + p.cap16;
-  const int tile0 = static_cast<int>(from / units), unit0 = static_cast<int>(from - int64_t(tile0) * units);
-  const int tile_end = tile0 + (unit0 + work + units - 1) / units;
+  // units of item k
+  auto unit_begin = [&](int k) { return (items.first + items.stride * k) % p.segs * units / p.segs; };
+  auto unit_end = [&](int k) { return ((items.first + items.stride * k) % p.segs + 1) * units / p.segs; };
 
-  if (work > 0) {
+  if (items.count > 0) {
     if (tid == 0) {
       for (int i = 0; i < kExpandSlots; ++i) {
         mbar_init(&s_full[i], 32);
@@ -625,107 +638,108 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       // columns: a warp's chain of waits and loads (about 2000 cycles) then spans two units.
       const int t4 = lane & 3;
       RowsAhead<4> ra;  // rows lane / 4 + 8 i of this warp's 32
-      ra.start(tiles, p.order, tile0, tile_end, (warp & 3) * 32 + (lane >> 2), 8);
-      int first = warp >> 2, u = unit0 + first;
-      if (u >= units) {
-        u -= units;
-        ra.advance();
-      }
-      float f = p.scale && ra.group >= 0 ? p.scale[ra.group] : 1.0f;
-      int slot = first, bs = first;
+      ra.start(tiles, p.order, items, (warp & 3) * 32 + (lane >> 2), 8);
+      int turn = warp >> 2;  // 0: the next unit is this warp's
+      int slot = 0, bs = 0;
       uint32_t ph = 0, bph = 0;
-      for (int i0 = first; i0 < work; i0 += 2) {
-        if (!warp_wait(&s_done[slot], ph, s_abort, kSiteDone)) break;
-        if (p.base && !warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull)) break;
-        tc_fence_after();
+      bool alive = true;
+      for (int k = 0; k < items.count && alive; ++k) {
+        const float f = p.scale ? p.scale[ra.group] : 1.0f;
+        const int ue = unit_end(k);
+        for (int u = unit_begin(k); u < ue; ++u) {
+          if (turn == 0) {
+            alive = warp_wait(&s_done[slot], ph, s_abort, kSiteDone) &&
+                    (!p.base || warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull));
+            if (!alive) break;
+            tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v[2][16];
-          const uint32_t ta =
-              tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + half * 32;
-          tmem_ld_16x256b_x4(ta, v[0]);
-          tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
-          uint4 b[4] = {};
-          if (p.base) {
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[2][16];
+              const uint32_t ta =
+                  tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + half * 32;
+              tmem_ld_16x256b_x4(ta, v[0]);
+              tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
+              uint4 b[4] = {};
+              if (p.base) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              b[i] = lds16(sb + bs * 16384 + sw128((warp & 3) * 32 + i * 8 + (lane >> 2), half * 4 + t4));
-          }
-          tmem_wait_ld();
-          if (half == 1) {  // everything of this unit is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&s_free[slot]);
-              mbar_arrive(&s_bfree[bs]);
+                for (int i = 0; i < 4; ++i)
+                  b[i] = lds16(sb + bs * 16384 +
+                               sw128((warp & 3) * 32 + i * 8 + (lane >> 2), half * 4 + t4));
+              }
+              tmem_wait_ld();
+              if (half == 1) {  // everything of this unit is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                  mbar_arrive(&s_free[slot]);
+                  mbar_arrive(&s_bfree[bs]);
+                }
+              }
+              const int col = u * 64 + half * 32 + t4 * 8;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float a[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
+                if constexpr (kTrans) quad_transpose(a, t4);
+                const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
+                if (ra.row[i] >= 0)
+                  st_stream(p.y + static_cast<int64_t>(ra.row[i]) * p.n + col,
+                            make_uint4(o[0], o[1], o[2], o[3]));
+              }
             }
           }
-          const int col = u * 64 + half * 32 + t4 * 8;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float a[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
-            if constexpr (kTrans) quad_transpose(a, t4);
-            const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
-            if (ra.row[i] >= 0)
-              st_stream(p.y + static_cast<int64_t>(ra.row[i]) * p.n + col,
-                        make_uint4(o[0], o[1], o[2], o[3]));
+          turn ^= 1;
+          if (++slot == p.slots) {
+            slot = 0;
+            ph ^= 1u;
+          }
+          if (++bs == p.bslots) {
+            bs = 0;
+            bph ^= 1u;
           }
         }
-        u += 2;
-        if (u >= units) {
-          u -= units;
-          ra.advance();
-          if (p.scale && ra.group >= 0) f = p.scale[ra.group];
-        }
-        slot += 2;
-        if (slot >= kExpandSlots) {
-          slot -= kExpandSlots;
-          ph ^= 1u;
-        }
-        bs += 2;
-        if (bs >= p.bslots) {
-          bs -= p.bslots;
-          bph ^= 1u;
-        }
+        ra.advance();
       }
     } else if (warp == 8) {
       if (lane == 0) {
         const uint32_t idesc = idesc_bf16(64) | (kTrans ? kBMajorMn : 0u);
-        int slot = 0, hs = 0, u = unit0;
+        int slot = 0, hs = 0, i = 0;
         uint32_t ph = 0, hph = 0;
-        for (int i = 0; i < work; ++i) {
-          if ((i == 0 || u == 0) && !wait(&s_hfull[hs], hph, s_abort, kSiteFull)) break;
-          if (!wait(&s_full[slot], ph, s_abort, kSiteFull)) break;
-          if (i >= kExpandSlots && !wait(&s_free[slot], ph ^ 1u, s_abort, kSiteAccEmpty)) break;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint32_t ws = sw + slot * p.stage_bytes, hb = sh + hs * kt * 16384;
-          for (int k = 0; k < p.rp / 16; ++k)
-            mma_bf16(tmem + slot * 64, smem_desc_sw128(hb + (k >> 2) * 16384 + (k & 3) * 32),
-                     kTrans ? smem_desc_mn(ws + k * 2048, 0)
-                            : smem_desc_sw128(ws + (k >> 2) * 8192 + (k & 3) * 32),
-                     idesc, k > 0);
-          mma_commit(&s_done[slot]);
-          if (++u == units) {
-            u = 0;
-            mma_commit(&s_hfree[hs]);
-            if (++hs == p.hslots) {
-              hs = 0;
-              hph ^= 1u;
+        bool alive = true;
+        for (int k = 0; k < items.count && alive; ++k) {
+          if (!wait(&s_hfull[hs], hph, s_abort, kSiteFull)) break;
+          const uint32_t hb = sh + hs * kt * 16384;
+          const int ue = unit_end(k);
+          for (int u = unit_begin(k); u < ue; ++u, ++i) {
+            alive = wait(&s_full[slot], ph, s_abort, kSiteFull) &&
+                    (i < p.slots || wait(&s_free[slot], ph ^ 1u, s_abort, kSiteAccEmpty));
+            if (!alive) break;
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint32_t ws = sw + slot * p.stage_bytes;
+            for (int q = 0; q < p.rp / 16; ++q)
+              mma_bf16(tmem + slot * 64, smem_desc_sw128(hb + (q >> 2) * 16384 + (q & 3) * 32),
+                       kTrans ? smem_desc_mn(ws + q * 2048, 0)
+                              : smem_desc_sw128(ws + (q >> 2) * 8192 + (q & 3) * 32),
+                       idesc, q > 0);
+            mma_commit(&s_done[slot]);
+            if (++slot == p.slots) {
+              slot = 0;
+              ph ^= 1u;
             }
           }
-          if (++slot == kExpandSlots) {
-            slot = 0;
-            ph ^= 1u;
+          mma_commit(&s_hfree[hs]);
+          if (++hs == p.hslots) {
+            hs = 0;
+            hph ^= 1u;
           }
         }
         mma_commit(s_end);
@@ -733,32 +747,34 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
       }
     } else {
       const int chunks = p.rp / 8;
-      int u = unit0;
+      bool alive = true;
       if (warp < 11) {
         const int r0 = (tid - 288) >> 3, ch = tid & 7;  // rows r0 + 8 j, chunk ch
         RowsAhead<16> ra;
-        ra.start(tiles, p.order, tile0, tile_end, r0, 8);
-        int hs = 0, seen = 0, bs = 0;
+        ra.start(tiles, p.order, items, r0, 8);
+        int hs = 0, bs = 0, i = 0;
         uint32_t hph = 0, bph = 0;
         pdl_wait();
-        for (int i = 0; i < work; ++i) {
-          if (i == 0 || u == 0) {
-            if (seen++ >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_abort, kSiteHEmpty)) break;
-            for (int c = ch; c < chunks; c += 8)
+        for (int k = 0; k < items.count && alive; ++k) {
+          if (k >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_abort, kSiteHEmpty)) break;
+          for (int c = ch; c < chunks; c += 8)
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const bool in = ra.row[j] >= 0 && c * 8 < p.r;
-                cp16(sh + (hs * kt + (c >> 3)) * 16384 + sw128(r0 + 8 * j, ch),
-                     p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
-              }
-            cp_arrive(&s_hfull[hs]);
-            if (++hs == p.hslots) {
-              hs = 0;
-              hph ^= 1u;
+            for (int j = 0; j < 16; ++j) {
+              const bool in = ra.row[j] >= 0 && c * 8 < p.r;
+              cp16(sh + (hs * kt + (c >> 3)) * 16384 + sw128(r0 + 8 * j, ch),
+                   p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
             }
+          cp_arrive(&s_hfull[hs]);
+          if (++hs == p.hslots) {
+            hs = 0;
+            hph ^= 1u;
           }
-          if (p.base) {
-            if (i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_abort, kSiteEmpty)) break;
+          const int ue = unit_end(k);
+          for (int u = unit_begin(k); p.base && u < ue; ++u, ++i) {
+            if (i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_abort, kSiteEmpty)) {
+              alive = false;
+              break;
+            }
             if (ra.run >= 0) {  // rows beyond a partial tile's end are read and not used
               if (tid == 288) {
                 mbar_arrive_expect_tx(&s_bfull[bs], 16384);
@@ -778,45 +794,45 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               bph ^= 1u;
             }
           }
-          if (++u == units) {
-            u = 0;
-            ra.advance();
-          }
+          ra.advance();
         }
       } else {
         const int r0 = lane >> 3, ch = lane & 7;
-        int tile = tile0, slot = 0, group = __ldg(&tiles[tile].x);
+        int slot = 0, i = 0, next = __ldg(&tiles[items.tile(0)].x);
         uint32_t ph = 0;
-        for (int i = 0; i < work; ++i) {
-          // the MMAs that read this stage are done when their accumulator is
-          if (i >= kExpandSlots && !warp_wait(&s_done[slot], ph ^ 1u, s_abort, kSiteEmpty)) break;
-          const uint16_t* wg = p.w + static_cast<int64_t>(group) * p.n * p.r;
-          const uint32_t ws = sw + slot * p.stage_bytes;
-          if constexpr (kTrans) {
-            for (int k = r0; k < p.rp; k += 4)
-              cp16(ws + sw128(k, ch), wg + static_cast<int64_t>(k < p.r ? k : 0) * p.n + u * 64 + ch * 8,
-                   k < p.r);
-          } else {
-            for (int c = ch; c < chunks; c += 8) {
-              const bool in = c * 8 < p.r;
+        for (int k = 0; k < items.count && alive; ++k) {
+          const uint16_t* wg = p.w + static_cast<int64_t>(next) * p.n * p.r;
+          if (k + 1 < items.count) next = __ldg(&tiles[items.tile(k + 1)].x);
+          const int ue = unit_end(k);
+          for (int u = unit_begin(k); u < ue; ++u, ++i) {
+            // the MMAs that read this stage are done when their accumulator is
+            if (i >= p.slots && !warp_wait(&s_done[slot], ph ^ 1u, s_abort, kSiteEmpty)) {
+              alive = false;
+              break;
+            }
+            const uint32_t ws = sw + slot * p.stage_bytes;
+            if constexpr (kTrans) {
+              for (int q = r0; q < p.rp; q += 4)
+                cp16(ws + sw128(q, ch), wg + static_cast<int64_t>(q < p.r ? q : 0) * p.n + u * 64 + ch * 8,
+                     q < p.r);
+            } else {
+              for (int c = ch; c < chunks; c += 8) {
+                const bool in = c * 8 < p.r;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int nr = r0 + 4 * j;
-                // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
-                const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
-                cp16(ws + (c >> 3) * 8192 + sw128(q, ch),
-                     wg + static_cast<int64_t>(u * 64 + nr) * p.r + (in ? c * 8 : 0), in);
+                for (int j = 0; j < 16; ++j) {
+                  const int nr = r0 + 4 * j;
+                  // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
+                  const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
+                  cp16(ws + (c >> 3) * 8192 + sw128(q, ch),
+                       wg + static_cast<int64_t>(u * 64 + nr) * p.r + (in ? c * 8 : 0), in);
+                }
               }
             }
-          }
-          cp_arrive(&s_full[slot]);
-          if (++slot == kExpandSlots) {
-            slot = 0;
-            ph ^= 1u;
-          }
-          if (++u == units && i + 1 < work) {
-            u = 0;
-            group = __ldg(&tiles[++tile].x);
+            cp_arrive(&s_full[slot]);
+            if (++slot == p.slots) {
+              slot = 0;
+              ph ^= 1u;
+            }
           }
         }
       }
@@ -832,8 +848,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   if (p.base == p.y) return;
   pdl_wait();
   const int bare = p.offsets[p.count];
-  const int64_t items = static_cast<int64_t>(p.b - bare) * (p.n / 8);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kExpandThreads + tid; i < items;
+  const int64_t pieces = static_cast<int64_t>(p.b - bare) * (p.n / 8);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kExpandThreads + tid; i < pieces;
        i += static_cast<int64_t>(gridDim.x) * kExpandThreads) {
     const int64_t rr = i / (p.n / 8);
     const int64_t at = static_cast<int64_t>(p.order[bare + rr]) * p.n + (i - rr * (p.n / 8)) * 8;
@@ -937,7 +953,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   if (warp < 8) {
     const int r0 = tid >> 3, ch = tid & 7;  // rows r0 + 32 j, chunk ch (or 16 codes)
     RowsAhead<4> ra;  // position of the loads: its tile, and the block in it
-    ra.start(tiles, p.order, begin, end, r0, 32);
+    ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, r0, 32);
     int lblk = 0;
     auto advance = [&]() {
       if (++lblk == nb) {
@@ -947,7 +963,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
     };
     int rs = 0;  // raw slot of the next fetch, the one that the current step has just read
     auto fetch = [&]() {
-      if (ra.tile < end) {
+      if (ra.at < end - begin) {
         const uint32_t at = sraw + rs * kOuterRawStep + tid * 16;
         const uint32_t st = sraw + rs * kOuterRawStep + 16384 + tid * 4;
 #pragma unroll
@@ -1193,7 +1209,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
     uint32_t phase = 0, hphase = 0;
     bool alive = true;
     RowsAhead<16> ra;
-    ra.start(tiles, p.order, begin, end, hr, 8);
+    ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, hr, 8);
     for (int tile = begin; tile < end && alive; ++tile) {
       if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
         break;
@@ -1421,19 +1437,31 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, c
                           const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r), kt = (rp + 63) / 64;
   ExpandArgs p{{}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, w, scale, c.base, y,
-               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, 0, 0, 0};
-  // two blocks per SM: 112 KB each, as much of it as is left for base (3 or 4 stages)
+               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, 0, 0, 0, 0, 1};
+  // Two blocks per SM, 112 KB each: 4 stages of W and of base and a second H tile as far as they
+  // fit (W's copies take 2 us and more while HBM is busy), 2 of each beyond rank 64.
   p.stage_bytes = trans ? rp * 128 : kt * 8192;
-  p.hslots = 1;
-  const int fixed = p.hslots * kt * 16384 + kExpandSlots * p.stage_bytes;
-  p.bslots = std::min(kBaseSlots, (112 * 1024 - fixed) / 16384);
+  p.slots = kt == 1 ? kExpandSlots : 2;
+  p.bslots = kt == 1 ? kBaseSlots : 2;
+  const int rest = p.slots * p.stage_bytes + p.bslots * 16384;
+  p.hslots = rest + 2 * kt * 16384 <= 112 * 1024 ? 2 : 1;
+  const int fixed = p.hslots * kt * 16384 + p.slots * p.stage_bytes;
   const int smem = fixed + p.bslots * 16384 + kExpandBars;
   if (c.base) {
     const cudaError_t e = encode_rows(&p.map, c.base, c.g.b, n, n);
     if (e != cudaSuccess) return e;
   }
-  const int64_t units = int64_t(row_tiles_cap(c.g.b, c.g.count, 128)) * (n / 64);
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(2 * kSms, units));
+  // Parts of a row tile: 4 to 12 units, so that the last turn of the blocks is nearly full (an
+  // item costs about one unit more than it has, for its H).
+  const int units = n / 64, tiles = tiles_estimate(c);
+  int64_t cost = INT64_MAX;
+  for (int s = std::max(1, units / 12); s <= std::max(1, units / 4); ++s) {
+    const int64_t turns = (int64_t(tiles) * s + 2 * kSms - 1) / (2 * kSms);
+    const int64_t all = turns * (1 + (units + s - 1) / s);
+    if (all < cost) cost = all, p.segs = s;
+  }
+  const unsigned blocks = static_cast<unsigned>(
+      std::min<int64_t>(2 * kSms, int64_t(row_tiles_cap(c.g.b, c.g.count, 128)) * p.segs));
   return launch(trans ? expand_kernel<true> : expand_kernel<false>, dim3(blocks), kExpandThreads, smem, 1,
                 pdl, p, st);
 }
