@@ -102,6 +102,22 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                          int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                          int y, int z, int u, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
+      : "memory");
+}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
                "r"(valid ? 4 : 0)
@@ -119,18 +135,34 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
   return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
 }
 
-// Operand whose contiguous dimension is M or N ("MN-major"): memory rows are the reduction
-// index, 128 bytes (64 elements) each; 64-element column blocks lie `block_bytes` apart.
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t block_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// Shared-memory matrix descriptors (128-byte swizzle) as two words. Low: address / 16 and the
+// leading byte offset / 16 (K-major: unused, 1; "MN-major", an operand whose memory rows are the
+// reduction index and whose 64-element column blocks lie block_bytes apart: that distance).
+// High: 8-row groups 1024 bytes apart, descriptor version 1, swizzle code 2. Steps along the
+// reduction add to the low word alone: built anew for each MMA, the descriptors took the one
+// issuing thread as long as the MMAs themselves (100 cycles each instead of 60).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// The address is masked to its field: in a cluster, bits above it say which block's memory it is.
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) {
+  return ((saddr >> 4) & 0x3FFFu) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t block_bytes) {
+  return ((saddr >> 4) & 0x3FFFu) | ((block_bytes >> 4) << 16);
 }
 constexpr uint32_t kAMajorMn = 1u << 15, kBMajorMn = 1u << 16;
+
+// D[tmem] (+)= A B^T, bf16 x bf16 -> fp32.
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                    bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %4};\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -139,18 +171,30 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // 4 int8 codes -> their values times s, rounded to BF16. The code plus 128 becomes the low
 // mantissa byte of 2^23, so the subtraction is exact and only the product is rounded. BF16
 // is the type that the activation had; an fp32 operand would halve the MMA rate.
-__device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
+__device__ __forceinline__ uint2 dequant4(uint32_t w, uint64_t s2) {
   const uint32_t u = w ^ 0x80808080u;
-  float f[4];
+  const uint64_t bias = f2_pack(-8388736.0f, -8388736.0f);
+  uint32_t o[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | i)) - 8388736.0f) * s;
-  return make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t q = f2_pack(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | (2 * i))),
+                               __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | (2 * i + 1))));
+    float lo, hi;
+    f2_unpack(f2_mul(f2_add(q, bias), s2), lo, hi);
+    o[i] = pack2(lo, hi);
+  }
+  return make_uint2(o[0], o[1]);
 }
-__device__ __forceinline__ void dequant16(uint4 q, float s, uint4& a, uint4& b) {
+__device__ __forceinline__ void dequant16(uint4 q, float scale, uint4& a, uint4& b) {
+  const uint64_t s = f2_pack(scale, scale);
   const uint2 p0 = dequant4(q.x, s), p1 = dequant4(q.y, s), p2 = dequant4(q.z, s),
               p3 = dequant4(q.w, s);
   a = make_uint4(p0.x, p0.y, p1.x, p1.y);
@@ -242,7 +286,8 @@ struct RowsAhead {
 
 // ------------------------------------------------------------------ shrink
 struct ShrinkArgs {
-  CUtensorMap map;  // Z: 128 rows x 64 columns
+  CUtensorMap map;   // Z: 128 rows x 64 columns
+  CUtensorMap wmap;  // W: rp rows x 64 of k, or (kTrans) 64 rows of k x 64 of r
   const int4* tiles;
   const int32_t* order;
   int cap16;
@@ -250,34 +295,40 @@ struct ShrinkArgs {
   int64_t ldz;
   const int8_t* q;
   const float* sq;
-  const uint16_t* w;  // count x r x k, or (kTrans) count x k x r
   const float* scale; // or null: 1
   uint16_t* out;      // b x r
   int k, r, rp;       // rp: r rounded up to 16
-  int stages, stage_bytes;
+  int stages, wstages;  // Z tiles of 128 x 64, W tiles of 64 of the reduction
 };
 
-constexpr int kShrinkThreads = 352;  // 8 warps load Z, then epilogue; MMA warp; 2 load W
-constexpr int kShrinkMaxStages = 6;
-// Codes are converted by the thread that loaded them: it keeps kAhead steps of its own codes
-// and scales in flight into a private part of shared memory, as it would in registers.
+constexpr int kShrinkThreads = 320;  // 8 warps load Z, then epilogue; MMA warp; TMA warp
+constexpr int kShrinkStages = 8;     // at most, of either kind
+// Codes are converted by the thread that loaded them: it keeps kAhead steps of its own codes in
+// flight into a private part of shared memory, as it would in registers.
 constexpr int kAhead = 4;
-constexpr int kRawStep = 8192 + 2048;  // 128 x 64 codes; a scale for each 16
 
-// One row tile per cluster, whose blocks split the reduction over k and add their parts
-// through distributed shared memory in rank order.
+// One row tile per cluster, whose blocks split the reduction over k (block `rank` takes the groups
+// of 128 columns rank, rank + splits, ..., so that they read neighbouring pieces of the rows at
+// about the same time) and add their parts through distributed shared memory in rank order.
 template <bool kCodes, bool kTrans>
-__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_constant__ ShrinkArgs p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2)
+    shrink_kernel(const __grid_constant__ ShrinkArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kShrinkMaxStages], s_empty[kShrinkMaxStages], s_done;
+  __shared__ uint64_t s_full[kShrinkStages], s_empty[kShrinkStages], s_wfull[kShrinkStages],
+      s_wempty[kShrinkStages], s_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  pdl_launch_dependents();
-  pdl_wait();
-  if (static_cast<int>(blockIdx.y) >= p.tiles[0].y) return;
-  const int4 t = p.tiles[1 + p.cap16 + blockIdx.y];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
+  if (tid == 288) {
+    if (!kCodes) tma_prefetch_desc(&p.map);
+    tma_prefetch_desc(&p.wmap);
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  const int number = p.tiles[0].y;
+  const int4 t = p.tiles[1 + p.cap16 + blockIdx.y];  // written or not, it is in the list's room
+  if (static_cast<int>(blockIdx.y) >= number) return;
   if (t.x < 0) {  // rows without adapter
     for (int i = rank * kShrinkThreads + tid; i < t.z * (p.r / 8); i += splits * kShrinkThreads) {
       const int64_t row = p.order[t.y + i / (p.r / 8)];
@@ -286,18 +337,51 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
     return;
   }
   uint8_t* smem = align1k(smem_raw);
-  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sz = smem_u32(smem);
+  const uint32_t sw = sz + p.stages * 16384;
+  const int wbytes = kTrans ? (p.rp + 63) / 64 * 8192 : p.rp * 128;
   const uint32_t tmem_cols = p.rp <= 32 ? 32 : (p.rp <= 64 ? 64 : 128);
   // rows beyond a partial tile's end then belong to others; their sums are not stored
   const bool tma = !kCodes && t.w >= 0;
-  if (tid == 0) {
+  const int steps = (p.k / 128 - rank + splits - 1) / splits * 2;  // of 64 columns
+  auto column = [&](int step) { return (rank + (step >> 1) * splits) * 128 + (step & 1) * 64; };
+  // W's tile of a step. Without kTrans the rows beyond r are the next adapter's (or zeros): they
+  // only reach accumulator columns that are not stored.
+  auto load_w = [&](int step, int slot, uint64_t* bar) {
+    const uint32_t dst = sw + slot * wbytes;
+    if constexpr (kTrans) {
+      tma_load3(dst, &p.wmap, bar, 0, column(step), t.x);
+      if (p.rp > 64) tma_load3(dst + 8192, &p.wmap, bar, 64, column(step), t.x);
+    } else {
+      tma_load(dst, &p.wmap, bar, column(step), t.x * p.r);
+    }
+  };
+  auto load_both = [&](int step, int slot) {
+    mbar_arrive_expect_tx(&s_full[slot], (tma ? 16384 : 0) + wbytes);
+    if (tma) tma_load(sz + slot * 16384, &p.map, &s_full[slot], column(step), t.w);
+    load_w(step, slot, &s_full[slot]);
+  };
+  if (tid == 288) {
+    // codes: 8 converting warps, and W's own barriers; else the loading threads and the TMA
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s_full[i], (kCodes ? 8 : tma ? 1 : 256) + 64);
+      mbar_init(&s_full[i], kCodes ? 8 : tma ? 1 : 257);
       mbar_init(&s_empty[i], 1);
+    }
+    for (int i = 0; kCodes && i < p.wstages; ++i) {
+      mbar_init(&s_wfull[i], 1);
+      mbar_init(&s_wempty[i], 1);
     }
     mbar_init(&s_done, 1);
     s_abort = 0;
     fence_barrier_init();
+    for (int step = 0; step < min(steps, kCodes ? p.wstages : p.stages); ++step) {
+      if (kCodes) {
+        mbar_arrive_expect_tx(&s_wfull[step], wbytes);
+        load_w(step, step, &s_wfull[step]);
+      } else {
+        load_both(step, step);
+      }
+    }
   }
   if (warp == 8) {
     tmem_alloc(&s_tmem, tmem_cols);
@@ -307,71 +391,74 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // 64-column steps rank, rank + splits, ...: the cluster's blocks read neighbouring pieces of
-  // the rows at about the same time
-  const int steps = (p.k / 64 - rank + splits - 1) / splits;
 
-  if (warp < 8 && tma) {
-    if (tid == 0) {
+  if (warp == 9) {
+    if (lane == 0) {
+      const int ring = kCodes ? p.wstages : p.stages;
       int slot = 0;
       uint32_t phase = 0;
-      for (int step = 0; step < steps; ++step) {
-        if (step >= p.stages && !wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
-        mbar_arrive_expect_tx(&s_full[slot], 16384);
-        tma_load(sbase + slot * p.stage_bytes, &p.map, &s_full[slot], (rank + step * splits) * 64, t.w);
-        if (++slot == p.stages) {
+      for (int step = ring; step < steps; ++step) {
+        if (!wait(kCodes ? &s_wempty[slot] : &s_empty[slot], phase, &s_abort, kSiteEmpty)) break;
+        if (kCodes) {
+          mbar_arrive_expect_tx(&s_wfull[slot], wbytes);
+          load_w(step, slot, &s_wfull[slot]);
+        } else {
+          load_both(step, slot);
+        }
+        if (++slot == ring) {
           slot = 0;
           phase ^= 1u;
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 8 && !tma) {
     // Thread: rows tid / 8 + 32 j, chunk tid % 8 (BF16); rows tid / 4 + 64 j, 16 codes (codes).
     constexpr int kRows = kCodes ? 2 : 4;
     const int r0 = kCodes ? tid >> 2 : tid >> 3;
     const int ch = kCodes ? tid & 3 : tid & 7;
-    int64_t row[kRows];
-    bool ok[kRows];
+    int row[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const int i = r0 + j * (128 / kRows);
-      ok[j] = i < t.z;
-      row[j] = ok[j] ? __ldg(p.order + t.y + i) : 0;
+      row[j] = i < t.z ? __ldg(p.order + t.y + i) : -1;
     }
-    const uint32_t raw = sbase + p.stages * p.stage_bytes;
+    const uint32_t raw = sw + p.wstages * wbytes + tid * 16;
+    const int8_t* src[2];   // codes: this thread's column of its rows
+    const float* ssrc[2] = {};
+    float sc[2], sc1[2], sc2[2];  // scales of the current group and the two after it
+    auto scale_of = [&](int j, int group) {
+      return row[j] >= 0 && group * 2 < steps ? __ldg(ssrc[j] + rank + group * splits) : 0.0f;
+    };
     auto fetch = [&](int step) {
-      if (step < steps) {
-        const uint32_t at = raw + step % kAhead * kRawStep + tid * 16;
-        const uint32_t st = raw + step % kAhead * kRawStep + 8192 + tid * 4;
-        const int col = (rank + step * splits) * 64;
+      if (step < steps)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          cp16(at + j * 4096, p.q + row[j] * p.k + col + ch * 16, ok[j]);
-          cp4(st + j * 1024, p.sq + row[j] * (p.k >> 7) + (col >> 7), ok[j]);
-        }
-      }
+        for (int j = 0; j < 2; ++j)
+          cp16(raw + (step % kAhead * 2 + j) * 4096, src[j] + column(step), row[j] >= 0);
       cp_commit();
     };
     if constexpr (kCodes) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t at = max(row[j], 0);
+        src[j] = p.q + at * p.k + ch * 16;
+        ssrc[j] = p.sq + at * (p.k >> 7);
+      }
       for (int a = 0; a < kAhead; ++a) fetch(a);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        sc[j] = scale_of(j, 0), sc1[j] = scale_of(j, 1), sc2[j] = scale_of(j, 2);
     }
     int slot = 0;
     uint32_t phase = 0;
     for (int step = 0; step < steps; ++step) {
       uint4 v[2];
-      float sc[2];
       if constexpr (kCodes) {
         cp_wait<kAhead - 1>();
-        const uint32_t at = raw + step % kAhead * kRawStep + tid * 16;
-        const uint32_t st = raw + step % kAhead * kRawStep + 8192 + tid * 4;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          v[j] = lds16(at + j * 4096);
-          sc[j] = lds4(st + j * 1024);
-        }
+        for (int j = 0; j < 2; ++j) v[j] = lds16(raw + (step % kAhead * 2 + j) * 4096);
       }
       if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
-      const uint32_t zs = sbase + slot * p.stage_bytes;
+      const uint32_t zs = sz + slot * 16384;
       if constexpr (kCodes) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -385,11 +472,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_full[slot]);
         fetch(step + kAhead);
+        if (step & 1) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            sc[j] = sc1[j], sc1[j] = sc2[j], sc2[j] = scale_of(j, (step >> 1) + 3);
+        }
       } else {
-        const int col = (rank + step * splits) * 64;
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
-          cp16(zs + sw128(r0 + j * 32, ch), p.z + row[j] * p.ldz + col + ch * 8, ok[j]);
+          cp16(zs + sw128(r0 + j * 32, ch), p.z + max(row[j], 0) * p.ldz + column(step) + ch * 8,
+               row[j] >= 0);
         cp_arrive(&s_full[slot]);
       }
       if (++slot == p.stages) {
@@ -398,54 +490,30 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
       }
     }
     cp_wait_all();
-  } else if (warp > 8) {
-    const int l = tid - 288;
-    const uint16_t* wg = p.w + static_cast<int64_t>(t.x) * p.r * p.k;
-    int slot = 0;
-    uint32_t phase = 0;
-    for (int step = 0; step < steps; ++step) {
-      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
-      const uint32_t ws = sbase + slot * p.stage_bytes + 16384;
-      const int col = (rank + step * splits) * 64;
-      if constexpr (kTrans) {  // 64 rows of W (r contiguous): 64-column blocks of 8 KB
-        const int chunks = p.rp / 8;
-        for (int i = l; i < 64 * chunks; i += 64) {
-          const int kr = i / chunks, c = i % chunks;
-          cp16(ws + (c >> 3) * 8192 + sw128(kr, c & 7),
-               wg + static_cast<int64_t>(col + kr) * p.r + (c * 8 < p.r ? c * 8 : 0), c * 8 < p.r);
-        }
-      } else {
-        for (int i = l; i < p.rp * 8; i += 64) {
-          const int c = i >> 3;
-          cp16(ws + sw128(c, i & 7),
-               wg + static_cast<int64_t>(c < p.r ? c : 0) * p.k + col + (i & 7) * 8, c < p.r);
-        }
-      }
-      cp_arrive(&s_full[slot]);
-      if (++slot == p.stages) {
-        slot = 0;
-        phase ^= 1u;
-      }
-    }
-    cp_wait_all();
   } else if (warp == 8 && lane == 0) {
     const uint32_t idesc = idesc_bf16(p.rp) | (kTrans ? kBMajorMn : 0u);
-    int slot = 0;
-    uint32_t phase = 0;
+    const int ring = kCodes ? p.wstages : p.stages;
+    int slot = 0, wslot = 0;
+    uint32_t phase = 0, wphase = 0;
     for (int step = 0; step < steps; ++step) {
+      if (kCodes && !wait(&s_wfull[wslot], wphase, &s_abort, kSiteFull)) break;
       if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) break;
-      fence_proxy_async_smem();
+      if (!kCodes && !tma) fence_proxy_async_smem();
       tc_fence_after();
-      const uint32_t zs = sbase + slot * p.stage_bytes, wsm = zs + 16384;
+      const uint32_t a = desc_k(sz + slot * 16384), ws = sw + wslot * wbytes;
+      const uint32_t b = kTrans ? desc_mn(ws, 8192) : desc_k(ws);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_bf16(tmem, smem_desc_sw128(zs + k * 32),
-                 kTrans ? smem_desc_mn(wsm + k * 2048, 8192) : smem_desc_sw128(wsm + k * 32), idesc,
-                 step > 0 || k > 0);
+        mma(tmem, a + k * 2, b + k * (kTrans ? 128 : 2), idesc, step > 0 || k > 0);
       mma_commit(&s_empty[slot]);
+      if (kCodes) mma_commit(&s_wempty[wslot]);
       if (++slot == p.stages) {
         slot = 0;
         phase ^= 1u;
+      }
+      if (++wslot == ring) {
+        wslot = 0;
+        wphase ^= 1u;
       }
     }
     mma_commit(&s_done);
@@ -456,6 +524,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
   // block of the cluster adds a share of the rows over the blocks.
   float* part = reinterpret_cast<float*>(smem);
   const int pitch = p.rp + 4;
+  const int lo = rank * 128 / splits, hi = min(t.z, (rank + 1) * 128 / splits);
+  const int quads = p.r / 4;
+  const float f = p.scale ? p.scale[t.x] : 1.0f;
+  const int row0 = lo + tid / quads < hi ? p.order[t.y + lo + tid / quads] : 0;
   wait_mmas(&s_done);
   __syncwarp();
   if (warp < 8) {
@@ -476,33 +548,34 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   if (warp == 8) tmem_dealloc(tmem, tmem_cols);
-  cluster_sync_startup();
-  const int lo = rank * 128 / splits, hi = min(t.z, (rank + 1) * 128 / splits);
-  const int quads = p.r / 4;
-  const float f = p.scale ? p.scale[t.x] : 1.0f;
+  if (splits > 1) cluster_sync_startup();
   for (int i = tid; i < (hi - lo) * quads; i += kShrinkThreads) {
     const int rr = lo + i / quads, c = i % quads * 4;
     const uint32_t at = smem_u32(part + rr * pitch + c);
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < splits; ++s) {
-      const float4 o = ld_peer16(map_peer(at, s));
-      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-    }
-    const int64_t orow = p.order[t.y + rr];
+    float4 o[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < splits) o[s] = ld_peer16(map_peer(at, s));
+    float4 v = o[0];
+#pragma unroll
+    for (int s = 1; s < 8; ++s)
+      if (s < splits) v.x += o[s].x, v.y += o[s].y, v.z += o[s].z, v.w += o[s].w;
+    const int64_t orow = i == tid ? row0 : p.order[t.y + rr];
     *reinterpret_cast<uint2*>(p.out + orow * p.r + c) =
         make_uint2(pack2(v.x * f, v.y * f), pack2(v.z * f, v.w * f));
   }
-  cluster_sync_startup();  // peers may still be reading this block's part
+  if (splits > 1) cluster_sync_startup();  // peers may still be reading this block's part
 }
 
 // ------------------------------------------------------------------ expand
 struct ExpandArgs {
-  CUtensorMap map;  // base: 128 rows x 64 columns
+  CUtensorMap map;   // base: 128 rows x 64 columns
+  CUtensorMap hmap;  // H: 128 rows x 64 of r
+  CUtensorMap wmap;  // W: 64 columns in accumulator order x 64 of r, or (kTrans) rp of r x 64 columns
   const int4* tiles;
   const int32_t* order;
   int cap16;
   const uint16_t* h;  // b x r
-  const uint16_t* w;  // count x n x r, or (kTrans) count x r x n
   const float* scale; // or null: 1
   const uint16_t* base;
   uint16_t* y;
@@ -513,7 +586,7 @@ struct ExpandArgs {
   int segs;
 };
 
-constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H and base, 1 loads W
+constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H and base; TMA of W
 // At most. The two halves of the epilogue warps take turns, so both numbers are even: a slot then
 // belongs to one half, and its barrier is never a whole turn ahead of a waiter.
 constexpr int kExpandSlots = 4;      // W stages, and accumulators of 64 columns
@@ -570,8 +643,8 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
 // blocks take them in turn, so that at any time they work on neighbouring columns of a few row
 // tiles (a copy by blocks with a long part of a row tile each: 4.6 TB/s; with short ones in
 // turn: 5.8). The accumulator is read in the 16x256b form,
-// where a quad of lanes holds 32 columns of a row in pairs; W's rows are stored permuted (or,
-// kTrans, the pairs are transposed over the quad), so that each lane owns 8 consecutive columns
+// where a quad of lanes holds 32 columns of a row in pairs; W's tensor map orders its rows so
+// (column 8 t + 2 j + e of 32 at 8 j + 2 t + e; kTrans: pairs are transposed over the quad) that a lane owns 8 consecutive columns
 // and a quad writes 64 bytes of a row. base comes through shared memory, several stages ahead;
 // it may be y itself, since the lane that writes an element is the only one that reads it, from
 // the stage, before that.
@@ -608,7 +681,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   if (items.count > 0) {
     if (tid == 0) {
       for (int i = 0; i < kExpandSlots; ++i) {
-        mbar_init(&s_full[i], 32);
+        mbar_init(&s_full[i], 1);
         mbar_init(&s_done[i], 1);
         mbar_init(&s_free[i], 4);
       }
@@ -716,20 +789,21 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         bool alive = true;
         for (int k = 0; k < items.count && alive; ++k) {
           if (!wait(&s_hfull[hs], hph, s_abort, kSiteFull)) break;
-          const uint32_t hb = sh + hs * kt * 16384;
+          fence_proxy_async_smem();  // H may have come by cp.async
+          const uint32_t hb = desc_k(sh + hs * kt * 16384);
           const int ue = unit_end(k);
           for (int u = unit_begin(k); u < ue; ++u, ++i) {
             alive = wait(&s_full[slot], ph, s_abort, kSiteFull) &&
                     (i < p.slots || wait(&s_free[slot], ph ^ 1u, s_abort, kSiteAccEmpty));
             if (!alive) break;
-            fence_proxy_async_smem();
             tc_fence_after();
-            const uint32_t ws = sw + slot * p.stage_bytes;
-            for (int q = 0; q < p.rp / 16; ++q)
-              mma_bf16(tmem + slot * 64, smem_desc_sw128(hb + (q >> 2) * 16384 + (q & 3) * 32),
-                       kTrans ? smem_desc_mn(ws + q * 2048, 0)
-                              : smem_desc_sw128(ws + (q >> 2) * 8192 + (q & 3) * 32),
-                       idesc, q > 0);
+            const uint32_t ws = sw + slot * p.stage_bytes, d = tmem + slot * 64;
+            const uint32_t b = kTrans ? desc_mn(ws, 0) : desc_k(ws);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q * 16 < p.rp)
+                mma(d, hb + (q >> 2) * 1024 + (q & 3) * 2,
+                    b + (kTrans ? q * 128 : (q >> 2) * 512 + (q & 3) * 2), idesc, q > 0);
             mma_commit(&s_done[slot]);
             if (++slot == p.slots) {
               slot = 0;
@@ -757,14 +831,23 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         pdl_wait();
         for (int k = 0; k < items.count && alive; ++k) {
           if (k >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_abort, kSiteHEmpty)) break;
-          for (int c = ch; c < chunks; c += 8)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const bool in = ra.row[j] >= 0 && c * 8 < p.r;
-              cp16(sh + (hs * kt + (c >> 3)) * 16384 + sw128(r0 + 8 * j, ch),
-                   p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+          if (ra.run >= 0) {  // rows beyond a partial tile's end are read and not used
+            if (tid == 288) {
+              mbar_arrive_expect_tx(&s_hfull[hs], kt * 16384);
+              for (int c = 0; c < kt; ++c)
+                tma_load(sh + (hs * kt + c) * 16384, &p.hmap, &s_hfull[hs], c * 64, ra.run);
+              mbar_arrive_n(&s_hfull[hs], 63);
             }
-          cp_arrive(&s_hfull[hs]);
+          } else {
+            for (int c = ch; c < chunks; c += 8)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const bool in = ra.row[j] >= 0 && c * 8 < p.r;
+                cp16(sh + (hs * kt + (c >> 3)) * 16384 + sw128(r0 + 8 * j, ch),
+                     p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+              }
+            cp_arrive(&s_hfull[hs]);
+          }
           if (++hs == p.hslots) {
             hs = 0;
             hph ^= 1u;
@@ -775,7 +858,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               alive = false;
               break;
             }
-            if (ra.run >= 0) {  // rows beyond a partial tile's end are read and not used
+            if (ra.run >= 0) {
               if (tid == 288) {
                 mbar_arrive_expect_tx(&s_bfull[bs], 16384);
                 tma_load(sb + bs * 16384, &p.map, &s_bfull[bs], u * 64, ra.run);
@@ -797,41 +880,31 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
           ra.advance();
         }
       } else {
-        const int r0 = lane >> 3, ch = lane & 7;
-        int slot = 0, i = 0, next = __ldg(&tiles[items.tile(0)].x);
-        uint32_t ph = 0;
-        for (int k = 0; k < items.count && alive; ++k) {
-          const uint16_t* wg = p.w + static_cast<int64_t>(next) * p.n * p.r;
-          if (k + 1 < items.count) next = __ldg(&tiles[items.tile(k + 1)].x);
-          const int ue = unit_end(k);
-          for (int u = unit_begin(k); u < ue; ++u, ++i) {
-            // the MMAs that read this stage are done when their accumulator is
-            if (i >= p.slots && !warp_wait(&s_done[slot], ph ^ 1u, s_abort, kSiteEmpty)) {
-              alive = false;
-              break;
-            }
-            const uint32_t ws = sw + slot * p.stage_bytes;
-            if constexpr (kTrans) {
-              for (int q = r0; q < p.rp; q += 4)
-                cp16(ws + sw128(q, ch), wg + static_cast<int64_t>(q < p.r ? q : 0) * p.n + u * 64 + ch * 8,
-                     q < p.r);
-            } else {
-              for (int c = ch; c < chunks; c += 8) {
-                const bool in = c * 8 < p.r;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const int nr = r0 + 4 * j;
-                  // column 8 t + 2 j + e of a group of 32 at accumulator column 8 j + 2 t + e
-                  const int q = (nr & 32) | ((nr & 6) << 2) | ((nr & 24) >> 2) | (nr & 1);
-                  cp16(ws + (c >> 3) * 8192 + sw128(q, ch),
-                       wg + static_cast<int64_t>(u * 64 + nr) * p.r + (in ? c * 8 : 0), in);
-                }
+        if (lane == 0) {
+          int slot = 0, i = 0, next = __ldg(&tiles[items.tile(0)].x);
+          uint32_t ph = 0;
+          for (int k = 0; k < items.count && alive; ++k) {
+            const int g = next;
+            if (k + 1 < items.count) next = __ldg(&tiles[items.tile(k + 1)].x);
+            const int ue = unit_end(k);
+            for (int u = unit_begin(k); u < ue; ++u, ++i) {
+              // the MMAs that read this stage are done when their accumulator is
+              if (i >= p.slots && !wait(&s_done[slot], ph ^ 1u, s_abort, kSiteEmpty)) {
+                alive = false;
+                break;
               }
-            }
-            cp_arrive(&s_full[slot]);
-            if (++slot == p.slots) {
-              slot = 0;
-              ph ^= 1u;
+              const uint32_t ws = sw + slot * p.stage_bytes;
+              mbar_arrive_expect_tx(&s_full[slot], p.stage_bytes);
+              if constexpr (kTrans) {
+                tma_load3(ws, &p.wmap, &s_full[slot], u * 64, 0, g);
+              } else {
+                for (int c = 0; c < kt; ++c)
+                  tma_load5(ws + c * 8192, &p.wmap, &s_full[slot], c * 64, 0, 0, 0, g * (p.n / 32) + u * 2);
+              }
+              if (++slot == p.slots) {
+                slot = 0;
+                ph ^= 1u;
+              }
             }
           }
         }
@@ -859,7 +932,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
 
 // ------------------------------------------------------------------- outer
 struct OuterArgs {
-  CUtensorMap map;  // Z: 128 rows x 64 columns
+  CUtensorMap map;   // Z: 128 rows x 64 columns
+  CUtensorMap hmap;  // H: 128 rows x 64 of r
+  CUtensorMap wmap;  // kDual: W: 128 rows of k x 64 of r
   const int4* tiles;
   const int32_t* order;
   const int32_t* first128;  // tiles of 128 rows before each group; [count]: all with adapter
@@ -872,7 +947,6 @@ struct OuterArgs {
   const float* scale; // or null: 1
   uint16_t* out;      // count x k x r, or (kByRank) count x r x k
   float* part;        // 2 gridDim.y slots shaped like one group's output
-  const uint16_t* w;  // kDual: count x k x r
   float* dpart;       // kDual: gridDim.x x b x r sums
   int64_t b;
   int k, r, rp;
@@ -881,7 +955,7 @@ struct OuterArgs {
   uint32_t tmem_cols;
 };
 
-constexpr int kOuterThreads = 512;  // 8 warps load Z; MMA warp; 4 drain; 2 load H, W; MMA of dh
+constexpr int kOuterThreads = 512;  // 8 warps load Z; MMA warp; 4 drain; 2: H, TMA of W; MMA of dh
 constexpr int kOuterStages = 4;     // at most
 constexpr int kOuterAhead = 3;      // as kAhead
 constexpr int kOuterRawStep = 16384 + 4096;
@@ -925,7 +999,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   const int4* tiles = p.tiles + 1 + p.cap16;
   if (tid == 0) {
     for (int i = 0; i < kOuterStages; ++i) {
-      mbar_init(&s_full[i], (kCodes ? 8 : 256) + (kDual ? 64 : 0));
+      mbar_init(&s_full[i], (kCodes ? 8 : 256) + (kDual ? 1 : 0));
       mbar_init(&s_empty[i], kDual ? 2 : 1);
       mbar_init(&s_hfull[i], 64);
       mbar_init(&s_hempty[i], 1);
@@ -1045,7 +1119,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       bool fresh = true;
       int run_end = min(end, p.first128[tiles[begin].x + 1]);
       for (int tile = begin; tile < end && alive; ++tile) {
-        const uint32_t hb = sh + hs * hbytes;
+        const uint32_t hb = desc_mn(sh + hs * hbytes, 16384);
         alive = wait(&s_hfull[hs], hphase, &s_abort, kSiteFull);
         if (!alive) break;
         for (int b = 0; b < nb; ++b) {
@@ -1055,11 +1129,10 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
           }
           fence_proxy_async_smem();
           tc_fence_after();
-          const uint32_t zs = sz + slot * kStage;
+          const uint32_t za = desc_mn(sz + slot * kStage, 16384), d = tmem + b * p.rp;
+          mma(d, za, hb, idesc, !fresh);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 128 rows: 8 steps of 16
-            mma_bf16(tmem + b * p.rp, smem_desc_mn(zs + k * 2048, 16384),
-                     smem_desc_mn(hb + k * 2048, 16384), idesc, !fresh || k > 0);
+          for (int k = 1; k < 8; ++k) mma(d, za + k * 128, hb + k * 128, idesc, true);  // 16 rows each
           mma_commit(&s_empty[slot]);
           if (++slot == stages) {
             slot = 0;
@@ -1104,11 +1177,11 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
           }
           fence_proxy_async_smem();
           tc_fence_after();
-          const uint32_t zs = sz + slot * kStage;
+          const uint32_t za = desc_k(sz + slot * kStage), wa = desc_mn(sz + slot * kStage + 32768, 0);
+          mma(dacc, za, wa, didesc, b > 0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 128 columns
-            mma_bf16(dacc, smem_desc_sw128(zs + (k >> 2) * 16384 + (k & 3) * 32),
-                     smem_desc_mn(zs + 32768 + k * 2048, 0), didesc, b > 0 || k > 0);
+          for (int k = 1; k < 8; ++k)  // 16 columns each
+            mma(dacc, za + (k >> 2) * 1024 + (k & 3) * 2, wa + k * 128, didesc, true);
           mma_commit(&s_empty[slot]);
           if (++slot == stages) {
             slot = 0;
@@ -1213,14 +1286,23 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
     for (int tile = begin; tile < end && alive; ++tile) {
       if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
         break;
-      for (int c = hc; c < rchunks; c += 8)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const bool in = ra.row[j] >= 0 && c * 8 < p.r;
-          cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(hr + 8 * j, hc),
-               p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+      if (ra.run >= 0 && ra.count == 128) {
+        if (l == 0) {
+          mbar_arrive_expect_tx(&s_hfull[hs], hbytes);
+          tma_load(sh + hs * hbytes, &p.hmap, &s_hfull[hs], 0, ra.run);
+          if (hbytes > 16384) tma_load(sh + hs * hbytes + 16384, &p.hmap, &s_hfull[hs], 64, ra.run);
+          mbar_arrive_n(&s_hfull[hs], 63);
         }
-      cp_arrive(&s_hfull[hs]);
+      } else {
+        for (int c = hc; c < rchunks; c += 8)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const bool in = ra.row[j] >= 0 && c * 8 < p.r;
+            cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(hr + 8 * j, hc),
+                 p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+          }
+        cp_arrive(&s_hfull[hs]);
+      }
       if (++hs == p.htiles) {
         hs = 0;
         hphase ^= 1u;
@@ -1228,20 +1310,15 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       const int group = ra.group;
       ra.advance();
       if constexpr (kDual) {
-        const uint16_t* wg = p.w + (static_cast<int64_t>(group) * p.k + blk0 * 128) * p.r;
         for (int b = 0; b < nb; ++b, ++step) {
           if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
             alive = false;
             break;
           }
-          const uint32_t ws = sz + slot * kStage + 32768;
-          if (hc < rchunks) {
-            const bool in = hc * 8 < p.r;
-            const uint16_t* src = wg + static_cast<int64_t>(b * 128 + hr) * p.r + (in ? hc * 8 : 0);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) cp16(ws + sw128(hr + 8 * j, hc), src + j * 8 * p.r, in);
+          if (l == 0) {
+            mbar_arrive_expect_tx(&s_full[slot], 16384);
+            tma_load3(sz + slot * kStage + 32768, &p.wmap, &s_full[slot], 0, (blk0 + b) * 128, group);
           }
-          cp_arrive(&s_full[slot]);
           if (++slot == stages) {
             slot = 0;
             phase ^= 1u;
@@ -1381,8 +1458,11 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// BF16 rows x cols, row stride `ld` elements, in boxes of 128 rows x 64 columns, 128-byte swizzle.
-cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, int64_t cols, int64_t ld) {
+// A tensor map of BF16, 128-byte swizzle, boxes of 64 of the contiguous dimension.
+// strides: of dimensions 1 .., in elements.
+template <int kRank>
+cudaError_t encode(CUtensorMap* map, const uint16_t* base, const int64_t (&dims)[kRank],
+                   const int64_t (&strides)[kRank - 1], const int (&box)[kRank]) {
   static std::atomic<EncodeTiledFn> known{nullptr};
   EncodeTiledFn fn = known.load(std::memory_order_acquire);
   if (!fn) {
@@ -1395,14 +1475,24 @@ cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, in
     fn = reinterpret_cast<EncodeTiledFn>(f);
     known.store(fn, std::memory_order_release);
   }
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box, estr,
+  cuuint64_t d[kRank], s[kRank];
+  cuuint32_t b[kRank], one[kRank];
+  for (int i = 0; i < kRank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    one[i] = 1;
+    if (i > 0) s[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
+  }
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kRank, const_cast<uint16_t*>(base), d, s, b, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
+}
+// rows x cols, row stride ld, boxes of `high` rows.
+cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, int64_t cols, int64_t ld,
+                        int high = 128) {
+  return encode<2>(map, base, {cols, rows}, {ld}, {64, high});
 }
 
 int round16(int r) { return (r + 15) / 16 * 16; }
@@ -1412,13 +1502,18 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
                           const uint16_t* w, const float* scale, uint16_t* out, cudaStream_t st) {
   const bool codes = !trans && c.xq8;
   const int rp = round16(c.r);
-  ShrinkArgs p{{}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
-               codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, w, scale, out, k, c.r, rp, 0, 0};
-  p.stage_bytes = 16384 + (trans ? (rp + 63) / 64 * 8192 : rp * 128);
-  // two blocks per SM: about 110 KB each, of which the parts need 128 x (rp + 4) fp32
-  const int raw = codes ? kAhead * kRawStep : 0;
-  p.stages = std::max(2, std::min(kShrinkMaxStages, (110 * 1024 - raw) / p.stage_bytes));
-  const int smem = std::max(p.stages * p.stage_bytes + raw, 128 * (rp + 4) * 4) + 1024;
+  ShrinkArgs p{{}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
+               codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, 0, 0};
+  // Two blocks per SM: 110 KB each, of which the parts need 128 x (rp + 4) fp32. As many W as Z
+  // stages; on codes (Z is converted from its own ring) two or three of Z and the rest of W,
+  // whose copies take 2 us and more while HBM is busy.
+  const int wbytes = trans ? (rp + 63) / 64 * 8192 : rp * 128, raw = codes ? kAhead * 8192 : 0;
+  p.stages = codes ? (rp > 64 ? 2 : 3)
+                   : std::max(2, std::min(kShrinkStages, 110 * 1024 / (16384 + wbytes)));
+  p.wstages = codes ? std::max(2, std::min(kShrinkStages, (110 * 1024 - raw - p.stages * 16384) / wbytes))
+                    : p.stages;
+  const int smem =
+      std::max(p.stages * 16384 + p.wstages * wbytes + raw, 128 * (rp + 4) * 4) + 1024;
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
   // Split the reduction over a cluster of up to 8 blocks, for about two blocks per SM (a few
@@ -1426,17 +1521,17 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   // tiles in clusters of 4 and of 2).
   const int splits = std::max(1, std::min(8, 290 / tiles_estimate(c)));
   const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
-  if (!codes) {
-    const cudaError_t e = encode_rows(&p.map, z, c.g.b, k, ldz);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = trans ? encode<3>(&p.wmap, w, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 64, 1})
+                        : encode_rows(&p.wmap, w, int64_t(c.g.count) * c.r, k, k, rp);
+  if (e == cudaSuccess && !codes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
+  if (e != cudaSuccess) return e;
   return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
 }
 
 cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, const uint16_t* w, int n,
                           const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r), kt = (rp + 63) / 64;
-  ExpandArgs p{{}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, w, scale, c.base, y,
+  ExpandArgs p{{}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, scale, c.base, y,
                first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, 0, 0, 0, 0, 1};
   // Two blocks per SM, 112 KB each: 4 stages of W and of base and a second H tile as far as they
   // fit (W's copies take 2 us and more while HBM is busy), 2 of each beyond rank 64.
@@ -1447,10 +1542,15 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, c
   p.hslots = rest + 2 * kt * 16384 <= 112 * 1024 ? 2 : 1;
   const int fixed = p.hslots * kt * 16384 + p.slots * p.stage_bytes;
   const int smem = fixed + p.bslots * 16384 + kExpandBars;
-  if (c.base) {
-    const cudaError_t e = encode_rows(&p.map, c.base, c.g.b, n, n);
-    if (e != cudaSuccess) return e;
-  }
+  const int64_t r = c.r;
+  // W (count x n x r): the 32 columns of a group as 8 t + 2 j + e, read in the order e, t, j
+  cudaError_t e =
+      trans ? encode<3>(&p.wmap, w, {n, r, c.g.count}, {n, r * n}, {64, rp, 1})
+            : encode<5>(&p.wmap, w, {r, 2, 4, 4, int64_t(c.g.count) * n / 32}, {r, 8 * r, 2 * r, 32 * r},
+                        {64, 2, 4, 4, 2});
+  if (e == cudaSuccess) e = encode_rows(&p.hmap, h, c.g.b, r, r);
+  if (e == cudaSuccess && c.base) e = encode_rows(&p.map, c.base, c.g.b, n, n);
+  if (e != cudaSuccess) return e;
   // Parts of a row tile: 4 to 12 units, so that the last turn of the blocks is nearly full (an
   // item costs about one unit more than it has, for its H).
   const int units = n / 64, tiles = tiles_estimate(c);
@@ -1512,12 +1612,13 @@ cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint
                          float* dpart, cudaStream_t st) {
   const int rp = round16(c.r);
   const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
-  OuterArgs p{{}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
-              out, part, c.bm, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols};
-  if (!kCodes) {
-    const cudaError_t e = encode_rows(&p.map, z, c.g.b, k, ldz);
-    if (e != cudaSuccess) return e;
-  }
+  OuterArgs p{{}, {}, {}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
+              out, part, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols};
+  cudaError_t e = encode_rows(&p.hmap, h, c.g.b, c.r, c.r);
+  if (e == cudaSuccess && !kCodes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
+  if (e == cudaSuccess && kDual)
+    e = encode<3>(&p.wmap, c.bm, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 128, 1});
+  if (e != cudaSuccess) return e;
   const int smem = plan.stages * (32768 + (kDual ? 16384 : 0)) +
                    plan.htiles * ((rp + 63) / 64) * 16384 + (kCodes ? kOuterAhead * kOuterRawStep : 0) +
                    1024;
