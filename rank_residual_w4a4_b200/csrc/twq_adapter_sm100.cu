@@ -422,71 +422,87 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
       const int i = r0 + j * (128 / kRows);
       row[j] = i < t.z ? __ldg(p.order + t.y + i) : -1;
     }
-    const uint32_t raw = sw + p.wstages * wbytes + tid * 16;
-    const int8_t* src[2];   // codes: this thread's column of its rows
-    const float* ssrc[2] = {};
-    float sc[2], sc1[2], sc2[2];  // scales of the current group and the two after it
-    auto scale_of = [&](int j, int group) {
-      return row[j] >= 0 && group * 2 < steps ? __ldg(ssrc[j] + rank + group * splits) : 0.0f;
-    };
-    auto fetch = [&](int step) {
-      if (step < steps)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          cp16(raw + (step % kAhead * 2 + j) * 4096, src[j] + column(step), row[j] >= 0);
-      cp_commit();
+    int slot = 0;
+    uint32_t phase = 0;
+    auto next_slot = [&]() {
+      if (++slot == p.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
     };
     if constexpr (kCodes) {
+      const uint32_t raw = sw + p.wstages * wbytes + tid * 16;
+      const int8_t* src[2];  // this thread's column of its rows
+      const float* ssrc[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int64_t at = max(row[j], 0);
         src[j] = p.q + at * p.k + ch * 16;
-        ssrc[j] = p.sq + at * (p.k >> 7);
+        ssrc[j] = p.sq + at * (p.k >> 7) + rank;
       }
-      for (int a = 0; a < kAhead; ++a) fetch(a);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        sc[j] = scale_of(j, 0), sc1[j] = scale_of(j, 1), sc2[j] = scale_of(j, 2);
-    }
-    int slot = 0;
-    uint32_t phase = 0;
-    for (int step = 0; step < steps; ++step) {
-      uint4 v[2];
-      if constexpr (kCodes) {
-        cp_wait<kAhead - 1>();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) v[j] = lds16(raw + (step % kAhead * 2 + j) * 4096);
-      }
-      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
-      const uint32_t zs = sz + slot * 16384;
-      if constexpr (kCodes) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint4 lo, hi;
-          dequant16(v[j], sc[j], lo, hi);
-          const int i = r0 + j * 64;
-          sts16(zs + sw128(i, 2 * ch), lo);
-          sts16(zs + sw128(i, 2 * ch + 1), hi);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_full[slot]);
-        fetch(step + kAhead);
-        if (step & 1) {
+      auto fetch = [&](int step) {
+        if (step < steps)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            sc[j] = sc1[j], sc1[j] = sc2[j], sc2[j] = scale_of(j, (step >> 1) + 3);
+            cp16(raw + (step % kAhead * 2 + j) * 4096, src[j] + column(step), row[j] >= 0);
+        cp_commit();
+      };
+      for (int a = 0; a < kAhead; ++a) fetch(a);
+      // Scales of three groups, each loaded into its own registers three groups ahead (a move
+      // between registers would wait for the load).
+      float sc[3][2];
+      auto load_scales = [&](float (&v)[2], int group) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          v[j] = row[j] >= 0 && group * 2 < steps ? __ldg(ssrc[j] + group * splits) : 0.0f;
+      };
+#pragma unroll
+      for (int u = 0; u < 3; ++u) load_scales(sc[u], u);
+      bool alive = true;
+      for (int base = 0; base * 2 < steps && alive; base += 3) {
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          const int group = base + u;
+          if (group * 2 >= steps || !alive) break;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int step = group * 2 + half;
+            cp_wait<kAhead - 1>();
+            uint4 v[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) v[j] = lds16(raw + (step % kAhead * 2 + j) * 4096);
+            if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
+              alive = false;
+              break;
+            }
+            const uint32_t zs = sz + slot * 16384;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint4 lo, hi;
+              dequant16(v[j], sc[u][j], lo, hi);
+              const int i = r0 + j * 64;
+              sts16(zs + sw128(i, 2 * ch), lo);
+              sts16(zs + sw128(i, 2 * ch + 1), hi);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_full[slot]);
+            fetch(step + kAhead);
+            next_slot();
+          }
+          load_scales(sc[u], group + 3);
         }
-      } else {
+      }
+    } else {
+      for (int step = 0; step < steps; ++step) {
+        if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+        const uint32_t zs = sz + slot * 16384;
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
           cp16(zs + sw128(r0 + j * 32, ch), p.z + max(row[j], 0) * p.ldz + column(step) + ch * 8,
                row[j] >= 0);
         cp_arrive(&s_full[slot]);
-      }
-      if (++slot == p.stages) {
-        slot = 0;
-        phase ^= 1u;
+        next_slot();
       }
     }
     cp_wait_all();
