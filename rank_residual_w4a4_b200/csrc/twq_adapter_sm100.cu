@@ -303,6 +303,7 @@ struct ShrinkArgs {
 
 constexpr int kShrinkThreads = 320;  // 8 warps load Z, then epilogue; MMA warp; TMA warp
 constexpr int kShrinkStages = 8;     // at most, of either kind
+constexpr uint32_t kShrinkTmemCols = 128;
 // Codes are converted by the thread that loaded them: it keeps kAhead steps of its own codes in
 // flight into a private part of shared memory, as it would in registers.
 constexpr int kAhead = 4;
@@ -340,7 +341,6 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   const uint32_t sz = smem_u32(smem);
   const uint32_t sw = sz + p.stages * 16384;
   const int wbytes = kTrans ? (p.rp + 63) / 64 * 8192 : p.rp * 128;
-  const uint32_t tmem_cols = p.rp <= 32 ? 32 : (p.rp <= 64 ? 64 : 128);
   // rows beyond a partial tile's end then belong to others; their sums are not stored
   const bool tma = !kCodes && t.w >= 0;
   const int steps = (p.k / 128 - rank + splits - 1) / splits * 2;  // of 64 columns
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     }
   }
   if (warp == 8) {
-    tmem_alloc(&s_tmem, tmem_cols);
+    tmem_alloc(&s_tmem, kShrinkTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, tmem_cols);
+  if (warp == 8) tmem_dealloc(tmem, kShrinkTmemCols);
   if (splits > 1) cluster_sync_startup();
   for (int i = tid; i < (hi - lo) * quads; i += kShrinkThreads) {
     const int rr = lo + i / quads, c = i % quads * 4;
@@ -1444,6 +1444,7 @@ template <typename Args>
 cudaError_t launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, bool pdl,
                    const Args& args, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -1513,6 +1514,39 @@ cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, in
 
 int round16(int r) { return (r + 15) / 16 * 16; }
 
+// Never launched: a kernel of the shrink kernels' shape that allocates no tensor memory. For one
+// that does, the occupancy calls answer one block per SM; two of 128 columns do run there.
+__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_shape_kernel(int* out) {
+  extern __shared__ int shape_smem[];
+  if (out) out[0] = shape_smem[threadIdx.x];
+}
+// Clusters of `size` shrink blocks with `smem` bytes that the GPU can hold at once (rank16, kind:
+// what smem depends on); asked once.
+int clusters_that_fit(int kind, int size, int rank16, int smem) {
+  static std::atomic<int> known[3][9][9];
+  int v = known[kind][size][rank16].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  cudaFuncSetAttribute(shrink_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + 1024);
+  cudaFuncSetAttribute(shrink_shape_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size, 2 * kSms);
+  cfg.blockDim = dim3(kShrinkThreads);
+  cfg.dynamicSmemBytes = smem + 1024;  // and the kernels' static part
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = size;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&v, shrink_shape_kernel, &cfg) != cudaSuccess || v < 1) {
+    cudaGetLastError();  // not a launch's error
+    v = std::max(1, 2 * kSms * 6 / 7 / size);
+  }
+  known[kind][size][rank16].store(v, std::memory_order_relaxed);
+  return v;
+}
+
 // trans: W is count x k x r (the backward pass's B).
 cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, int64_t ldz, int k,
                           const uint16_t* w, const float* scale, uint16_t* out, cudaStream_t st) {
@@ -1532,10 +1566,12 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
       std::max(p.stages * 16384 + p.wstages * wbytes + raw, 128 * (rp + 4) * 4) + 1024;
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
-  // Split the reduction over a cluster of up to 8 blocks, for about two blocks per SM (a few
-  // clusters that start late cost less than SMs that hold one block: 24 against 31 us for 67
-  // tiles in clusters of 4 and of 2).
-  const int splits = std::max(1, std::min(8, 290 / tiles_estimate(c)));
+  // Split the reduction over a cluster of up to 8 blocks, as many as let all tiles run at once (a
+  // cluster keeps within a GPC: 33 clusters of 7 fit, or 44 of 6, and a second wave doubles the
+  // time: 45 against 25 us for 38 tiles of codes); one cluster in 20 may come late.
+  int splits = 8;
+  while (splits > 1 && tiles_estimate(c) * 20 > clusters_that_fit(trans ? 2 : codes, splits, rp / 16, smem) * 21)
+    --splits;
   const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
   cudaError_t e = trans ? encode<3>(&p.wmap, w, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 64, 1})
                         : encode_rows(&p.wmap, w, int64_t(c.g.count) * c.r, k, k, rp);
