@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtwq.so")
 SOURCES = ["twq_api.cu", "twq_gemm_sm100.cu", "twq_pair_sm100.cu", "twq_decode_sm100.cu",
-           "twq_quant.cu", "twq_noalloc.cu", "twq_fold.cu", "twq_group.cu", "twq_adapter_sm100.cu"]
+           "twq_quant.cu", "twq_noalloc.cu", "twq_fold.cu", "twq_group.cu", "twq_adapter_sm100.cu",
+           "twq_adapter_small.cu"]
 HEADERS = ["sm100_ptx.cuh", "twq_internal.h", "twq_eq1.cuh", "twq_hrequant.cuh",
            "twq_adapter.h"]
 

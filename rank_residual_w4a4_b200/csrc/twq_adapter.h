@@ -60,6 +60,8 @@ struct AdapterCall {
 };
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st);
+// The forward pass for small batches (16-row tiles, one launch).
+cudaError_t launch_adapter_small(const AdapterCall& c, cudaStream_t st);
 cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st);
 cudaError_t read_and_clear_adapter_status(int* code);
 size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count);

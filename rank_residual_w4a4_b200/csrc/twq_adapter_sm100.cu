@@ -32,6 +32,7 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a wait that lasts 2 s is a failure
 constexpr int kSms = 148;
+constexpr int kSmallBatch = 512;
 
 // Site codes of the bounded waits.
 enum : int { kSiteEmpty = 61, kSiteFull, kSiteAccEmpty, kSiteDone, kSiteHEmpty, kSiteDrain, kSiteEnd };
@@ -1708,6 +1709,7 @@ cudaError_t read_and_clear_adapter_status(int* code) {
 }
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
+  if (c.g.b <= kSmallBatch) return launch_adapter_small(c, st);
   cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
   if (e != cudaSuccess) return e;
   return launch_expand(c, false, c.h, c.bm, c.n, c.scale, c.y, true, st);
