@@ -32,6 +32,7 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a wait that lasts 2 s is a failure
 constexpr int kSms = 148;
+constexpr int kMaxSmem = 226 * 1024;  // dynamic; the kernels' static part is 1 KB
 constexpr int kSmallBatch = 512;
 
 // Site codes of the bounded waits.
@@ -1444,9 +1445,10 @@ int tiles_estimate(const AdapterCall& c) {
 template <typename Args>
 cudaError_t launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, bool pdl,
                    const Args& args, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e != cudaSuccess) return e;
+  if (smem > 0) {
+    const cudaError_t e = allow_smem(kernel, kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);

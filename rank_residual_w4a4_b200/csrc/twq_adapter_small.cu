@@ -250,7 +250,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 template <bool kCodes, int kR>
 cudaError_t launch(const AdapterCall& c, cudaStream_t st) {
   const int smem = kWarps * 16 * kR * 4;
-  cudaError_t e = cudaFuncSetAttribute(small_kernel<kCodes, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(small_kernel<kCodes, kR>, smem);
   if (e != cudaSuccess) return e;
   small_kernel<kCodes, kR><<<dim3(kRanks, row_tiles_cap(c.g.b, c.g.count, 16)), kThreads, smem, st>>>(c);
   return cudaGetLastError();

@@ -168,8 +168,8 @@ cudaError_t launch(const int32_t* ids, int b, const RowGroupsView& g, cudaStream
   int chunk = (b + warps - 1) / warps;
   chunk = (chunk + 31) / 32 * 32;
   const int bytes = 3 * (keys + 1) * 4 + warps * keys * static_cast<int>(sizeof(T));
-  cudaError_t e = cudaFuncSetAttribute(group_rows_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e =
+      allow_smem(group_rows_kernel<T>, 3 * (static_cast<int>(kMaxGroups) + 2) * 4 + kCountBytes);
   if (e != cudaSuccess) return e;
   group_rows_kernel<T><<<1, kThreads, bytes, st>>>(
       ids, b, g.count, warps, chunk, g.order, g.offsets, g.tiles, first128_of(g),

@@ -548,13 +548,16 @@ def group_rows(ids: torch.Tensor, count: int, groups: RowGroups | None = None,
     if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
         raise TypeError("ids must be a 1-D torch tensor")
     p = _dev(ids, "ids", torch.int32)
-    with _on(ids.device):
-        if groups is None:
-            groups = RowGroups(ids.shape[0], count, ids.device)
-            _keep(stream, groups._buf)
-        elif (groups.b, groups.count) != (ids.shape[0], count) or groups.device != ids.device:
-            raise ValueError("groups must have the sizes and the device of this call")
-        _check(load().twq_group_rows(p or None, groups._ref, _stream(stream)), "twq_group_rows")
+    if groups is None:
+        groups = RowGroups(ids.shape[0], count, ids.device)
+        _keep(stream, groups._buf)
+    elif (groups.b, groups.count) != (ids.shape[0], count) or groups.device != ids.device:
+        raise ValueError("groups must have the sizes and the device of this call")
+    st, back = _on(ids.device, stream)
+    status = _lib.twq_group_rows(p, groups._ref, st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, "twq_group_rows")
     return groups
 
 
@@ -564,6 +567,7 @@ class Adapters:
     updates in place are seen."""
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor):
+        load()
         pa, pb = _dev(a, "a", torch.bfloat16), _dev(b, "b", torch.bfloat16)
         ps = _dev(scale, "scale", torch.float32)
         if a.dim() != 3 or b.dim() != 3 or scale.dim() != 1:
@@ -579,22 +583,17 @@ class Adapters:
         self._ref = ctypes.byref(self._c)
 
 
-class _on:
-    """Make `device` current for a call (kernels are launched on the current device)."""
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without its Python object
 
-    __slots__ = ("_dev", "_prev")
 
-    def __init__(self, device):
-        self._dev = device.index
-
-    def __enter__(self):
-        self._prev = torch.cuda.current_device()
-        if self._prev != self._dev:
-            torch.cuda.set_device(self._dev)
-
-    def __exit__(self, *exc):
-        if self._prev != self._dev:
-            torch.cuda.set_device(self._prev)
+def _on(device, stream):
+    """Make `device` current (kernels are launched on the current device): the stream to
+    launch on, and the device to go back to, or None."""
+    back = None
+    if torch.cuda.current_device() != device.index:
+        back = torch.cuda.current_device()
+        torch.cuda.set_device(device)
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream, back
 
 
 def _keep(stream, *tensors):
@@ -607,7 +606,7 @@ def _keep(stream, *tensors):
 def _mat(t, name, dtype, rows, cols, device) -> int:
     """A contiguous rows x cols tensor on `device`: its address."""
     p = _dev(t, name, dtype)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError("%s must be (%d, %d)" % (name, rows, cols))
     if t.device != device:
         raise ValueError("%s must be on the adapters' device" % name)
@@ -636,18 +635,20 @@ def _adapter_sizes(ad: Adapters, groups: RowGroups) -> int:
 
 
 def _adapter_linear(fn, args, ad, groups, base, y, h, stream):
-    b, dev = groups.b, ad.device
-    with _on(dev):
-        pb = None if base is None else _mat(base, "base", torch.bfloat16, b, ad.n, dev)
-        if y is None:
-            y = torch.empty((b, ad.n), dtype=torch.bfloat16, device=dev)
-            _keep(stream, y)
-        if h is None:
-            h = torch.empty((b, ad.r), dtype=torch.bfloat16, device=dev)
-            _keep(stream, h)
-        _check(getattr(load(), fn)(*args, b, ad._ref, groups._ref, pb,
-                                   _mat(h, "h", torch.bfloat16, b, ad.r, dev),
-                                   _mat(y, "y", torch.bfloat16, b, ad.n, dev), _stream(stream)), fn)
+    b, dev, bf = groups.b, ad.device, torch.bfloat16
+    pb = None if base is None else _mat(base, "base", bf, b, ad.n, dev)
+    if y is None:
+        y = torch.empty((b, ad.n), dtype=bf, device=dev)
+        _keep(stream, y)
+    if h is None:
+        h = torch.empty((b, ad.r), dtype=bf, device=dev)
+        _keep(stream, h)
+    ph, py = _mat(h, "h", bf, b, ad.r, dev), _mat(y, "y", bf, b, ad.n, dev)
+    st, back = _on(dev, stream)
+    status = getattr(_lib, fn)(*args, b, ad._ref, groups._ref, pb, ph, py, st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, fn)
     return y, h
 
 
@@ -679,32 +680,35 @@ def adapter_backward_workspace_bytes(b: int, m: int, n: int, r: int, count: int)
 
 def _adapter_backward(fn, dy, args, h, ad, groups, dx_base, dx, da, db, workspace, stream):
     b, dev, bf = groups.b, ad.device, torch.bfloat16
-    with _on(dev):
-        pdy, ph = _mat(dy, "dy", bf, b, ad.n, dev), _mat(h, "h", bf, b, ad.r, dev)
-        pb = None if dx_base is None else _mat(dx_base, "dx_base", bf, b, ad.m, dev)
-        if dx is None:
-            dx = torch.empty((b, ad.m), dtype=bf, device=dev)
-            _keep(stream, dx)
-        if da is None:
-            da = torch.empty_like(ad.a)
-            _keep(stream, da)
-        if db is None:
-            db = torch.empty_like(ad.b)
-            _keep(stream, db)
-        for t, like, name in ((da, ad.a, "da"), (db, ad.b, "db")):
-            if t.shape != like.shape or t.device != dev:
-                raise ValueError("%s must have the shape and device of the adapters' weights" % name)
-        if workspace is None:
-            workspace = torch.empty(
-                max(adapter_backward_workspace_bytes(b, ad.m, ad.n, ad.r, ad.count), 16),
-                dtype=torch.uint8, device=dev)
-            _keep(stream, workspace)
-        elif workspace.device != dev:
-            raise ValueError("workspace must be on the adapters' device")
-        _check(getattr(load(), fn)(pdy, *args, ph, b, ad._ref, groups._ref, pb,
-                                   _mat(dx, "dx", bf, b, ad.m, dev), _dev(da, "da", bf),
-                                   _dev(db, "db", bf), _dev(workspace, "workspace", torch.uint8),
-                                   workspace.numel(), _stream(stream)), fn)
+    pdy, ph = _mat(dy, "dy", bf, b, ad.n, dev), _mat(h, "h", bf, b, ad.r, dev)
+    pb = None if dx_base is None else _mat(dx_base, "dx_base", bf, b, ad.m, dev)
+    if dx is None:
+        dx = torch.empty((b, ad.m), dtype=bf, device=dev)
+        _keep(stream, dx)
+    if da is None:
+        da = torch.empty_like(ad.a)
+        _keep(stream, da)
+    if db is None:
+        db = torch.empty_like(ad.b)
+        _keep(stream, db)
+    for t, like, name in ((da, ad.a, "da"), (db, ad.b, "db")):
+        if t.shape != like.shape or t.device != dev:
+            raise ValueError("%s must have the shape and device of the adapters' weights" % name)
+    if workspace is None:
+        workspace = torch.empty(
+            max(adapter_backward_workspace_bytes(b, ad.m, ad.n, ad.r, ad.count), 16),
+            dtype=torch.uint8, device=dev)
+        _keep(stream, workspace)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the adapters' device")
+    pdx, pa, pbb = _mat(dx, "dx", bf, b, ad.m, dev), _dev(da, "da", bf), _dev(db, "db", bf)
+    pw = _dev(workspace, "workspace", torch.uint8)
+    st, back = _on(dev, stream)
+    status = getattr(_lib, fn)(pdy, *args, ph, b, ad._ref, groups._ref, pb, pdx, pa, pbb, pw,
+                               workspace.numel(), st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, fn)
     return dx, da, db
 
 
