@@ -104,6 +104,21 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
+// The same for what is read once: first to leave L2, which then keeps what is read again (weights,
+// H, and the parts that the backward pass adds up).
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_once(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                              int y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
                                           int y, int z) {
   asm volatile(
@@ -360,7 +375,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   };
   auto load_both = [&](int step, int slot) {
     mbar_arrive_expect_tx(&s_full[slot], (tma ? 16384 : 0) + wbytes);
-    if (tma) tma_load(sz + slot * 16384, &p.map, &s_full[slot], column(step), t.w);
+    if (tma)
+      tma_load_once(sz + slot * 16384, &p.map, &s_full[slot], column(step), t.w, read_once_policy());
     load_w(step, slot, &s_full[slot]);
   };
   if (tid == 288) {
@@ -671,6 +687,7 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
 template <bool kTrans>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // no other shared memory: two blocks fill an SM
+  if (kTrans) pdl_launch_dependents();  // the backward pass: another kernel of the call follows
   const int kt = (p.rp + 63) / 64;  // 64-wide tiles of the reduction
   const uint32_t sh = smem_u32(smem);
   const uint32_t sw = sh + p.hslots * kt * 16384;
@@ -879,7 +896,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             if (ra.run >= 0) {
               if (tid == 288) {
                 mbar_arrive_expect_tx(&s_bfull[bs], 16384);
-                tma_load(sb + bs * 16384, &p.map, &s_bfull[bs], u * 64, ra.run);
+                tma_load_once(sb + bs * 16384, &p.map, &s_bfull[bs], u * 64, ra.run, read_once_policy());
                 mbar_arrive_n(&s_bfull[bs], 63);
               }
             } else {
@@ -936,8 +953,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   }
 
   // Rows without adapter: base itself.
-  if (p.base == p.y) return;
   pdl_wait();
+  if (p.base == p.y) return;
   const int bare = p.offsets[p.count];
   const int64_t pieces = static_cast<int64_t>(p.b - bare) * (p.n / 8);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kExpandThreads + tid; i < pieces;
@@ -971,12 +988,18 @@ struct OuterArgs {
   int stages, htiles; // Z stages, H tiles in shared memory
   int dcol;           // kDual: first tensor-memory column of the two row accumulators
   uint32_t tmem_cols;
+  bool zeros;         // one chunk: no finish kernel follows, which would write them
 };
 
-constexpr int kOuterThreads = 512;  // 8 warps load Z; MMA warp; 4 drain; 2: H, TMA of W; MMA of dh
+// Warps: 8 that load Z (16 convert codes: 8 of them took 0.9 us for a block that HBM delivers in
+// 0.4), then MMA, 4 that drain, 2 that load H and W, MMA of dh.
+__host__ __device__ constexpr int outer_z_warps(bool codes) { return codes ? 16 : 8; }
+__host__ __device__ constexpr int outer_threads(bool codes) { return 32 * (outer_z_warps(codes) + 8); }
 constexpr int kOuterStages = 4;     // at most
-constexpr int kOuterAhead = 3;      // as kAhead
-constexpr int kOuterRawStep = 16384 + 4096;
+// As kAhead, with 2 us between a request and its data while HBM is busy: 3 steps of 16 KB are 24
+// of the 44 KB per us that an SM can get.
+constexpr int kOuterAhead = 5;
+constexpr int kOuterRawStep = 16384 + 512;  // codes; a scale for each row
 
 __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles) {
   return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
@@ -992,18 +1015,29 @@ __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles
 // tile's 128 x r sums over this slice go to `dpart` ([slice][rank / 4][position][4]), and dY is
 // read once for both gradients.
 template <bool kCodes, bool kByRank, bool kDual>
-__global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_constant__ OuterArgs p) {
+__global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const __grid_constant__ OuterArgs p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kOuterStages], s_empty[kOuterStages], s_hfull[kOuterStages],
       s_hempty[kOuterStages], s_dfull[2], s_dfree[2], s_run, s_free, s_end;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   constexpr int kStage = 32768 + (kDual ? 16384 : 0);
+  constexpr int kZ = outer_z_warps(kCodes), kMma = kZ, kDrain = kZ + 1, kLoad = kZ + 5, kMma2 = kZ + 7;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
+  pdl_launch_dependents();
   const int total = p.first128[p.count];
   const int chunks = min(static_cast<int>(gridDim.y), total);  // none of them empty
-  if (static_cast<int>(blockIdx.y) >= chunks) return;
+  if (total == 0) {  // no rows with an adapter at all
+    pdl_wait();
+    if (blockIdx.x == 0 && p.zeros)
+      for (int64_t i = tid; i < static_cast<int64_t>(p.count) * p.k * p.r / 8; i += blockDim.x)
+        reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  if (static_cast<int>(blockIdx.y) >= chunks) {
+    pdl_wait();
+    return;
+  }
   const int begin = chunk_begin(blockIdx.y, chunks, total);
   const int end = chunk_begin(blockIdx.y + 1, chunks, total);
   const int blk0 = blockIdx.x * (p.k / 128) / gridDim.x;
@@ -1017,7 +1051,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   const int4* tiles = p.tiles + 1 + p.cap16;
   if (tid == 0) {
     for (int i = 0; i < kOuterStages; ++i) {
-      mbar_init(&s_full[i], (kCodes ? 8 : 256) + (kDual ? 1 : 0));
+      mbar_init(&s_full[i], (kCodes ? kZ : 256) + (kDual ? 1 : 0));
       mbar_init(&s_empty[i], kDual ? 2 : 1);
       mbar_init(&s_hfull[i], 64);
       mbar_init(&s_hempty[i], 1);
@@ -1032,7 +1066,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
     s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == kMma) {
     tmem_alloc(&s_tmem, p.tmem_cols);
     tmem_relinquish();
   }
@@ -1041,11 +1075,13 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int steps = (end - begin) * nb;
-
-  if (warp < 8) {
-    const int r0 = tid >> 3, ch = tid & 7;  // rows r0 + 32 j, chunk ch (or 16 codes)
-    RowsAhead<4> ra;  // position of the loads: its tile, and the block in it
-    ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, r0, 32);
+  // Up to here only the grouping was read, which no kernel of the same call writes.
+  if (warp < kZ) {
+    constexpr int kRows = 128 / (kZ * 4);   // rows r0 + kZ * 4 j, chunk ch (or 16 codes)
+    const int r0 = tid >> 3, ch = tid & 7;
+    RowsAhead<kRows> ra;  // position of the loads: its tile, and the block in it
+    ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, r0, kZ * 4);
+    pdl_wait();
     int lblk = 0;
     auto advance = [&]() {
       if (++lblk == nb) {
@@ -1057,13 +1093,21 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
     auto fetch = [&]() {
       if (ra.at < end - begin) {
         const uint32_t at = sraw + rs * kOuterRawStep + tid * 16;
-        const uint32_t st = sraw + rs * kOuterRawStep + 16384 + tid * 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kRows; ++j) {
           const int64_t row = max(ra.row[j], 0);
-          cp16(at + j * 4096, p.q + row * p.k + (blk0 + lblk) * 128 + ch * 16, ra.row[j] >= 0);
-          cp4(st + j * 1024, p.sq + row * (p.k >> 7) + blk0 + lblk, ra.row[j] >= 0);
+          cp16(at + j * (kZ * 512), p.q + row * p.k + (blk0 + lblk) * 128 + ch * 16, ra.row[j] >= 0);
         }
+        // the warp's rows, one lane each
+        int srow = -1;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          const int other = __shfl_sync(0xFFFFFFFFu, ra.row[j], (lane & 3) * 8);
+          if (lane >> 2 == j) srow = other;
+        }
+        if (lane < 4 * kRows)
+          cp4(sraw + rs * kOuterRawStep + 16384 + (warp * 4 + (lane & 3) + (lane >> 2) * kZ * 4) * 4,
+              p.sq + static_cast<int64_t>(max(srow, 0)) * (p.k >> 7) + blk0 + lblk, srow >= 0);
         advance();
       }
       cp_commit();
@@ -1075,28 +1119,30 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
     int slot = 0;
     uint32_t phase = 0;
     for (int step = 0; step < steps; ++step) {
-      uint4 v[4];
-      float sc[4];
+      uint4 v[kRows];
+      float sc[kRows];
       if constexpr (kCodes) {
         cp_wait<kOuterAhead - 1>();
+        __syncwarp();  // the scales came by other lanes of the warp
         const uint32_t at = sraw + rs * kOuterRawStep + tid * 16;
-        const uint32_t st = sraw + rs * kOuterRawStep + 16384 + tid * 4;
+        const uint32_t st = sraw + rs * kOuterRawStep + 16384 + r0 * 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = lds16(at + j * 4096);
-          sc[j] = lds4(st + j * 1024);
+        for (int j = 0; j < kRows; ++j) {
+          v[j] = lds16(at + j * (kZ * 512));
+          sc[j] = lds4(st + j * (kZ * 16));
         }
+        __syncwarp();  // before a lane's next copies take their place
       }
       if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
       const uint32_t zs = sz + slot * kStage;
       if constexpr (kCodes) {
         const uint32_t half = zs + (ch >> 2) * 16384;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kRows; ++j) {
           uint4 lo, hi;
           dequant16(v[j], sc[j], lo, hi);
-          sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3)), lo);
-          sts16(half + sw128(r0 + 32 * j, 2 * (ch & 3) + 1), hi);
+          sts16(half + sw128(r0 + kZ * 4 * j, 2 * (ch & 3)), lo);
+          sts16(half + sw128(r0 + kZ * 4 * j, 2 * (ch & 3) + 1), hi);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1106,16 +1152,17 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
         if (ra.run >= 0 && ra.count == 128) {
           if (tid == 0) {
             mbar_arrive_expect_tx(&s_full[slot], 32768);
-            tma_load(zs, &p.map, &s_full[slot], (blk0 + lblk) * 128, ra.run);
-            tma_load(zs + 16384, &p.map, &s_full[slot], (blk0 + lblk) * 128 + 64, ra.run);
+            const uint64_t once = read_once_policy();
+            tma_load_once(zs, &p.map, &s_full[slot], (blk0 + lblk) * 128, ra.run, once);
+            tma_load_once(zs + 16384, &p.map, &s_full[slot], (blk0 + lblk) * 128 + 64, ra.run, once);
             mbar_arrive_n(&s_full[slot], 255);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < kRows; ++j)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-              cp16(zs + half * 16384 + sw128(r0 + 32 * j, ch),
+              cp16(zs + half * 16384 + sw128(r0 + kZ * 4 * j, ch),
                    p.z + max(ra.row[j], 0) * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8,
                    ra.row[j] >= 0);
           cp_arrive(&s_full[slot]);
@@ -1128,7 +1175,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       }
     }
     cp_wait_all();
-  } else if (warp == 8) {
+  } else if (warp == kMma) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(p.rp) | kAMajorMn | kBMajorMn;
       int runs = 0, slot = 0, hs = 0;
@@ -1177,7 +1224,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       mma_commit(&s_end);
       wait_mmas(&s_end);
     }
-  } else if (warp == 15) {
+  } else if (warp == kMma2) {
     // An MMA of so few columns takes its issuer 60 to 100 cycles whatever its size, so the row
     // sums have an issuer of their own.
     if (kDual && lane == 0) {
@@ -1211,10 +1258,20 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       mma_commit(&s_end);
       wait_mmas(&s_end);
     }
-  } else if (warp > 8 && warp < 13) {
+  } else if (warp >= kDrain && warp < kLoad) {
     const int sub = warp & 3;  // tensor-memory lanes of this warp
     const uint32_t lanes = static_cast<uint32_t>(sub * 32) << 16;
     const int64_t size = static_cast<int64_t>(p.k) * p.r;
+    pdl_wait();  // the kernels before may still read or write what this one writes
+    if (p.zeros && blockIdx.y == 0)
+      for (int g = 0; g < p.count; ++g) {  // adapters without rows
+        if (p.first128[g] != p.first128[g + 1]) continue;
+        uint4* out = reinterpret_cast<uint4*>(p.out + g * size);
+        const int l = tid - kDrain * 32, per = kByRank ? nb * 16 : nb * 16 * p.r;
+        for (int i = l; i < (kByRank ? per * p.r : per); i += 128)
+          out[kByRank ? static_cast<int64_t>(i / per) * (p.k / 8) + blk0 * 16 + i % per
+                      : static_cast<int64_t>(blk0) * 16 * p.r + i] = make_uint4(0, 0, 0, 0);
+      }
     int runs = 0;
     bool alive = true;
     for (int tile = begin; tile < end && alive;) {
@@ -1293,14 +1350,15 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free);
     }
-  } else if (warp > 12) {
-    const int l = tid - 416, rchunks = p.rp / 8;
+  } else {
+    const int l = tid - kLoad * 32, rchunks = p.rp / 8;
     const int hr = l >> 3, hc = l & 7;  // H: rows hr + 8 j, chunks hc, hc + 8
     int slot = 0, hs = 0, step = 0;
     uint32_t phase = 0, hphase = 0;
     bool alive = true;
     RowsAhead<16> ra;
     ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, hr, 8);
+    pdl_wait();
     for (int tile = begin; tile < end && alive; ++tile) {
       if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
         break;
@@ -1349,7 +1407,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) outer_kernel(const __grid_co
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, p.tmem_cols);
+  if (warp == kMma) tmem_dealloc(tmem, p.tmem_cols);
 }
 
 // dh (b x r) from the slices' parts, added in slice order. A thread: 4 ranks of a position.
@@ -1362,9 +1420,14 @@ struct ReduceArgs {
 };
 
 __global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
+  pdl_launch_dependents();
   const int64_t pos = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (pos >= p.offsets[p.count]) return;
+  if (pos >= p.offsets[p.count]) {
+    pdl_wait();
+    return;
+  }
   const int64_t row = p.order[pos];
+  pdl_wait();
   const float* part = p.dpart + (blockIdx.y * p.b + pos) * 4;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
@@ -1377,16 +1440,15 @@ __global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
 }
 
 // The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
-// zeros for the groups without rows. 4 elements a thread.
+// zeros for the groups without rows. A thread: 8 ranks of a column.
 struct FinishArgs {
   const int32_t* first128;
   int count;
   struct {
     const float* part;
     uint16_t* out;
-    int64_t size;  // elements of a group, a multiple of 1024
-    int chunks;
-  } side[2];       // dA (count x r x k), dB (count x k x r)
+    int k, chunks;
+  } side[2];  // dA (count x r x k), dB (count x k x r)
   int r;
 };
 
@@ -1398,41 +1460,49 @@ __device__ __forceinline__ int chunk_of(int tile, int chunks, int tiles) {
 }
 
 __global__ void __launch_bounds__(256) finish_kernel(const FinishArgs p) {
-  const float* part = blockIdx.z ? p.side[1].part : p.side[0].part;
-  uint16_t* dst = blockIdx.z ? p.side[1].out : p.side[0].out;
-  const int64_t size = blockIdx.z ? p.side[1].size : p.side[0].size;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x * 4;
-  if (at >= size) return;
+  pdl_wait();
+  const bool by_rank = blockIdx.z == 0;
+  const int k = by_rank ? p.side[0].k : p.side[1].k, all = by_rank ? p.side[0].chunks : p.side[1].chunks;
+  if (all == 1) return;  // written by the outer kernel
+  const int oct = p.r / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t blk = i / (oct * 128);
+  if (blk >= k / 128) return;
+  const int rest = static_cast<int>(i - blk * (oct * 128));
+  const int c = rest / 128 * 8, j = static_cast<int>(blk) * 128 + rest % 128;
   const int g = blockIdx.y, total = p.first128[p.count];
   const int gb = p.first128[g], ge = p.first128[g + 1];
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int64_t size = static_cast<int64_t>(k) * p.r;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = v;
   if (gb < ge) {
-    const int chunks = min(blockIdx.z ? p.side[1].chunks : p.side[0].chunks, total);
+    const int chunks = min(all, total);
     const int c0 = chunk_of(gb, chunks, total), c1 = chunk_of(ge - 1, chunks, total);
     if (c0 == c1) return;  // inside one chunk: already written
-    // the group's run is a chunk's second one only where the group starts inside it
-    v = __ldg(reinterpret_cast<const float4*>(
-        part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size + at));
-#pragma unroll 8
-    for (int c = c0 + 1; c <= c1; ++c) {
-      const float4 o = __ldg(reinterpret_cast<const float4*>(part + 2 * c * size + at));
-      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    // parts: [block][rank / 4][column of the block][4]; the group's run is a chunk's second one
+    // only where the group starts inside it
+    const float* part = (by_rank ? p.side[0].part : p.side[1].part) + (blk * (p.r / 4) + c / 4) * 512 +
+                        rest % 128 * 4;
+    const float* first = part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size;
+    v = __ldg(reinterpret_cast<const float4*>(first));
+    w = __ldg(reinterpret_cast<const float4*>(first + 512));
+#pragma unroll 4
+    for (int x = c0 + 1; x <= c1; ++x) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(part + 2 * x * size));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(part + 2 * x * size + 512));
+      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+      w.x += b.x, w.y += b.y, w.z += b.z, w.w += b.w;
     }
   }
-  // [block][rank / 4][column of the block][4] -> the output's place
-  const int64_t quad = at / 512, blk = quad / (p.r / 4);
-  const int c = static_cast<int>(quad - blk * (p.r / 4)) * 4;
-  const int64_t j = blk * 128 + (at >> 2) % 128;
-  uint16_t* out = dst + g * size;
-  if (blockIdx.z) {
-    *reinterpret_cast<uint2*>(out + j * p.r + c) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  const uint32_t o[4] = {pack2(v.x, v.y), pack2(v.z, v.w), pack2(w.x, w.y), pack2(w.z, w.w)};
+  uint16_t* out = (by_rank ? p.side[0].out : p.side[1].out) + g * size;
+  if (by_rank) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      out[static_cast<int64_t>(c + 2 * e) * k + j] = static_cast<uint16_t>(o[e]);
+      out[static_cast<int64_t>(c + 2 * e + 1) * k + j] = static_cast<uint16_t>(o[e] >> 16);
+    }
   } else {
-    const int64_t k = size / p.r;
-    const uint32_t lo = pack2(v.x, v.y), hi = pack2(v.z, v.w);
-    out[c * k + j] = static_cast<uint16_t>(lo);
-    out[(c + 1) * k + j] = static_cast<uint16_t>(lo >> 16);
-    out[(c + 2) * k + j] = static_cast<uint16_t>(hi);
-    out[(c + 3) * k + j] = static_cast<uint16_t>(hi >> 16);
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * p.r + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -1627,6 +1697,9 @@ struct OuterPlan {
   int slices, chunks, stages, htiles, dcol;
   uint32_t cols;
 };
+// What a block could have moved in the time of one more launch (the finish kernel's).
+constexpr double kLaunchBytes = 110e3;
+
 OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool dual) {
   const int rp = round16(r), blocks = k / 128;
   const int tiles = static_cast<int>(
@@ -1635,17 +1708,18 @@ OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool du
   double cost = 1e30;
   for (int nb = 1; nb <= 512 / rp - (dual ? 2 : 0) && nb <= blocks; ++nb) {
     const int slices = (blocks + nb - 1) / nb;
-    const int chunks = std::max(1, std::min(tiles, kSms / slices));
+    for (int chunks : {std::max(1, std::min(tiles, kSms / slices)), 1}) {
     const double waves = double((int64_t(slices) * chunks + kSms - 1) / kSms);
     const double each = double((tiles + chunks - 1) / chunks) *
                             (nb * 32768.0 + 256.0 * rp + (dual ? 512.0 * rp : 0.0)) +
-                        (chunks > 1 ? 2.0 * nb * 128 * rp * 4 : 0.0);
+                        (chunks > 1 ? 2.0 * nb * 128 * rp * 4 + kLaunchBytes : 0.0);
     const double all = waves * each + (dual ? double(slices) * tiles * 512 * rp / kSms : 0.0);
     if (all < cost) {
       cost = all;
       best.slices = slices;
       best.chunks = chunks;
       best.dcol = nb * rp;
+    }
     }
   }
   const int used = best.dcol + (dual ? 2 * rp : 0);
@@ -1654,7 +1728,7 @@ OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool du
   // As many H tiles as the Z stages reach ahead (nb_min: the blocks of the smallest slice).
   const int nb_min = blocks / best.slices, hbytes = (rp + 63) / 64 * 16384;
   const int stage = 32768 + (dual ? 16384 : 0), raw = codes ? kOuterAhead * kOuterRawStep : 0;
-  for (best.stages = kOuterStages;; --best.stages) {
+  for (best.stages = codes ? 2 : kOuterStages;; --best.stages) {
     best.htiles = std::max(2, 1 + (best.stages - 1 + nb_min - 1) / nb_min);
     if (best.stages * stage + best.htiles * hbytes + raw <= 224 * 1024) break;
   }
@@ -1664,11 +1738,11 @@ OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool du
 template <bool kCodes, bool kByRank, bool kDual>
 cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint16_t* z, int64_t ldz,
                          int k, const uint16_t* h, const float* scale, uint16_t* out, float* part,
-                         float* dpart, cudaStream_t st) {
+                         float* dpart, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r);
   const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
   OuterArgs p{{}, {}, {}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
-              out, part, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols};
+              out, part, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols, plan.chunks == 1};
   cudaError_t e = encode_rows(&p.hmap, h, c.g.b, c.r, c.r);
   if (e == cudaSuccess && !kCodes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
   if (e == cudaSuccess && kDual)
@@ -1677,8 +1751,8 @@ cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint
   const int smem = plan.stages * (32768 + (kDual ? 16384 : 0)) +
                    plan.htiles * ((rp + 63) / 64) * 16384 + (kCodes ? kOuterAhead * kOuterRawStep : 0) +
                    1024;
-  return launch(outer_kernel<kCodes, kByRank, kDual>, dim3(plan.slices, plan.chunks), kOuterThreads, smem,
-                1, false, p, st);
+  return launch(outer_kernel<kCodes, kByRank, kDual>, dim3(plan.slices, plan.chunks), outer_threads(kCodes),
+                smem, 1, pdl, p, st);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -1732,26 +1806,28 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (c.g.b > 0) {
     if (s.dual) {
-      e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, st);
+      e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, false, st);
       if (e != cudaSuccess) return e;
       const ReduceArgs ra{pd, c.g.order, c.g.offsets, dh, c.g.b, c.g.count, c.r, s.b.slices};
-      e = launch(reduce_kernel, dim3(static_cast<unsigned>((c.g.b + 255) / 256), c.r / 4), 256, 0, 1, false, ra, st);
+      e = launch(reduce_kernel, dim3(static_cast<unsigned>((c.g.b + 255) / 256), c.r / 4), 256, 0, 1, true, ra, st);
     } else {
       e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
       if (e == cudaSuccess)
-        e = launch_outer<false, false, false>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, nullptr, st);
+        e = launch_outer<false, false, false>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, nullptr, true, st);
     }
     if (e == cudaSuccess)
-      e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, st)
-                : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, st);
-    if (e == cudaSuccess) e = launch_expand(c, true, dh, c.a, c.m, nullptr, c.dx, false, st);
+      e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, true, st)
+                : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, true, st);
+    if (e == cudaSuccess) e = launch_expand(c, true, dh, c.a, c.m, nullptr, c.dx, true, st);
     if (e != cudaSuccess) return e;
   }
+  if (c.g.b > 0 && s.a.chunks == 1 && s.b.chunks == 1) return cudaSuccess;
+  // with no rows at all, both sides are zeros that no outer kernel writes
   FinishArgs f{first128_of(c.g), c.g.count, {}, c.r};
-  f.side[0] = {pa, c.da, int64_t(c.m) * c.r, s.a.chunks};
-  f.side[1] = {pb, c.db, int64_t(c.n) * c.r, s.b.chunks};
-  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 1023) / 1024;
-  return launch(finish_kernel, dim3(static_cast<unsigned>(blocks), c.g.count, 2), 256, 0, 1, false, f, st);
+  f.side[0] = {pa, c.da, c.m, c.g.b > 0 ? s.a.chunks : 2};
+  f.side[1] = {pb, c.db, c.n, c.g.b > 0 ? s.b.chunks : 2};
+  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 2047) / 2048;
+  return launch(finish_kernel, dim3(static_cast<unsigned>(blocks), c.g.count, 2), 256, 0, 1, c.g.b > 0, f, st);
 }
 
 }  // namespace twq
