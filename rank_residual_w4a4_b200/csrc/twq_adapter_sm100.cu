@@ -321,9 +321,11 @@ struct ShrinkArgs {
 constexpr int kShrinkThreads = 320;  // 8 warps load Z, then epilogue; MMA warp; TMA warp
 constexpr int kShrinkStages = 8;     // at most, of either kind
 constexpr uint32_t kShrinkTmemCols = 128;
-// Codes are converted by the thread that loaded them: it keeps kAhead steps of its own codes in
-// flight into a private part of shared memory, as it would in registers.
-constexpr int kAhead = 4;
+// Codes are converted by the thread that loaded them: it keeps kAhead groups (128 columns, two
+// steps) of its own codes in flight into a private part of shared memory, as it would in
+// registers. A group at a time, because a warp's waits, proxy fence and arrival take 650 cycles
+// however much it converts (steps of 64 columns: 1000 cycles each, of 250 that convert).
+constexpr int kAhead = 2;
 
 // One row tile per cluster, whose blocks split the reduction over k (block `rank` takes the groups
 // of 128 columns rank, rank + splits, ..., so that they read neighbouring pieces of the rows at
@@ -331,6 +333,9 @@ constexpr int kAhead = 4;
 template <bool kCodes, bool kTrans>
 __global__ void __launch_bounds__(kShrinkThreads, 2)
     shrink_kernel(const __grid_constant__ ShrinkArgs p) {
+  // A stage of Z and one of W: 64 columns, or a group of 128 with codes, where the issuing
+  // thread's waits and commits weigh more beside the converting warps.
+  constexpr int kPer = kCodes ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kShrinkStages], s_empty[kShrinkStages], s_wfull[kShrinkStages],
       s_wempty[kShrinkStages], s_done;
@@ -356,21 +361,25 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   }
   uint8_t* smem = align1k(smem_raw);
   const uint32_t sz = smem_u32(smem);
-  const uint32_t sw = sz + p.stages * 16384;
+  const uint32_t sw = sz + p.stages * kPer * 16384;
   const int wbytes = kTrans ? (p.rp + 63) / 64 * 8192 : p.rp * 128;
   // rows beyond a partial tile's end then belong to others; their sums are not stored
   const bool tma = !kCodes && t.w >= 0;
-  const int steps = (p.k / 128 - rank + splits - 1) / splits * 2;  // of 64 columns
-  auto column = [&](int step) { return (rank + (step >> 1) * splits) * 128 + (step & 1) * 64; };
-  // W's tile of a step. Without kTrans the rows beyond r are the next adapter's (or zeros): they
+  const int groups = (p.k / 128 - rank + splits - 1) / splits;
+  const int steps = groups * 2 / kPer;
+  auto column = [&](int tile) { return (rank + (tile >> 1) * splits) * 128 + (tile & 1) * 64; };
+  // W's part of a step. Without kTrans the rows beyond r are the next adapter's (or zeros): they
   // only reach accumulator columns that are not stored.
   auto load_w = [&](int step, int slot, uint64_t* bar) {
-    const uint32_t dst = sw + slot * wbytes;
-    if constexpr (kTrans) {
-      tma_load3(dst, &p.wmap, bar, 0, column(step), t.x);
-      if (p.rp > 64) tma_load3(dst + 8192, &p.wmap, bar, 64, column(step), t.x);
-    } else {
-      tma_load(dst, &p.wmap, bar, column(step), t.x * p.r);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t dst = sw + (slot * kPer + i) * wbytes;
+      if constexpr (kTrans) {
+        tma_load3(dst, &p.wmap, bar, 0, column(step * kPer + i), t.x);
+        if (p.rp > 64) tma_load3(dst + 8192, &p.wmap, bar, 64, column(step * kPer + i), t.x);
+      } else {
+        tma_load(dst, &p.wmap, bar, column(step * kPer + i), t.x * p.r);
+      }
     }
   };
   auto load_both = [&](int step, int slot) {
@@ -394,7 +403,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     fence_barrier_init();
     for (int step = 0; step < min(steps, kCodes ? p.wstages : p.stages); ++step) {
       if (kCodes) {
-        mbar_arrive_expect_tx(&s_wfull[step], wbytes);
+        mbar_arrive_expect_tx(&s_wfull[step], kPer * wbytes);
         load_w(step, step, &s_wfull[step]);
       } else {
         load_both(step, step);
@@ -418,7 +427,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
       for (int step = ring; step < steps; ++step) {
         if (!wait(kCodes ? &s_wempty[slot] : &s_empty[slot], phase, &s_abort, kSiteEmpty)) break;
         if (kCodes) {
-          mbar_arrive_expect_tx(&s_wfull[slot], wbytes);
+          mbar_arrive_expect_tx(&s_wfull[slot], kPer * wbytes);
           load_w(step, slot, &s_wfull[slot]);
         } else {
           load_both(step, slot);
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
       }
     };
     if constexpr (kCodes) {
-      const uint32_t raw = sw + p.wstages * wbytes + tid * 16;
+      const uint32_t raw = sw + p.wstages * kPer * wbytes + tid * 16;
       const int8_t* src[2];  // this thread's column of its rows
       const float* ssrc[2];
 #pragma unroll
@@ -458,11 +467,12 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
         src[j] = p.q + at * p.k + ch * 16;
         ssrc[j] = p.sq + at * (p.k >> 7) + rank;
       }
-      auto fetch = [&](int step) {
-        if (step < steps)
+      auto fetch = [&](int group) {
+        if (group < groups)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            cp16(raw + (step % kAhead * 2 + j) * 4096, src[j] + column(step), row[j] >= 0);
+          for (int j = 0; j < 4; ++j)  // row j % 2, half j / 2 of the group
+            cp16(raw + (group % kAhead * 4 + j) * 4096,
+                 src[j & 1] + (rank + group * splits) * 128 + (j >> 1) * 64, row[j & 1] >= 0);
         cp_commit();
       };
       for (int a = 0; a < kAhead; ++a) fetch(a);
@@ -472,42 +482,38 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
       auto load_scales = [&](float (&v)[2], int group) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          v[j] = row[j] >= 0 && group * 2 < steps ? __ldg(ssrc[j] + group * splits) : 0.0f;
+          v[j] = row[j] >= 0 && group < groups ? __ldg(ssrc[j] + group * splits) : 0.0f;
       };
 #pragma unroll
       for (int u = 0; u < 3; ++u) load_scales(sc[u], u);
       bool alive = true;
-      for (int base = 0; base * 2 < steps && alive; base += 3) {
+      for (int base = 0; base < groups && alive; base += 3) {
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           const int group = base + u;
-          if (group * 2 >= steps || !alive) break;
+          if (group >= groups || !alive) break;
+          cp_wait<kAhead - 1>();
+          uint4 v[4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int step = group * 2 + half;
-            cp_wait<kAhead - 1>();
-            uint4 v[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) v[j] = lds16(raw + (step % kAhead * 2 + j) * 4096);
-            if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
-              alive = false;
-              break;
-            }
-            const uint32_t zs = sz + slot * 16384;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint4 lo, hi;
-              dequant16(v[j], sc[u][j], lo, hi);
-              const int i = r0 + j * 64;
-              sts16(zs + sw128(i, 2 * ch), lo);
-              sts16(zs + sw128(i, 2 * ch + 1), hi);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_full[slot]);
-            fetch(step + kAhead);
-            next_slot();
+          for (int j = 0; j < 4; ++j) v[j] = lds16(raw + (group % kAhead * 4 + j) * 4096);
+          if (group >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
+            alive = false;
+            break;
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 lo, hi;
+            dequant16(v[j], sc[u][j & 1], lo, hi);
+            const int i = r0 + (j & 1) * 64;
+            const uint32_t zs = sz + (slot * 2 + (j >> 1)) * 16384;
+            sts16(zs + sw128(i, 2 * ch), lo);
+            sts16(zs + sw128(i, 2 * ch + 1), hi);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_full[slot]);
+          next_slot();
+          fetch(group + kAhead);
           load_scales(sc[u], group + 3);
         }
       }
@@ -534,11 +540,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
       if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) break;
       if (!kCodes && !tma) fence_proxy_async_smem();
       tc_fence_after();
-      const uint32_t a = desc_k(sz + slot * 16384), ws = sw + wslot * wbytes;
+      const uint32_t a = desc_k(sz + slot * kPer * 16384), ws = sw + wslot * kPer * wbytes;
       const uint32_t b = kTrans ? desc_mn(ws, 8192) : desc_k(ws);
+      mma(tmem, a, b, idesc, step > 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma(tmem, a + k * 2, b + k * (kTrans ? 128 : 2), idesc, step > 0 || k > 0);
+      for (int k = 1; k < 4 * kPer; ++k)
+        mma(tmem, a + (k >> 2) * 1024 + (k & 3) * 2,
+            b + (k >> 2) * (wbytes >> 4) + (k & 3) * (kTrans ? 128 : 2), idesc, true);
       mma_commit(&s_empty[slot]);
       if (kCodes) mma_commit(&s_wempty[wslot]);
       if (++slot == p.stages) {
@@ -1628,15 +1636,16 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   ShrinkArgs p{{}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
                codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, 0, 0};
   // Two blocks per SM: 110 KB each, of which the parts need 128 x (rp + 4) fp32. As many W as Z
-  // stages; on codes (Z is converted from its own ring) two or three of Z and the rest of W,
+  // stages; on codes (Z is converted from its own ring) one or two groups of Z and the rest of W,
   // whose copies take 2 us and more while HBM is busy.
-  const int wbytes = trans ? (rp + 63) / 64 * 8192 : rp * 128, raw = codes ? kAhead * 8192 : 0;
-  p.stages = codes ? (rp > 64 ? 2 : 3)
+  const int wbytes = trans ? (rp + 63) / 64 * 8192 : rp * 128, per = codes ? 2 : 1;
+  const int raw = codes ? kAhead * 16384 : 0;
+  p.stages = codes ? (rp > 32 ? 1 : 2)
                    : std::max(2, std::min(kShrinkStages, 110 * 1024 / (16384 + wbytes)));
-  p.wstages = codes ? std::max(2, std::min(kShrinkStages, (110 * 1024 - raw - p.stages * 16384) / wbytes))
+  p.wstages = codes ? std::max(1, std::min(kShrinkStages, (110 * 1024 - raw - p.stages * 32768) / (2 * wbytes)))
                     : p.stages;
   const int smem =
-      std::max(p.stages * 16384 + p.wstages * wbytes + raw, 128 * (rp + 4) * 4) + 1024;
+      std::max(per * (p.stages * 16384 + p.wstages * wbytes) + raw, 128 * (rp + 4) * 4) + 1024;
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
   // Split the reduction over a cluster of up to 8 blocks, as many as let all tiles run at once (a
