@@ -248,6 +248,22 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// Four columns of a row of a BF16 matrix of rank r; split: of rows of 2 r, the values rounded and,
+// r columns on, what the rounding left (together 16 bits of the value).
+__device__ __forceinline__ void store_value(uint16_t* out, int64_t row, int r, int c, float4 v, bool split) {
+  const uint2 hi = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  if (!split) {
+    *reinterpret_cast<uint2*>(out + row * r + c) = hi;
+    return;
+  }
+  *reinterpret_cast<uint2*>(out + row * 2 * r + c) = hi;
+  // nothing is left of an infinity (or of what rounds to one)
+  auto left = [](float x, float h) { return fabsf(h) <= 3.4e38f ? x - h : 0.0f; };
+  *reinterpret_cast<uint2*>(out + row * 2 * r + r + c) =
+      make_uint2(pack2(left(v.x, lo_f(hi.x)), left(v.y, hi_f(hi.x))),
+                 pack2(left(v.z, lo_f(hi.y)), left(v.w, hi_f(hi.y))));
+}
+
 // A block's work items, each a part of a row tile: item k is number first + stride k, in tile
 // number / parts.
 struct Items {
@@ -313,8 +329,9 @@ struct ShrinkArgs {
   const int8_t* q;
   const float* sq;
   const float* scale; // or null: 1
-  uint16_t* out;      // b x r
+  uint16_t* out;      // b x r, or (split) b x 2 r: the value in BF16, and what that leaves
   int k, r, rp;       // rp: r rounded up to 16
+  bool split;
   int stages, wstages;  // Z tiles of 128 x 64, W tiles of 64 of the reduction
 };
 
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   if (t.x < 0) {  // rows without adapter
     for (int i = rank * kShrinkThreads + tid; i < t.z * (p.r / 8); i += splits * kShrinkThreads) {
       const int64_t row = p.order[t.y + i / (p.r / 8)];
-      *reinterpret_cast<uint4*>(p.out + row * p.r + i % (p.r / 8) * 8) = make_uint4(0, 0, 0, 0);
+      if (!p.split) *reinterpret_cast<uint4*>(p.out + row * p.r + i % (p.r / 8) * 8) = make_uint4(0, 0, 0, 0);
     }
     return;
   }
@@ -603,8 +620,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     for (int s = 1; s < 8; ++s)
       if (s < splits) v.x += o[s].x, v.y += o[s].y, v.z += o[s].z, v.w += o[s].w;
     const int64_t orow = i == tid ? row0 : p.order[t.y + rr];
-    *reinterpret_cast<uint2*>(p.out + orow * p.r + c) =
-        make_uint2(pack2(v.x * f, v.y * f), pack2(v.z * f, v.w * f));
+    store_value(p.out, orow, p.r, c, make_float4(v.x * f, v.y * f, v.z * f, v.w * f), p.split);
   }
   if (splits > 1) cluster_sync_startup();  // peers may still be reading this block's part
 }
@@ -617,13 +633,13 @@ struct ExpandArgs {
   const int4* tiles;
   const int32_t* order;
   int cap16;
-  const uint16_t* h;  // b x r
+  const uint16_t* h;  // b rows of r, ldh apart
   const float* scale; // or null: 1
   const uint16_t* base;
   uint16_t* y;
   const int32_t *first128, *offsets;
   int b, count;
-  int n, r, rp;
+  int n, r, rp, ldh;
   int stage_bytes, slots, hslots, bslots;  // a W stage; W stages; H tiles; base stages of 16 KB
   int segs;
 };
@@ -887,7 +903,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               for (int j = 0; j < 16; ++j) {
                 const bool in = ra.row[j] >= 0 && c * 8 < p.r;
                 cp16(sh + (hs * kt + (c >> 3)) * 16384 + sw128(r0 + 8 * j, ch),
-                     p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+                     p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.ldh + c * 8 : 0), in);
               }
             cp_arrive(&s_hfull[hs]);
           }
@@ -986,13 +1002,14 @@ struct OuterArgs {
   int64_t ldz;
   const int8_t* q;
   const float* sq;
-  const uint16_t* h;  // b x r
+  const uint16_t* h;  // b x r, or (kByRank) b x 2 r, two terms (store_value)
   const float* scale; // or null: 1
   uint16_t* out;      // count x k x r, or (kByRank) count x r x k
   float* part;        // 2 gridDim.y slots shaped like one group's output
   float* dpart;       // kDual: gridDim.x x b x r sums
   int64_t b;
-  int k, r, rp;
+  int k, r;
+  int hr, rp;         // columns of H: r or 2 r; rounded up to 16
   int stages, htiles; // Z stages, H tiles in shared memory
   int dcol;           // kDual: first tensor-memory column of the two row accumulators
   uint32_t tmem_cols;
@@ -1019,6 +1036,9 @@ __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles
 // sums in the chunk's slot (0: the run starts the chunk, else 1) for the finish kernel, in the
 // order [block][rank / 4][column of the block][4], in which a warp writes 512 bytes at a time
 // (rows of the output would be 32 pieces in 32 lines: 6 us a run at 768 columns of rank 64).
+// kByRank (dA): H is dh in two BF16 terms side by side, 2 r accumulator columns, added at the end:
+// rounded once to BF16, dh would put as large an error into dA as dA's own rounding, for 8 MMAs
+// of a few more columns.
 // kDual (r <= 64): the same Z stage also serves the product over its columns, dh = Z W: a
 // tile's 128 x r sums over this slice go to `dpart` ([slice][rank / 4][position][4]), and dY is
 // read once for both gradients.
@@ -1326,31 +1346,25 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
       for (int b = 0; b < nb; ++b) {
         const int64_t j = (blk0 + b) * 128 + sub * 32 + lane;
         float* quads = part + static_cast<int64_t>(blk0 + b) * 128 * p.r + (sub * 32 + lane) * 4;
-        for (int c = 0; c < p.rp; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tmem + lanes + b * p.rp + c, v);
+        for (int c = 0; c < p.r; c += 8) {
+          uint32_t v[8], w[8];
+          tmem_ld8(tmem + lanes + b * p.rp + c, v);
+          if (kByRank) tmem_ld8(tmem + lanes + b * p.rp + p.r + c, w);
           tmem_wait_ld();
-          float o[16];
+          float o[8];
 #pragma unroll
-          for (int u = 0; u < 16; ++u) o[u] = f * __uint_as_float(v[u]);
+          for (int u = 0; u < 8; ++u)
+            o[u] = f * (kByRank ? __uint_as_float(v[u]) + __uint_as_float(w[u]) : __uint_as_float(v[u]));
+          if (!whole) {
+            *reinterpret_cast<float4*>(quads + c * 128) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(quads + (c + 4) * 128) = make_float4(o[4], o[5], o[6], o[7]);
+          } else if (kByRank) {
 #pragma unroll
-          for (int u = 0; u < 16; u += 8) {
-            if (c + u >= p.r) break;
-            if (!whole) {
-              *reinterpret_cast<float4*>(quads + (c + u) * 128) =
-                  make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]);
-              *reinterpret_cast<float4*>(quads + (c + u + 4) * 128) =
-                  make_float4(o[u + 4], o[u + 5], o[u + 6], o[u + 7]);
-            } else if (kByRank) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                out[(c + u + e) * static_cast<int64_t>(p.k) + j] =
-                    static_cast<uint16_t>(pack2(o[u + e], 0.0f));
-            } else {
-              *reinterpret_cast<uint4*>(out + j * p.r + c + u) =
-                  make_uint4(pack2(o[u], o[u + 1]), pack2(o[u + 2], o[u + 3]),
-                             pack2(o[u + 4], o[u + 5]), pack2(o[u + 6], o[u + 7]));
-            }
+            for (int e = 0; e < 8; ++e)
+              out[(c + e) * static_cast<int64_t>(p.k) + j] = static_cast<uint16_t>(pack2(o[e], 0.0f));
+          } else {
+            *reinterpret_cast<uint4*>(out + j * p.r + c) = make_uint4(
+                pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
           }
         }
       }
@@ -1373,17 +1387,17 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
       if (ra.run >= 0 && ra.count == 128) {
         if (l == 0) {
           mbar_arrive_expect_tx(&s_hfull[hs], hbytes);
-          tma_load(sh + hs * hbytes, &p.hmap, &s_hfull[hs], 0, ra.run);
-          if (hbytes > 16384) tma_load(sh + hs * hbytes + 16384, &p.hmap, &s_hfull[hs], 64, ra.run);
+          for (int c = 0; c < hbytes / 16384; ++c)
+            tma_load(sh + hs * hbytes + c * 16384, &p.hmap, &s_hfull[hs], c * 64, ra.run);
           mbar_arrive_n(&s_hfull[hs], 63);
         }
       } else {
         for (int c = hc; c < rchunks; c += 8)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const bool in = ra.row[j] >= 0 && c * 8 < p.r;
+            const bool in = ra.row[j] >= 0 && c * 8 < p.hr;
             cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(hr + 8 * j, hc),
-                 p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.r + c * 8 : 0), in);
+                 p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.hr + c * 8 : 0), in);
           }
         cp_arrive(&s_hfull[hs]);
       }
@@ -1418,7 +1432,8 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   if (warp == kMma) tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// dh (b x r) from the slices' parts, added in slice order. A thread: 4 ranks of a position.
+// dh from the slices' parts, added in slice order, as rows of 2 r (store_value). A thread: 4 ranks
+// of a position.
 struct ReduceArgs {
   const float* dpart;  // slices x r / 4 x b x 4
   const int32_t *order, *offsets;
@@ -1443,8 +1458,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
     const float4 o = __ldg(reinterpret_cast<const float4*>(part + s * p.b * p.r));
     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
   }
-  *reinterpret_cast<uint2*>(p.dh + row * p.r + blockIdx.y * 4) =
-      make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  store_value(p.dh, row, p.r, blockIdx.y * 4, v, true);
 }
 
 // The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
@@ -1634,7 +1648,7 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   const bool codes = !trans && c.xq8;
   const int rp = round16(c.r);
   ShrinkArgs p{{}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
-               codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, 0, 0};
+               codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, trans, 0, 0};
   // Two blocks per SM: 110 KB each, of which the parts need 128 x (rp + 4) fp32. As many W as Z
   // stages; on codes (Z is converted from its own ring) one or two groups of Z and the rest of W,
   // whose copies take 2 us and more while HBM is busy.
@@ -1662,11 +1676,11 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
 }
 
-cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, const uint16_t* w, int n,
-                          const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
+cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, int ldh, const uint16_t* w,
+                          int n, const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r), kt = (rp + 63) / 64;
   ExpandArgs p{{}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, scale, c.base, y,
-               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, 0, 0, 0, 0, 1};
+               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, ldh, 0, 0, 0, 0, 1};
   // Two blocks per SM, 112 KB each: 4 stages of W and of base and a second H tile as far as they
   // fit (W's copies take 2 us and more while HBM is busy), 2 of each beyond rank 64.
   p.stage_bytes = trans ? rp * 128 : kt * 8192;
@@ -1682,7 +1696,7 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, c
       trans ? encode<3>(&p.wmap, w, {n, r, c.g.count}, {n, r * n}, {64, rp, 1})
             : encode<5>(&p.wmap, w, {r, 2, 4, 4, int64_t(c.g.count) * n / 32}, {r, 8 * r, 2 * r, 32 * r},
                         {64, 2, 4, 4, 2});
-  if (e == cudaSuccess) e = encode_rows(&p.hmap, h, c.g.b, r, r);
+  if (e == cudaSuccess) e = encode_rows(&p.hmap, h, c.g.b, r, ldh);
   if (e == cudaSuccess && c.base) e = encode_rows(&p.map, c.base, c.g.b, n, n);
   if (e != cudaSuccess) return e;
   // Parts of a row tile: 4 to 12 units, so that the last turn of the blocks is nearly full (an
@@ -1709,8 +1723,9 @@ struct OuterPlan {
 // What a block could have moved in the time of one more launch (the finish kernel's).
 constexpr double kLaunchBytes = 110e3;
 
-OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool dual) {
-  const int rp = round16(r), blocks = k / 128;
+// hr: columns of H.
+OuterPlan outer_plan(int64_t b, int64_t count, int k, int hr, bool codes, bool dual) {
+  const int rp = round16(hr), blocks = k / 128;
   const int tiles = static_cast<int>(
       std::max<int64_t>(1, std::min<int64_t>(row_tiles_cap(b, count, 128), b / 128 + (count + 1) / 2)));
   OuterPlan best{};
@@ -1737,10 +1752,12 @@ OuterPlan outer_plan(int64_t b, int64_t count, int k, int r, bool codes, bool du
   // As many H tiles as the Z stages reach ahead (nb_min: the blocks of the smallest slice).
   const int nb_min = blocks / best.slices, hbytes = (rp + 63) / 64 * 16384;
   const int stage = 32768 + (dual ? 16384 : 0), raw = codes ? kOuterAhead * kOuterRawStep : 0;
-  for (best.stages = codes ? 2 : kOuterStages;; --best.stages) {
+  for (best.stages = codes ? 2 : kOuterStages; best.stages > 1; --best.stages) {
     best.htiles = std::max(2, 1 + (best.stages - 1 + nb_min - 1) / nb_min);
-    if (best.stages * stage + best.htiles * hbytes + raw <= 224 * 1024) break;
+    if (best.stages * stage + best.htiles * hbytes + raw <= 224 * 1024) return best;
   }
+  best.stages = 2;  // codes beyond rank 64: one H tile of 64 KB
+  best.htiles = 1;
   return best;
 }
 
@@ -1748,11 +1765,11 @@ template <bool kCodes, bool kByRank, bool kDual>
 cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint16_t* z, int64_t ldz,
                          int k, const uint16_t* h, const float* scale, uint16_t* out, float* part,
                          float* dpart, bool pdl, cudaStream_t st) {
-  const int rp = round16(c.r);
+  const int hr = kByRank ? 2 * c.r : c.r, rp = round16(hr);
   const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
   OuterArgs p{{}, {}, {}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
-              out, part, dpart, c.g.b, k, c.r, rp, plan.stages, plan.htiles, plan.dcol, plan.cols, plan.chunks == 1};
-  cudaError_t e = encode_rows(&p.hmap, h, c.g.b, c.r, c.r);
+              out, part, dpart, c.g.b, k, c.r, hr, rp, plan.stages, plan.htiles, plan.dcol, plan.cols, plan.chunks == 1};
+  cudaError_t e = encode_rows(&p.hmap, h, c.g.b, hr, hr);
   if (e == cudaSuccess && !kCodes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
   if (e == cudaSuccess && kDual)
     e = encode<3>(&p.wmap, c.bm, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 128, 1});
@@ -1774,10 +1791,10 @@ struct BackwardPlan {
 BackwardPlan backward_plan(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count, bool codes) {
   BackwardPlan s;
   s.dual = r <= 64;
-  s.a = outer_plan(b, count, int(m), int(r), codes, false);
+  s.a = outer_plan(b, count, int(m), int(2 * r), codes, false);
   s.b = outer_plan(b, count, int(n), int(r), false, s.dual);
   s.dh = 0;
-  s.pa = up256(size_t(b) * r * 2);
+  s.pa = up256(size_t(b) * 2 * r * 2);
   s.pb = s.pa + up256(size_t(2) * s.a.chunks * m * r * 4);
   s.pd = s.pb + up256(size_t(2) * s.b.chunks * n * r * 4);
   s.bytes = s.pd + (s.dual ? up256(size_t(s.b.slices) * b * r * 4) : 0);
@@ -1797,7 +1814,7 @@ cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
   if (c.g.b <= kSmallBatch) return launch_adapter_small(c, st);
   cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
   if (e != cudaSuccess) return e;
-  return launch_expand(c, false, c.h, c.bm, c.n, c.scale, c.y, true, st);
+  return launch_expand(c, false, c.h, c.r, c.bm, c.n, c.scale, c.y, true, st);
 }
 
 size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
@@ -1827,7 +1844,7 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
     if (e == cudaSuccess)
       e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, true, st)
                 : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, true, st);
-    if (e == cudaSuccess) e = launch_expand(c, true, dh, c.a, c.m, nullptr, c.dx, true, st);
+    if (e == cudaSuccess) e = launch_expand(c, true, dh, 2 * c.r, c.a, c.m, nullptr, c.dx, true, st);
     if (e != cudaSuccess) return e;
   }
   if (c.g.b > 0 && s.a.chunks == 1 && s.b.chunks == 1) return cudaSuccess;

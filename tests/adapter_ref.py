@@ -3,8 +3,9 @@ error: every rounding counted at half a step relative to the value it rounds.
 
 u = 2^-8 is half a BF16 step; f32 sums of k terms are bounded by (k + 32) 2^-23 times the
 sum of the terms' magnitudes (tensor cores may truncate an addition: a whole step of
-2^-23 each). BF16 intermediates: h (by definition of the operator), dh, and X when it
-comes from codes (code * scale is rounded once to BF16 where a kernel uses it so)."""
+2^-23 each). BF16 intermediates: h (by definition of the operator), dh (rounded once for dx;
+for dA in two terms, the second one the rounding of what the first left, so u^2), and X when
+it comes from codes (code * scale is rounded once to BF16 where a kernel uses it so)."""
 import torch
 
 U = 2.0 ** -8
@@ -65,13 +66,13 @@ def backward(dy, x, h, a, b, scale, ids, dx_base, codes):
         dh = s * (dyk @ bk)
         mag = s.abs() * (dyk.abs() @ bk.abs())
         e = (n + 34) * F * mag
-        dhe = e + U * (dh.abs() + e)
+        dhe, dhe2 = e + U * (dh.abs() + e), e + U * U * (dh.abs() + e)
         d = dx[rows] + dh @ ak
         de = dhe @ ak.abs() + (r + 34) * F * (dh.abs() @ ak.abs() + dx[rows].abs())
         dx[rows], dx_err[rows] = d, de + U * (d.abs() + de)
         da[k] = dh.T @ xk
         mag = dh.abs().T @ xk.abs()
-        e = dhe.T @ xk.abs() + (t + 34) * F * mag + (U * 1.01 * mag if codes else 0.0)
+        e = dhe2.T @ xk.abs() + (2 * t + 34) * F * mag + (U * 1.01 * mag if codes else 0.0)
         da_err[k] = e + U * (da[k].abs() + e)
         db[k] = s * (dyk.T @ hk)
         e = (t + 34) * F * s.abs() * (dyk.abs().T @ hk.abs())
