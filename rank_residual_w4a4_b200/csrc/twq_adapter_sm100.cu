@@ -33,7 +33,6 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a wait that lasts 2 s is a failure
 constexpr int kSms = 148;
 constexpr int kMaxSmem = 226 * 1024;  // dynamic; the kernels' static part is 1 KB
-constexpr int kSmallBatch = 512;
 
 // Site codes of the bounded waits.
 enum : int { kSiteEmpty = 61, kSiteFull, kSiteAccEmpty, kSiteDone, kSiteHEmpty, kSiteDrain, kSiteEnd };
@@ -90,7 +89,9 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// More arrivals of one thread, for a barrier that counts the threads of the other way to load.
+// The arrivals of a warp by its lane 0, for a barrier that counts the threads of the other way to
+// load. Each loading warp makes its own: a warp that only waited, for its turn in the ring, could
+// fall two turns behind the one that issues the copies, and then wait for a phase long past.
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
                "r"(count)
@@ -118,6 +119,18 @@ __device__ __forceinline__ void tma_load_once(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
       : "memory");
+}
+// 64 columns of `rows` rows from row y on, in boxes of 128 rows or, for a part of that, of 16: the
+// bytes that this will complete, and the copies.
+__device__ __forceinline__ uint32_t rows_bytes(int rows) { return (rows + 15) / 16 * 2048; }
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, const CUtensorMap* map16,
+                                              uint64_t* bar, int x, int y, int rows) {
+  const uint64_t once = read_once_policy();
+  if (rows > 112) {
+    tma_load_once(dst, map, bar, x, y, once);
+  } else {
+    for (int i = 0; i < rows; i += 16) tma_load_once(dst + i * 128, map16, bar, x, y + i, once);
+  }
 }
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
                                           int y, int z) {
@@ -319,7 +332,7 @@ struct RowsAhead {
 
 // ------------------------------------------------------------------ shrink
 struct ShrinkArgs {
-  CUtensorMap map;   // Z: 128 rows x 64 columns
+  CUtensorMap map, map16;  // Z: 128 or 16 rows x 64 columns
   CUtensorMap wmap;  // W: rp rows x 64 of k, or (kTrans) 64 rows of k x 64 of r
   const int4* tiles;
   const int32_t* order;
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   const uint32_t sz = smem_u32(smem);
   const uint32_t sw = sz + p.stages * kPer * 16384;
   const int wbytes = kTrans ? (p.rp + 63) / 64 * 8192 : p.rp * 128;
-  // rows beyond a partial tile's end then belong to others; their sums are not stored
+  // rows beyond a partial tile's end then hold anything; their sums are not stored
   const bool tma = !kCodes && t.w >= 0;
   const int groups = (p.k / 128 - rank + splits - 1) / splits;
   const int steps = groups * 2 / kPer;
@@ -400,9 +413,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     }
   };
   auto load_both = [&](int step, int slot) {
-    mbar_arrive_expect_tx(&s_full[slot], (tma ? 16384 : 0) + wbytes);
-    if (tma)
-      tma_load_once(sz + slot * 16384, &p.map, &s_full[slot], column(step), t.w, read_once_policy());
+    mbar_arrive_expect_tx(&s_full[slot], (tma ? rows_bytes(t.z) : 0) + wbytes);
+    if (tma) tma_load_rows(sz + slot * 16384, &p.map, &p.map16, &s_full[slot], column(step), t.w, t.z);
     load_w(step, slot, &s_full[slot]);
   };
   if (tid == 288) {
@@ -627,7 +639,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 
 // ------------------------------------------------------------------ expand
 struct ExpandArgs {
-  CUtensorMap map;   // base: 128 rows x 64 columns
+  CUtensorMap map, map16;  // base: 128 or 16 rows x 64 columns
   CUtensorMap hmap;  // H: 128 rows x 64 of r
   CUtensorMap wmap;  // W: 64 columns in accumulator order x 64 of r, or (kTrans) rp of r x 64 columns
   const int4* tiles;
@@ -784,8 +796,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
                     (!p.base || warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull));
             if (!alive) break;
             tc_fence_after();
+            const bool any = (warp & 3) * 32 < ra.count;  // rows of the tile among this warp's 32
+            if (!any && lane == 0) {
+              mbar_arrive(&s_free[slot]);
+              mbar_arrive(&s_bfree[bs]);
+            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+              if (!any) break;
               uint32_t v[2][16];
               const uint32_t ta =
                   tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + half * 32;
@@ -895,8 +913,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               mbar_arrive_expect_tx(&s_hfull[hs], kt * 16384);
               for (int c = 0; c < kt; ++c)
                 tma_load(sh + (hs * kt + c) * 16384, &p.hmap, &s_hfull[hs], c * 64, ra.run);
-              mbar_arrive_n(&s_hfull[hs], 63);
             }
+            if (lane == 0) mbar_arrive_n(&s_hfull[hs], tid == 288 ? 31 : 32);
           } else {
             for (int c = ch; c < chunks; c += 8)
 #pragma unroll
@@ -919,10 +937,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             }
             if (ra.run >= 0) {
               if (tid == 288) {
-                mbar_arrive_expect_tx(&s_bfull[bs], 16384);
-                tma_load_once(sb + bs * 16384, &p.map, &s_bfull[bs], u * 64, ra.run, read_once_policy());
-                mbar_arrive_n(&s_bfull[bs], 63);
+                mbar_arrive_expect_tx(&s_bfull[bs], rows_bytes(ra.count));
+                tma_load_rows(sb + bs * 16384, &p.map, &p.map16, &s_bfull[bs], u * 64, ra.run, ra.count);
               }
+              if (lane == 0) mbar_arrive_n(&s_bfull[bs], tid == 288 ? 31 : 32);
             } else {
               const uint16_t* src = p.base + u * 64 + ch * 8;
 #pragma unroll
@@ -1183,16 +1201,17 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
             const uint64_t once = read_once_policy();
             tma_load_once(zs, &p.map, &s_full[slot], (blk0 + lblk) * 128, ra.run, once);
             tma_load_once(zs + 16384, &p.map, &s_full[slot], (blk0 + lblk) * 128 + 64, ra.run, once);
-            mbar_arrive_n(&s_full[slot], 255);
           }
+          if (lane == 0) mbar_arrive_n(&s_full[slot], tid == 0 ? 31 : 32);
         } else {
 #pragma unroll
           for (int j = 0; j < kRows; ++j)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-              cp16(zs + half * 16384 + sw128(r0 + kZ * 4 * j, ch),
-                   p.z + max(ra.row[j], 0) * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8,
-                   ra.row[j] >= 0);
+              if (r0 + kZ * 4 * j < (ra.count + 15) / 16 * 16)
+                cp16(zs + half * 16384 + sw128(r0 + kZ * 4 * j, ch),
+                     p.z + max(ra.row[j], 0) * p.ldz + (blk0 + lblk) * 128 + half * 64 + ch * 8,
+                     ra.row[j] >= 0);
           cp_arrive(&s_full[slot]);
         }
         advance();
@@ -1211,8 +1230,11 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
       bool alive = true;
       bool fresh = true;
       int run_end = min(end, p.first128[tiles[begin].x + 1]);
+      int rows = tiles[begin].z;
       for (int tile = begin; tile < end && alive; ++tile) {
         const uint32_t hb = desc_mn(sh + hs * hbytes, 16384);
+        const int ksteps = (rows + 15) / 16;
+        if (tile + 1 < end) rows = tiles[tile + 1].z;
         alive = wait(&s_hfull[hs], hphase, &s_abort, kSiteFull);
         if (!alive) break;
         for (int b = 0; b < nb; ++b) {
@@ -1225,7 +1247,8 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
           const uint32_t za = desc_mn(sz + slot * kStage, 16384), d = tmem + b * p.rp;
           mma(d, za, hb, idesc, !fresh);
 #pragma unroll
-          for (int k = 1; k < 8; ++k) mma(d, za + k * 128, hb + k * 128, idesc, true);  // 16 rows each
+          for (int k = 1; k < 8; ++k)  // 16 rows each, as far as the tile has any
+            if (k < ksteps) mma(d, za + k * 128, hb + k * 128, idesc, true);
           mma_commit(&s_empty[slot]);
           if (++slot == stages) {
             slot = 0;
@@ -1389,12 +1412,13 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
           mbar_arrive_expect_tx(&s_hfull[hs], hbytes);
           for (int c = 0; c < hbytes / 16384; ++c)
             tma_load(sh + hs * hbytes + c * 16384, &p.hmap, &s_hfull[hs], c * 64, ra.run);
-          mbar_arrive_n(&s_hfull[hs], 63);
         }
+        if (lane == 0) mbar_arrive_n(&s_hfull[hs], l == 0 ? 31 : 32);
       } else {
         for (int c = hc; c < rchunks; c += 8)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
+            if (hr + 8 * j >= (ra.count + 15) / 16 * 16) break;
             const bool in = ra.row[j] >= 0 && c * 8 < p.hr;
             cp16(sh + hs * hbytes + (c >> 3) * 16384 + sw128(hr + 8 * j, hc),
                  p.h + (in ? static_cast<int64_t>(ra.row[j]) * p.hr + c * 8 : 0), in);
@@ -1407,7 +1431,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
       }
       const int group = ra.group;
       ra.advance();
-      if constexpr (kDual) {
+      if (kDual && warp == kLoad) {  // one warp alone, as the copies of W are its own
         for (int b = 0; b < nb; ++b, ++step) {
           if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
             alive = false;
@@ -1647,7 +1671,7 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
                           const uint16_t* w, const float* scale, uint16_t* out, cudaStream_t st) {
   const bool codes = !trans && c.xq8;
   const int rp = round16(c.r);
-  ShrinkArgs p{{}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
+  ShrinkArgs p{{}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
                codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, trans, 0, 0};
   // Two blocks per SM: 110 KB each, of which the parts need 128 x (rp + 4) fp32. As many W as Z
   // stages; on codes (Z is converted from its own ring) one or two groups of Z and the rest of W,
@@ -1672,6 +1696,7 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   cudaError_t e = trans ? encode<3>(&p.wmap, w, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 64, 1})
                         : encode_rows(&p.wmap, w, int64_t(c.g.count) * c.r, k, k, rp);
   if (e == cudaSuccess && !codes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
+  if (e == cudaSuccess && !codes) e = encode_rows(&p.map16, z, c.g.b, k, ldz, 16);
   if (e != cudaSuccess) return e;
   return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
 }
@@ -1679,7 +1704,7 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
 cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, int ldh, const uint16_t* w,
                           int n, const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r), kt = (rp + 63) / 64;
-  ExpandArgs p{{}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, scale, c.base, y,
+  ExpandArgs p{{}, {}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, scale, c.base, y,
                first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, ldh, 0, 0, 0, 0, 1};
   // Two blocks per SM, 112 KB each: 4 stages of W and of base and a second H tile as far as they
   // fit (W's copies take 2 us and more while HBM is busy), 2 of each beyond rank 64.
@@ -1698,6 +1723,7 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, i
                         {64, 2, 4, 4, 2});
   if (e == cudaSuccess) e = encode_rows(&p.hmap, h, c.g.b, r, ldh);
   if (e == cudaSuccess && c.base) e = encode_rows(&p.map, c.base, c.g.b, n, n);
+  if (e == cudaSuccess && c.base) e = encode_rows(&p.map16, c.base, c.g.b, n, n, 16);
   if (e != cudaSuccess) return e;
   // Parts of a row tile: 4 to 12 units, so that the last turn of the blocks is nearly full (an
   // item costs about one unit more than it has, for its H).
@@ -1811,7 +1837,10 @@ cudaError_t read_and_clear_adapter_status(int* code) {
 }
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
-  if (c.g.b <= kSmallBatch) return launch_adapter_small(c, st);
+  // The one-launch kernel's time goes with rows x rank (it reads an adapter again for every 16
+  // rows). At 4096 x 4096 it meets the two kernels at about 850 rows of rank 16 (13.5 us), 380 of
+  // rank 64 (14 us) and 150 of rank 128 (14.5 us); at 4096 x 14336 at 600, 220 and 120.
+  if (int64_t(c.g.b) * std::max(c.r, 16) <= 12288) return launch_adapter_small(c, st);
   cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
   if (e != cudaSuccess) return e;
   return launch_expand(c, false, c.h, c.r, c.bm, c.n, c.scale, c.y, true, st);

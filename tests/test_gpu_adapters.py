@@ -332,3 +332,19 @@ def test_gradients_against_differences(twq, device, b):
                   for y, h in ((y0, h0), (y1, h1))) + 2 * ((grad.double() * step) ** 2).sum()
         dev = ref.U / 3 ** 0.5 * var.sqrt().item()
         assert abs(left - right) <= 6 * dev, (name, left, right, dev)
+
+
+@pytest.mark.parametrize("b,m,n,r,kind", [(1700, 512, 6400, 64, "runs"), (1300, 2048, 512, 16, "mixed"),
+                                          (900, 512, 2048, 128, "runs")])
+def test_many_calls_give_equal_bits(twq, device, b, m, n, r, kind):
+    """Hundreds of calls in a row, whose warps meet at other times in each: no wait runs out
+    and every call gives the first one's bits."""
+    c = Case(twq, device, b, m, n, r, 4, kind, False)
+    want = (c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+            + c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base))
+    for _ in range(10):
+        for _ in range(30):
+            got = (c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+                   + c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base))
+        assert twq.device_status() == 0
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
