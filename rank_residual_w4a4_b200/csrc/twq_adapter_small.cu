@@ -58,16 +58,17 @@ __device__ __forceinline__ void st16(void* p, uint4 v) {
                : "memory");
 }
 
-// 8 codes times their scale, rounded to BF16 (the type that the activation had).
-__device__ __forceinline__ uint4 dequant8(uint2 q, float s) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int w = static_cast<int>(i < 2 ? q.x : q.y) >> ((i & 1) * 16);
-    o[i] = pack2(static_cast<float>(static_cast<int8_t>(w)) * s,
-                 static_cast<float>(static_cast<int8_t>(w >> 8)) * s);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+// 8 codes as BF16, which holds them exactly: |c| <= 127 or -128. With 0x43 above it a byte's low
+// seven bits make 128 + (c & 127), and its sign bit the 128 or 256 to take off.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t select) {
+  const uint32_t t = __byte_perm(w, 0x43434343u, select);
+  uint32_t v = t & 0xFF7FFF7Fu, off = t & 0xFF80FF80u;
+  const __nv_bfloat162 d =
+      __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), *reinterpret_cast<__nv_bfloat162*>(&off));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint4 codes8(uint2 q) {
+  return make_uint4(codes2(q.x, 0x4140), codes2(q.x, 0x4342), codes2(q.y, 0x4140), codes2(q.y, 0x4342));
 }
 
 // kR: r rounded up to 16, 32, 64 or 128; ranks from r on are zeros.
@@ -167,11 +168,18 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if constexpr (kCodes) x0[u] = dequant8(q0[u], s0[u]), x1[u] = dequant8(q1[u], s1[u]);
+      if constexpr (kCodes) x0[u] = codes8(q0[u]), x1[u] = codes8(q1[u]);
 #pragma unroll
       for (int j = 0; j < kTiles; ++j) {
-        mma16816(acc[j], x0[u].x, x1[u].x, x0[u].y, x1[u].y, w[u][j].x, w[u][j].y);
-        mma16816(acc[j], x0[u].z, x1[u].z, x0[u].w, x1[u].w, w[u][j].z, w[u][j].w);
+        // codes: the chunk's sums of code times weight, then each row's scale in fp32
+        float part[4] = {};
+        float(&d)[4] = kCodes ? part : acc[j];
+        mma16816(d, x0[u].x, x1[u].x, x0[u].y, x1[u].y, w[u][j].x, w[u][j].y);
+        mma16816(d, x0[u].z, x1[u].z, x0[u].w, x1[u].w, w[u][j].z, w[u][j].w);
+        if constexpr (kCodes) {
+          acc[j][0] = fmaf(s0[u], part[0], acc[j][0]), acc[j][1] = fmaf(s0[u], part[1], acc[j][1]);
+          acc[j][2] = fmaf(s1[u], part[2], acc[j][2]), acc[j][3] = fmaf(s1[u], part[3], acc[j][3]);
+        }
       }
     }
   }
