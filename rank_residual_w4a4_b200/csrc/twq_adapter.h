@@ -22,8 +22,19 @@ inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
   return static_cast<int>(cap < b ? cap : b);
 }
 
+// The forward pass takes the one-launch kernel, on 16-row tiles, for batches up to this many rows
+// times rank (from 16 on): its time goes with that, since it reads an adapter again for every 16
+// rows. At 4096 x 4096 it meets the two kernels at about 850 rows of rank 16 (13.5 us), 380 of
+// rank 64 (14 us) and 150 of rank 128 (14.5 us); at 4096 x 14336 at 600, 220 and 120.
+constexpr int64_t kSmallWork = 12288;
+inline bool small_batch(int64_t b, int64_t r) { return b * (r > 16 ? r : 16) <= kSmallWork; }
+// Room for 16-row tiles: none where no rank makes the batch a small one.
+inline int small_tiles_cap(int64_t b, int64_t count) {
+  return small_batch(b, 1) ? row_tiles_cap(b, count, 16) : 0;
+}
+
 // tiles: {number of 16-row tiles, number of 128-row tiles, 0, 0}, then room for
-// row_tiles_cap(b, count, 16) entries of the first list and ..., 128) of the second;
+// small_tiles_cap(b, count) entries of the first list and row_tiles_cap(b, count, 128) of the second;
 // an entry is {group or -1, first position in order, rows, first row where the rows follow one
 // another in the batch, else -1}. After the entries: for each group, then for the rows without
 // one, the 128-row tiles before it (count + 1 integers).
@@ -35,7 +46,7 @@ struct RowGroupsView {
 };
 
 inline int32_t* first128_of(const RowGroupsView& g) {
-  return reinterpret_cast<int32_t*>(g.tiles + 1 + row_tiles_cap(g.b, g.count, 16) +
+  return reinterpret_cast<int32_t*>(g.tiles + 1 + small_tiles_cap(g.b, g.count) +
                                     row_tiles_cap(g.b, g.count, 128));
 }
 

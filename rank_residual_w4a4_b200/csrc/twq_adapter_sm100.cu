@@ -1671,7 +1671,7 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
                           const uint16_t* w, const float* scale, uint16_t* out, cudaStream_t st) {
   const bool codes = !trans && c.xq8;
   const int rp = round16(c.r);
-  ShrinkArgs p{{}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), z, ldz,
+  ShrinkArgs p{{}, {}, {}, c.g.tiles, c.g.order, small_tiles_cap(c.g.b, c.g.count), z, ldz,
                codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, trans, 0, 0};
   // Two blocks per SM: 110 KB each, of which the parts need 128 x (rp + 4) fp32. As many W as Z
   // stages; on codes (Z is converted from its own ring) one or two groups of Z and the rest of W,
@@ -1704,7 +1704,7 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
 cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, int ldh, const uint16_t* w,
                           int n, const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
   const int rp = round16(c.r), kt = (rp + 63) / 64;
-  ExpandArgs p{{}, {}, {}, {}, c.g.tiles, c.g.order, row_tiles_cap(c.g.b, c.g.count, 16), h, scale, c.base, y,
+  ExpandArgs p{{}, {}, {}, {}, c.g.tiles, c.g.order, small_tiles_cap(c.g.b, c.g.count), h, scale, c.base, y,
                first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, ldh, 0, 0, 0, 0, 1};
   // Two blocks per SM, 112 KB each: 4 stages of W and of base and a second H tile as far as they
   // fit (W's copies take 2 us and more while HBM is busy), 2 of each beyond rank 64.
@@ -1792,7 +1792,7 @@ cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint
                          int k, const uint16_t* h, const float* scale, uint16_t* out, float* part,
                          float* dpart, bool pdl, cudaStream_t st) {
   const int hr = kByRank ? 2 * c.r : c.r, rp = round16(hr);
-  const int cap16 = row_tiles_cap(c.g.b, c.g.count, 16);
+  const int cap16 = small_tiles_cap(c.g.b, c.g.count);
   OuterArgs p{{}, {}, {}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
               out, part, dpart, c.g.b, k, c.r, hr, rp, plan.stages, plan.htiles, plan.dcol, plan.cols, plan.chunks == 1};
   cudaError_t e = encode_rows(&p.hmap, h, c.g.b, hr, hr);
@@ -1837,10 +1837,7 @@ cudaError_t read_and_clear_adapter_status(int* code) {
 }
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
-  // The one-launch kernel's time goes with rows x rank (it reads an adapter again for every 16
-  // rows). At 4096 x 4096 it meets the two kernels at about 850 rows of rank 16 (13.5 us), 380 of
-  // rank 64 (14 us) and 150 of rank 128 (14.5 us); at 4096 x 14336 at 600, 220 and 120.
-  if (int64_t(c.g.b) * std::max(c.r, 16) <= 12288) return launch_adapter_small(c, st);
+  if (small_batch(c.g.b, c.r)) return launch_adapter_small(c, st);
   cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
   if (e != cudaSuccess) return e;
   return launch_expand(c, false, c.h, c.r, c.bm, c.n, c.scale, c.y, true, st);

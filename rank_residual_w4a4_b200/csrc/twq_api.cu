@@ -449,7 +449,7 @@ twq_status twq_row_groups_sizes(int64_t b, int64_t count, size_t bytes_out[3]) {
   if (s != TWQ_OK) return s;
   bytes_out[0] = static_cast<size_t>(b) * 4;
   bytes_out[1] = static_cast<size_t>(count + 1) * 4;
-  bytes_out[2] = 16 * (1 + static_cast<size_t>(twq::row_tiles_cap(b, count, 16)) +
+  bytes_out[2] = 16 * (1 + static_cast<size_t>(twq::small_tiles_cap(b, count)) +
                        static_cast<size_t>(twq::row_tiles_cap(b, count, 128))) +
                  4 * static_cast<size_t>(count + 1);
   return TWQ_OK;

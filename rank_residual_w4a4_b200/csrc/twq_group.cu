@@ -52,6 +52,20 @@ __device__ __forceinline__ int find_key(const int* first, int n, int t) {
   return lo;
 }
 
+// The keys of rows at, at + 32, ... (-1 from hi on). Their loads go out together: one by one, each
+// costs its latency, 16 times over and twice for 16384 rows.
+constexpr int kBatch = 16;
+__device__ __forceinline__ void load_keys(const int32_t* ids, int at, int hi, int count, int (&key)[kBatch]) {
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int i = at + 32 * u;
+    key[u] = i < hi ? __ldg(ids + i) : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u)
+    if (at + 32 * u < hi && (key[u] < 0 || key[u] >= count)) key[u] = count;
+}
+
 // Keys are 0 .. count, key `count` collecting every row whose id is outside [0, count).
 // Warp w takes the rows [w * chunk, (w + 1) * chunk) in order: lanes with equal keys
 // find each other by a warp match, so a row's rank among its warp's rows of that key
@@ -76,15 +90,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int lo = min(b, warp * chunk), hi = warp < warps ? min(b, lo + chunk) : lo;
   T* mine = cnt + (warp < warps ? warp : 0) * keys;
-  for (int i = lo; i < hi; i += 32) {
-    int key = -1;
-    if (i + lane < hi) {
-      const int id = __ldg(ids + i + lane);
-      key = (id < 0 || id >= count) ? count : id;
+  int key[kBatch];
+  for (int i = lo; i < hi; i += 32 * kBatch) {
+    load_keys(ids, i + lane, hi, count, key);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (i + 32 * u >= hi) break;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, key[u]);
+      if (key[u] >= 0 && lane == __ffs(same) - 1) mine[key[u]] = mine[key[u]] + __popc(same);
+      __syncwarp();
     }
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
-    if (key >= 0 && lane == __ffs(same) - 1) mine[key] = mine[key] + __popc(same);
-    __syncwarp();
   }
   __syncthreads();
 
@@ -126,20 +141,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  for (int i = lo; i < hi; i += 32) {
-    int key = -1;
-    if (i + lane < hi) {
-      const int id = __ldg(ids + i + lane);
-      key = (id < 0 || id >= count) ? count : id;
+  for (int i = lo; i < hi; i += 32 * kBatch) {
+    // a warp's rows are often few enough for the keys to be at hand still
+    if (hi - lo > 32 * kBatch) load_keys(ids, i + lane, hi, count, key);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (i + 32 * u >= hi) break;
+      const int k = key[u];
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
+      const int at = k >= 0 ? static_cast<int>(mine[k]) : 0;
+      __syncwarp();
+      if (k >= 0) {
+        order[start[k] + at + __popc(same & ((1u << lane) - 1u))] = i + 32 * u + lane;
+        if (lane == __ffs(same) - 1) mine[k] = static_cast<T>(at + __popc(same));
+      }
+      __syncwarp();
     }
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
-    const int at = key >= 0 ? static_cast<int>(mine[key]) : 0;
-    __syncwarp();
-    if (key >= 0) {
-      order[start[key] + at + __popc(same & ((1u << lane) - 1u))] = i + lane;
-      if (lane == __ffs(same) - 1) mine[key] = static_cast<T>(at + __popc(same));
-    }
-    __syncwarp();
   }
 
   // Tile lists. The rows of a group ascend, so they follow one another in the batch where the
@@ -150,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = order[at], last = order[at + rows - 1];
     return make_int4(k < count ? k : -1, at, rows, last - first == rows - 1 ? first : -1);
   };
-  for (int t = tid; t < sum[1]; t += kThreads) {
+  for (int t = tid; cap16 > 0 && t < sum[1]; t += kThreads) {
     const int k = find_key(first16, keys, t);
     tiles[1 + t] = make_tile(k, start[k] + (t - first16[k]) * 16, 16);
   }
@@ -173,7 +190,7 @@ cudaError_t launch(const int32_t* ids, int b, const RowGroupsView& g, cudaStream
   if (e != cudaSuccess) return e;
   group_rows_kernel<T><<<1, kThreads, bytes, st>>>(
       ids, b, g.count, warps, chunk, g.order, g.offsets, g.tiles, first128_of(g),
-      row_tiles_cap(b, g.count, 16));
+      small_tiles_cap(b, g.count));
   return cudaGetLastError();
 }
 

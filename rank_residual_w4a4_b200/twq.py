@@ -9,6 +9,7 @@ if the library is missing or a tensor is not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -511,18 +512,26 @@ def unfused_linear_noalloc(xq, sx, w: Weights, y=None, stream=None):
     return _layer("twq_unfused_linear_noalloc", xq, sx, w, y, stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _group_words(b: int, count: int):
+    """First words of the offsets and the tiles behind the order, and all words (parts are
+    16-byte aligned)."""
+    arr = (ctypes.c_size_t * 3)()
+    _check(load().twq_row_groups_sizes(b, count, arr), "twq_row_groups_sizes")
+    o = (arr[0] + 15) // 16 * 4
+    t = o + (arr[1] + 15) // 16 * 4
+    return o, t, t + arr[2] // 4
+
+
 class RowGroups:
     """Rows of a batch grouped by adapter (group_rows): `order`, the b row numbers sorted
     by id with the rows without adapter last, and `offsets` (count + 1), both int32;
     group g is order[offsets[g]:offsets[g + 1]]."""
 
     def __init__(self, b: int, count: int, device):
-        arr = (ctypes.c_size_t * 3)()
-        _check(load().twq_row_groups_sizes(b, count, arr), "twq_row_groups_sizes")
         self.b, self.count = b, count
-        self._o = (arr[0] + 15) // 16 * 4   # offsets' first word; 16-byte aligned parts
-        self._t = self._o + (arr[1] + 15) // 16 * 4
-        self._buf = torch.empty(self._t + arr[2] // 4, dtype=torch.int32, device=device)
+        self._o, self._t, words = _group_words(b, count)
+        self._buf = torch.empty(words, dtype=torch.int32, device=device)
         p = self._buf.data_ptr()
         self._c = _RowGroups(b, count, p, p + 4 * self._o, p + 4 * self._t)
         self._ref = ctypes.byref(self._c)

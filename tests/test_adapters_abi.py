@@ -39,6 +39,8 @@ def test_group_sizes_hold_every_tile(lib, b, count):
     assert arr[0] == 4 * b and arr[1] == 4 * (count + 1)
     need = 1
     for rows in (16, 128):
+        if rows == 16 and b > 768:  # no forward pass takes the small tiles then
+            continue
         keys = min(b, count + 1)
         need += (keys - 1) + -(-(b - keys + 1) // rows) if b else 0
     assert arr[2] >= 16 * need
