@@ -723,7 +723,6 @@ __device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
 template <bool kTrans>
 __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_constant__ ExpandArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // no other shared memory: two blocks fill an SM
-  if (kTrans) pdl_launch_dependents();  // the backward pass: another kernel of the call follows
   const int kt = (p.rp + 63) / 64;  // 64-wide tiles of the reduction
   const uint32_t sh = smem_u32(smem);
   const uint32_t sw = sh + p.hslots * kt * 16384;
@@ -1031,7 +1030,7 @@ struct OuterArgs {
   int stages, htiles; // Z stages, H tiles in shared memory
   int dcol;           // kDual: first tensor-memory column of the two row accumulators
   uint32_t tmem_cols;
-  bool zeros;         // one chunk: no finish kernel follows, which would write them
+  bool zeros;         // one chunk: no sum kernel follows, which would write them
 };
 
 // Warps: 8 that load Z (16 convert codes: 8 of them took 0.9 us for a block that HBM delivers in
@@ -1051,7 +1050,7 @@ __host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles
 // A slice of Z's 128-column blocks (blockIdx.x), the row tiles of chunk blockIdx.y. Tiles of one
 // group form a run, summed in tensor memory (lane = column of Z, column = rank). A run that
 // is its whole group is rounded into `out`; one that the chunk's ends cut leaves its fp32
-// sums in the chunk's slot (0: the run starts the chunk, else 1) for the finish kernel, in the
+// sums in the chunk's slot (0: the run starts the chunk, else 1) for the sum kernel, in the
 // order [block][rank / 4][column of the block][4], in which a warp writes 512 bytes at a time
 // (rows of the output would be 32 pieces in 32 lines: 6 us a run at 768 columns of rank 64).
 // kByRank (dA): H is dh in two BF16 terms side by side, 2 r accumulator columns, added at the end:
@@ -1456,46 +1455,23 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   if (warp == kMma) tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// dh from the slices' parts, added in slice order, as rows of 2 r (store_value). A thread: 4 ranks
-// of a position.
-struct ReduceArgs {
-  const float* dpart;  // slices x r / 4 x b x 4
-  const int32_t *order, *offsets;
+// What the outer products leave to be added up, in one launch: dh from its slices' parts, and the
+// groups of dA and dB that the chunks cut. Right after the kernel that wrote them, while the parts
+// are in L2 (at the end of the call they were not: 18 us instead of 11 at 8192 x 5120 x 25600).
+struct SumArgs {
+  const int4* tiles;
+  const int32_t *order, *offsets, *first128;
+  int b, count, r;
+  // dh, as rows of 2 r (store_value), from slices x r / 4 x b x 4
+  const float* dpart;
   uint16_t* dh;
-  int64_t b;
-  int count, r, slices;
-};
-
-__global__ void __launch_bounds__(256) reduce_kernel(const ReduceArgs p) {
-  pdl_launch_dependents();
-  const int64_t pos = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (pos >= p.offsets[p.count]) {
-    pdl_wait();
-    return;
-  }
-  const int64_t row = p.order[pos];
-  pdl_wait();
-  const float* part = p.dpart + (blockIdx.y * p.b + pos) * 4;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int s = 0; s < p.slices; ++s) {
-    const float4 o = __ldg(reinterpret_cast<const float4*>(part + s * p.b * p.r));
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-  }
-  store_value(p.dh, row, p.r, blockIdx.y * 4, v, true);
-}
-
-// The groups that the outer kernel's chunks cut: their parts, added in chunk order; and
-// zeros for the groups without rows. A thread: 8 ranks of a column.
-struct FinishArgs {
-  const int32_t* first128;
-  int count;
+  int slices, dh_blocks;
+  // parts [block][rank / 4][column of the block][4]; out count x r x k (dA) or count x k x r (dB)
   struct {
     const float* part;
     uint16_t* out;
-    int k, chunks;
-  } side[2];  // dA (count x r x k), dB (count x k x r)
-  int r;
+    int k, chunks, blocks;  // blocks of threads for each group
+  } side[2];
 };
 
 // Largest c with chunk_begin(c) <= tile.
@@ -1505,51 +1481,73 @@ __device__ __forceinline__ int chunk_of(int tile, int chunks, int tiles) {
   return c;
 }
 
-__global__ void __launch_bounds__(256) finish_kernel(const FinishArgs p) {
-  pdl_wait();
-  const bool by_rank = blockIdx.z == 0;
-  const int k = by_rank ? p.side[0].k : p.side[1].k, all = by_rank ? p.side[0].chunks : p.side[1].chunks;
-  if (all == 1) return;  // written by the outer kernel
-  const int oct = p.r / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+// A thread: 4 ranks of a position; slices in order.
+__device__ __forceinline__ void sum_dh(const SumArgs& p, int block) {
+  const int wide = (p.b + 255) / 256, quad = block / wide;
+  const int64_t pos = static_cast<int64_t>(block - quad * wide) * 256 + threadIdx.x;
+  if (pos >= p.offsets[p.count]) return;
+  const int64_t row = p.order[pos], step = static_cast<int64_t>(p.b) * p.r;
+  const float* part = p.dpart + (static_cast<int64_t>(quad) * p.b + pos) * 4;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < p.slices; ++s) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(part + s * step));
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  store_value(p.dh, row, p.r, quad * 4, v, true);
+}
+
+// A thread: 8 ranks of a column of group g; chunks in order. Zeros for a group without rows.
+template <bool kByRank>
+__device__ __forceinline__ void sum_group(const SumArgs& p, int block) {
+  const auto& side = p.side[kByRank ? 0 : 1];
+  const int g = block / side.blocks, oct = p.r / 8;
+  const int64_t i = static_cast<int64_t>(block - g * side.blocks) * 256 + threadIdx.x;
   const int64_t blk = i / (oct * 128);
-  if (blk >= k / 128) return;
+  if (blk >= side.k / 128) return;
   const int rest = static_cast<int>(i - blk * (oct * 128));
   const int c = rest / 128 * 8, j = static_cast<int>(blk) * 128 + rest % 128;
-  const int g = blockIdx.y, total = p.first128[p.count];
-  const int gb = p.first128[g], ge = p.first128[g + 1];
-  const int64_t size = static_cast<int64_t>(k) * p.r;
+  const int gb = p.first128[g], ge = p.first128[g + 1], total = p.first128[p.count];
+  const int64_t size = static_cast<int64_t>(side.k) * p.r;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = v;
   if (gb < ge) {
-    const int chunks = min(all, total);
+    const int chunks = min(side.chunks, total);
     const int c0 = chunk_of(gb, chunks, total), c1 = chunk_of(ge - 1, chunks, total);
     if (c0 == c1) return;  // inside one chunk: already written
-    // parts: [block][rank / 4][column of the block][4]; the group's run is a chunk's second one
-    // only where the group starts inside it
-    const float* part = (by_rank ? p.side[0].part : p.side[1].part) + (blk * (p.r / 4) + c / 4) * 512 +
-                        rest % 128 * 4;
+    // the group's run is a chunk's second one only where the group starts inside it
+    const float* part = side.part + (blk * (p.r / 4) + c / 4) * 512 + rest % 128 * 4;
     const float* first = part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size;
-    v = __ldg(reinterpret_cast<const float4*>(first));
-    w = __ldg(reinterpret_cast<const float4*>(first + 512));
+    v = __ldcg(reinterpret_cast<const float4*>(first));
+    w = __ldcg(reinterpret_cast<const float4*>(first + 512));
 #pragma unroll 4
     for (int x = c0 + 1; x <= c1; ++x) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(part + 2 * x * size));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(part + 2 * x * size + 512));
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size + 512));
       v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
       w.x += b.x, w.y += b.y, w.z += b.z, w.w += b.w;
     }
   }
   const uint32_t o[4] = {pack2(v.x, v.y), pack2(v.z, v.w), pack2(w.x, w.y), pack2(w.z, w.w)};
-  uint16_t* out = (by_rank ? p.side[0].out : p.side[1].out) + g * size;
-  if (by_rank) {
+  uint16_t* out = side.out + g * size;
+  if (kByRank) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      out[static_cast<int64_t>(c + 2 * e) * k + j] = static_cast<uint16_t>(o[e]);
-      out[static_cast<int64_t>(c + 2 * e + 1) * k + j] = static_cast<uint16_t>(o[e] >> 16);
+      out[static_cast<int64_t>(c + 2 * e) * side.k + j] = static_cast<uint16_t>(o[e]);
+      out[static_cast<int64_t>(c + 2 * e + 1) * side.k + j] = static_cast<uint16_t>(o[e] >> 16);
     }
   } else {
     *reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * p.r + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+}
+
+__global__ void __launch_bounds__(256) sum_kernel(const SumArgs p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  int block = blockIdx.x;
+  if (block < p.dh_blocks) return sum_dh(p, block);
+  block -= p.dh_blocks;
+  if (block < p.side[0].blocks * p.count) return sum_group<true>(p, block);
+  sum_group<false>(p, block - p.side[0].blocks * p.count);
 }
 
 // -------------------------------------------------------------------- host
@@ -1746,7 +1744,7 @@ struct OuterPlan {
   int slices, chunks, stages, htiles, dcol;
   uint32_t cols;
 };
-// What a block could have moved in the time of one more launch (the finish kernel's).
+// What a block could have moved in the time of one more launch (the sum kernel's).
 constexpr double kLaunchBytes = 110e3;
 
 // hr: columns of H.
@@ -1855,31 +1853,34 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
   float* pa = reinterpret_cast<float*>(ws + s.pa);
   float* pb = reinterpret_cast<float*>(ws + s.pb);
   float* pd = reinterpret_cast<float*>(ws + s.pd);
-  cudaError_t e = cudaSuccess;
-  if (c.g.b > 0) {
-    if (s.dual) {
-      e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, false, st);
-      if (e != cudaSuccess) return e;
-      const ReduceArgs ra{pd, c.g.order, c.g.offsets, dh, c.g.b, c.g.count, c.r, s.b.slices};
-      e = launch(reduce_kernel, dim3(static_cast<unsigned>((c.g.b + 255) / 256), c.r / 4), 256, 0, 1, true, ra, st);
-    } else {
-      e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
-      if (e == cudaSuccess)
-        e = launch_outer<false, false, false>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, nullptr, true, st);
-    }
+  const SumArgs none{c.g.tiles, c.g.order, c.g.offsets, first128_of(c.g), c.g.b, c.g.count, c.r,
+                     pd, dh, s.b.slices, 0, {{pa, c.da, c.m, s.a.chunks, 0}, {pb, c.db, c.n, s.b.chunks, 0}}};
+  auto sum = [&](bool with_dh, bool with_a, bool with_b, bool pdl) {
+    SumArgs p = none;
+    if (with_dh) p.dh_blocks = (c.g.b + 255) / 256 * (c.r / 4);
+    if (with_a) p.side[0].blocks = static_cast<int>((int64_t(c.m) * c.r + 2047) / 2048);
+    if (with_b) p.side[1].blocks = static_cast<int>((int64_t(c.n) * c.r + 2047) / 2048);
+    const int64_t blocks = p.dh_blocks + int64_t(p.side[0].blocks + p.side[1].blocks) * c.g.count;
+    if (blocks == 0) return cudaSuccess;
+    return launch(sum_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, pdl, p, st);
+  };
+  if (c.g.b == 0) return sum(false, true, true, false);  // zeros
+  cudaError_t e;
+  const bool a_cut = s.a.chunks > 1, b_cut = s.b.chunks > 1;
+  if (s.dual) {
+    e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, false, st);
+    if (e == cudaSuccess) e = sum(true, false, b_cut, true);
+  } else {
+    e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
     if (e == cudaSuccess)
-      e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, true, st)
-                : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, true, st);
-    if (e == cudaSuccess) e = launch_expand(c, true, dh, 2 * c.r, c.a, c.m, nullptr, c.dx, true, st);
-    if (e != cudaSuccess) return e;
+      e = launch_outer<false, false, false>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, nullptr, true, st);
   }
-  if (c.g.b > 0 && s.a.chunks == 1 && s.b.chunks == 1) return cudaSuccess;
-  // with no rows at all, both sides are zeros that no outer kernel writes
-  FinishArgs f{first128_of(c.g), c.g.count, {}, c.r};
-  f.side[0] = {pa, c.da, c.m, c.g.b > 0 ? s.a.chunks : 2};
-  f.side[1] = {pb, c.db, c.n, c.g.b > 0 ? s.b.chunks : 2};
-  const int64_t blocks = (int64_t(std::max(c.m, c.n)) * c.r + 2047) / 2048;
-  return launch(finish_kernel, dim3(static_cast<unsigned>(blocks), c.g.count, 2), 256, 0, 1, c.g.b > 0, f, st);
+  if (e == cudaSuccess)
+    e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, true, st)
+              : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, true, st);
+  if (e == cudaSuccess) e = sum(false, a_cut, b_cut && !s.dual, true);
+  if (e != cudaSuccess) return e;
+  return launch_expand(c, true, dh, 2 * c.r, c.a, c.m, nullptr, c.dx, true, st);
 }
 
 }  // namespace twq
