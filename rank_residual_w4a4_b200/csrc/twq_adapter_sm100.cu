@@ -9,8 +9,8 @@
 //
 // All three are bound by HBM: 2 r operations for each element of X, Y or their gradients
 // that is read or written, against some 250 per byte that the tensor cores could do. So
-// each streams its large operand once through shared memory (or, expand, registers) and
-// leaves the products to tcgen05.mma with fp32 accumulators in tensor memory.
+// each streams its large operand once through shared memory and leaves the products to
+// tcgen05.mma with fp32 accumulators in tensor memory.
 // A tile whose rows follow one another in the batch (a request's prompt) comes by TMA; rows that
 // stand anywhere by 16-byte cp.async, into the same 128-byte-swizzle layout. Measured on 8192 rows
 // of 25600: TMA tiles 6.0 TB/s, TMA row gathers (4 rows an instruction) 3.8, cp.async 4.8.
@@ -123,13 +123,20 @@ __device__ __forceinline__ void tma_load_once(uint32_t dst, const CUtensorMap* m
 // 64 columns of `rows` rows from row y on, in boxes of 128 rows or, for a part of that, of 16: the
 // bytes that this will complete, and the copies.
 __device__ __forceinline__ uint32_t rows_bytes(int rows) { return (rows + 15) / 16 * 2048; }
+template <bool kOnce>
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, const CUtensorMap* map16,
                                               uint64_t* bar, int x, int y, int rows) {
-  const uint64_t once = read_once_policy();
+  const uint64_t once = kOnce ? read_once_policy() : 0;
+  auto load = [&](uint32_t d, const CUtensorMap* m, int yy) {
+    if (kOnce)
+      tma_load_once(d, m, bar, x, yy, once);
+    else
+      tma_load(d, m, bar, x, yy);
+  };
   if (rows > 112) {
-    tma_load_once(dst, map, bar, x, y, once);
+    load(dst, map, y);
   } else {
-    for (int i = 0; i < rows; i += 16) tma_load_once(dst + i * 128, map16, bar, x, y + i, once);
+    for (int i = 0; i < rows; i += 16) load(dst + i * 128, map16, y + i);
   }
 }
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
@@ -138,14 +145,6 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                          int y, int z, int u, int v) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
       : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   };
   auto load_both = [&](int step, int slot) {
     mbar_arrive_expect_tx(&s_full[slot], (tma ? rows_bytes(t.z) : 0) + wbytes);
-    if (tma) tma_load_rows(sz + slot * 16384, &p.map, &p.map16, &s_full[slot], column(step), t.w, t.z);
+    if (tma) tma_load_rows<true>(sz + slot * 16384, &p.map, &p.map16, &s_full[slot], column(step), t.w, t.z);
     load_w(step, slot, &s_full[slot]);
   };
   if (tid == 288) {
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 struct ExpandArgs {
   CUtensorMap map, map16;  // base: 128 or 16 rows x 64 columns
   CUtensorMap hmap;  // H: 128 rows x 64 of r
-  CUtensorMap wmap;  // W: 64 columns in accumulator order x 64 of r, or (kTrans) rp of r x 64 columns
+  CUtensorMap wmap;  // W: 64 columns x 64 of r, or (kTrans) rp of r x 64 columns
   const int4* tiles;
   const int32_t* order;
   int cap16;
@@ -663,16 +662,6 @@ constexpr int kExpandSlots = 4;      // W stages, and accumulators of 64 columns
 constexpr int kBaseSlots = 4;        // base stages
 constexpr int kExpandBars = 256;     // bytes of barriers in front of the tiles' space
 
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ uint4 ld_stream(const void* ptr) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -687,37 +676,16 @@ __device__ __forceinline__ void st_stream(void* ptr, uint4 v) {
                : "memory");
 }
 
-// Pairs (columns 8 j + 2 t, + 1) of lane t of a quad, j = 0 .. 3, become the eight
-// columns 8 t .. 8 t + 7: a 4 x 4 transpose of pairs over the quad's lanes.
-__device__ __forceinline__ void quad_transpose(float (&v)[8], int t) {
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1) {
-    const bool up = (t & bit) != 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j & bit) continue;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float give = up ? v[2 * j + e] : v[2 * (j | bit) + e];
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, give, bit);
-        if (up)
-          v[2 * j + e] = got;
-        else
-          v[2 * (j | bit) + e] = got;
-      }
-    }
-  }
-}
-
 // Items: `segs` parts of each tile with an adapter, of about 8 units of 64 columns; the grid's
 // blocks take them in turn, so that at any time they work on neighbouring columns of a few row
 // tiles (a copy by blocks with a long part of a row tile each: 4.6 TB/s; with short ones in
-// turn: 5.8). The accumulator is read in the 16x256b form,
-// where a quad of lanes holds 32 columns of a row in pairs; W's tensor map orders its rows so
-// (column 8 t + 2 j + e of 32 at 8 j + 2 t + e; kTrans: pairs are transposed over the quad) that a lane owns 8 consecutive columns
-// and a quad writes 64 bytes of a row. base comes through shared memory, several stages ahead;
-// it may be y itself, since the lane that writes an element is the only one that reads it, from
-// the stage, before that.
+// turn: 5.8). base comes through shared memory, several stages ahead. A lane of the epilogue takes
+// a row: it adds its accumulators to the row's base in the stage, in place, and its warp copies the
+// stage out, 128 bytes of a row at a time; base may be y itself: an element is written after the
+// only read of it. Measured, 8192 x 25600, rank 64: 168 us. With the hint that base is read once,
+// which the other kernels gain by: 173. Sent out by TMA, the stages are free later: 191. With
+// accumulators read in the 16x256b form and stores from registers, 1.5 times the instructions:
+// 178, and for 5120 columns of W^T 43 instead of 39.
 // Launched so that it may start before the kernel that writes H has ended: until then it reads
 // only what that kernel does not write (the grouping, W, base) and writes nothing.
 template <bool kTrans>
@@ -779,71 +747,68 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     if (warp < 8) {
       // Warps 0 .. 3 take the even units of this block, 4 .. 7 the odd ones, each 32 rows of all 64
       // columns: a warp's chain of waits and loads (about 2000 cycles) then spans two units.
-      const int t4 = lane & 3;
-      RowsAhead<4> ra;  // rows lane / 4 + 8 i of this warp's 32
-      ra.start(tiles, p.order, items, (warp & 3) * 32 + (lane >> 2), 8);
+      const int sub = warp & 3, rr = sub * 32 + lane;
+      RowsAhead<1> ra;
+      ra.start(tiles, p.order, items, rr, 0);
       int turn = warp >> 2;  // 0: the next unit is this warp's
       int slot = 0, bs = 0;
       uint32_t ph = 0, bph = 0;
       bool alive = true;
       for (int k = 0; k < items.count && alive; ++k) {
         const float f = p.scale ? p.scale[ra.group] : 1.0f;
+        const uint64_t f2 = f2_pack(f, f);
         const int ue = unit_end(k);
         for (int u = unit_begin(k); u < ue; ++u) {
           if (turn == 0) {
             alive = warp_wait(&s_done[slot], ph, s_abort, kSiteDone) &&
-                    (!p.base || warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull));
+                    warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull);
             if (!alive) break;
             tc_fence_after();
-            const bool any = (warp & 3) * 32 < ra.count;  // rows of the tile among this warp's 32
-            if (!any && lane == 0) {
-              mbar_arrive(&s_free[slot]);
-              mbar_arrive(&s_bfree[bs]);
-            }
+            const uint32_t stage = sb + bs * 16384;
+            if (sub * 32 < ra.count) {  // else no row of the tile among this warp's 32
+              const uint32_t ta = tmem + (static_cast<uint32_t>(sub * 32) << 16) + slot * 64;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!any) break;
-              uint32_t v[2][16];
-              const uint32_t ta =
-                  tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * 64 + half * 32;
-              tmem_ld_16x256b_x4(ta, v[0]);
-              tmem_ld_16x256b_x4(ta + (16u << 16), v[1]);
-              uint4 b[4] = {};
-              if (p.base) {
+              for (int half = 0; half < 2; ++half) {
+                uint32_t v[32];
+                tmem_ld32(ta + half * 32, v);
+                tmem_wait_ld();
+                if (half == 1) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&s_free[slot]);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  b[i] = lds16(sb + bs * 16384 +
-                               sw128((warp & 3) * 32 + i * 8 + (lane >> 2), half * 4 + t4));
-              }
-              tmem_wait_ld();
-              if (half == 1) {  // everything of this unit is in registers
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                  mbar_arrive(&s_free[slot]);
-                  mbar_arrive(&s_bfree[bs]);
+                for (int q = 0; q < 4; ++q) {
+                  const uint32_t at = stage + sw128(rr, half * 4 + q);
+                  const uint4 b = p.base ? lds16(at) : make_uint4(0, 0, 0, 0);
+                  const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
+                  uint32_t o[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    float lo, hi;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q * 8 + 2 * j]),
+                                             __uint_as_float(v[q * 8 + 2 * j + 1])),
+                                     f2, f2_pack(lo_f(bb[j]), hi_f(bb[j]))),
+                              lo, hi);
+                    o[j] = pack2(lo, hi);
+                  }
+                  sts16(at, make_uint4(o[0], o[1], o[2], o[3]));
                 }
               }
-              const int col = u * 64 + half * 32 + t4 * 8;
+              __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float a[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    a[2 * j + e] = __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + e]);
-                if constexpr (kTrans) quad_transpose(a, t4);
-                const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  o[j] = pack2(fmaf(f, a[2 * j], lo_f(bb[j])), fmaf(f, a[2 * j + 1], hi_f(bb[j])));
-                if (ra.row[i] >= 0)
-                  st_stream(p.y + static_cast<int64_t>(ra.row[i]) * p.n + col,
-                            make_uint4(o[0], o[1], o[2], o[3]));
+              for (int i = 0; i < 8; ++i) {
+                const int from = (lane >> 3) + 4 * i;
+                const int row = __shfl_sync(0xffffffffu, ra.row[0], from);
+                if (row >= 0)
+                  st_stream(p.y + static_cast<int64_t>(row) * p.n + u * 64 + (lane & 7) * 8,
+                            lds16(stage + sw128(sub * 32 + from, lane & 7)));
               }
+            } else if (lane == 0) {
+              mbar_arrive(&s_free[slot]);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_bfree[bs]);
           }
           turn ^= 1;
           if (++slot == p.slots) {
@@ -929,15 +894,17 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             hph ^= 1u;
           }
           const int ue = unit_end(k);
-          for (int u = unit_begin(k); p.base && u < ue; ++u, ++i) {
+          for (int u = unit_begin(k); u < ue; ++u, ++i) {
             if (i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_abort, kSiteEmpty)) {
               alive = false;
               break;
             }
-            if (ra.run >= 0) {
+            if (!p.base) {
+              if (lane == 0) mbar_arrive_n(&s_bfull[bs], 32);
+            } else if (ra.run >= 0) {
               if (tid == 288) {
                 mbar_arrive_expect_tx(&s_bfull[bs], rows_bytes(ra.count));
-                tma_load_rows(sb + bs * 16384, &p.map, &p.map16, &s_bfull[bs], u * 64, ra.run, ra.count);
+                tma_load_rows<false>(sb + bs * 16384, &p.map, &p.map16, &s_bfull[bs], u * 64, ra.run, ra.count);
               }
               if (lane == 0) mbar_arrive_n(&s_bfull[bs], tid == 288 ? 31 : 32);
             } else {
@@ -975,7 +942,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
                 tma_load3(ws, &p.wmap, &s_full[slot], u * 64, 0, g);
               } else {
                 for (int c = 0; c < kt; ++c)
-                  tma_load5(ws + c * 8192, &p.wmap, &s_full[slot], c * 64, 0, 0, 0, g * (p.n / 32) + u * 2);
+                  tma_load3(ws + c * 8192, &p.wmap, &s_full[slot], c * 64, u * 64, g);
               }
               if (++slot == p.slots) {
                 slot = 0;
@@ -1714,11 +1681,9 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, i
   const int fixed = p.hslots * kt * 16384 + p.slots * p.stage_bytes;
   const int smem = fixed + p.bslots * 16384 + kExpandBars;
   const int64_t r = c.r;
-  // W (count x n x r): the 32 columns of a group as 8 t + 2 j + e, read in the order e, t, j
   cudaError_t e =
       trans ? encode<3>(&p.wmap, w, {n, r, c.g.count}, {n, r * n}, {64, rp, 1})
-            : encode<5>(&p.wmap, w, {r, 2, 4, 4, int64_t(c.g.count) * n / 32}, {r, 8 * r, 2 * r, 32 * r},
-                        {64, 2, 4, 4, 2});
+            : encode<3>(&p.wmap, w, {r, n, c.g.count}, {r, r * n}, {64, 64, 1});
   if (e == cudaSuccess) e = encode_rows(&p.hmap, h, c.g.b, r, ldh);
   if (e == cudaSuccess && c.base) e = encode_rows(&p.map, c.base, c.g.b, n, n);
   if (e == cudaSuccess && c.base) e = encode_rows(&p.map16, c.base, c.g.b, n, n, 16);
