@@ -193,6 +193,18 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, ui
       : "memory");
 }
 
+// The same with A in tensor memory: a lane per row, two elements a column.
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -331,7 +343,7 @@ struct RowsAhead {
 
 // ------------------------------------------------------------------ shrink
 struct ShrinkArgs {
-  CUtensorMap map, map16;  // Z: 128 or 16 rows x 64 columns
+  CUtensorMap map, map16;  // Z: 128 or 16 rows x 64 columns; with codes, map: 32 rows x 64 pairs
   CUtensorMap wmap;  // W: rp rows x 64 of k, or (kTrans) 64 rows of k x 64 of r
   const int4* tiles;
   const int32_t* order;
@@ -344,36 +356,35 @@ struct ShrinkArgs {
   uint16_t* out;      // b x r, or (split) b x 2 r: the value in BF16, and what that leaves
   int k, r, rp;       // rp: r rounded up to 16
   bool split;
-  int stages, wstages;  // Z tiles of 128 x 64, W tiles of 64 of the reduction
+  // Tiles of Z, 128 x 64, each with its W; with codes: groups of a team, groups of W.
+  int stages, wstages;
 };
 
 constexpr int kShrinkThreads = 320;  // 8 warps load Z, then epilogue; MMA warp; TMA warp
 constexpr int kShrinkStages = 8;     // at most, of either kind
-constexpr uint32_t kShrinkTmemCols = 128;
-// Codes are converted by the thread that loaded them: it keeps kAhead groups (128 columns, two
-// steps) of its own codes in flight into a private part of shared memory, as it would in
-// registers. A group at a time, because a warp's waits, proxy fence and arrival take 650 cycles
-// however much it converts (steps of 64 columns: 1000 cycles each, of 250 that convert).
-constexpr int kAhead = 2;
-
+constexpr uint32_t kShrinkTmemCols = 128;  // and as many for two groups of converted codes
+// Codes are converted by two teams of four warps, which take the groups of 128 columns in turn. A
+// warp has 32 rows, for which it keeps its own ring of raw codes (TMA where the rows follow one
+// another), a lane a row, and leaves the BF16 in tensor memory, where the MMA takes A from: no
+// proxy fence and no second turn through shared memory. 4096 x 14336, rank 16: TIME us, against 31
+// with all eight warps on each group and A in shared memory.
 // One row tile per cluster, whose blocks split the reduction over k (block `rank` takes the groups
 // of 128 columns rank, rank + splits, ..., so that they read neighbouring pieces of the rows at
 // about the same time) and add their parts through distributed shared memory in rank order.
 template <bool kCodes, bool kTrans>
 __global__ void __launch_bounds__(kShrinkThreads, 2)
     shrink_kernel(const __grid_constant__ ShrinkArgs p) {
-  // A stage of Z and one of W: 64 columns, or a group of 128 with codes, where the issuing
-  // thread's waits and commits weigh more beside the converting warps.
+  // A step: 64 columns, or a group of 128 with codes.
   constexpr int kPer = kCodes ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kShrinkStages], s_empty[kShrinkStages], s_wfull[kShrinkStages],
-      s_wempty[kShrinkStages], s_done;
+      s_wempty[kShrinkStages], s_raw[kCodes ? 16 : 1], s_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
   if (tid == 288) {
-    if (!kCodes) tma_prefetch_desc(&p.map);
+    tma_prefetch_desc(&p.map);
     tma_prefetch_desc(&p.wmap);
   }
   pdl_launch_dependents();
@@ -390,10 +401,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   }
   uint8_t* smem = align1k(smem_raw);
   const uint32_t sz = smem_u32(smem);
-  const uint32_t sw = sz + p.stages * kPer * 16384;
+  const uint32_t sw = sz + p.stages * kPer * 16384;  // with codes: two teams' groups of 16 KB
   const int wbytes = kTrans ? (p.rp + 63) / 64 * 8192 : p.rp * 128;
   // rows beyond a partial tile's end then hold anything; their sums are not stored
-  const bool tma = !kCodes && t.w >= 0;
+  const bool tma = t.w >= 0;
   const int groups = (p.k / 128 - rank + splits - 1) / splits;
   const int steps = groups * 2 / kPer;
   auto column = [&](int tile) { return (rank + (tile >> 1) * splits) * 128 + (tile & 1) * 64; };
@@ -417,15 +428,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     load_w(step, slot, &s_full[slot]);
   };
   if (tid == 288) {
-    // codes: 8 converting warps, and W's own barriers; else the loading threads and the TMA
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s_full[i], kCodes ? 8 : tma ? 1 : 257);
+    // codes: a team's four warps, and W's own barriers; else the loading threads and the TMA
+    for (int i = 0; i < (kCodes ? 2 : p.stages); ++i) {
+      mbar_init(&s_full[i], kCodes ? 4 : tma ? 1 : 257);
       mbar_init(&s_empty[i], 1);
     }
     for (int i = 0; kCodes && i < p.wstages; ++i) {
       mbar_init(&s_wfull[i], 1);
       mbar_init(&s_wempty[i], 1);
     }
+    for (int i = 0; kCodes && i < 16; ++i) mbar_init(&s_raw[i], 1);
     mbar_init(&s_done, 1);
     s_abort = 0;
     fence_barrier_init();
@@ -438,8 +450,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
       }
     }
   }
+  constexpr uint32_t kCols = kShrinkTmemCols * (kCodes ? 2 : 1);
   if (warp == 8) {
-    tmem_alloc(&s_tmem, kShrinkTmemCols);
+    tmem_alloc(&s_tmem, kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -466,124 +479,146 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
         }
       }
     }
-  } else if (warp < 8 && !tma) {
-    // Thread: rows tid / 8 + 32 j, chunk tid % 8 (BF16); rows tid / 4 + 64 j, 16 codes (codes).
-    constexpr int kRows = kCodes ? 2 : 4;
-    const int r0 = kCodes ? tid >> 2 : tid >> 3;
-    const int ch = kCodes ? tid & 3 : tid & 7;
-    int row[kRows];
+  } else if (kCodes && warp < 8) {
+    if constexpr (kCodes) {
+      const int team = warp >> 2, sub = warp & 3;
+      const bool any = sub * 32 < t.z;  // else this warp has no row
+      const int mine = (groups + 1 - team) / 2;  // groups team, team + 2, ...
+      const int row = sub * 32 + lane < t.z ? __ldg(p.order + t.y + sub * 32 + lane) : -1;
+      const int two = p.stages - 1;  // 1 or 2 groups in the ring
+      const uint32_t raw = sz + warp * p.stages * 4096;
+      const uint64_t once = read_once_policy();
+      auto fetch = [&](int j) {
+        if (any && j < mine) {
+          const int col = (rank + (team + 2 * j) * splits) * 128;
+          const uint32_t dst = raw + (j & two) * 4096;
+          if (tma) {
+            if (lane == 0) {
+              uint64_t* bar = &s_raw[warp * 2 + (j & two)];
+              mbar_arrive_expect_tx(bar, 4096);
+              tma_load_once(dst, &p.map, bar, col / 2, t.w + sub * 32, once);
+            }
+          } else {
+            const int ch = lane & 7;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int i = r0 + j * (128 / kRows);
-      row[j] = i < t.z ? __ldg(p.order + t.y + i) : -1;
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 4 * i + (lane >> 3);
+              const int from = __shfl_sync(0xffffffffu, row, rr);
+              cp16(dst + sw128(rr, ch), p.q + static_cast<int64_t>(max(from, 0)) * p.k + col + ch * 16,
+                   from >= 0);
+            }
+          }
+        }
+        if (!tma) cp_commit();
+      };
+      for (int j = 0; j <= two; ++j) fetch(j);
+      // Scales of three groups, each loaded into its own register three groups ahead (a move
+      // between registers would wait for the load).
+      const float* scales = p.sq + static_cast<int64_t>(max(row, 0)) * (p.k >> 7) + rank + team * splits;
+      auto scale_of = [&](int j) { return row >= 0 && j < mine ? __ldg(scales + j * 2 * splits) : 0.0f; };
+      float sc[3];
+#pragma unroll
+      for (int u = 0; u < 3; ++u) sc[u] = scale_of(u);
+      const uint32_t ta = tmem + (static_cast<uint32_t>(sub * 32) << 16) + kShrinkTmemCols + team * 64;
+      bool alive = true;
+      for (int base = 0; base < mine && alive; base += 3) {
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          const int j = base + u;
+          if (j >= mine || !alive) break;
+          uint4 v[8];
+          if (any) {
+            if (tma) {
+              alive = warp_wait(&s_raw[warp * 2 + (j & two)], (j >> two) & 1, &s_abort, kSiteFull);
+            } else if (two) {
+              cp_wait<1>();
+            } else {
+              cp_wait<0>();
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = lds16(raw + (j & two) * 4096 + sw128(lane, q));
+            __syncwarp();
+          }
+          if (alive) fetch(j + 1 + two);
+          alive = alive && (j == 0 || warp_wait(&s_empty[team], (j - 1) & 1, &s_abort, kSiteEmpty));
+          if (!alive) break;
+          if (any) {
+            tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t o[32];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint4 a, b;
+                dequant16(v[half * 4 + q], sc[u], a, b);
+                o[q * 8] = a.x, o[q * 8 + 1] = a.y, o[q * 8 + 2] = a.z, o[q * 8 + 3] = a.w;
+                o[q * 8 + 4] = b.x, o[q * 8 + 5] = b.y, o[q * 8 + 6] = b.z, o[q * 8 + 7] = b.w;
+              }
+              tmem_st32(ta + half * 32, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+          }
+          sc[u] = scale_of(j + 3);
+          if (lane == 0) mbar_arrive(&s_full[team]);
+        }
+      }
+      cp_wait_all();
     }
+  } else if (warp < 8 && !tma) {
+    // Thread: rows tid / 8 + 32 j, chunk tid % 8.
+    const int r0 = tid >> 3, ch = tid & 7;
+    int row[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) row[j] = r0 + j * 32 < t.z ? __ldg(p.order + t.y + r0 + j * 32) : -1;
     int slot = 0;
     uint32_t phase = 0;
-    auto next_slot = [&]() {
+    for (int step = 0; step < steps; ++step) {
+      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+      const uint32_t zs = sz + slot * 16384;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        cp16(zs + sw128(r0 + j * 32, ch), p.z + max(row[j], 0) * p.ldz + column(step) + ch * 8,
+             row[j] >= 0);
+      cp_arrive(&s_full[slot]);
       if (++slot == p.stages) {
         slot = 0;
         phase ^= 1u;
-      }
-    };
-    if constexpr (kCodes) {
-      const uint32_t raw = sw + p.wstages * kPer * wbytes + tid * 16;
-      const int8_t* src[2];  // this thread's column of its rows
-      const float* ssrc[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t at = max(row[j], 0);
-        src[j] = p.q + at * p.k + ch * 16;
-        ssrc[j] = p.sq + at * (p.k >> 7) + rank;
-      }
-      auto fetch = [&](int group) {
-        if (group < groups)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)  // row j % 2, half j / 2 of the group
-            cp16(raw + (group % kAhead * 4 + j) * 4096,
-                 src[j & 1] + (rank + group * splits) * 128 + (j >> 1) * 64, row[j & 1] >= 0);
-        cp_commit();
-      };
-      for (int a = 0; a < kAhead; ++a) fetch(a);
-      // Scales of three groups, each loaded into its own registers three groups ahead (a move
-      // between registers would wait for the load).
-      float sc[3][2];
-      auto load_scales = [&](float (&v)[2], int group) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          v[j] = row[j] >= 0 && group < groups ? __ldg(ssrc[j] + group * splits) : 0.0f;
-      };
-#pragma unroll
-      for (int u = 0; u < 3; ++u) load_scales(sc[u], u);
-      bool alive = true;
-      for (int base = 0; base < groups && alive; base += 3) {
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const int group = base + u;
-          if (group >= groups || !alive) break;
-          cp_wait<kAhead - 1>();
-          uint4 v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = lds16(raw + (group % kAhead * 4 + j) * 4096);
-          if (group >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
-            alive = false;
-            break;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 lo, hi;
-            dequant16(v[j], sc[u][j & 1], lo, hi);
-            const int i = r0 + (j & 1) * 64;
-            const uint32_t zs = sz + (slot * 2 + (j >> 1)) * 16384;
-            sts16(zs + sw128(i, 2 * ch), lo);
-            sts16(zs + sw128(i, 2 * ch + 1), hi);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[slot]);
-          next_slot();
-          fetch(group + kAhead);
-          load_scales(sc[u], group + 3);
-        }
-      }
-    } else {
-      for (int step = 0; step < steps; ++step) {
-        if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
-        const uint32_t zs = sz + slot * 16384;
-#pragma unroll
-        for (int j = 0; j < kRows; ++j)
-          cp16(zs + sw128(r0 + j * 32, ch), p.z + max(row[j], 0) * p.ldz + column(step) + ch * 8,
-               row[j] >= 0);
-        cp_arrive(&s_full[slot]);
-        next_slot();
       }
     }
     cp_wait_all();
   } else if (warp == 8 && lane == 0) {
     const uint32_t idesc = idesc_bf16(p.rp) | (kTrans ? kBMajorMn : 0u);
-    const int ring = kCodes ? p.wstages : p.stages;
-    int slot = 0, wslot = 0;
+    int slot = 0, wslot = 0;  // with codes, slot: the team whose group it is
     uint32_t phase = 0, wphase = 0;
     for (int step = 0; step < steps; ++step) {
       if (kCodes && !wait(&s_wfull[wslot], wphase, &s_abort, kSiteFull)) break;
       if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) break;
       if (!kCodes && !tma) fence_proxy_async_smem();
       tc_fence_after();
-      const uint32_t a = desc_k(sz + slot * kPer * 16384), ws = sw + wslot * kPer * wbytes;
-      const uint32_t b = kTrans ? desc_mn(ws, 8192) : desc_k(ws);
-      mma(tmem, a, b, idesc, step > 0);
+      if constexpr (kCodes) {
+        const uint32_t a = tmem + kShrinkTmemCols + slot * 64, b = desc_k(sw + wslot * 2 * wbytes);
 #pragma unroll
-      for (int k = 1; k < 4 * kPer; ++k)
-        mma(tmem, a + (k >> 2) * 1024 + (k & 3) * 2,
-            b + (k >> 2) * (wbytes >> 4) + (k & 3) * (kTrans ? 128 : 2), idesc, true);
+        for (int k = 0; k < 8; ++k)
+          mma_tmem_a(tmem, a + k * 8, b + (k >> 2) * (wbytes >> 4) + (k & 3) * 2, idesc, step + k > 0);
+        mma_commit(&s_wempty[wslot]);
+        if (++wslot == p.wstages) {
+          wslot = 0;
+          wphase ^= 1u;
+        }
+      } else {
+        const uint32_t a = desc_k(sz + slot * 16384), ws = sw + slot * wbytes;
+        const uint32_t b = kTrans ? desc_mn(ws, 8192) : desc_k(ws);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma(tmem, a + k * 2, b + k * (kTrans ? 128 : 2), idesc, step + k > 0);
+      }
       mma_commit(&s_empty[slot]);
-      if (kCodes) mma_commit(&s_wempty[wslot]);
-      if (++slot == p.stages) {
+      if (++slot == (kCodes ? 2 : p.stages)) {
         slot = 0;
         phase ^= 1u;
-      }
-      if (++wslot == ring) {
-        wslot = 0;
-        wphase ^= 1u;
       }
     }
     mma_commit(&s_done);
@@ -617,7 +652,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, kShrinkTmemCols);
+  if (warp == 8) tmem_dealloc(tmem, kCols);
   if (splits > 1) cluster_sync_startup();
   for (int i = tid; i < (hi - lo) * quads; i += kShrinkThreads) {
     const int rr = lo + i / quads, c = i % quads * 4;
@@ -1599,7 +1634,7 @@ cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, in
 int round16(int r) { return (r + 15) / 16 * 16; }
 
 // Never launched: a kernel of the shrink kernels' shape that allocates no tensor memory. For one
-// that does, the occupancy calls answer one block per SM; two of 128 columns do run there.
+// that does, the occupancy calls answer one block per SM; two of at most 256 columns do run there.
 __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_shape_kernel(int* out) {
   extern __shared__ int shape_smem[];
   if (out) out[0] = shape_smem[threadIdx.x];
@@ -1639,16 +1674,13 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   ShrinkArgs p{{}, {}, {}, c.g.tiles, c.g.order, small_tiles_cap(c.g.b, c.g.count), z, ldz,
                codes ? c.xq8 : nullptr, codes ? c.sx : nullptr, scale, out, k, c.r, rp, trans, 0, 0};
   // Two blocks per SM: 110 KB each, of which the parts need 128 x (rp + 4) fp32. As many W as Z
-  // stages; on codes (Z is converted from its own ring) one or two groups of Z and the rest of W,
-  // whose copies take 2 us and more while HBM is busy.
+  // stages; with codes two raw groups a team (one beyond rank 64) and the rest for W, whose copies
+  // take 2 us and more while HBM is busy.
   const int wbytes = trans ? (rp + 63) / 64 * 8192 : rp * 128, per = codes ? 2 : 1;
-  const int raw = codes ? kAhead * 16384 : 0;
-  p.stages = codes ? (rp > 32 ? 1 : 2)
+  p.stages = codes ? (rp > 64 ? 1 : 2)
                    : std::max(2, std::min(kShrinkStages, 110 * 1024 / (16384 + wbytes)));
-  p.wstages = codes ? std::max(1, std::min(kShrinkStages, (110 * 1024 - raw - p.stages * 32768) / (2 * wbytes)))
-                    : p.stages;
-  const int smem =
-      std::max(per * (p.stages * 16384 + p.wstages * wbytes) + raw, 128 * (rp + 4) * 4) + 1024;
+  p.wstages = codes ? std::min(kShrinkStages, (110 * 1024 - p.stages * 32768) / (2 * wbytes)) : p.stages;
+  const int smem = std::max(per * (p.stages * 16384 + p.wstages * wbytes), 128 * (rp + 4) * 4) + 1024;
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
   // Split the reduction over a cluster of up to 8 blocks, as many as let all tiles run at once (a
@@ -1662,6 +1694,9 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
                         : encode_rows(&p.wmap, w, int64_t(c.g.count) * c.r, k, k, rp);
   if (e == cudaSuccess && !codes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
   if (e == cudaSuccess && !codes) e = encode_rows(&p.map16, z, c.g.b, k, ldz, 16);
+  // a pair of codes as one element: the copies are the same bytes
+  if (e == cudaSuccess && codes)
+    e = encode_rows(&p.map, reinterpret_cast<const uint16_t*>(c.xq8), c.g.b, k / 2, k / 2, 32);
   if (e != cudaSuccess) return e;
   return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
 }
