@@ -366,8 +366,11 @@ constexpr uint32_t kShrinkTmemCols = 128;  // and as many for two groups of conv
 // Codes are converted by two teams of four warps, which take the groups of 128 columns in turn. A
 // warp has 32 rows, for which it keeps its own ring of raw codes (TMA where the rows follow one
 // another), a lane a row, and leaves the BF16 in tensor memory, where the MMA takes A from: no
-// proxy fence and no second turn through shared memory. 4096 x 14336, rank 16: TIME us, against 31
-// with all eight warps on each group and A in shared memory.
+// proxy fence and no second turn through shared memory. 4096 x 14336, rank 16: 28 us, against 31
+// with all eight warps on each group and A in shared memory. What is left is the conversion, seven
+// operations of the half-rate integer pipe for four codes: 1.2 of the 1.6 us that a team takes for
+// a group.
+
 // One row tile per cluster, whose blocks split the reduction over k (block `rank` takes the groups
 // of 128 columns rank, rank + splits, ..., so that they read neighbouring pieces of the rows at
 // about the same time) and add their parts through distributed shared memory in rank order.
@@ -1040,8 +1043,8 @@ struct OuterArgs {
 __host__ __device__ constexpr int outer_z_warps(bool codes) { return codes ? 16 : 8; }
 __host__ __device__ constexpr int outer_threads(bool codes) { return 32 * (outer_z_warps(codes) + 8); }
 constexpr int kOuterStages = 4;     // at most
-// As kAhead, with 2 us between a request and its data while HBM is busy: 3 steps of 16 KB are 24
-// of the 44 KB per us that an SM can get.
+// Steps of 128 x 128 codes under way to a block, in registers' stead. 2 us pass between a request
+// and its data while HBM is busy: 3 steps of 16 KB are 24 of the 44 KB per us that an SM can get.
 constexpr int kOuterAhead = 5;
 constexpr int kOuterRawStep = 16384 + 512;  // codes; a scale for each row
 
