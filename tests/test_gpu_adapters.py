@@ -348,3 +348,59 @@ def test_many_calls_give_equal_bits(twq, device, b, m, n, r, kind):
                    + c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base))
         assert twq.device_status() == 0
         assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("r", [8, 72])
+@pytest.mark.parametrize("m,n", [(128, 131072), (131072, 128)])
+def test_offsets_beyond_32_bits(twq, device, m, n, r, codes):
+    """X, dY or Y of more than 2^31 elements: the rows at both ends and in the middle. The
+    gradients of the weights are those of these rows, dY being 0 elsewhere."""
+    b, count, bf = 17000, 2, torch.bfloat16
+    gen = torch.Generator(device=device).manual_seed(r)
+
+    def normal(*shape, std=1.0):
+        return torch.randn(shape, generator=gen, dtype=bf, device=device) * std
+
+    pick = torch.tensor([0, 1, b // 2, b - 2, b - 1], device=device)
+    ids = torch.arange(b, dtype=torch.int32) % 3 - 1
+    ids[b // 3:2 * b // 3] = 1  # tiles whose rows follow one another, too
+    ids = ids.to(device)
+    ad = twq.Adapters(normal(count, r, m, std=m ** -0.5), normal(count, n, r, std=0.05),
+                      torch.tensor([0.5, -2.0], device=device))
+    groups = twq.group_rows(ids, count)
+    if codes:
+        xargs = (torch.randint(-127, 128, (b, m), generator=gen, dtype=torch.int8, device=device),
+                 torch.rand((b, m // 128), generator=gen, device=device) * 0.02)
+        x64 = ref.x_of_codes(xargs[0][pick], xargs[1][pick])
+        linear, backward = twq.adapter_linear_i8, twq.adapter_backward_i8
+    else:
+        xargs = (normal(b, m),)
+        x64 = xargs[0][pick].double()
+        linear, backward = twq.adapter_linear, twq.adapter_backward
+    y = normal(b, n)
+    base64 = y[pick].double()
+    y, h = linear(*xargs, ad, groups, base=y, y=y)
+    want = ref.linear(x64, ad.a, ad.b, ad.scale, ids[pick], base64, codes)
+    for got, w, e, name in zip((y, h), *want, ("y", "h")):
+        ref.check(got[pick], w, e, name)
+    del y
+    dy = torch.zeros((b, n), dtype=bf, device=device)
+    dy[pick] = normal(5, n, std=0.01)
+    dx, da, db = backward(dy, *xargs, h, ad, groups)
+    want = ref.backward(dy[pick].double(), x64, h[pick].double(), ad.a, ad.b, ad.scale, ids[pick],
+                        None, codes)
+    for got, w, e, name in zip((dx[pick], da, db), *want, ("dx", "da", "db")):
+        ref.check(got, w, e, name)
+    dx[pick] = 0
+    assert not bool(dx.any())  # rows without dY
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("b", [40, 1300])
+def test_most_adapters(twq, device, b, codes):
+    c = Case(twq, device, b, 256, 128, 16, 4096, "mixed", codes)
+    c.check_linear(c.base, c.linear(*c.xargs, c.ad, c.groups, base=c.base))
+    c.check_backward(None, c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups))
+    assert twq.device_status() == 0
