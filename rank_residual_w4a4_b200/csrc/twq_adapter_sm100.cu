@@ -907,6 +907,31 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         ra.start(tiles, p.order, items, r0, 8);
         int hs = 0, bs = 0, i = 0;
         uint32_t hph = 0, bph = 0;
+        auto load_base = [&](int u) {
+          if (!p.base) {
+            if (lane == 0) mbar_arrive_n(&s_bfull[bs], 32);
+          } else if (ra.run >= 0) {
+            if (tid == 288) {
+              mbar_arrive_expect_tx(&s_bfull[bs], rows_bytes(ra.count));
+              tma_load_rows<false>(sb + bs * 16384, &p.map, &p.map16, &s_bfull[bs], u * 64, ra.run, ra.count);
+            }
+            if (lane == 0) mbar_arrive_n(&s_bfull[bs], tid == 288 ? 31 : 32);
+          } else {
+            const uint16_t* src = p.base + u * 64 + ch * 8;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              cp16(sb + bs * 16384 + sw128(r0 + 8 * j, ch),
+                   src + static_cast<int64_t>(max(ra.row[j], 0)) * p.n, ra.row[j] >= 0);
+            cp_arrive(&s_bfull[bs]);
+          }
+          if (++bs == p.bslots) {
+            bs = 0;
+            bph ^= 1u;
+          }
+        };
+        // the first stages of base, then H
+        const int early = min(p.bslots, unit_end(0) - unit_begin(0));
+        for (; i < early; ++i) load_base(unit_begin(0) + i);
         pdl_wait();
         for (int k = 0; k < items.count && alive; ++k) {
           if (k >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_abort, kSiteHEmpty)) break;
@@ -932,31 +957,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             hph ^= 1u;
           }
           const int ue = unit_end(k);
-          for (int u = unit_begin(k); u < ue; ++u, ++i) {
+          for (int u = unit_begin(k) + (k == 0 ? early : 0); u < ue; ++u, ++i) {
             if (i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_abort, kSiteEmpty)) {
               alive = false;
               break;
             }
-            if (!p.base) {
-              if (lane == 0) mbar_arrive_n(&s_bfull[bs], 32);
-            } else if (ra.run >= 0) {
-              if (tid == 288) {
-                mbar_arrive_expect_tx(&s_bfull[bs], rows_bytes(ra.count));
-                tma_load_rows<false>(sb + bs * 16384, &p.map, &p.map16, &s_bfull[bs], u * 64, ra.run, ra.count);
-              }
-              if (lane == 0) mbar_arrive_n(&s_bfull[bs], tid == 288 ? 31 : 32);
-            } else {
-              const uint16_t* src = p.base + u * 64 + ch * 8;
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                cp16(sb + bs * 16384 + sw128(r0 + 8 * j, ch),
-                     src + static_cast<int64_t>(max(ra.row[j], 0)) * p.n, ra.row[j] >= 0);
-              cp_arrive(&s_bfull[bs]);
-            }
-            if (++bs == p.bslots) {
-              bs = 0;
-              bph ^= 1u;
-            }
+            load_base(u);
           }
           ra.advance();
         }
@@ -1125,13 +1131,13 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int steps = (end - begin) * nb;
-  // Up to here only the grouping was read, which no kernel of the same call writes.
+  // The grouping and Z are read before the kernel in front has ended: no kernel of the same call
+  // writes them.
   if (warp < kZ) {
     constexpr int kRows = 128 / (kZ * 4);   // rows r0 + kZ * 4 j, chunk ch (or 16 codes)
     const int r0 = tid >> 3, ch = tid & 7;
     RowsAhead<kRows> ra;  // position of the loads: its tile, and the block in it
     ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, r0, kZ * 4);
-    pdl_wait();
     int lblk = 0;
     auto advance = [&]() {
       if (++lblk == nb) {
@@ -1524,7 +1530,7 @@ __device__ __forceinline__ void sum_group(const SumArgs& p, int block) {
     const float* first = part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size;
     v = __ldcg(reinterpret_cast<const float4*>(first));
     w = __ldcg(reinterpret_cast<const float4*>(first + 512));
-#pragma unroll 4
+#pragma unroll 8
     for (int x = c0 + 1; x <= c1; ++x) {
       const float4 a = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size));
       const float4 b = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size + 512));
