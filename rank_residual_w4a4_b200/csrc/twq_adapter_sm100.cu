@@ -1135,7 +1135,10 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   // writes them.
   if (warp < kZ) {
     constexpr int kRows = 128 / (kZ * 4);   // rows r0 + kZ * 4 j, chunk ch (or 16 codes)
-    const int r0 = tid >> 3, ch = tid & 7;
+    // Eight lanes: a row, or, with codes, two rows of four chunks, which go to even chunks of one and
+    // odd ones of the other (of one row the eight would meet in four).
+    const int r0 = kCodes ? warp * 4 + (lane >> 4) * 2 + (lane >> 2 & 1) : tid >> 3;
+    const int ch = kCodes ? (lane >> 3 & 1) * 4 + (lane & 3) : tid & 7;
     RowsAhead<kRows> ra;  // position of the loads: its tile, and the block in it
     ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, r0, kZ * 4);
     int lblk = 0;
@@ -1158,7 +1161,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         int srow = -1;
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-          const int other = __shfl_sync(0xFFFFFFFFu, ra.row[j], (lane & 3) * 8);
+          const int other = __shfl_sync(0xFFFFFFFFu, ra.row[j], (lane & 2) * 8 + (lane & 1) * 4);
           if (lane >> 2 == j) srow = other;
         }
         if (lane < 4 * kRows)
