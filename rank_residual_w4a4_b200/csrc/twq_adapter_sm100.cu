@@ -674,6 +674,109 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   if (splits > 1) cluster_sync_startup();  // peers may still be reading this block's part
 }
 
+// --------------------------------------------------------------------- sum
+__host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles) {
+  return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
+}
+
+// What the outer products leave to be added up: dh from its slices' parts, and the groups of dA and
+// dB that the chunks cut. Right after the kernel that wrote them, while the parts are in L2 (at the
+// end of the call those of dY were not: 18 us instead of 11 at 8192 x 5120 x 25600).
+struct SumArgs {
+  const int4* tiles;
+  const int32_t *order, *offsets, *first128;
+  int b, count, r;
+  // dh, as rows of 2 r (store_value), from slices x r / 4 x b x 4
+  const float* dpart;
+  uint16_t* dh;
+  int slices, dh_blocks;
+  // parts [block][rank / 4][column of the block][4]; out count x r x k (dA) or count x k x r (dB)
+  struct {
+    const float* part;
+    uint16_t* out;
+    int k, chunks, blocks;  // blocks of threads for each group
+  } side[2];
+};
+
+// Largest c with chunk_begin(c) <= tile.
+__device__ __forceinline__ int chunk_of(int tile, int chunks, int tiles) {
+  int c = static_cast<int>(static_cast<int64_t>(tile) * chunks / tiles);
+  while (chunk_begin(c + 1, chunks, tiles) <= tile) ++c;
+  return c;
+}
+
+// A thread: 4 ranks of a position; slices in order.
+__device__ __forceinline__ void sum_dh(const SumArgs& p, int block) {
+  const int wide = (p.b + 255) / 256, quad = block / wide;
+  const int64_t pos = static_cast<int64_t>(block - quad * wide) * 256 + threadIdx.x;
+  if (pos >= p.offsets[p.count]) return;
+  const int64_t row = p.order[pos], step = static_cast<int64_t>(p.b) * p.r;
+  const float* part = p.dpart + (static_cast<int64_t>(quad) * p.b + pos) * 4;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < p.slices; ++s) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(part + s * step));
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  store_value(p.dh, row, p.r, quad * 4, v, true);
+}
+
+// A thread: 8 ranks of a column of group g; chunks in order. Zeros for a group without rows.
+template <bool kByRank>
+__device__ __forceinline__ void sum_group(const SumArgs& p, int block) {
+  const auto& side = p.side[kByRank ? 0 : 1];
+  const int g = block / side.blocks, oct = p.r / 8;
+  const int64_t i = static_cast<int64_t>(block - g * side.blocks) * 256 + threadIdx.x;
+  const int64_t blk = i / (oct * 128);
+  if (blk >= side.k / 128) return;
+  const int rest = static_cast<int>(i - blk * (oct * 128));
+  const int c = rest / 128 * 8, j = static_cast<int>(blk) * 128 + rest % 128;
+  const int gb = p.first128[g], ge = p.first128[g + 1], total = p.first128[p.count];
+  const int64_t size = static_cast<int64_t>(side.k) * p.r;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = v;
+  if (gb < ge) {
+    const int chunks = min(side.chunks, total);
+    const int c0 = chunk_of(gb, chunks, total), c1 = chunk_of(ge - 1, chunks, total);
+    if (c0 == c1) return;  // inside one chunk: already written
+    // the group's run is a chunk's second one only where the group starts inside it
+    const float* part = side.part + (blk * (p.r / 4) + c / 4) * 512 + rest % 128 * 4;
+    const float* first = part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size;
+    v = __ldcg(reinterpret_cast<const float4*>(first));
+    w = __ldcg(reinterpret_cast<const float4*>(first + 512));
+#pragma unroll 8
+    for (int x = c0 + 1; x <= c1; ++x) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size + 512));
+      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+      w.x += b.x, w.y += b.y, w.z += b.z, w.w += b.w;
+    }
+  }
+  const uint32_t o[4] = {pack2(v.x, v.y), pack2(v.z, v.w), pack2(w.x, w.y), pack2(w.z, w.w)};
+  uint16_t* out = side.out + g * size;
+  if (kByRank) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      out[static_cast<int64_t>(c + 2 * e) * side.k + j] = static_cast<uint16_t>(o[e]);
+      out[static_cast<int64_t>(c + 2 * e + 1) * side.k + j] = static_cast<uint16_t>(o[e] >> 16);
+    }
+  } else {
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * p.r + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+__device__ __forceinline__ void sum_block(const SumArgs& p, int block) {
+  if (block < p.dh_blocks) return sum_dh(p, block);
+  block -= p.dh_blocks;
+  if (block < p.side[0].blocks * p.count) return sum_group<true>(p, block);
+  sum_group<false>(p, block - p.side[0].blocks * p.count);
+}
+
+__global__ void __launch_bounds__(256) sum_kernel(const SumArgs p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  sum_block(p, blockIdx.x);
+}
+
 // ------------------------------------------------------------------ expand
 struct ExpandArgs {
   CUtensorMap map, map16;  // base: 128 or 16 rows x 64 columns
@@ -691,6 +794,8 @@ struct ExpandArgs {
   int n, r, rp, ldh;
   int stage_bytes, slots, hslots, bslots;  // a W stage; W stages; H tiles; base stages of 16 KB
   int segs;
+  SumArgs sum;  // kTrans: what the kernel in front left to be added up, `sums` blocks of 256 threads
+  int sums;
 };
 
 constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H and base; TMA of W
@@ -754,7 +859,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   auto unit_begin = [&](int k) { return (items.first + items.stride * k) % p.segs * units / p.segs; };
   auto unit_end = [&](int k) { return ((items.first + items.stride * k) % p.segs + 1) * units / p.segs; };
 
-  if (items.count > 0) {
+  auto add_up = [&]() {  // by warps 0 .. 7, while the first copies are under way
+    if (!kTrans || p.sums == 0) return;
+    pdl_wait();
+    for (int i = blockIdx.x; i < p.sums; i += gridDim.x) sum_block(p.sum, i);
+  };
+  if (items.count <= 0) {
+    if (warp < 8) add_up();
+  } else {
     if (tid == 0) {
       for (int i = 0; i < kExpandSlots; ++i) {
         mbar_init(&s_full[i], 1);
@@ -785,6 +897,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     if (warp < 8) {
       // Warps 0 .. 3 take the even units of this block, 4 .. 7 the odd ones, each 32 rows of all 64
       // columns: a warp's chain of waits and loads (about 2000 cycles) then spans two units.
+      add_up();
       const int sub = warp & 3, rr = sub * 32 + lane;
       RowsAhead<1> ra;
       ra.start(tiles, p.order, items, rr, 0);
@@ -1053,10 +1166,6 @@ constexpr int kOuterStages = 4;     // at most
 // and its data while HBM is busy: 3 steps of 16 KB are 24 of the 44 KB per us that an SM can get.
 constexpr int kOuterAhead = 5;
 constexpr int kOuterRawStep = 16384 + 512;  // codes; a scale for each row
-
-__host__ __device__ __forceinline__ int chunk_begin(int c, int chunks, int tiles) {
-  return static_cast<int>(static_cast<int64_t>(c) * tiles / chunks);
-}
 
 // A slice of Z's 128-column blocks (blockIdx.x), the row tiles of chunk blockIdx.y. Tiles of one
 // group form a run, summed in tensor memory (lane = column of Z, column = rank). A run that
@@ -1469,101 +1578,6 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   if (warp == kMma) tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// What the outer products leave to be added up, in one launch: dh from its slices' parts, and the
-// groups of dA and dB that the chunks cut. Right after the kernel that wrote them, while the parts
-// are in L2 (at the end of the call they were not: 18 us instead of 11 at 8192 x 5120 x 25600).
-struct SumArgs {
-  const int4* tiles;
-  const int32_t *order, *offsets, *first128;
-  int b, count, r;
-  // dh, as rows of 2 r (store_value), from slices x r / 4 x b x 4
-  const float* dpart;
-  uint16_t* dh;
-  int slices, dh_blocks;
-  // parts [block][rank / 4][column of the block][4]; out count x r x k (dA) or count x k x r (dB)
-  struct {
-    const float* part;
-    uint16_t* out;
-    int k, chunks, blocks;  // blocks of threads for each group
-  } side[2];
-};
-
-// Largest c with chunk_begin(c) <= tile.
-__device__ __forceinline__ int chunk_of(int tile, int chunks, int tiles) {
-  int c = static_cast<int>(static_cast<int64_t>(tile) * chunks / tiles);
-  while (chunk_begin(c + 1, chunks, tiles) <= tile) ++c;
-  return c;
-}
-
-// A thread: 4 ranks of a position; slices in order.
-__device__ __forceinline__ void sum_dh(const SumArgs& p, int block) {
-  const int wide = (p.b + 255) / 256, quad = block / wide;
-  const int64_t pos = static_cast<int64_t>(block - quad * wide) * 256 + threadIdx.x;
-  if (pos >= p.offsets[p.count]) return;
-  const int64_t row = p.order[pos], step = static_cast<int64_t>(p.b) * p.r;
-  const float* part = p.dpart + (static_cast<int64_t>(quad) * p.b + pos) * 4;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int s = 0; s < p.slices; ++s) {
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(part + s * step));
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-  }
-  store_value(p.dh, row, p.r, quad * 4, v, true);
-}
-
-// A thread: 8 ranks of a column of group g; chunks in order. Zeros for a group without rows.
-template <bool kByRank>
-__device__ __forceinline__ void sum_group(const SumArgs& p, int block) {
-  const auto& side = p.side[kByRank ? 0 : 1];
-  const int g = block / side.blocks, oct = p.r / 8;
-  const int64_t i = static_cast<int64_t>(block - g * side.blocks) * 256 + threadIdx.x;
-  const int64_t blk = i / (oct * 128);
-  if (blk >= side.k / 128) return;
-  const int rest = static_cast<int>(i - blk * (oct * 128));
-  const int c = rest / 128 * 8, j = static_cast<int>(blk) * 128 + rest % 128;
-  const int gb = p.first128[g], ge = p.first128[g + 1], total = p.first128[p.count];
-  const int64_t size = static_cast<int64_t>(side.k) * p.r;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = v;
-  if (gb < ge) {
-    const int chunks = min(side.chunks, total);
-    const int c0 = chunk_of(gb, chunks, total), c1 = chunk_of(ge - 1, chunks, total);
-    if (c0 == c1) return;  // inside one chunk: already written
-    // the group's run is a chunk's second one only where the group starts inside it
-    const float* part = side.part + (blk * (p.r / 4) + c / 4) * 512 + rest % 128 * 4;
-    const float* first = part + (2 * c0 + (gb > chunk_begin(c0, chunks, total) ? 1 : 0)) * size;
-    v = __ldcg(reinterpret_cast<const float4*>(first));
-    w = __ldcg(reinterpret_cast<const float4*>(first + 512));
-#pragma unroll 8
-    for (int x = c0 + 1; x <= c1; ++x) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size));
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(part + 2 * x * size + 512));
-      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
-      w.x += b.x, w.y += b.y, w.z += b.z, w.w += b.w;
-    }
-  }
-  const uint32_t o[4] = {pack2(v.x, v.y), pack2(v.z, v.w), pack2(w.x, w.y), pack2(w.z, w.w)};
-  uint16_t* out = side.out + g * size;
-  if (kByRank) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      out[static_cast<int64_t>(c + 2 * e) * side.k + j] = static_cast<uint16_t>(o[e]);
-      out[static_cast<int64_t>(c + 2 * e + 1) * side.k + j] = static_cast<uint16_t>(o[e] >> 16);
-    }
-  } else {
-    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * p.r + c) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-}
-
-__global__ void __launch_bounds__(256) sum_kernel(const SumArgs p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  int block = blockIdx.x;
-  if (block < p.dh_blocks) return sum_dh(p, block);
-  block -= p.dh_blocks;
-  if (block < p.side[0].blocks * p.count) return sum_group<true>(p, block);
-  sum_group<false>(p, block - p.side[0].blocks * p.count);
-}
-
 // -------------------------------------------------------------------- host
 int tiles_estimate(const AdapterCall& c) {
   // full tiles and half a partial one per adapter
@@ -1643,6 +1657,12 @@ cudaError_t encode_rows(CUtensorMap* map, const uint16_t* base, int64_t rows, in
   return encode<2>(map, base, {cols, rows}, {ld}, {64, high});
 }
 
+// Up to three turns of its blocks, the expand kernel adds up what the last outer product left, while
+// its first copies are under way: a launch less (gradients of 4096 x 4096, rank 16: 53 instead of
+// 55.5 us; 8192 x 5120, rank 64, 640 blocks: 184 instead of 185). More are a launch of their own,
+// with eight blocks on an SM instead of two.
+constexpr int kMaxExpandSums = 3 * 2 * kSms;
+
 int round16(int r) { return (r + 15) / 16 * 16; }
 
 // Never launched: a kernel of the shrink kernels' shape that allocates no tensor memory. For one
@@ -1713,11 +1733,14 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   return launch(kernel, grid, kShrinkThreads, smem, splits, false, p, st);
 }
 
+int sum_blocks(const SumArgs& p) { return p.dh_blocks + (p.side[0].blocks + p.side[1].blocks) * p.count; }
+
 cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, int ldh, const uint16_t* w,
-                          int n, const float* scale, uint16_t* y, bool pdl, cudaStream_t st) {
+                          int n, const float* scale, uint16_t* y, const SumArgs& sum, bool pdl,
+                          cudaStream_t st) {
   const int rp = round16(c.r), kt = (rp + 63) / 64;
   ExpandArgs p{{}, {}, {}, {}, c.g.tiles, c.g.order, small_tiles_cap(c.g.b, c.g.count), h, scale, c.base, y,
-               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, ldh, 0, 0, 0, 0, 1};
+               first128_of(c.g), c.g.offsets, c.g.b, c.g.count, n, c.r, rp, ldh, 0, 0, 0, 0, 1, sum, sum_blocks(sum)};
   // Two blocks per SM, 112 KB each: 4 stages of W and of base and a second H tile as far as they
   // fit (W's copies take 2 us and more while HBM is busy), 2 of each beyond rank 64.
   p.stage_bytes = trans ? rp * 128 : kt * 8192;
@@ -1744,8 +1767,8 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, i
     const int64_t all = turns * (1 + (units + s - 1) / s);
     if (all < cost) cost = all, p.segs = s;
   }
-  const unsigned blocks = static_cast<unsigned>(
-      std::min<int64_t>(2 * kSms, int64_t(row_tiles_cap(c.g.b, c.g.count, 128)) * p.segs));
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(
+      2 * kSms, std::max<int64_t>(p.sums, int64_t(row_tiles_cap(c.g.b, c.g.count, 128)) * p.segs)));
   return launch(trans ? expand_kernel<true> : expand_kernel<false>, dim3(blocks), kExpandThreads, smem, 1,
                 pdl, p, st);
 }
@@ -1850,7 +1873,7 @@ cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
   if (small_batch(c.g.b, c.r)) return launch_adapter_small(c, st);
   cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
   if (e != cudaSuccess) return e;
-  return launch_expand(c, false, c.h, c.r, c.bm, c.n, c.scale, c.y, true, st);
+  return launch_expand(c, false, c.h, c.r, c.bm, c.n, c.scale, c.y, SumArgs{}, true, st);
 }
 
 size_t adapter_backward_workspace(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
@@ -1867,21 +1890,23 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
   float* pd = reinterpret_cast<float*>(ws + s.pd);
   const SumArgs none{c.g.tiles, c.g.order, c.g.offsets, first128_of(c.g), c.g.b, c.g.count, c.r,
                      pd, dh, s.b.slices, 0, {{pa, c.da, c.m, s.a.chunks, 0}, {pb, c.db, c.n, s.b.chunks, 0}}};
-  auto sum = [&](bool with_dh, bool with_a, bool with_b, bool pdl) {
+  auto sums = [&](bool with_dh, bool with_a, bool with_b) {
     SumArgs p = none;
     if (with_dh) p.dh_blocks = (c.g.b + 255) / 256 * (c.r / 4);
     if (with_a) p.side[0].blocks = static_cast<int>((int64_t(c.m) * c.r + 2047) / 2048);
     if (with_b) p.side[1].blocks = static_cast<int>((int64_t(c.n) * c.r + 2047) / 2048);
-    const int64_t blocks = p.dh_blocks + int64_t(p.side[0].blocks + p.side[1].blocks) * c.g.count;
-    if (blocks == 0) return cudaSuccess;
-    return launch(sum_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, pdl, p, st);
+    return p;
   };
-  if (c.g.b == 0) return sum(false, true, true, false);  // zeros
+  auto add_up = [&](const SumArgs& p, bool pdl) {
+    const int blocks = sum_blocks(p);
+    return blocks ? launch(sum_kernel, dim3(blocks), 256, 0, 1, pdl, p, st) : cudaSuccess;
+  };
+  if (c.g.b == 0) return add_up(sums(false, true, true), false);  // zeros
   cudaError_t e;
   const bool a_cut = s.a.chunks > 1, b_cut = s.b.chunks > 1;
   if (s.dual) {
     e = launch_outer<false, false, true>(c, s.b, c.dy, c.n, c.n, c.h, c.scale, c.db, pb, pd, false, st);
-    if (e == cudaSuccess) e = sum(true, false, b_cut, true);
+    if (e == cudaSuccess) e = add_up(sums(true, false, b_cut), true);
   } else {
     e = launch_shrink(c, true, c.dy, c.n, c.n, c.bm, c.scale, dh, st);
     if (e == cudaSuccess)
@@ -1890,9 +1915,13 @@ cudaError_t launch_adapter_backward(const AdapterCall& c, cudaStream_t st) {
   if (e == cudaSuccess)
     e = c.xq8 ? launch_outer<true, true, false>(c, s.a, nullptr, 0, c.m, dh, nullptr, c.da, pa, nullptr, true, st)
               : launch_outer<false, true, false>(c, s.a, c.x, c.ldx, c.m, dh, nullptr, c.da, pa, nullptr, true, st);
-  if (e == cudaSuccess) e = sum(false, a_cut, b_cut && !s.dual, true);
+  SumArgs last = sums(false, a_cut, b_cut && !s.dual);
+  if (sum_blocks(last) > kMaxExpandSums) {
+    if (e == cudaSuccess) e = add_up(last, true);
+    last = SumArgs{};
+  }
   if (e != cudaSuccess) return e;
-  return launch_expand(c, true, dh, 2 * c.r, c.a, c.m, nullptr, c.dx, true, st);
+  return launch_expand(c, true, dh, 2 * c.r, c.a, c.m, nullptr, c.dx, last, true, st);
 }
 
 }  // namespace twq
