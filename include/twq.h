@@ -394,6 +394,8 @@ TWQ_API twq_status twq_fold_transforms(const float* Q, const float* G, const uin
  *     y = base + s h B^T           base: the layer's Y, from any twq_*_linear call
  *
  * Rows whose id is outside [0, count) have no adapter: h = 0, y = base.
+ * Outputs overlap no other argument of a call, except where said. Calls on streams of
+ * their own may share a grouping and the adapters.
  */
 
 /* Rows grouped by adapter (device pointers, caller-allocated; twq_row_groups_sizes). */
@@ -525,7 +527,9 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
  */
 TWQ_API void twq_release_cache(void);
 
-/* Number of kernels each entry point launches (for launch accounting). */
+/* Number of kernels each entry point launches (for launch accounting); of the adapter
+ * calls, the most: a small forward batch takes one, gradients one less where few parts
+ * are left to add up. */
 TWQ_API int twq_launches_per_call(const char* entry_point);
 
 #ifdef __cplusplus

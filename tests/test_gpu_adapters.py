@@ -404,3 +404,26 @@ def test_most_adapters(twq, device, b, codes):
     c.check_linear(c.base, c.linear(*c.xargs, c.ad, c.groups, base=c.base))
     c.check_backward(None, c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups))
     assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("b,m,n,r,kind", [
+    (40, 2048, 1024, 16, "mixed"), (3000, 6144, 256, 48, "runs"), (2500, 4096, 512, 128, "runs"),
+    (2000, 1024, 2048, 24, "mixed"),
+])
+def test_equal_bits_from_cold_caches(twq, device, b, m, n, r, kind, codes):
+    """What a copy brings late must not be read early, nor overwritten while it is read."""
+    c = Case(twq, device, b, m, n, r, 6, kind, codes)
+    want = c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+    wantb = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    c.check_linear(c.base, want)
+    c.check_backward(c.dx_base, wantb)
+    other = torch.empty(256 << 20, dtype=torch.uint8, device=device)  # twice the L2
+    for i in range(24):
+        other.fill_(i)
+        got = c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+        if i % 2:
+            other.fill_(i + 100)
+        gotb = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+        assert all(torch.equal(p, q) for p, q in zip(got + gotb, want + wantb))
+    assert twq.device_status() == 0
