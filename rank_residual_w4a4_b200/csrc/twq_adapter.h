@@ -26,11 +26,20 @@ inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
 // times rank (from 16 on): its time goes with that, since it reads an adapter again for every 16
 // rows. At 4096 x 4096 it meets the two kernels at about 850 rows of rank 16 (13.5 us), 380 of
 // rank 64 (14 us) and 150 of rank 128 (14.5 us); at 4096 x 14336 at 600, 220 and 120.
+//
+// Twice as many up to rank 16 where the adapters may have 16 rows each or fewer: a row tile of 128
+// then holds few rows, but takes the two kernels as long as a full one. 512 rows with 64 adapters of
+// 4096 x 4096: 15 us instead of 37, of 4096 x 14336: 33 instead of 70; 1536 rows with 128: 39
+// instead of 60, 67 instead of 117. If only 4 of them are used: 23 instead of 25, 43 instead of 34.
+// (At rank 32: 39 to 39 us, 22 to 22, and 81 to 61 at 14336 x 4096, so not there.)
 constexpr int64_t kSmallWork = 12288;
-inline bool small_batch(int64_t b, int64_t r) { return b * (r > 16 ? r : 16) <= kSmallWork; }
+inline bool small_batch(int64_t b, int64_t count, int64_t r) {
+  const int64_t work = b * (r > 16 ? r : 16);
+  return work <= kSmallWork || (work <= 2 * kSmallWork && r <= 16 && b <= 16 * count);
+}
 // Room for 16-row tiles: none where no rank makes the batch a small one.
 inline int small_tiles_cap(int64_t b, int64_t count) {
-  return small_batch(b, 1) ? row_tiles_cap(b, count, 16) : 0;
+  return small_batch(b, count, 1) ? row_tiles_cap(b, count, 16) : 0;
 }
 
 // tiles: {number of 16-row tiles, number of 128-row tiles, 0, 0}, then room for

@@ -1877,7 +1877,7 @@ cudaError_t read_and_clear_adapter_status(int* code) {
 }
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st) {
-  if (small_batch(c.g.b, c.r)) return launch_adapter_small(c, st);
+  if (small_batch(c.g.b, c.g.count, c.r)) return launch_adapter_small(c, st);
   cudaError_t e = launch_shrink(c, false, c.x, c.ldx, c.m, c.a, nullptr, c.h, st);
   if (e != cudaSuccess) return e;
   return launch_expand(c, false, c.h, c.r, c.bm, c.n, c.scale, c.y, SumArgs{}, true, st);

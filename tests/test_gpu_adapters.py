@@ -112,6 +112,7 @@ SHAPES = [
     (333, 128, 128, 96, 3, "mixed"), (1000, 512, 768, 72, 17, "mixed"),
     (1500, 256, 1024, 16, 300, "mixed"), (2500, 768, 512, 128, 2, "runs"),
     (5000, 256, 256, 48, 1, "one"), (700, 4096, 128, 112, 1, "runs"),
+    (1536, 512, 384, 16, 96, "mixed"), (1537, 512, 384, 16, 97, "runs"), (1500, 384, 512, 8, 93, "mixed"),
 ]
 
 
