@@ -24,8 +24,8 @@ inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
 
 // The forward pass takes the one-launch kernel, on 16-row tiles, for batches up to this many rows
 // times rank (from 16 on): its time goes with that, since it reads an adapter again for every 16
-// rows. At 4096 x 4096 it meets the two kernels at about 850 rows of rank 16 (13.5 us), 380 of
-// rank 64 (14 us) and 150 of rank 128 (14.5 us); at 4096 x 14336 at 600, 220 and 120.
+// rows. With 4 adapters of 4096 x 4096 it meets the two kernels at about 1000 rows of rank 16
+// (16 us), 430 of rank 64 (16 us) and 180 of rank 128 (17 us); of 4096 x 14336 at 620, 260 and 130.
 //
 // Twice as many up to rank 16 where the adapters may have 16 rows each or fewer: a row tile of 128
 // then holds few rows, but takes the two kernels as long as a full one. 512 rows with 64 adapters of
