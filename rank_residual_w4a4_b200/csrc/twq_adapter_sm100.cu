@@ -962,6 +962,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             } else if (lane == 0) {
               mbar_arrive(&s_free[slot]);
             }
+            // The next copy into this stage may be TMA's, which the barrier alone does not order
+            // behind the stores above (nor behind the cp.async that filled the stage).
+            if (p.base) fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_bfree[bs]);
           }

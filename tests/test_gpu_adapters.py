@@ -428,3 +428,30 @@ def test_equal_bits_from_cold_caches(twq, device, b, m, n, r, kind, codes):
         gotb = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
         assert all(torch.equal(p, q) for p, q in zip(got + gotb, want + wantb))
     assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("b,m,n,r,count", [
+    (2900, 256, 8192, 16, 7),   # forward pass: partial tiles of rows that follow one another
+    (1500, 6400, 256, 48, 3),   # gradients: dx of 100 units of 64 columns
+    (700, 5120, 4096, 128, 2),  # two stages of base only
+])
+def test_base_stages_are_refilled(twq, device, b, m, n, r, count):
+    """A stage of base is combined in place and then filled again, by TMA where a tile's rows
+    follow one another and by single copies where they do not; both kinds of tiles in turn,
+    full and partial, base apart from the output and in its place."""
+    c = Case(twq, device, b, m, n, r, count, "runs", False)
+    ids = c.ids.clone()
+    scattered = torch.randperm(b // 3, generator=torch.Generator().manual_seed(2))
+    ids[:b // 3] = ids[:b // 3][scattered]
+    c.ids = ids
+    c.groups = twq.group_rows(ids.to(device), count)
+    want = c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+    wantb = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    c.check_linear(c.base, want)
+    c.check_backward(c.dx_base, wantb)
+    for _ in range(20):
+        y, dx = c.base.clone(), c.dx_base.clone()
+        got = c.linear(*c.xargs, c.ad, c.groups, base=y, y=y)
+        gotb = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=dx, dx=dx)
+        assert all(torch.equal(p, q) for p, q in zip(got + gotb, want + wantb))
+    assert twq.device_status() == 0
