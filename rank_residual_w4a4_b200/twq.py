@@ -528,10 +528,10 @@ class RowGroups:
     by id with the rows without adapter last, and `offsets` (count + 1), both int32;
     group g is order[offsets[g]:offsets[g + 1]]."""
 
-    def __init__(self, b: int, count: int, device):
+    def __init__(self, b: int, count: int, device, stream=None):
         self.b, self.count = b, count
         self._o, self._t, words = _group_words(b, count)
-        self._buf = torch.empty(words, dtype=torch.int32, device=device)
+        self._buf = _empty(words, torch.int32, device, stream)
         p = self._buf.data_ptr()
         self._c = _RowGroups(b, count, p, p + 4 * self._o, p + 4 * self._t)
         self._ref = ctypes.byref(self._c)
@@ -558,8 +558,7 @@ def group_rows(ids: torch.Tensor, count: int, groups: RowGroups | None = None,
         raise TypeError("ids must be a 1-D torch tensor")
     p = _dev(ids, "ids", torch.int32)
     if groups is None:
-        groups = RowGroups(ids.shape[0], count, ids.device)
-        _keep(stream, groups._buf)
+        groups = RowGroups(ids.shape[0], count, ids.device, stream)
     elif (groups.b, groups.count) != (ids.shape[0], count) or groups.device != ids.device:
         raise ValueError("groups must have the sizes and the device of this call")
     st, back = _on(ids.device, stream)
@@ -605,11 +604,16 @@ def _on(device, stream):
     return _raw_stream(device.index) if stream is None else stream.cuda_stream, back
 
 
-def _keep(stream, *tensors):
-    """Buffers allocated here for work on another stream stay reserved until it is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _empty(shape, dtype, device, stream):
+    """A buffer for a call on `stream`, out of that stream's own memory: what the caller's stream
+    has freed may still be in use by work queued there, which `stream` does not wait for. Once
+    freed, it stays reserved until the caller's stream, too, is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _mat(t, name, dtype, rows, cols, device) -> int:
@@ -647,11 +651,9 @@ def _adapter_linear(fn, args, ad, groups, base, y, h, stream):
     b, dev, bf = groups.b, ad.device, torch.bfloat16
     pb = None if base is None else _mat(base, "base", bf, b, ad.n, dev)
     if y is None:
-        y = torch.empty((b, ad.n), dtype=bf, device=dev)
-        _keep(stream, y)
+        y = _empty((b, ad.n), bf, dev, stream)
     if h is None:
-        h = torch.empty((b, ad.r), dtype=bf, device=dev)
-        _keep(stream, h)
+        h = _empty((b, ad.r), bf, dev, stream)
     ph, py = _mat(h, "h", bf, b, ad.r, dev), _mat(y, "y", bf, b, ad.n, dev)
     st, back = _on(dev, stream)
     status = getattr(_lib, fn)(*args, b, ad._ref, groups._ref, pb, ph, py, st)
@@ -692,22 +694,18 @@ def _adapter_backward(fn, dy, args, h, ad, groups, dx_base, dx, da, db, workspac
     pdy, ph = _mat(dy, "dy", bf, b, ad.n, dev), _mat(h, "h", bf, b, ad.r, dev)
     pb = None if dx_base is None else _mat(dx_base, "dx_base", bf, b, ad.m, dev)
     if dx is None:
-        dx = torch.empty((b, ad.m), dtype=bf, device=dev)
-        _keep(stream, dx)
+        dx = _empty((b, ad.m), bf, dev, stream)
     if da is None:
-        da = torch.empty_like(ad.a)
-        _keep(stream, da)
+        da = _empty(ad.a.shape, bf, dev, stream)
     if db is None:
-        db = torch.empty_like(ad.b)
-        _keep(stream, db)
+        db = _empty(ad.b.shape, bf, dev, stream)
     for t, like, name in ((da, ad.a, "da"), (db, ad.b, "db")):
         if t.shape != like.shape or t.device != dev:
             raise ValueError("%s must have the shape and device of the adapters' weights" % name)
     if workspace is None:
-        workspace = torch.empty(
+        workspace = _empty(
             max(adapter_backward_workspace_bytes(b, ad.m, ad.n, ad.r, ad.count), 16),
-            dtype=torch.uint8, device=dev)
-        _keep(stream, workspace)
+            torch.uint8, dev, stream)
     elif workspace.device != dev:
         raise ValueError("workspace must be on the adapters' device")
     pdx, pa, pbb = _mat(dx, "dx", bf, b, ad.m, dev), _dev(da, "da", bf), _dev(db, "db", bf)

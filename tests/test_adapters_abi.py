@@ -131,3 +131,60 @@ def test_binding_refuses_host_tensors(lib):
     bf = torch.bfloat16
     with pytest.raises(ValueError):
         twq.Adapters(torch.zeros(1, 8, 128, dtype=bf), torch.zeros(1, 128, 8, dtype=bf), torch.zeros(1))
+
+
+def test_buffers_come_from_the_stream_of_the_call(lib, monkeypatch):
+    """With stream=s, what a call allocates is s's memory (a block freed on the caller's stream
+    may have work queued there that s does not wait for) and is kept for the caller's stream,
+    which reads it next. On the host: streams and tensors are stand-ins."""
+    import contextlib
+    from types import SimpleNamespace
+
+    now, made = ["caller"], []
+
+    class Buffer:
+        def __init__(self, shape, device):
+            self.shape, self.device, self.home, self.kept = shape, device, now[0], []
+            made.append(self)
+
+        def record_stream(self, stream):
+            self.kept.append(stream)
+
+        def data_ptr(self):
+            return A
+
+        def numel(self):
+            return 1 << 20
+
+    @contextlib.contextmanager
+    def on(stream):
+        now[0], back = stream, now[0]
+        yield
+        now[0] = back
+
+    ok = lambda *args: 0
+    monkeypatch.setattr(twq, "_lib", SimpleNamespace(
+        twq_row_groups_sizes=lib.twq_row_groups_sizes, twq_group_rows=ok, twq_adapter_linear=ok,
+        twq_adapter_backward=ok, twq_adapter_backward_workspace_bytes=lambda *args: 64))
+    monkeypatch.setattr(twq, "_on", lambda device, stream: (0, None))
+    monkeypatch.setattr(twq, "_mat", lambda *args: A)
+    monkeypatch.setattr(twq, "_dev", lambda *args: A)
+    monkeypatch.setattr(twq, "_strided_x", lambda *args: (A, 256))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now[0])
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: Buffer(shape, device))
+    monkeypatch.setattr(torch, "empty_like", lambda t: Buffer(t.shape, "gpu"))
+    ad = SimpleNamespace(m=256, n=128, r=8, count=2, device="gpu", _ref=None, a=Buffer((2, 8, 256), "gpu"),
+                         b=Buffer((2, 128, 8), "gpu"))
+    ids = torch.zeros(5, dtype=torch.int32)
+    for stream, home in ((None, "caller"), ("s", "s")):
+        del made[:]
+        groups = twq.group_rows(ids, 2, stream=stream)
+        y, h = twq.adapter_linear(None, ad, SimpleNamespace(b=5, count=2, device="gpu", _ref=None),
+                                  stream=stream)
+        grads = twq.adapter_backward(None, None, None, ad,
+                                     SimpleNamespace(b=5, count=2, device="gpu", _ref=None), stream=stream)
+        assert [t.shape for t in (y, h, *grads)] == [(5, 128), (5, 8), (5, 256), (2, 8, 256), (2, 128, 8)]
+        assert len(made) == 7 and groups._buf in made
+        assert all(t.home == home for t in made)
+        assert all(t.kept == ([] if stream is None else ["caller"]) for t in made)

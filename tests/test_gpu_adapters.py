@@ -455,3 +455,27 @@ def test_base_stages_are_refilled(twq, device, b, m, n, r, count):
         gotb = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=dx, dx=dx)
         assert all(torch.equal(p, q) for p, q in zip(got + gotb, want + wantb))
     assert twq.device_status() == 0
+
+
+def test_call_on_another_stream_while_the_callers_is_busy(twq, device):
+    """A block that the caller has freed while work on it is still queued: a call on another
+    stream, whose inputs are ready, must not be given that block."""
+    c = Case(twq, device, 64, 512, 1024, 16, 3, "mixed", False)
+    want = (twq.adapter_linear(c.x, c.ad, c.groups, base=c.base)
+            + twq.adapter_backward(c.dy, c.x, c.h, c.ad, c.groups))
+    ids = c.ids.to(device)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = [t.numel() * 2 for t in want]
+    sizes += [twq.adapter_backward_workspace_bytes(64, 512, 1024, 16, 3), c.groups._buf.numel() * 4]
+    blocks = [torch.empty(k, dtype=torch.uint8, device=device) for k in sizes]
+    torch.cuda._sleep(200000000)  # some 0.1 s
+    for t in blocks:
+        t.fill_(255)
+    del blocks, t
+    g = twq.group_rows(ids, 3, stream=s)
+    got = (twq.adapter_linear(c.x, c.ad, g, base=c.base, stream=s)
+           + twq.adapter_backward(c.dy, c.x, c.h, c.ad, g, stream=s))
+    torch.cuda.synchronize()
+    assert torch.equal(g.order, c.groups.order) and torch.equal(g.offsets, c.groups.offsets)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
