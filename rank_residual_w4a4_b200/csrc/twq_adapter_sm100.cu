@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "sm100_ptx.cuh"
 #include "twq_adapter.h"
@@ -1682,31 +1683,46 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_shape_kernel(int* ou
   extern __shared__ int shape_smem[];
   if (out) out[0] = shape_smem[threadIdx.x];
 }
-// Clusters of `size` shrink blocks with `smem` bytes that the GPU can hold at once (rank16, kind:
-// what smem depends on); asked once.
-int clusters_that_fit(int kind, int size, int rank16, int smem) {
-  static std::atomic<int> known[3][9][9];
-  int v = known[kind][size][rank16].load(std::memory_order_relaxed);
-  if (v > 0) return v;
-  cudaFuncSetAttribute(shrink_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + 1024);
-  cudaFuncSetAttribute(shrink_shape_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(size, 2 * kSms);
-  cfg.blockDim = dim3(kShrinkThreads);
-  cfg.dynamicSmemBytes = smem + 1024;  // and the kernels' static part
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = size;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&v, shrink_shape_kernel, &cfg) != cudaSuccess || v < 1) {
-    cudaGetLastError();  // not a launch's error
-    v = std::max(1, 2 * kSms * 6 / 7 / size);
+// The cluster size for `tiles` row tiles of a shrink kernel with `smem` bytes of shared memory
+// (kind, rank16: what smem depends on): at most 8 blocks, as many as let all clusters run at once (a
+// cluster keeps within a GPC: 33 clusters of 7 fit, or 44 of 6, and a second wave doubles the time:
+// 45 against 25 us for 38 tiles of codes); one cluster in 20 may come late.
+// How many fit is asked once per device, under a lock, and only an answer is kept: the size sets the
+// order of the sums, so it must not depend on which call comes first or on which thread.
+cudaError_t cluster_size(int tiles, int kind, int rank16, int smem, int* size) {
+  constexpr int kDevices = 64;
+  static std::mutex mu;
+  static int known[kDevices][3][9][9];  // clusters that fit, plus 1; 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  for (*size = 8; *size > 1; --*size) {
+    int fit = dev < kDevices ? known[dev][kind][*size][rank16] - 1 : -1;
+    if (fit < 0) {
+      e = allow_smem(shrink_shape_kernel, kMaxSmem);
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(*size, 2 * kSms);
+      cfg.blockDim = dim3(kShrinkThreads);
+      cfg.dynamicSmemBytes = smem + 1024;  // and the kernels' static part
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = *size;
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&fit, shrink_shape_kernel, &cfg);
+      if (e != cudaSuccess) {
+        cudaGetLastError();  // returned here; not a later launch's error
+        return e;
+      }
+      if (dev < kDevices) known[dev][kind][*size][rank16] = fit + 1;
+    }
+    if (int64_t(tiles) * 20 <= int64_t(fit) * 21) break;
   }
-  known[kind][size][rank16].store(v, std::memory_order_relaxed);
-  return v;
+  return cudaSuccess;
 }
 
 // trans: W is count x k x r (the backward pass's B).
@@ -1726,15 +1742,12 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
   const int smem = std::max(per * (p.stages * 16384 + p.wstages * wbytes), 128 * (rp + 4) * 4) + 1024;
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
-  // Split the reduction over a cluster of up to 8 blocks, as many as let all tiles run at once (a
-  // cluster keeps within a GPC: 33 clusters of 7 fit, or 44 of 6, and a second wave doubles the
-  // time: 45 against 25 us for 38 tiles of codes); one cluster in 20 may come late.
-  int splits = 8;
-  while (splits > 1 && tiles_estimate(c) * 20 > clusters_that_fit(trans ? 2 : codes, splits, rp / 16, smem) * 21)
-    --splits;
+  int splits = 1;  // blocks of a cluster, over which the reduction is split
+  cudaError_t e = cluster_size(tiles_estimate(c), trans ? 2 : codes, rp / 16, smem, &splits);
+  if (e != cudaSuccess) return e;
   const dim3 grid(splits, row_tiles_cap(c.g.b, c.g.count, 128));
-  cudaError_t e = trans ? encode<3>(&p.wmap, w, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 64, 1})
-                        : encode_rows(&p.wmap, w, int64_t(c.g.count) * c.r, k, k, rp);
+  e = trans ? encode<3>(&p.wmap, w, {c.r, k, c.g.count}, {c.r, int64_t(c.r) * k}, {64, 64, 1})
+            : encode_rows(&p.wmap, w, int64_t(c.g.count) * c.r, k, k, rp);
   if (e == cudaSuccess && !codes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
   if (e == cudaSuccess && !codes) e = encode_rows(&p.map16, z, c.g.b, k, ldz, 16);
   // a pair of codes as one element: the copies are the same bytes

@@ -479,3 +479,70 @@ def test_call_on_another_stream_while_the_callers_is_busy(twq, device):
     torch.cuda.synchronize()
     assert torch.equal(g.order, c.groups.order) and torch.equal(g.offsets, c.groups.offsets)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+FIRST = [(1300, 1024, 256, r, 3, codes) for r in (16, 48, 80, 112, 128) for codes in (False, True)]
+
+
+def first_calls(binding, device, how):
+    """Digests of the outputs of FIRST's calls: one after another, at once on a thread each, or
+    each captured into a graph without a call before."""
+    import hashlib
+    import threading
+
+    def digest(tensors):
+        torch.cuda.synchronize()
+        return hashlib.sha256(b"".join(t.view(torch.int16).cpu().numpy().tobytes() for t in tensors)).hexdigest()
+
+    cases = [Case(binding, device, b, m, n, r, count, "mixed", codes) for b, m, n, r, count, codes in FIRST]
+    torch.cuda.synchronize()
+
+    def call(c):
+        return (*c.linear(*c.xargs, c.ad, c.groups, base=c.base),
+                *c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base))
+
+    out = [None] * len(cases)
+    if how == "in turn":
+        out = [call(c) for c in cases]
+    elif how == "threads":
+        gate = threading.Barrier(len(cases))
+
+        def run(i):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                gate.wait()
+                out[i] = call(cases[i])
+                torch.cuda.current_stream().synchronize()
+
+        threads = [threading.Thread(target=run, args=(i,)) for i in range(len(cases))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    else:
+        for i, c in enumerate(cases):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                out[i] = call(c)
+            graph.replay()
+            torch.cuda.synchronize()
+    return [digest(o) for o in out]
+
+
+@pytest.mark.parametrize("how", ["threads", "captured"])
+def test_first_calls_of_a_process(twq, device, how):
+    """What the library asks once (how many clusters fit) has the same answer, so the calls the
+    same bits, whichever call comes first: from several threads at once, or under capture."""
+    import os
+    import subprocess
+    import sys
+
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import torch, test_gpu_adapters as t\n"
+            "from rank_residual_w4a4_b200 import twq\n"
+            "twq.load()\n"
+            "print('\\n'.join(t.first_calls(twq, torch.device('cuda:0'), %r)))\n"
+            % (os.path.dirname(os.path.abspath(__file__)),
+               os.path.dirname(os.path.dirname(os.path.abspath(__file__))), how))
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+    assert run.stdout.split() == first_calls(twq, device, "in turn")
