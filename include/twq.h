@@ -517,11 +517,12 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
  * Drops the library's host-side caches: the encoded TMA tensor maps of the
  * decode path (a direct-mapped table of 256 entries keyed by base pointer,
  * shape, stride and box; an entry only encodes an address and a shape, so a hit
- * is always exact and the table never needs clearing for correctness) and the
- * resolved device addresses of twq_unfused_linear_noalloc's scratch array.
+ * is always exact and the table never needs clearing for correctness), the
+ * resolved device addresses of twq_unfused_linear_noalloc's scratch array, and
+ * the record of which adapter kernels have their shared-memory limit set.
  * After a cudaDeviceReset in the caller's process, call this before the next
  * call into the library: the reset ends the context that the cached scratch
- * address belonged to. Host only; launches nothing; safe to call at any time
+ * address belonged to, and the limits with it. Host only; launches nothing; safe to call at any time
  * from any thread (calls in flight on other threads keep the entries they
  * already read).
  */

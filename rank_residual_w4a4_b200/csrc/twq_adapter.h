@@ -5,8 +5,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "../../include/twq.h"
 
 namespace twq {
@@ -61,26 +59,15 @@ inline int32_t* first128_of(const RowGroupsView& g) {
 
 cudaError_t launch_group_rows(const int32_t* ids, const RowGroupsView& g, cudaStream_t st);
 
-// Allows `kernel` `smem` bytes of dynamic shared memory (its largest use), once per device.
+// Allows `kernel` `smem` bytes of dynamic shared memory (its largest use), once per device and again
+// after twq_release_cache.
+cudaError_t allow_smem(const void* kernel, int smem);
 template <typename Kernel>
 cudaError_t allow_smem(Kernel* kernel, int smem) {
-  static std::atomic<const void*> known[64][16];  // by device; a kernel's pointer where it is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const void* k = reinterpret_cast<const void*>(kernel);
-  std::atomic<const void*>* list = known[dev & 63];
-  for (int i = 0; dev < 64 && i < 16; ++i)
-    if (list[i].load(std::memory_order_acquire) == k) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e != cudaSuccess) return e;
-  for (int i = 0; dev < 64 && i < 16; ++i) {
-    const void* none = nullptr;
-    if (list[i].compare_exchange_strong(none, k, std::memory_order_acq_rel) || none == k) break;
-  }
-  return cudaSuccess;
+  return allow_smem(reinterpret_cast<const void*>(kernel), smem);
 }
+// twq_release_cache: forget for which kernels that was done (a reset of the device undoes it).
+void release_adapter_cache();
 
 struct AdapterCall {
   RowGroupsView g;

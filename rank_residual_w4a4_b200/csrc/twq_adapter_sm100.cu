@@ -1885,7 +1885,36 @@ BackwardPlan backward_plan(int64_t b, int64_t m, int64_t n, int64_t r, int64_t c
   return s;
 }
 
+// By device; a kernel's pointer where its limit is set. More places than the adapters have kernels.
+constexpr int kKnownDevices = 64, kKnownKernels = 40;
+std::atomic<const void*> g_allowed[kKnownDevices][kKnownKernels];
+
 }  // namespace
+
+cudaError_t allow_smem(const void* kernel, int smem) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<const void*>* list = dev < kKnownDevices ? g_allowed[dev] : nullptr;
+  for (int i = 0; list && i < kKnownKernels; ++i) {
+    const void* k = list[i].load(std::memory_order_acquire);
+    if (k == kernel) return cudaSuccess;
+    if (!k) break;
+  }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e != cudaSuccess) return e;
+  for (int i = 0; list && i < kKnownKernels; ++i) {
+    const void* none = nullptr;
+    if (list[i].compare_exchange_strong(none, kernel, std::memory_order_acq_rel) || none == kernel) break;
+  }
+  return cudaSuccess;
+}
+
+void release_adapter_cache() {
+  for (auto& list : g_allowed)
+    for (auto& k : list) k.store(nullptr, std::memory_order_release);
+}
 
 cudaError_t read_and_clear_adapter_status(int* code) {
   cudaError_t e = cudaMemcpyFromSymbol(code, g_adapter_status, sizeof(int));

@@ -550,6 +550,7 @@ twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx, int64_t
 void twq_release_cache(void) {
   twq::release_decode_cache();
   twq::release_noalloc_cache();
+  twq::release_adapter_cache();
 }
 
 int twq_launches_per_call(const char* ep) {

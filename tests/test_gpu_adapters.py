@@ -546,3 +546,15 @@ def test_first_calls_of_a_process(twq, device, how):
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
     assert run.stdout.split() == first_calls(twq, device, "in turn")
+
+
+def test_calls_after_a_reset_of_the_device(twq, device):
+    """twq_release_cache is all that a program has to call after a cudaDeviceReset. In a process
+    of its own, whose context is the one that ends."""
+    import os
+    import subprocess
+    import sys
+    run = subprocess.run([sys.executable, os.path.join(os.path.dirname(os.path.abspath(__file__)),
+                                                       "device_reset.py")],
+                         capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
