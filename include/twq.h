@@ -519,7 +519,8 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
  * shape, stride and box; an entry only encodes an address and a shape, so a hit
  * is always exact and the table never needs clearing for correctness), the
  * resolved device addresses of twq_unfused_linear_noalloc's scratch array, and
- * the record of which adapter kernels have their shared-memory limit set.
+ * the record of which decode and adapter kernels have their shared-memory limit
+ * set.
  * After a cudaDeviceReset in the caller's process, call this before the next
  * call into the library: the reset ends the context that the cached scratch
  * address belonged to, and the limits with it. Host only; launches nothing; safe to call at any time

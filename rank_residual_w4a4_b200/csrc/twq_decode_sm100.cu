@@ -898,6 +898,9 @@ bool d_encode_raw(CUtensorMap* map, CUtensorMapDataType dt, const void* base, ui
                   CUtensorMapSwizzle sw);
 
 // Drops every cached map (twq_release_cache).
+// Counts twq_release_cache's calls: what was set in an earlier epoch is set again.
+std::atomic<uint32_t> g_smem_epoch{1};
+
 void clear_map_cache() {
   std::lock_guard<std::mutex> lock(g_map_mutex);
   for (MapEntry& e : g_map_cache) e.valid = false;
@@ -978,16 +981,17 @@ cudaError_t launch_decode_mode(const GemmCall& c, cudaStream_t st) {
   }
   if (!ok) return cudaErrorInvalidValue;
   auto kern = twq_decode_kernel<kMode, KS, kQ, kA8, kS2Q>;
-  // The shared-memory opt-in is a driver call: once per instantiation and device.
-  static std::atomic<uint64_t> smem_set{0};
+  // The shared-memory opt-in is a driver call: once per instantiation and device (and again
+  // after twq_release_cache: a reset of the device undoes it).
+  static std::atomic<uint32_t> smem_set[64];  // the epoch in which it was done
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-  if (!bit || !(smem_set.load(std::memory_order_relaxed) & bit)) {
+  const uint32_t epoch = g_smem_epoch.load(std::memory_order_acquire);
+  if (dev >= 64 || smem_set[dev].load(std::memory_order_relaxed) != epoch) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DLayout::kAlloc);
     if (e != cudaSuccess) return e;
-    smem_set.fetch_or(bit);
+    if (dev < 64) smem_set[dev].store(epoch, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(KS, a.n / 128, 1);
@@ -1065,6 +1069,9 @@ cudaError_t read_and_clear_decode_status(int* code) {
   return e;
 }
 
-void release_decode_cache() { clear_map_cache(); }
+void release_decode_cache() {
+  clear_map_cache();
+  g_smem_epoch.fetch_add(1, std::memory_order_acq_rel);
+}
 
 }  // namespace twq

@@ -1,5 +1,5 @@
-"""Run as a program, without torch: adapter calls, a cudaDeviceReset, twq_release_cache, and the
-same calls on new buffers. Exits 0 if every call succeeds and the outputs are equal."""
+"""Run as a program, without torch: adapter and layer calls, a cudaDeviceReset, twq_release_cache,
+and the same calls on new buffers. Exits 0 if every call succeeds and the outputs are equal."""
 import ctypes
 import importlib.util
 import os
@@ -11,6 +11,10 @@ P, I = ctypes.c_void_p, ctypes.c_int64
 
 class Groups(ctypes.Structure):
     _fields_ = [("b", I), ("count", I), ("order", P), ("offsets", P), ("tiles", P)]
+
+
+class Weights(ctypes.Structure):
+    _fields_ = [("m", I), ("n", I), ("r", I), ("rq", P), ("sr", P), ("l1q", P), ("sl1", P), ("l2t", P)]
 
 
 class Adapters(ctypes.Structure):
@@ -27,15 +31,38 @@ def cudart():
     raise OSError("libcudart.so.12 not found")
 
 
-def run(rt, lib, b):
-    m, n, r, count = 512, 256, 16, 2
-
+def alloc_on(rt):
     def alloc(nbytes, byte=0):
         p = P()
         assert rt.cudaMalloc(ctypes.byref(p), ctypes.c_size_t(max(nbytes, 256))) == 0
         assert rt.cudaMemset(p, byte, ctypes.c_size_t(max(nbytes, 256))) == 0
         return p.value
+    return alloc
 
+
+def fetch(rt, p, nbytes):
+    host = ctypes.create_string_buffer(nbytes)
+    assert rt.cudaMemcpy(host, P(p), ctypes.c_size_t(nbytes), 2) == 0
+    return host.raw
+
+
+def run_layer(rt, lib, b):
+    m, n, r = 512, 512, 32
+    alloc = alloc_on(rt)
+    w = Weights(m, n, r, alloc(n * m // 2, 0x11), alloc(m // 128 * n * 4, 0x3c), alloc(r * m // 2, 0x11),
+                alloc(m // 128 * r * 4, 0x3c), alloc(n * r * 2, 0x3c))
+    y = alloc(b * n * 2)
+    status = lib.twq_fused_linear(P(alloc(b * m // 2, 0x11)), P(alloc(b * m // 128 * 4, 0x3c)), I(b),
+                                  ctypes.byref(w), P(y), None)
+    assert status == 0, status
+    out = fetch(rt, y, b * n * 2)
+    assert any(out)
+    return out
+
+
+def run(rt, lib, b):
+    m, n, r, count = 512, 256, 16, 2
+    alloc = alloc_on(rt)
     sizes = (ctypes.c_size_t * 3)()
     assert lib.twq_row_groups_sizes(I(b), I(count), sizes) == 0
     g = Groups(b, count, *[alloc(s) for s in sizes])
@@ -55,11 +82,8 @@ def run(rt, lib, b):
     ]
     assert status == [0, 0, 0], status
     assert rt.cudaDeviceSynchronize() == 0
-    out = []
-    for p, nbytes in ((y, b * n * 2), (dx, b * m * 2), (da, count * r * m * 2), (db, count * n * r * 2)):
-        host = ctypes.create_string_buffer(nbytes)
-        assert rt.cudaMemcpy(host, P(p), ctypes.c_size_t(nbytes), 2) == 0
-        out.append(host.raw)
+    out = [fetch(rt, p, nbytes) for p, nbytes in ((y, b * n * 2), (dx, b * m * 2), (da, count * r * m * 2),
+                                                  (db, count * n * r * 2))]
     assert any(out[0])
     return out
 
@@ -67,10 +91,14 @@ def run(rt, lib, b):
 def main():
     rt = cudart()
     lib = ctypes.CDLL(os.path.join(ROOT, "rank_residual_w4a4_b200", "libtwq.so"))
-    before = [run(rt, lib, b) for b in (40, 2000)]
+
+    def calls():
+        return [run(rt, lib, b) for b in (40, 2000)] + [run_layer(rt, lib, b) for b in (4, 300)]
+
+    before = calls()
     assert rt.cudaDeviceReset() == 0
     lib.twq_release_cache()
-    assert [run(rt, lib, b) for b in (40, 2000)] == before
+    assert calls() == before
 
 
 if __name__ == "__main__":
