@@ -289,6 +289,10 @@ __device__ __forceinline__ void store_value(uint16_t* out, int64_t row, int r, i
                  pack2(left(v.z, lo_f(hi.y)), left(v.w, hi_f(hi.y))));
 }
 
+// The sum of the two terms' products. Where X holds an infinity the first term alone has the sign:
+// the second, which may be zero or of the other sign, would make a NaN of it.
+__device__ __forceinline__ float both_terms(float v, float w) { return isfinite(v) ? v + w : v; }
+
 // A block's work items, each a part of a row tile: item k is number first + stride k, in tile
 // number / parts.
 struct Items {
@@ -1511,7 +1515,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
           float o[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            o[u] = f * (kByRank ? __uint_as_float(v[u]) + __uint_as_float(w[u]) : __uint_as_float(v[u]));
+            o[u] = f * (kByRank ? both_terms(__uint_as_float(v[u]), __uint_as_float(w[u])) : __uint_as_float(v[u]));
           if (!whole) {
             *reinterpret_cast<float4*>(quads + c * 128) = make_float4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<float4*>(quads + (c + 4) * 128) = make_float4(o[4], o[5], o[6], o[7]);

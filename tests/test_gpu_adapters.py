@@ -558,3 +558,63 @@ def test_calls_after_a_reset_of_the_device(twq, device):
                                                        "device_reset.py")],
                          capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def check_infinities(got, want, bound, what):
+    """As the definition: NaN where it has NaN, an infinity of its sign where it has one, and
+    within the bound elsewhere."""
+    g = got.double()
+    assert torch.equal(g.isnan(), want.isnan()), "NaN of %s" % what
+    inf = want.isinf()
+    assert torch.equal(g[inf], want[inf]), "infinities of %s" % what
+    fin = want.isfinite()
+    assert bool(g[fin].isfinite().all()) and bool(bound[fin].isfinite().all()), what
+    assert bool(((g[fin] - want[fin]).abs() <= bound[fin]).all()), what
+
+
+def with_infinite_x(twq, device, b, r, codes):
+    """A case with an infinity in the X of one row, positive A and B, so that no two infinities
+    meet in a sum: (the case, the row, the columns of the infinity)."""
+    c = Case(twq, device, b, 512, 256, r, 2, "one", codes)
+    c.ad.a.abs_(), c.ad.b.abs_()
+    i = b // 2
+    if codes:
+        xq8, sx = c.xargs
+        xq8[i, 130], xq8[i, 128:256] = 1, xq8[i, 128:256].abs().clamp(min=1)
+        sx[i, 1] = float("inf")
+        c.x64 = ref.x_of_codes(xq8, sx)
+        return c, i, slice(128, 256)
+    c.x[i, 130] = float("inf")
+    c.x64 = c.x.double()
+    return c, i, slice(130, 131)
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 72, 120])
+@pytest.mark.parametrize("b", [3, 1700])
+def test_gradients_with_an_infinite_x(twq, device, b, r, codes):
+    """The gradient of A is infinite, of the sign that dh has, in the infinity's columns, and
+    nothing else is."""
+    c, _, columns = with_infinite_x(twq, device, b, r, codes)
+    got = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    want = c.ref_backward(c.dx_base)
+    assert bool(want[0][1][-1][:, columns].isinf().all()) and int(want[0][1].isfinite().sum()) > 0
+    for g, w, e, name in zip(got, *want, ("dx", "da", "db")):
+        check_infinities(g, w, e, name)
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("r", [8, 24, 80])
+@pytest.mark.parametrize("b", [3, 1700])
+def test_infinite_dy_of_a_row_with_an_adapter(twq, device, b, r):
+    """An infinity in dY: dh of its row is infinite, so dx of that row (A is positive) and, where
+    the row's X is not zero, all of dA; dB in the infinity's column."""
+    c = Case(twq, device, b, 512, 256, r, 2, "one", False)
+    c.ad.a.abs_(), c.ad.b.abs_()
+    c.dy[b // 2, 200] = float("-inf")
+    got = c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    want = c.ref_backward(c.dx_base)
+    assert bool(want[0][0][b // 2].isinf().all())
+    for g, w, e, name in zip(got, *want, ("dx", "da", "db")):
+        check_infinities(g, w, e, name)
+    assert twq.device_status() == 0
