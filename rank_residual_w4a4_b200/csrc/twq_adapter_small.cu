@@ -210,7 +210,8 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
     for (int s = 0; s < kRanks; ++s) v += o[s];
     const int rr = i / kR, col = i % kR;
-    const uint16_t h = static_cast<uint16_t>(pack2(v, 0.0f));
+    // ranks from r on: zero whatever x holds (an infinity times their zero weights is a NaN)
+    const uint16_t h = col < c.r ? static_cast<uint16_t>(pack2(v, 0.0f)) : 0;
     s_h[rr * (kR + 8) + col] = h;
     if (rank == 0 && rr < t.z && col < c.r) c.h[static_cast<int64_t>(c.g.order[t.y + rr]) * c.r + col] = h;
   }

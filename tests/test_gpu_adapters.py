@@ -592,6 +592,20 @@ def with_infinite_x(twq, device, b, r, codes):
 @pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
 @pytest.mark.parametrize("r", [8, 16, 24, 40, 72, 120])
 @pytest.mark.parametrize("b", [3, 1700])
+def test_infinite_x_of_a_row_with_an_adapter(twq, device, b, r, codes):
+    """h and y of the infinity's row are infinite, and no other row's."""
+    c, i, _ = with_infinite_x(twq, device, b, r, codes)
+    got = c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+    want = c.ref_linear(c.base)
+    assert bool(want[0][0][i].isinf().all()) and bool(want[0][1][i].isinf().all())
+    for g, w, e, name in zip(got, *want, ("y", "h")):
+        check_infinities(g, w, e, name)
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 72, 120])
+@pytest.mark.parametrize("b", [3, 1700])
 def test_gradients_with_an_infinite_x(twq, device, b, r, codes):
     """The gradient of A is infinite, of the sign that dh has, in the infinity's columns, and
     nothing else is."""
