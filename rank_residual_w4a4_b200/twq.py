@@ -591,7 +591,8 @@ class Adapters:
         self._ref = ctypes.byref(self._c)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without its Python object
+# current_stream() without its Python object; not in a torch that is built without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(device, stream):
@@ -601,7 +602,9 @@ def _on(device, stream):
     if torch.cuda.current_device() != device.index:
         back = torch.cuda.current_device()
         torch.cuda.set_device(device)
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream, back
+    if stream is None:
+        return (_raw_stream(device.index) if _raw_stream else _stream(None)), back
+    return stream.cuda_stream, back
 
 
 def _empty(shape, dtype, device, stream):

@@ -188,3 +188,17 @@ def test_buffers_come_from_the_stream_of_the_call(lib, monkeypatch):
         assert len(made) == 7 and groups._buf in made
         assert all(t.home == home for t in made)
         assert all(t.kept == ([] if stream is None else ["caller"]) for t in made)
+
+
+def test_binding_imports_with_a_torch_without_cuda(monkeypatch):
+    """Such a torch lacks the private call that tells the current stream; the host-side checks
+    still run there."""
+    import importlib.util
+    import sys
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("rank_residual_w4a4_b200.twq_again", twq.__file__)
+    module = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(sys.modules, spec.name, module)  # dataclasses look their module up
+    spec.loader.exec_module(module)
+    with pytest.raises(ValueError):
+        module.group_rows(torch.zeros(4, dtype=torch.int32), 2)
