@@ -376,7 +376,8 @@ twq_status check_adapters(int64_t b, const twq_adapters* ad, const twq_row_group
   if (s != TWQ_OK) return s;
   if (g->b != b || g->count != ad->count) return TWQ_ERR_INVALID_ARG;
   if (!ad->a || !ad->b || !ad->scale) return TWQ_ERR_INVALID_ARG;
-  if (!g->order || !g->offsets || !g->tiles) return TWQ_ERR_INVALID_ARG;
+  // twq_group_rows' own rule: an empty batch has no order
+  if ((b > 0 && !g->order) || !g->offsets || !g->tiles) return TWQ_ERR_INVALID_ARG;
   if (!aligned16(ad->a) || !aligned16(ad->b) || !aligned16(ad->scale) || !aligned16(g->order) ||
       !aligned16(g->offsets) || !aligned16(g->tiles))
     return TWQ_ERR_MISALIGNED;

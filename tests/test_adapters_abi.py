@@ -202,3 +202,22 @@ def test_binding_imports_with_a_torch_without_cuda(monkeypatch):
     spec.loader.exec_module(module)
     with pytest.raises(ValueError):
         module.group_rows(torch.zeros(4, dtype=torch.int32), 2)
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+def test_empty_batch_needs_no_order(lib, codes):
+    """The order of an empty batch has 0 bytes, so it may be null, as twq_group_rows takes it."""
+    arr = (ctypes.c_size_t * 3)()
+    assert lib.twq_row_groups_sizes(0, 3, arr) == 0 and arr[0] == 0
+    empty = groups(b=0, order=None)
+    if codes:
+        assert lib.twq_adapter_linear_i8(None, None, 0, adapters(), empty, None, None, None, None) == 0
+    else:
+        assert lib.twq_adapter_linear(None, 512, 0, adapters(), empty, None, None, None, None) == 0
+    assert lib.twq_adapter_linear(A, 512, 0, adapters(), groups(b=0, offsets=None), None, A, A, None) == 1
+    # the gradients of an empty batch are zeros that are written: refused for what it lacks alone
+    need = lib.twq_adapter_backward_workspace_bytes(0, 512, 256, 16, 3)
+    args = (None, None, None, None, 0) if codes else (None, None, 512, None, 0)
+    f = lib.twq_adapter_backward_i8 if codes else lib.twq_adapter_backward
+    assert f(*args, adapters(), empty, None, None, None, A, A, need, None) == 1       # da
+    assert f(*args, adapters(), empty, None, None, A, A, A + 8, need, None) == 3      # workspace
