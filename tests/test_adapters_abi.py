@@ -221,3 +221,21 @@ def test_empty_batch_needs_no_order(lib, codes):
     f = lib.twq_adapter_backward_i8 if codes else lib.twq_adapter_backward
     assert f(*args, adapters(), empty, None, None, None, A, A, need, None) == 1       # da
     assert f(*args, adapters(), empty, None, None, A, A, A + 8, need, None) == 3      # workspace
+
+
+@pytest.mark.parametrize("b,count", [(0, 4), (1, 1), (768, 1), (768, 4096), (769, 48), (769, 49),
+                                     (1536, 95), (1536, 96), (1536, 4096), (1537, 97), (1537, 4096),
+                                     (70001, 4096)])
+def test_group_sizes_hold_both_lists_and_the_tiles_before(lib, b, count):
+    """Room for the worst split in both tile lists, for a count of their tiles and for count + 1
+    integers behind them. The 16-row list is there where some rank's forward pass takes it: up to
+    768 rows, and up to 1536 where the adapters may have 16 rows or fewer each."""
+    arr = (ctypes.c_size_t * 3)()
+    assert lib.twq_row_groups_sizes(b, count, arr) == 0
+    entries = 1
+    for rows in (16, 128):
+        if rows == 16 and not (b <= 768 or (b <= 1536 and b <= 16 * count)):
+            continue
+        keys = min(b, count + 1)  # all of them with rows, all but one with one row only
+        entries += (keys - 1) + -(-(b - keys + 1) // rows) if b else 0
+    assert arr[2] >= 16 * entries + 4 * (count + 1)

@@ -632,3 +632,44 @@ def test_infinite_dy_of_a_row_with_an_adapter(twq, device, b, r):
     for g, w, e, name in zip(got, *want, ("dx", "da", "db")):
         check_infinities(g, w, e, name)
     assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("b,count", [(0, 4), (1, 1), (768, 1), (768, 4096), (769, 48), (769, 49),
+                                     (1536, 95), (1536, 96), (1536, 4096), (1537, 97), (1537, 4096),
+                                     (20001, 4096)])
+def test_grouping_stays_inside_its_buffers(twq, device, b, count):
+    """As many tiles as a batch can have (every key has rows, all but one of them one row only):
+    the words around order, offsets and tiles keep their values, and the forward pass of these
+    tiles is right."""
+    import ctypes
+
+    keys = min(b, count + 1)
+    ids = torch.zeros(b, dtype=torch.int32)
+    ids[:keys] = torch.arange(keys, dtype=torch.int32) - 1 + (0 if keys > count else 1)
+    ids = ids[torch.randperm(b, generator=torch.Generator().manual_seed(b))]
+    sizes = (ctypes.c_size_t * 3)()
+    assert twq.load().twq_row_groups_sizes(b, count, sizes) == 0
+    bufs = [torch.full((s // 4 + 128,), 77, dtype=torch.int32, device=device) for s in sizes]
+    g = twq.RowGroups(b, count, device)
+    g._c = twq._RowGroups(b, count, *[t.data_ptr() + 256 for t in bufs])
+    g._ref = ctypes.byref(g._c)
+    twq.group_rows(ids.to(device), count, groups=g)
+    order, offsets = (t[64:-64] for t in bufs[:2])
+    key = torch.where(ids < 0, count, ids).long()
+    assert torch.equal(order.cpu(), torch.sort(key, stable=True).indices.int())
+    assert int(offsets[-1]) == int((ids >= 0).sum())
+    for t in bufs:
+        assert bool((t[:64] == 77).all()) and bool((t[-64:] == 77).all())
+    if b:
+        gen = torch.Generator(device=device).manual_seed(count)
+        normal = lambda *shape: torch.randn(shape, generator=gen, device=device).to(torch.bfloat16)
+        ad = twq.Adapters(normal(count, 8, 128) / 11, normal(count, 128, 8) / 20,
+                          torch.ones(count, device=device))
+        x, base = normal(b, 128), normal(b, 128)
+        got = twq.adapter_linear(x, ad, g, base=base)
+        want = ref.linear(x.double(), ad.a, ad.b, ad.scale, ids.to(device), base.double(), False)
+        for p, w, e, name in zip(got, *want, ("y", "h")):
+            ref.check(p, w, e, name)
+        for t in bufs:
+            assert bool((t[:64] == 77).all()) and bool((t[-64:] == 77).all())
+    assert twq.device_status() == 0
