@@ -514,6 +514,16 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
                                              int64_t wait_limit_ns, twq_stream_t stream);
 
 /*
+ * The same for the adapter kernels: while wait_limit_ns (1 us .. 1 s) is set, the
+ * calling thread's adapter calls of more than one launch run with a loading warp of
+ * each kernel that stops early and with that limit of every wait, so the waits on it
+ * run out. The calls succeed, their outputs are left unspecified, and
+ * twq_device_status() reports a site code (61..67; 68: a copy in flight did not land).
+ * 0 (the initial state) sets it back. Launches nothing itself.
+ */
+TWQ_API twq_status twq_selftest_adapter_stall(int64_t wait_limit_ns);
+
+/*
  * Drops the library's host-side caches: the encoded TMA tensor maps of the
  * decode path (a direct-mapped table of 256 entries keyed by base pointer,
  * shape, stride and box; an entry only encodes an address and a shape, so a hit

@@ -87,7 +87,10 @@ struct AdapterCall {
   uint16_t* da;         // count x r x m
   uint16_t* db;         // count x n x r
   void* workspace;
+  uint64_t wait_ns;     // limit of the kernels' waits
+  int stall;            // self-test: a loading warp stops early, so that the waits on it run out
 };
+constexpr uint64_t kAdapterWaitNs = 2000000000ull;
 
 cudaError_t launch_adapter_linear(const AdapterCall& c, cudaStream_t st);
 // The forward pass for small batches (16-row tiles, one launch).

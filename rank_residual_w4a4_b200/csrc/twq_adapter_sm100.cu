@@ -31,38 +31,41 @@ __device__ int g_adapter_status;
 
 namespace {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a wait that lasts 2 s is a failure
+// A wait that lasts 2 s is a failure (the kernels' limit: AdapterCall::wait_ns, which is this but in
+// the self-test).
+constexpr uint64_t kWaitLimitNs = kAdapterWaitNs;
 constexpr int kSms = 148;
 constexpr int kMaxSmem = 226 * 1024;  // dynamic; the kernels' static part is 1 KB
 
 // Site codes of the bounded waits.
-enum : int { kSiteEmpty = 61, kSiteFull, kSiteAccEmpty, kSiteDone, kSiteHEmpty, kSiteDrain, kSiteEnd };
+enum : int { kSiteEmpty = 61, kSiteFull, kSiteAccEmpty, kSiteDone, kSiteHEmpty, kSiteDrain, kSiteEnd, kSiteLand };
 
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                       int site) {
+struct WaitState {  // a block's, in shared memory
+  int gave_up;
+  uint64_t ns;  // limit of a wait
+};
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
   const uint64_t t0 = global_timer_ns();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    if (w->gave_up) return false;
+    if (global_timer_ns() - t0 > w->ns) {
       atomicCAS(&g_adapter_status, 0, site);
-      *abort_flag = 1;
+      w->gave_up = 1;
       return false;
     }
   }
 }
 // Bounded wait; false once the block is giving up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                     int site) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, site);
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, w, site);
 }
 
 // The same for a whole warp: one answer for all of its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int site) {
-  return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort_flag, site));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, w, site));
 }
 // Waits for MMAs in flight, which complete by themselves, on every way out of a kernel (their
 // issuer may take kWaitLimitNs to give up its own wait, so twice that).
@@ -74,6 +77,29 @@ __device__ __forceinline__ void wait_mmas(uint64_t* bar) {
       break;
     }
   }
+}
+
+// What a block that gives up does about its TMA copies in flight: they must land before it leaves.
+// The copies of steps [issued - slots, issued) of a ring may be; every earlier one has been used.
+// `missing`: how many of a step's arrivals will not come any more, because their threads gave up
+// before it; they are made up for here, so that the step's phase ends once its bytes are there.
+__device__ __noinline__ void land(uint64_t* bar, uint32_t parity, int missing) {
+  if (missing > 0)
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
+                 "r"(missing)
+                 : "memory");
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(&g_adapter_status, kSiteLand);
+      return;
+    }
+  }
+}
+template <typename Missing>
+__device__ __forceinline__ void land_ring(uint64_t* full, int slots, int issued, Missing missing) {
+  for (int step = max(0, issued - slots); step < issued; ++step)
+    land(&full[step % slots], (step / slots) & 1, missing(step));
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
@@ -363,6 +389,8 @@ struct ShrinkArgs {
   bool split;
   // Tiles of Z, 128 x 64, each with its W; with codes: groups of a team, groups of W.
   int stages, wstages;
+  uint64_t wait_ns;
+  int stall;          // self-test: the copies of Z end half way (codes: they are not used)
 };
 
 constexpr int kShrinkThreads = 320;  // 8 warps load Z, then epilogue; MMA warp; TMA warp
@@ -390,7 +418,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   __shared__ uint64_t s_full[kShrinkStages], s_empty[kShrinkStages], s_wfull[kShrinkStages],
       s_wempty[kShrinkStages], s_raw[kCodes ? 16 : 1], s_done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ WaitState s_wait;
+  __shared__ int s_steps[8], s_issued;  // of each loading warp; of the TMA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
   if (tid == 288) {
@@ -417,6 +446,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   const bool tma = t.w >= 0;
   const int groups = (p.k / 128 - rank + splits - 1) / splits;
   const int steps = groups * 2 / kPer;
+  const int z_steps = p.stall ? steps / 2 : steps;
+  const int tma_steps = !kCodes && tma ? z_steps : steps;
   auto column = [&](int tile) { return (rank + (tile >> 1) * splits) * 128 + (tile & 1) * 64; };
   // W's part of a step. Without kTrans the rows beyond r are the next adapter's (or zeros): they
   // only reach accumulator columns that are not stored.
@@ -449,9 +480,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     }
     for (int i = 0; kCodes && i < 16; ++i) mbar_init(&s_raw[i], 1);
     mbar_init(&s_done, 1);
-    s_abort = 0;
+    s_wait.gave_up = 0;
+    s_wait.ns = p.wait_ns;
     fence_barrier_init();
-    for (int step = 0; step < min(steps, kCodes ? p.wstages : p.stages); ++step) {
+    s_issued = min(tma_steps, kCodes ? p.wstages : p.stages);
+    for (int step = 0; step < s_issued; ++step) {
       if (kCodes) {
         mbar_arrive_expect_tx(&s_wfull[step], kPer * wbytes);
         load_w(step, step, &s_wfull[step]);
@@ -473,10 +506,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   if (warp == 9) {
     if (lane == 0) {
       const int ring = kCodes ? p.wstages : p.stages;
-      int slot = 0;
+      int slot = 0, step = s_issued;
       uint32_t phase = 0;
-      for (int step = ring; step < steps; ++step) {
-        if (!wait(kCodes ? &s_wempty[slot] : &s_empty[slot], phase, &s_abort, kSiteEmpty)) break;
+      for (; step < tma_steps; ++step) {
+        if (!wait(kCodes ? &s_wempty[slot] : &s_empty[slot], phase, &s_wait, kSiteEmpty)) break;
         if (kCodes) {
           mbar_arrive_expect_tx(&s_wfull[slot], kPer * wbytes);
           load_w(step, slot, &s_wfull[slot]);
@@ -488,6 +521,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
           phase ^= 1u;
         }
       }
+      s_issued = step;
     }
   } else if (kCodes && warp < 8) {
     if constexpr (kCodes) {
@@ -530,7 +564,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 #pragma unroll
       for (int u = 0; u < 3; ++u) sc[u] = scale_of(u);
       const uint32_t ta = tmem + (static_cast<uint32_t>(sub * 32) << 16) + kShrinkTmemCols + team * 64;
-      bool alive = true;
+      bool alive = !p.stall;
+      int asked = two + 1;  // groups that fetch was called for
       for (int base = 0; base < mine && alive; base += 3) {
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
@@ -539,7 +574,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
           uint4 v[8];
           if (any) {
             if (tma) {
-              alive = warp_wait(&s_raw[warp * 2 + (j & two)], (j >> two) & 1, &s_abort, kSiteFull);
+              alive = warp_wait(&s_raw[warp * 2 + (j & two)], (j >> two) & 1, &s_wait, kSiteFull);
             } else if (two) {
               cp_wait<1>();
             } else {
@@ -549,7 +584,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = lds16(raw + (j & two) * 4096 + sw128(lane, q));
           }
-          alive = alive && (j == 0 || warp_wait(&s_empty[team], (j - 1) & 1, &s_abort, kSiteEmpty));
+          alive = alive && (j == 0 || warp_wait(&s_empty[team], (j - 1) & 1, &s_wait, kSiteEmpty));
           if (!alive) break;
           if (any) {
             tc_fence_after();
@@ -574,9 +609,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
           // memory. (Requested right behind the loads of v, new codes reached some lanes instead
           // of the old ones when this warp then waited for the MMAs.)
           fetch(j + 1 + two);
+          asked = j + 2 + two;
           sc[u] = scale_of(j + 3);
         }
       }
+      if (!alive && any && tma && lane == 0)
+        for (int j = max(0, asked - 1 - two); j < min(asked, mine); ++j)
+          land(&s_raw[warp * 2 + (j & two)], (j >> two) & 1, 0);
       cp_wait_all();
     }
   } else if (warp < 8 && !tma) {
@@ -585,10 +624,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     int row[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) row[j] = r0 + j * 32 < t.z ? __ldg(p.order + t.y + r0 + j * 32) : -1;
-    int slot = 0;
+    int slot = 0, step = 0;
     uint32_t phase = 0;
-    for (int step = 0; step < steps; ++step) {
-      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+    for (; step < z_steps; ++step) {
+      if (step >= p.stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_wait, kSiteEmpty)) break;
       const uint32_t zs = sz + slot * 16384;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -600,14 +639,15 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
         phase ^= 1u;
       }
     }
+    if (lane == 0) s_steps[warp] = step;
     cp_wait_all();
   } else if (warp == 8 && lane == 0) {
     const uint32_t idesc = idesc_bf16(p.rp) | (kTrans ? kBMajorMn : 0u);
     int slot = 0, wslot = 0;  // with codes, slot: the team whose group it is
     uint32_t phase = 0, wphase = 0;
     for (int step = 0; step < steps; ++step) {
-      if (kCodes && !wait(&s_wfull[wslot], wphase, &s_abort, kSiteFull)) break;
-      if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) break;
+      if (kCodes && !wait(&s_wfull[wslot], wphase, &s_wait, kSiteFull)) break;
+      if (!wait(&s_full[slot], phase, &s_wait, kSiteFull)) break;
       if (!kCodes && !tma) fence_proxy_async_smem();
       tc_fence_after();
       if constexpr (kCodes) {
@@ -664,6 +704,18 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
+  if (s_wait.gave_up && tid == 288) {
+    if constexpr (kCodes) {
+      land_ring(s_wfull, p.wstages, s_issued, [](int) { return 0; });
+    } else {
+      land_ring(s_full, p.stages, s_issued, [&](int step) {
+        int missing = 0;
+        for (int w = 0; !tma && w < 8; ++w) missing += s_steps[w] <= step ? 32 : 0;
+        return missing;
+      });
+    }
+  }
+  __syncwarp();
   if (warp == 8) tmem_dealloc(tmem, kCols);
   if (splits > 1) cluster_sync_startup();
   for (int i = tid; i < (hi - lo) * quads; i += kShrinkThreads) {
@@ -805,6 +857,8 @@ struct ExpandArgs {
   int segs;
   SumArgs sum;  // kSums: what the kernel in front left to be added up, `sums` blocks of 256 threads
   int sums;
+  uint64_t wait_ns;
+  int stall;    // self-test: one of the two loading warps stops at the first unit
 };
 
 constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H and base; TMA of W
@@ -856,8 +910,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
   uint64_t* s_hfull = s_bfree + kBaseSlots;
   uint64_t* s_hfree = s_hfull + 2;
   uint64_t* s_end = s_hfree + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_end + 1);
-  int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  WaitState* s_wait = reinterpret_cast<WaitState*>(s_end + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_wait + 1);
+  int* s_units = reinterpret_cast<int*>(s_tmem + 1);  // what each loading warp has asked for: base,
+  int* s_items = s_units + 2;                         // H,
+  int* s_w = s_items + 2;                             // W
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int units = p.n / 64;
   const int total = p.first128[p.count] * p.segs;
@@ -891,7 +948,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         mbar_init(&s_hfree[i], 1);
       }
       mbar_init(s_end, 1);
-      *s_abort = 0;
+      s_wait->gave_up = 0;
+      s_wait->ns = p.wait_ns;
       fence_barrier_init();
     }
     if (warp == 8) {
@@ -920,8 +978,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         const int ue = unit_end(k);
         for (int u = unit_begin(k); u < ue; ++u) {
           if (turn == 0) {
-            alive = warp_wait(&s_done[slot], ph, s_abort, kSiteDone) &&
-                    warp_wait(&s_bfull[bs], bph, s_abort, kSiteFull);
+            alive = warp_wait(&s_done[slot], ph, s_wait, kSiteDone) &&
+                    warp_wait(&s_bfull[bs], bph, s_wait, kSiteFull);
             if (!alive) break;
             tc_fence_after();
             const uint32_t stage = sb + bs * 16384;
@@ -992,13 +1050,13 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         uint32_t ph = 0, hph = 0;
         bool alive = true;
         for (int k = 0; k < items.count && alive; ++k) {
-          if (!wait(&s_hfull[hs], hph, s_abort, kSiteFull)) break;
+          if (!wait(&s_hfull[hs], hph, s_wait, kSiteFull)) break;
           fence_proxy_async_smem();  // H may have come by cp.async
           const uint32_t hb = desc_k(sh + hs * kt * 16384);
           const int ue = unit_end(k);
           for (int u = unit_begin(k); u < ue; ++u, ++i) {
-            alive = wait(&s_full[slot], ph, s_abort, kSiteFull) &&
-                    (i < p.slots || wait(&s_free[slot], ph ^ 1u, s_abort, kSiteAccEmpty));
+            alive = wait(&s_full[slot], ph, s_wait, kSiteFull) &&
+                    (i < p.slots || wait(&s_free[slot], ph ^ 1u, s_wait, kSiteAccEmpty));
             if (!alive) break;
             tc_fence_after();
             const uint32_t ws = sw + slot * p.stage_bytes, d = tmem + slot * 64;
@@ -1059,8 +1117,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
         const int early = kTrans ? min(p.bslots, unit_end(0) - unit_begin(0)) : 0;
         for (; i < early; ++i) load_base(unit_begin(0) + i);
         pdl_wait();
+        int loaded = 0;  // tiles of H
         for (int k = 0; k < items.count && alive; ++k) {
-          if (k >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_abort, kSiteHEmpty)) break;
+          if (k >= p.hslots && !warp_wait(&s_hfree[hs], hph ^ 1u, s_wait, kSiteHEmpty)) break;
           if (ra.run >= 0) {  // rows beyond a partial tile's end are read and not used
             if (tid == 288) {
               mbar_arrive_expect_tx(&s_hfull[hs], kt * 16384);
@@ -1082,9 +1141,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             hs = 0;
             hph ^= 1u;
           }
+          ++loaded;
           const int ue = unit_end(k);
           for (int u = unit_begin(k) + (k == 0 ? early : 0); u < ue; ++u, ++i) {
-            if (i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_abort, kSiteEmpty)) {
+            if ((i >= p.bslots && !warp_wait(&s_bfree[bs], bph ^ 1u, s_wait, kSiteEmpty)) ||
+                (p.stall && warp == 10)) {
               alive = false;
               break;
             }
@@ -1092,6 +1153,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
           }
           ra.advance();
         }
+        if (lane == 0) s_units[warp - 9] = i, s_items[warp - 9] = loaded;
       } else {
         if (lane == 0) {
           int slot = 0, i = 0, next = __ldg(&tiles[items.tile(0)].x);
@@ -1102,7 +1164,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
             const int ue = unit_end(k);
             for (int u = unit_begin(k); u < ue; ++u, ++i) {
               // the MMAs that read this stage are done when their accumulator is
-              if (i >= p.slots && !wait(&s_done[slot], ph ^ 1u, s_abort, kSiteEmpty)) {
+              if (i >= p.slots && !wait(&s_done[slot], ph ^ 1u, s_wait, kSiteEmpty)) {
                 alive = false;
                 break;
               }
@@ -1120,6 +1182,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
               }
             }
           }
+          *s_w = i;
         }
       }
       cp_wait_all();
@@ -1127,6 +1190,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const __grid_
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (s_wait->gave_up && tid == 0) {  // warp 9 issues base's and H's copies, its and warp 10's arrivals count
+      land_ring(s_full, p.slots, *s_w, [](int) { return 0; });
+      land_ring(s_bfull, p.bslots, s_units[0], [&](int step) { return s_units[1] <= step ? 32 : 0; });
+      land_ring(s_hfull, p.hslots, s_items[0], [&](int step) { return s_items[1] <= step ? 32 : 0; });
+    }
+    __syncwarp();
     if (warp == 8) tmem_dealloc(tmem, 64 * kExpandSlots);
   }
 
@@ -1168,6 +1237,8 @@ struct OuterArgs {
   int dcol;           // kDual: first tensor-memory column of the two row accumulators
   uint32_t tmem_cols;
   bool zeros;         // one chunk: no sum kernel follows, which would write them
+  uint64_t wait_ns;
+  int stall;          // self-test: one of the warps that load Z stops at once
 };
 
 // Warps: 8 that load Z (16 convert codes: 8 of them took 0.9 us for a block that HBM delivers in
@@ -1201,7 +1272,8 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   __shared__ uint64_t s_full[kOuterStages], s_empty[kOuterStages], s_hfull[kOuterStages],
       s_hempty[kOuterStages], s_dfull[2], s_dfree[2], s_run, s_free, s_end;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ WaitState s_wait;
+  __shared__ int s_z[kCodes ? 1 : 8], s_w, s_h[2];  // steps of each warp that loads Z; of W; tiles of H
   constexpr int kStage = 32768 + (kDual ? 16384 : 0);
   constexpr int kZ = outer_z_warps(kCodes), kMma = kZ, kDrain = kZ + 1, kLoad = kZ + 5, kMma2 = kZ + 7;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1244,7 +1316,8 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
     mbar_init(&s_end, kDual ? 2 : 1);
     mbar_init(&s_run, 1);
     mbar_init(&s_free, 4);
-    s_abort = 0;
+    s_wait.gave_up = 0;
+    s_wait.ns = p.wait_ns;
     fence_barrier_init();
   }
   if (warp == kMma) {
@@ -1300,9 +1373,10 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
     if constexpr (kCodes) {
       for (int a = 0; a < kOuterAhead; ++a) fetch();
     }
-    int slot = 0;
+    int slot = 0, step = 0;
     uint32_t phase = 0;
-    for (int step = 0; step < steps; ++step) {
+    for (; step < steps; ++step) {
+      if (p.stall && warp == 1) break;
       uint4 v[kRows];
       float sc[kRows];
       if constexpr (kCodes) {
@@ -1317,7 +1391,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         }
         __syncwarp();  // before a lane's next copies take their place
       }
-      if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) break;
+      if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_wait, kSiteEmpty)) break;
       const uint32_t zs = sz + slot * kStage;
       if constexpr (kCodes) {
         const uint32_t half = zs + (ch >> 2) * 16384;
@@ -1359,6 +1433,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         phase ^= 1u;
       }
     }
+    if (!kCodes && lane == 0) s_z[kCodes ? 0 : warp] = step;
     cp_wait_all();
   } else if (warp == kMma) {
     if (lane == 0) {
@@ -1373,10 +1448,10 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         const uint32_t hb = desc_mn(sh + hs * hbytes, 16384);
         const int ksteps = (rows + 15) / 16;
         if (tile + 1 < end) rows = tiles[tile + 1].z;
-        alive = wait(&s_hfull[hs], hphase, &s_abort, kSiteFull);
+        alive = wait(&s_hfull[hs], hphase, &s_wait, kSiteFull);
         if (!alive) break;
         for (int b = 0; b < nb; ++b) {
-          if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) {
+          if (!wait(&s_full[slot], phase, &s_wait, kSiteFull)) {
             alive = false;
             break;
           }
@@ -1404,7 +1479,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
           mma_commit(&s_run);
           if (run_end < end) {
             run_end = min(end, p.first128[tiles[run_end].x + 1]);
-            alive = wait(&s_free, runs & 1, &s_abort, kSiteAccEmpty);
+            alive = wait(&s_free, runs & 1, &s_wait, kSiteAccEmpty);
           }
           ++runs;
           tc_fence_after();
@@ -1423,9 +1498,9 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
       bool alive = true;
       for (int nth = 0; nth < end - begin && alive; ++nth) {
         const uint32_t dacc = tmem + p.dcol + (nth & 1) * p.rp;
-        if (nth >= 2 && !wait(&s_dfree[nth & 1], ((nth >> 1) & 1) ^ 1u, &s_abort, kSiteAccEmpty)) break;
+        if (nth >= 2 && !wait(&s_dfree[nth & 1], ((nth >> 1) & 1) ^ 1u, &s_wait, kSiteAccEmpty)) break;
         for (int b = 0; b < nb; ++b) {
-          if (!wait(&s_full[slot], phase, &s_abort, kSiteFull)) {
+          if (!wait(&s_full[slot], phase, &s_wait, kSiteFull)) {
             alive = false;
             break;
           }
@@ -1473,7 +1548,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         for (; tile < stop; ++tile) {
           const int nth = tile - begin;
           const int4 t = tiles[tile];
-          if (!warp_wait(&s_dfull[nth & 1], (nth >> 1) & 1, &s_abort, kSiteDrain)) {
+          if (!warp_wait(&s_dfull[nth & 1], (nth >> 1) & 1, &s_wait, kSiteDrain)) {
             alive = false;
             break;
           }
@@ -1498,7 +1573,7 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         if (!alive) break;
       }
       tile = stop;
-      if (!warp_wait(&s_run, runs & 1, &s_abort, kSiteDrain)) break;
+      if (!warp_wait(&s_run, runs & 1, &s_wait, kSiteDrain)) break;
       ++runs;
       tc_fence_after();
       const bool whole = first == gb && stop == ge;
@@ -1536,14 +1611,14 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
   } else {
     const int l = tid - kLoad * 32, rchunks = p.rp / 8;
     const int hr = l >> 3, hc = l & 7;  // H: rows hr + 8 j, chunks hc, hc + 8
-    int slot = 0, hs = 0, step = 0;
+    int slot = 0, hs = 0, step = 0, loaded = 0;
     uint32_t phase = 0, hphase = 0;
     bool alive = true;
     RowsAhead<16> ra;
     ra.start(tiles, p.order, Items{begin, 1, 1, end - begin}, hr, 8);
     pdl_wait();
     for (int tile = begin; tile < end && alive; ++tile) {
-      if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_abort, kSiteHEmpty))
+      if (tile - begin >= p.htiles && !warp_wait(&s_hempty[hs], hphase ^ 1u, &s_wait, kSiteHEmpty))
         break;
       if (ra.run >= 0 && ra.count == 128) {
         if (l == 0) {
@@ -1567,11 +1642,12 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         hs = 0;
         hphase ^= 1u;
       }
+      ++loaded;
       const int group = ra.group;
       ra.advance();
       if (kDual && warp == kLoad) {  // one warp alone, as the copies of W are its own
         for (int b = 0; b < nb; ++b, ++step) {
-          if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_abort, kSiteEmpty)) {
+          if (step >= stages && !warp_wait(&s_empty[slot], phase ^ 1u, &s_wait, kSiteEmpty)) {
             alive = false;
             break;
           }
@@ -1586,11 +1662,25 @@ __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const _
         }
       }
     }
+    if (lane == 0) {
+      s_h[warp - kLoad] = loaded;
+      if (warp == kLoad) s_w = step;
+    }
     cp_wait_all();
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (s_wait.gave_up && tid == 0) {
+    if constexpr (!kCodes)  // Z comes by warp 0's TMA, W by kLoad's; whichever went further
+      land_ring(s_full, stages, max(s_z[0], s_w), [&](int at) {
+        int missing = kDual && s_w <= at ? 1 : 0;
+        for (int w = 0; w < kZ; ++w) missing += s_z[w] <= at ? 32 : 0;
+        return missing;
+      });
+    land_ring(s_hfull, p.htiles, s_h[0], [&](int at) { return s_h[1] <= at ? 32 : 0; });
+  }
+  __syncwarp();
   if (warp == kMma) tmem_dealloc(tmem, p.tmem_cols);
 }
 
@@ -1744,6 +1834,8 @@ cudaError_t launch_shrink(const AdapterCall& c, bool trans, const uint16_t* z, i
                    : std::max(2, std::min(kShrinkStages, 110 * 1024 / (16384 + wbytes)));
   p.wstages = codes ? std::min(kShrinkStages, (110 * 1024 - p.stages * 32768) / (2 * wbytes)) : p.stages;
   const int smem = std::max(per * (p.stages * 16384 + p.wstages * wbytes), 128 * (rp + 4) * 4) + 1024;
+  p.wait_ns = c.wait_ns;
+  p.stall = c.stall;
   auto kernel = trans ? shrink_kernel<false, true>
                       : (codes ? shrink_kernel<true, false> : shrink_kernel<false, false>);
   int splits = 1;  // blocks of a cluster, over which the reduction is split
@@ -1778,6 +1870,8 @@ cudaError_t launch_expand(const AdapterCall& c, bool trans, const uint16_t* h, i
   p.hslots = rest + 2 * kt * 16384 <= 112 * 1024 ? 2 : 1;
   const int fixed = p.hslots * kt * 16384 + p.slots * p.stage_bytes;
   const int smem = fixed + p.bslots * 16384 + kExpandBars;
+  p.wait_ns = c.wait_ns;
+  p.stall = c.stall;
   const int64_t r = c.r;
   cudaError_t e =
       trans ? encode<3>(&p.wmap, w, {n, r, c.g.count}, {n, r * n}, {64, rp, 1})
@@ -1856,7 +1950,8 @@ cudaError_t launch_outer(const AdapterCall& c, const OuterPlan& plan, const uint
   const int hr = kByRank ? 2 * c.r : c.r, rp = round16(hr);
   const int cap16 = small_tiles_cap(c.g.b, c.g.count);
   OuterArgs p{{}, {}, {}, c.g.tiles, c.g.order, first128_of(c.g), cap16, c.g.count, z, ldz, c.xq8, c.sx, h, scale,
-              out, part, dpart, c.g.b, k, c.r, hr, rp, plan.stages, plan.htiles, plan.dcol, plan.cols, plan.chunks == 1};
+              out, part, dpart, c.g.b, k, c.r, hr, rp, plan.stages, plan.htiles, plan.dcol, plan.cols, plan.chunks == 1,
+              c.wait_ns, c.stall};
   cudaError_t e = encode_rows(&p.hmap, h, c.g.b, hr, hr);
   if (e == cudaSuccess && !kCodes) e = encode_rows(&p.map, z, c.g.b, k, ldz);
   if (e == cudaSuccess && kDual)

@@ -367,6 +367,9 @@ twq_status adapter_shape_ok(int64_t m, int64_t n, int64_t r) {
   return TWQ_OK;
 }
 
+// twq_selftest_adapter_stall: the calling thread's limit of the waits, or 0.
+thread_local int64_t t_stall_ns = 0;
+
 // Everything of an adapter call that does not depend on how X is stored.
 twq_status check_adapters(int64_t b, const twq_adapters* ad, const twq_row_groups* g,
                           twq::AdapterCall* c) {
@@ -390,6 +393,8 @@ twq_status check_adapters(int64_t b, const twq_adapters* ad, const twq_row_group
   c->a = ad->a;
   c->bm = ad->b;
   c->scale = ad->scale;
+  c->wait_ns = t_stall_ns ? static_cast<uint64_t>(t_stall_ns) : twq::kAdapterWaitNs;
+  c->stall = t_stall_ns != 0;
   return TWQ_OK;
 }
 
@@ -546,6 +551,12 @@ twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx, int64_t
   if (!twq::pair_eligible(c)) return TWQ_ERR_UNSUPPORTED;
   return from_cuda(twq::launch_pair_stall_selftest(c, reinterpret_cast<cudaStream_t>(stream),
                                                    static_cast<unsigned long long>(wait_limit_ns)));
+}
+
+twq_status twq_selftest_adapter_stall(int64_t wait_limit_ns) {
+  if (wait_limit_ns != 0 && (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)) return TWQ_ERR_INVALID_ARG;
+  t_stall_ns = wait_limit_ns;
+  return TWQ_OK;
 }
 
 void twq_release_cache(void) {

@@ -35,7 +35,7 @@ EXPORTS = ("twq_version", "twq_status_string", "twq_weights_sizes", "twq_act_siz
            "twq_quantize_act_i8", "twq_fused_linear_i8", "twq_row_groups_sizes",
            "twq_group_rows", "twq_adapter_linear", "twq_adapter_linear_i8",
            "twq_adapter_backward_workspace_bytes", "twq_adapter_backward",
-           "twq_adapter_backward_i8")
+           "twq_adapter_backward_i8", "twq_selftest_adapter_stall")
 
 
 class TwqError(RuntimeError):
@@ -103,6 +103,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "twq_selftest_wait_timeout": ([P, P, I, P, P, I, P], ctypes.c_int),
         "twq_quantize_act_i8": ([P, I, I, I, P, P, P], ctypes.c_int),
         "twq_fused_linear_i8": ([P, P, I, P, P, P], ctypes.c_int),
+        "twq_selftest_adapter_stall": ([I], ctypes.c_int),
         "twq_row_groups_sizes": ([I, I, P], ctypes.c_int),
         "twq_group_rows": ([P, P, P], ctypes.c_int),
         "twq_adapter_linear": ([P, I, I, P, P, P, P, P, P], ctypes.c_int),
@@ -739,6 +740,11 @@ def adapter_backward_i8(dy, xq8, sx, h, ad: Adapters, groups: RowGroups, dx_base
                              _codes(xq8, sx, _adapter_sizes(ad, groups), ad), h, ad, groups,
                              dx_base, dx, da, db, workspace, stream)
 
+
+def selftest_adapter_stall(wait_limit_ns: int) -> None:
+    """Until called with 0: this thread's adapter calls of more than one launch run into their
+    kernels' bounded waits (see twq_selftest_adapter_stall). Read device_status() after them."""
+    _check(load().twq_selftest_adapter_stall(int(wait_limit_ns)), "twq_selftest_adapter_stall")
 
 
 def device_status() -> int:

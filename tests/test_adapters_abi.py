@@ -239,3 +239,9 @@ def test_group_sizes_hold_both_lists_and_the_tiles_before(lib, b, count):
         keys = min(b, count + 1)  # all of them with rows, all but one with one row only
         entries += (keys - 1) + -(-(b - keys + 1) // rows) if b else 0
     assert arr[2] >= 16 * entries + 4 * (count + 1)
+
+
+def test_stall_selftest_validation(lib):
+    f = lib.twq_selftest_adapter_stall
+    assert f(-1) == 1 and f(999) == 1 and f(1000000001) == 1
+    assert f(1000) == 0 and f(1000000000) == 0 and f(0) == 0

@@ -673,3 +673,33 @@ def test_grouping_stays_inside_its_buffers(twq, device, b, count):
         for t in bufs:
             assert bool((t[:64] == 77).all()) and bool((t[-64:] == 77).all())
     assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("kind", ["one", "mixed"])  # rows by TMA, rows one by one
+@pytest.mark.parametrize("b,m,n,r", [(2000, 2048, 2560, 16), (1300, 4096, 4096, 64), (1200, 2560, 2048, 128),
+                                     (130, 128, 128, 104)])
+def test_waits_that_run_out(twq, device, b, m, n, r, kind, codes):
+    """A loading warp of each kernel stops early: the waits on it run out after 0.2 ms, the copies
+    under way land (a wait of their own, of up to 2 s each, that would be seen here), the kernels
+    leave, the status tells, and the next calls are right."""
+    import time
+
+    c = Case(twq, device, b, m, n, r, 2, kind, codes)
+    forward = lambda: c.linear(*c.xargs, c.ad, c.groups, base=c.base)
+    backward = lambda: c.backward(c.dy, *c.xargs, c.h, c.ad, c.groups, dx_base=c.dx_base)
+    want = forward() + backward()
+    assert twq.device_status() == 0
+    for call in (forward, backward):
+        twq.selftest_adapter_stall(200000)
+        try:
+            t0 = time.perf_counter()
+            call()
+            code = twq.device_status()
+            spent = time.perf_counter() - t0
+        finally:
+            twq.selftest_adapter_stall(0)
+        assert 61 <= code <= 67 and spent < 1.0, (code, spent)
+        assert twq.device_status() == 0
+        assert all(torch.equal(p, q) for p, q in zip(forward() + backward(), want))
+    assert twq.device_status() == 0
