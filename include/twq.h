@@ -433,8 +433,9 @@ typedef struct {
  *   base  b x n BF16, or NULL (0); may be y itself
  *   h     b x r BF16 (output; the backward pass reads it)
  *   y     b x n BF16 (output, every row is written)
- * h is summed in fp32 and rounded to BF16 once; s h B^T + base is summed in fp32 and
- * rounded once. Rows are independent: an infinity or NaN in one row stays in that row.
+ * h is summed in fp32 and rounded to BF16 once; y is made from the rounded h, and
+ * s h B^T + base is summed in fp32 and rounded once. Rows are independent: an infinity
+ * or NaN in one row stays in that row.
  * Shapes: m % 128 == 0, n % 128 == 0 (the layer's rule), both <= 2^20; r % 8 == 0,
  *   8 <= r <= 128. b == 0 is a no-op.
  * Errors: TWQ_ERR_INVALID_ARG on a null pointer, a bad shape, or g->b / g->count that do
@@ -451,6 +452,10 @@ TWQ_API twq_status twq_adapter_linear(const uint16_t* x, int64_t ldx, int64_t b,
  * sx[i, k / 128]. Half of the bytes of BF16 X; a trainer that keeps the 8-bit codes and
  * scales as its checkpoint of X uses them again in twq_adapter_backward_i8.
  *   xq8  b x m int8;  sx  b x (m/128) fp32;  otherwise as twq_adapter_linear.
+ * Batches of one launch (decode steps, a few short prompts) take the codes exactly and
+ * multiply fp32 sums by the scales; in larger ones each code * scale is first rounded to
+ * BF16, the type that the activation had. A row's h may differ by that rounding between
+ * batches of different sizes.
  */
 TWQ_API twq_status twq_adapter_linear_i8(const int8_t* xq8, const float* sx, int64_t b,
                                          const twq_adapters* ad, const twq_row_groups* g,
@@ -469,8 +474,10 @@ TWQ_API twq_status twq_adapter_linear_i8(const int8_t* xq8, const float* sx, int
  *   da, db   count x r x m and count x n x r BF16 (outputs; adapters without rows: 0)
  *   workspace  device buffer of twq_adapter_backward_workspace_bytes(b, m, n, r, count)
  *       bytes, 16-byte aligned; calls that overlap on the GPU need one each
- * Sums are held in fp32 and rounded once; their order depends only on the arguments'
- * sizes and the grouping, so equal calls give equal bits. b == 0 writes da = db = 0.
+ * Sums are held in fp32 and the outputs rounded once. Before that dh is rounded to BF16
+ * for dx, and to two BF16 terms (16 bits) for dA. The order of the sums depends only on
+ * the arguments' sizes and the grouping, so equal calls give equal bits. b == 0 writes
+ * da = db = 0.
  * Shapes and errors as twq_adapter_linear; TWQ_ERR_INVALID_ARG on a short workspace.
  */
 TWQ_API size_t twq_adapter_backward_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r,
@@ -481,7 +488,8 @@ TWQ_API twq_status twq_adapter_backward(const uint16_t* dy, const uint16_t* x, i
                                         uint16_t* dx, uint16_t* da, uint16_t* db, void* workspace,
                                         size_t workspace_bytes, twq_stream_t stream);
 
-/* twq_adapter_backward with X from its 8-bit checkpoint (codes and scales). */
+/* twq_adapter_backward with X from its 8-bit checkpoint (codes and scales); for dA each
+ * code * scale is rounded to BF16. */
 TWQ_API twq_status twq_adapter_backward_i8(const uint16_t* dy, const int8_t* xq8, const float* sx,
                                            const uint16_t* h, int64_t b, const twq_adapters* ad,
                                            const twq_row_groups* g, const uint16_t* dx_base,

@@ -24,11 +24,13 @@ inline int row_tiles_cap(int64_t b, int64_t count, int rows) {
 // times rank (from 16 on): its time goes with that, since it reads an adapter again for every 16
 // rows. With 4 adapters of 4096 x 4096 it meets the two kernels at about 1000 rows of rank 16
 // (16 us), 430 of rank 64 (16 us) and 180 of rank 128 (17 us); of 4096 x 14336 at 620, 260 and 130.
+// The rule knows neither m nor n: it changes over at 768, 192 and 96 rows, between or before these.
 //
 // Twice as many up to rank 16 where the adapters may have 16 rows each or fewer: a row tile of 128
 // then holds few rows, but takes the two kernels as long as a full one. 512 rows with 64 adapters of
 // 4096 x 4096: 15 us instead of 37, of 4096 x 14336: 33 instead of 70; 1536 rows with 128: 39
-// instead of 60, 67 instead of 117. If only 4 of them are used: 23 instead of 25, 43 instead of 34.
+// instead of 60, 67 instead of 117. If only 4 of them are used: 23 instead of 25, but 43 instead of
+// 34 (which adapters are used is known on the GPU alone).
 // (At rank 32: 39 to 39 us, 22 to 22, and 81 to 61 at 14336 x 4096, so not there.)
 constexpr int64_t kSmallWork = 12288;
 inline bool small_batch(int64_t b, int64_t count, int64_t r) {

@@ -400,9 +400,11 @@ constexpr uint32_t kShrinkTmemCols = 128;  // and as many for two groups of conv
 // warp has 32 rows, for which it keeps its own ring of raw codes (TMA where the rows follow one
 // another), a lane a row, and leaves the BF16 in tensor memory, where the MMA takes A from: no
 // proxy fence and no second turn through shared memory. 4096 x 14336, rank 16: 28 us, against 31
-// with all eight warps on each group and A in shared memory. What is left is the conversion, seven
-// operations of the half-rate integer pipe for four codes: 1.2 of the 1.6 us that a team takes for
-// a group.
+// with all eight warps on each group and A in shared memory. Of the 28 us the eight groups of a team
+// are 13 (1.6 a group, 1.2 of it conversion while four teams share the SM's integer pipe); the rest
+// is the start, the first copies and the joining of the parts. The conversion of all codes, seven
+// operations at half rate for four, would take that pipe 5.7 us. A team has one buffer in tensor
+// memory, so it waits for the products of its last group before it writes the next.
 
 // One row tile per cluster, whose blocks split the reduction over k (block `rank` takes the groups
 // of 128 columns rank, rank + splits, ..., so that they read neighbouring pieces of the rows at
@@ -866,7 +868,7 @@ constexpr int kExpandThreads = 384;  // 8 epilogue warps; MMA; 2 warps load H an
 // belongs to one half, and its barrier is never a whole turn ahead of a waiter.
 constexpr int kExpandSlots = 4;      // W stages, and accumulators of 64 columns
 constexpr int kBaseSlots = 4;        // base stages
-constexpr int kExpandBars = 256;     // bytes of barriers in front of the tiles' space
+constexpr int kExpandBars = 256;     // bytes behind the base stages: barriers, what goes with them
 
 __device__ __forceinline__ uint4 ld_stream(const void* ptr) {
   uint4 v;
@@ -888,10 +890,14 @@ __device__ __forceinline__ void st_stream(void* ptr, uint4 v) {
 // turn: 5.8). base comes through shared memory, several stages ahead. A lane of the epilogue takes
 // a row: it adds its accumulators to the row's base in the stage, in place, and its warp copies the
 // stage out, 128 bytes of a row at a time; base may be y itself: an element is written after the
-// only read of it. Measured, 8192 x 25600, rank 64: 168 us. With the hint that base is read once,
-// which the other kernels gain by: 173. Sent out by TMA, the stages are free later: 191. With
-// accumulators read in the 16x256b form and stores from registers, 1.5 times the instructions:
-// 178, and for 5120 columns of W^T 43 instead of 39.
+// only read of it. Measured, whole calls of 8192 x 5120 x 25600, rank 64: 174 us, of which this
+// kernel is some 150 (842 MB, 5.6 TB/s; a copy of as much takes 129). With the hint that base is
+// read once, which the other kernels gain by: 186 (with four sets of buffers in turn, base apart
+// from y, the other way round: 188, and 181 with it). Slower when they were tried: stages sent out
+// by TMA, free later (191); accumulators read in the 16x256b form and stores from registers, 1.5
+// times the instructions (by 10 us, and for 5120 columns of W^T 43 instead of 39).
+// dx is made from dh's first term alone: with both, a tile of H would take 16 KB more at rank 64,
+// the room of two stages of W.
 // Launched so that it may start before the kernel that writes H has ended: until then it reads
 // only what that kernel does not write (the grouping, W, base) and writes nothing.
 template <bool kTrans, bool kSums>
@@ -1263,9 +1269,10 @@ constexpr int kOuterRawStep = 16384 + 512;  // codes; a scale for each row
 // kDual (r <= 64): the same Z stage also serves the product over its columns, dh = Z W: a
 // tile's 128 x r sums over this slice go to `dpart` ([slice][rank / 4][position][4]), and dY is
 // read once for both gradients. One block on an SM, for the accumulators and for as few slices, so
-// parts of dh, as they allow. 8192 x 25600, rank 64: 92 us, 420 MB of dY and 52 MB of parts
-// written (5.1 TB/s); X, 8192 x 5120: 26 us; X in codes, 8192 x 4096, rank 32: 28 us, where each
-// step's loads, conversion and products wait for one another.
+// parts of dh, as they allow. 8192 x 25600, rank 64: 92 us, 420 MB of dY read and 71 MB of parts of
+// dh written, of which 52 reach DRAM before they are added up (5.1 TB/s); X, 8192 x 5120: 26 us; X
+// in codes, 8192 x 4096, rank 32: 28 us, where each step's loads, conversion and products wait for
+// one another (the conversion alone would take the integer pipe 3.3 us).
 template <bool kCodes, bool kByRank, bool kDual>
 __global__ void __launch_bounds__(outer_threads(kCodes), 1) outer_kernel(const __grid_constant__ OuterArgs p) {
   extern __shared__ uint8_t smem_raw[];

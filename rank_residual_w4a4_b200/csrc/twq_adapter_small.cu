@@ -10,8 +10,11 @@
 // by one warp only, so shared memory or tensor memory would only add a step), by giving a lane
 // eight consecutive elements of the reduction and both operands the same order.
 //
+// h takes the place of a BF16 output, and y is made from those same rounded values.
+//
 // Measured: one row of 4096 x 4096, rank 16, 4.5 us; 48 rows with 20 adapters of 4096 x 14336,
-// 7.9 us (15 MB, 1.9 TB/s); 333 rows with 11 of 5120 x 5120, rank 24, 10 us.
+// 7.9 us (15 MB, 1.9 TB/s); 333 rows with 11 of 5120 x 5120, rank 24, 10 us. A warp's groups of 32
+// columns of n follow one another, one ahead of the products: two at 4096 columns, seven at 14336.
 #include <cuda_bf16.h>
 
 #include <algorithm>

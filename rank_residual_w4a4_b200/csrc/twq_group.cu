@@ -1,8 +1,9 @@
 // Rows of a batch grouped by adapter: a stable counting sort of the row numbers by id,
 // and the lists of row tiles (runs of at most 16 and at most 128 rows of one group) that
 // the adapter kernels walk. One block; nothing is read back by the host. Bound by latency: the
-// passes over the ids and the barriers between them take 4.5 us for 48 rows and 9.5 us for 16384
-// (several blocks would have to wait for one another's counts, or be another launch).
+// passes over the ids and the barriers between them take 4.5 us for 48 rows and 9.5 us for 16384.
+// (Not built: a cluster of blocks for large batches, which could join its counts over distributed
+// shared memory.)
 #include "twq_adapter.h"
 
 namespace twq {

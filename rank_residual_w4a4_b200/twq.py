@@ -671,7 +671,8 @@ def adapter_linear(x: torch.Tensor, ad: Adapters, groups: RowGroups, base=None, 
                    stream=None):
     """y = base + s (x A^T) B^T with each row's own adapter, and h = x A^T: (y, h), both
     BF16. x is BF16 (b x m, rows may be strided); base is the layer's Y (may be y itself) or
-    None (0). A row without adapter has y = base and h = 0."""
+    None (0). A row without adapter has y = base and h = 0. autograd does not record the call,
+    whatever requires_grad says: its gradients are adapter_backward's."""
     return _adapter_linear("twq_adapter_linear", _strided_x(x, _adapter_sizes(ad, groups), ad), ad,
                            groups, base, y, h, stream)
 
@@ -684,7 +685,8 @@ def _codes(xq8, sx, b, ad):
 def adapter_linear_i8(xq8: torch.Tensor, sx: torch.Tensor, ad: Adapters, groups: RowGroups,
                       base=None, y=None, h=None, stream=None):
     """adapter_linear on the layer's activation codes stored one per byte (from
-    quantize_act_a8 or quantize_act_i8) and their scales."""
+    quantize_act_a8 or quantize_act_i8) and their scales. Beyond the batches of one launch,
+    code * scale is rounded to BF16 first, so a row's h may differ by that between batch sizes."""
     return _adapter_linear("twq_adapter_linear_i8", _codes(xq8, sx, _adapter_sizes(ad, groups), ad),
                            ad, groups, base, y, h, stream)
 
@@ -726,8 +728,9 @@ def _adapter_backward(fn, dy, args, h, ad, groups, dx_base, dx, da, db, workspac
 def adapter_backward(dy, x, h, ad: Adapters, groups: RowGroups, dx_base=None, dx=None, da=None,
                      db=None, workspace=None, stream=None):
     """The adapters' gradients from dy (b x n), the forward pass's x and h: (dx, da, db),
-    BF16, with dx = dx_base + dh A (dx_base: the gradient through the frozen layer, may be
-    dx itself, or None) and da, db shaped like the adapters' a, b (adapters without rows: 0)."""
+    BF16, with dx = dx_base + dh A (dx_base: the gradient through the frozen layer, which this
+    library does not compute; may be dx itself, or None) and da, db shaped like the adapters'
+    a, b (adapters without rows: 0)."""
     return _adapter_backward("twq_adapter_backward", dy,
                              _strided_x(x, _adapter_sizes(ad, groups), ad), h, ad, groups, dx_base,
                              dx, da, db, workspace, stream)
