@@ -498,6 +498,104 @@ TWQ_API twq_status twq_adapter_backward_i8(const uint16_t* dy, const int8_t* xq8
                                            twq_stream_t stream);
 
 /*
+ * The layer on BF16 activations, for few tokens (weight-only quantization, W4A16): the packed
+ * weights are those of every other call, X is not quantized. With D() the codes times their
+ * scales, in groups of 128 along m:
+ *
+ *     h = bf16(x D(L1))        y = bf16(x D(R) + h L2)
+ *
+ *   x   b x m BF16, row stride ldx elements (ldx >= m, ldx % 8 == 0)
+ *   w   from twq_pack_weights
+ *   h   b x r BF16 (output; NULL iff r == 0);  y  b x n BF16 (output)
+ * Each group's sum of code * x is exact products summed in fp32, then multiplied by the group's
+ * scale; the groups' sums and h L2 are added in fp32 and y is rounded once. Equal calls give equal
+ * bits. Rows are independent: an infinity or NaN in one row stays in that row.
+ * Limits: 1 <= b <= 64 (b == 0 is a no-op), m and n <= 2^20; larger batches return
+ * TWQ_ERR_UNSUPPORTED (quantize the activations: twq_fused_linear_a8). r == 0 is one launch, else
+ * two. Launched with programmatic stream serialization like twq_fused_linear: X may come from the
+ * preceding kernel; the weights must not be written by a kernel that signals early.
+ */
+TWQ_API twq_status twq_fused_linear_a16(const uint16_t* x, int64_t ldx, int64_t b,
+                                        const twq_weights* w, uint16_t* h, uint16_t* y,
+                                        twq_stream_t stream);
+
+/*
+ * Mixture of experts for few tokens, experts of packed 4-bit weights and BF16 activations. The
+ * pages have no counterpart: this is the feed-forward block of a mixture model whose experts are
+ * layers as above. A router's product (the caller's) gives each token logits over the experts;
+ * twq_moe_route chooses, twq_moe_experts multiplies, twq_moe_layer does both.
+ */
+
+/*
+ * The choice of experts: for each row the k largest logits, largest first, equal ones in the
+ * order of their indices (-0 equals +0; a NaN counts as larger than any number).
+ *   logits  b x count, row stride ld elements (ld >= count): fp32 (4-byte aligned), or BF16
+ *           (2-byte aligned) in twq_moe_route_bf16
+ *   ids     b x k int32 (output);  weights  b x k fp32 (output)
+ * weights: softmax over all logits of the row (renormalize == 0) or over the chosen ones. A logit
+ * of -inf is never chosen: where fewer than k others are left, the last ids are -1 and their
+ * weights 0. Logits of +inf share the weight. A NaN makes the row's weights NaN.
+ * One launch, any b <= 2^24; 1 <= count <= 1024; 1 <= k <= 16, k <= count.
+ */
+TWQ_API twq_status twq_moe_route(const float* logits, int64_t ld, int64_t b, int64_t count,
+                                 int64_t k, int renormalize, int32_t* ids, float* weights,
+                                 twq_stream_t stream);
+TWQ_API twq_status twq_moe_route_bf16(const uint16_t* logits, int64_t ld, int64_t b, int64_t count,
+                                      int64_t k, int renormalize, int32_t* ids, float* weights,
+                                      twq_stream_t stream);
+
+/* The experts of one block: `count` layers in each of up and down, whose buffers follow one
+ * another (buffer of expert e: e times the bytes of twq_weights_sizes further on).
+ *   up    m x 2f: the gate's f columns, then the f columns that it multiplies
+ *   down  f x m */
+typedef struct {
+  int64_t count;
+  twq_weights up, down;
+} twq_experts;
+
+/*
+ * The chosen experts' products, for each token and slot with id e:
+ *
+ *     [g u] = x D(R_up) + bf16(x D(L1_up)) L2_up      a = silu(g) u
+ *     y_e   = a D(R_down) + bf16(a D(L1_down)) L2_down
+ *     y     = bf16(base + sum over the slots of weight * y_e)
+ *
+ *   x          b x m BF16, row stride ldx elements (ldx >= m, ldx % 8 == 0)
+ *   ids        b x k int32, weights  b x k fp32 (4-byte aligned): from twq_moe_route or the
+ *              caller. An id outside [0, count) adds nothing (experts that are elsewhere, padding);
+ *              an expert twice in one token's slots counts twice
+ *   base       b x m BF16 (for instance the residual stream), or NULL (0); may be y itself
+ *   y          b x m BF16 (output, every row is written)
+ *   workspace  device buffer of twq_moe_workspace_bytes(b, k, e) bytes, 16-byte aligned; calls
+ *              that overlap on the GPU need one each
+ * Sums are held in fp32. a is kept as two BF16 terms (16 bits), g and u are not rounded. Each
+ * expert's weights are read once for all its tokens (beyond 32 of them again for every 32, beyond
+ * 16 for down). The sum over slots follows the experts' order; equal calls give equal bits.
+ * Limits: b <= 64 (b == 0 is a no-op), k <= 16, count <= 1024, m and f multiples of 128, m and 2f
+ * <= 2^20, ranks as twq_weights (up's and down's may differ).
+ * Errors: TWQ_ERR_INVALID_ARG on a null pointer, a bad shape (down.n != up.m, up.n != 2 down.m) or
+ * a short workspace; TWQ_ERR_UNSUPPORTED beyond the limits.
+ * Two launches, and one more for each of the ranks that is not 0.
+ */
+TWQ_API size_t twq_moe_workspace_bytes(int64_t b, int64_t k, const twq_experts* e);
+TWQ_API twq_status twq_moe_experts(const uint16_t* x, int64_t ldx, int64_t b, const int32_t* ids,
+                                   const float* weights, int64_t k, const twq_experts* e,
+                                   const uint16_t* base, uint16_t* y, void* workspace,
+                                   size_t workspace_bytes, twq_stream_t stream);
+
+/* twq_moe_route (logits over e->count experts) and twq_moe_experts on its ids and weights (both
+ * are outputs). */
+TWQ_API twq_status twq_moe_layer(const uint16_t* x, int64_t ldx, int64_t b, const float* logits,
+                                 int64_t ld, int64_t k, int renormalize, const twq_experts* e,
+                                 const uint16_t* base, int32_t* ids, float* weights, uint16_t* y,
+                                 void* workspace, size_t workspace_bytes, twq_stream_t stream);
+TWQ_API twq_status twq_moe_layer_bf16(const uint16_t* x, int64_t ldx, int64_t b,
+                                      const uint16_t* logits, int64_t ld, int64_t k,
+                                      int renormalize, const twq_experts* e, const uint16_t* base,
+                                      int32_t* ids, float* weights, uint16_t* y, void* workspace,
+                                      size_t workspace_bytes, twq_stream_t stream);
+
+/*
  * Reads and clears the device-side status word (SYNCHRONIZES the device).
  * *code = 0 if no kernel's bounded wait has run out since the last call, else
  * a site code (which wait gave up). Returns TWQ_ERR_DEVICE if *code != 0.
@@ -549,7 +647,8 @@ TWQ_API void twq_release_cache(void);
 
 /* Number of kernels each entry point launches (for launch accounting); of the adapter
  * calls, the most: a small forward batch takes one, gradients one less where few parts
- * are left to add up. */
+ * are left to add up. Of the calls on BF16 activations, the most too: one less for each
+ * rank that is 0. */
 TWQ_API int twq_launches_per_call(const char* entry_point);
 
 #ifdef __cplusplus

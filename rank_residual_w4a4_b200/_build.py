@@ -17,9 +17,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtwq.so")
 SOURCES = ["twq_api.cu", "twq_gemm_sm100.cu", "twq_pair_sm100.cu", "twq_decode_sm100.cu",
            "twq_quant.cu", "twq_noalloc.cu", "twq_fold.cu", "twq_group.cu", "twq_adapter_sm100.cu",
-           "twq_adapter_small.cu"]
+           "twq_adapter_small.cu", "twq_a16_sm100.cu", "twq_route.cu"]
 HEADERS = ["sm100_ptx.cuh", "twq_internal.h", "twq_eq1.cuh", "twq_hrequant.cuh",
-           "twq_adapter.h"]
+           "twq_adapter.h", "twq_a16.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

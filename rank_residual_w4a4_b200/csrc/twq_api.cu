@@ -2,6 +2,7 @@
 // stream-ordered launches. No entry point allocates device memory.
 #include <string.h>
 
+#include "twq_a16.h"
 #include "twq_adapter.h"
 #include "twq_internal.h"
 
@@ -527,6 +528,152 @@ twq_status twq_adapter_backward_i8(const uint16_t* dy, const int8_t* xq8, const 
                                     stream);
 }
 
+namespace {
+
+// Weights that a BF16-activation call reads; `count` layers of them lie one after another.
+twq_status check_a16_weights(const twq_weights& w) {
+  const twq_status s = shape_ok(w.m, w.n, w.r);
+  if (s != TWQ_OK) return s;
+  if (w.m > twq::kA16MaxDim || w.n > twq::kA16MaxDim) return TWQ_ERR_UNSUPPORTED;
+  if (!w.rq || !w.sr || (w.r > 0 && (!w.l1q || !w.sl1 || !w.l2t))) return TWQ_ERR_INVALID_ARG;
+  if (!aligned16(w.rq) || !aligned16(w.sr)) return TWQ_ERR_MISALIGNED;
+  if (w.r > 0 && (!aligned16(w.l1q) || !aligned16(w.sl1) || !aligned16(w.l2t)))
+    return TWQ_ERR_MISALIGNED;
+  return TWQ_OK;
+}
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+twq_status check_route(const void* logits, bool bf16, int64_t ld, int64_t b, int64_t count,
+                       int64_t k, int renormalize, int32_t* ids, float* weights,
+                       twq::RouteCall* c) {
+  if (b < 0 || count < 1 || k < 1 || k > count || ld < count) return TWQ_ERR_INVALID_ARG;
+  if (count > twq::kMoeMaxExperts || k > twq::kMoeMaxChoices || b > (int64_t(1) << 24))
+    return TWQ_ERR_UNSUPPORTED;
+  if (b == 0) return TWQ_OK;
+  if (!logits || !ids || !weights) return TWQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % (bf16 ? 2 : 4) || !aligned4(ids) || !aligned4(weights))
+    return TWQ_ERR_MISALIGNED;
+  *c = twq::RouteCall{logits, bf16, ld, b, static_cast<int>(count), static_cast<int>(k),
+                      renormalize != 0, ids, weights};
+  return TWQ_OK;
+}
+
+twq_status check_experts_shape(int64_t b, int64_t k, const twq_experts* e) {
+  if (!e || b < 0 || k < 1 || e->count < 1) return TWQ_ERR_INVALID_ARG;
+  twq_status s = shape_ok(e->up.m, e->up.n, e->up.r);
+  if (s == TWQ_OK) s = shape_ok(e->down.m, e->down.n, e->down.r);
+  if (s != TWQ_OK) return s;
+  if (e->down.n != e->up.m || e->up.n != 2 * e->down.m) return TWQ_ERR_INVALID_ARG;
+  if (b > twq::kA16MaxRows || k > twq::kMoeMaxChoices || e->count > twq::kMoeMaxExperts ||
+      e->up.m > twq::kA16MaxDim || e->up.n > twq::kA16MaxDim)
+    return TWQ_ERR_UNSUPPORTED;
+  return TWQ_OK;
+}
+
+twq_status check_moe(const uint16_t* x, int64_t ldx, int64_t b, const int32_t* ids,
+                     const float* weights, int64_t k, const twq_experts* e, const uint16_t* base,
+                     uint16_t* y, void* workspace, size_t workspace_bytes, twq::MoeCall* c) {
+  twq_status s = check_experts_shape(b, k, e);
+  if (s != TWQ_OK) return s;
+  if (ldx < e->up.m) return TWQ_ERR_INVALID_ARG;
+  if (b == 0) return TWQ_OK;
+  if (!x || !ids || !weights || !y || !workspace) return TWQ_ERR_INVALID_ARG;
+  s = check_a16_weights(e->up);
+  if (s == TWQ_OK) s = check_a16_weights(e->down);
+  if (s != TWQ_OK) return s;
+  if (!aligned16(x) || ldx % 8 || !aligned16(base) || !aligned16(y) || !aligned16(workspace) ||
+      !aligned4(ids) || !aligned4(weights))
+    return TWQ_ERR_MISALIGNED;
+  if (workspace_bytes < twq_moe_workspace_bytes(b, k, e)) return TWQ_ERR_INVALID_ARG;
+  *c = twq::MoeCall{x, ldx, static_cast<int>(b), static_cast<int>(k), ids, weights,
+                    e, base, y, workspace};
+  return TWQ_OK;
+}
+
+twq_status run_moe_layer(const uint16_t* x, int64_t ldx, int64_t b, const void* logits, bool bf16,
+                         int64_t ld, int64_t k, int renormalize, const twq_experts* e,
+                         const uint16_t* base, int32_t* ids, float* weights, uint16_t* y,
+                         void* workspace, size_t workspace_bytes, twq_stream_t stream) {
+  twq::MoeCall m;
+  twq::RouteCall r;
+  twq_status s = check_moe(x, ldx, b, ids, weights, k, e, base, y, workspace, workspace_bytes, &m);
+  if (s == TWQ_OK) s = check_route(logits, bf16, ld, b, e->count, k, renormalize, ids, weights, &r);
+  if (s != TWQ_OK || b == 0) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err = twq::launch_moe_route(r, st);
+  if (err == cudaSuccess) err = twq::launch_moe_experts(m, st);
+  return from_cuda(err);
+}
+
+}  // namespace
+
+twq_status twq_fused_linear_a16(const uint16_t* x, int64_t ldx, int64_t b, const twq_weights* w,
+                                uint16_t* h, uint16_t* y, twq_stream_t stream) {
+  if (!w) return TWQ_ERR_INVALID_ARG;
+  twq_status s = shape_ok(w->m, w->n, w->r);
+  if (s != TWQ_OK) return s;
+  if (b < 0 || ldx < w->m) return TWQ_ERR_INVALID_ARG;
+  if (b > twq::kA16MaxRows) return TWQ_ERR_UNSUPPORTED;
+  if (b == 0) return TWQ_OK;
+  if (!x || !y || (w->r > 0 && !h)) return TWQ_ERR_INVALID_ARG;
+  s = check_a16_weights(*w);
+  if (s != TWQ_OK) return s;
+  if (!aligned16(x) || ldx % 8 || !aligned16(h) || !aligned16(y)) return TWQ_ERR_MISALIGNED;
+  const twq::A16LinearCall c{x, ldx, static_cast<int>(b), w, h, y};
+  return from_cuda(twq::launch_a16_linear(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+twq_status twq_moe_route(const float* logits, int64_t ld, int64_t b, int64_t count, int64_t k,
+                         int renormalize, int32_t* ids, float* weights, twq_stream_t stream) {
+  twq::RouteCall c;
+  const twq_status s =
+      check_route(logits, false, ld, b, count, k, renormalize, ids, weights, &c);
+  if (s != TWQ_OK || b == 0) return s;
+  return from_cuda(twq::launch_moe_route(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+twq_status twq_moe_route_bf16(const uint16_t* logits, int64_t ld, int64_t b, int64_t count,
+                              int64_t k, int renormalize, int32_t* ids, float* weights,
+                              twq_stream_t stream) {
+  twq::RouteCall c;
+  const twq_status s = check_route(logits, true, ld, b, count, k, renormalize, ids, weights, &c);
+  if (s != TWQ_OK || b == 0) return s;
+  return from_cuda(twq::launch_moe_route(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t twq_moe_workspace_bytes(int64_t b, int64_t k, const twq_experts* e) {
+  if (check_experts_shape(b, k, e) != TWQ_OK) return 0;
+  return twq::moe_workspace(b * k, e);
+}
+
+twq_status twq_moe_experts(const uint16_t* x, int64_t ldx, int64_t b, const int32_t* ids,
+                           const float* weights, int64_t k, const twq_experts* e,
+                           const uint16_t* base, uint16_t* y, void* workspace,
+                           size_t workspace_bytes, twq_stream_t stream) {
+  twq::MoeCall c;
+  const twq_status s =
+      check_moe(x, ldx, b, ids, weights, k, e, base, y, workspace, workspace_bytes, &c);
+  if (s != TWQ_OK || b == 0) return s;
+  return from_cuda(twq::launch_moe_experts(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+twq_status twq_moe_layer(const uint16_t* x, int64_t ldx, int64_t b, const float* logits, int64_t ld,
+                         int64_t k, int renormalize, const twq_experts* e, const uint16_t* base,
+                         int32_t* ids, float* weights, uint16_t* y, void* workspace,
+                         size_t workspace_bytes, twq_stream_t stream) {
+  return run_moe_layer(x, ldx, b, logits, false, ld, k, renormalize, e, base, ids, weights, y,
+                       workspace, workspace_bytes, stream);
+}
+
+twq_status twq_moe_layer_bf16(const uint16_t* x, int64_t ldx, int64_t b, const uint16_t* logits,
+                              int64_t ld, int64_t k, int renormalize, const twq_experts* e,
+                              const uint16_t* base, int32_t* ids, float* weights, uint16_t* y,
+                              void* workspace, size_t workspace_bytes, twq_stream_t stream) {
+  return run_moe_layer(x, ldx, b, logits, true, ld, k, renormalize, e, base, ids, weights, y,
+                       workspace, workspace_bytes, stream);
+}
+
 twq_status twq_device_status(int* code) {
   if (!code) return TWQ_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
@@ -583,6 +730,10 @@ int twq_launches_per_call(const char* ep) {
   if (!strcmp(ep, "twq_group_rows")) return 1;
   if (!strcmp(ep, "twq_adapter_linear") || !strcmp(ep, "twq_adapter_linear_i8")) return 2;
   if (!strcmp(ep, "twq_adapter_backward") || !strcmp(ep, "twq_adapter_backward_i8")) return 5;
+  if (!strcmp(ep, "twq_fused_linear_a16")) return 2;
+  if (!strcmp(ep, "twq_moe_route") || !strcmp(ep, "twq_moe_route_bf16")) return 1;
+  if (!strcmp(ep, "twq_moe_experts")) return 4;
+  if (!strcmp(ep, "twq_moe_layer") || !strcmp(ep, "twq_moe_layer_bf16")) return 5;
   return -1;
 }
 

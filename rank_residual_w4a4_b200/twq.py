@@ -35,7 +35,9 @@ EXPORTS = ("twq_version", "twq_status_string", "twq_weights_sizes", "twq_act_siz
            "twq_quantize_act_i8", "twq_fused_linear_i8", "twq_row_groups_sizes",
            "twq_group_rows", "twq_adapter_linear", "twq_adapter_linear_i8",
            "twq_adapter_backward_workspace_bytes", "twq_adapter_backward",
-           "twq_adapter_backward_i8", "twq_selftest_adapter_stall")
+           "twq_adapter_backward_i8", "twq_selftest_adapter_stall", "twq_fused_linear_a16",
+           "twq_moe_route", "twq_moe_route_bf16", "twq_moe_workspace_bytes", "twq_moe_experts",
+           "twq_moe_layer", "twq_moe_layer_bf16")
 
 
 class TwqError(RuntimeError):
@@ -48,6 +50,10 @@ class _Weights(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("r", ctypes.c_int64),
                 ("rq", ctypes.c_void_p), ("sr", ctypes.c_void_p), ("l1q", ctypes.c_void_p),
                 ("sl1", ctypes.c_void_p), ("l2t", ctypes.c_void_p)]
+
+
+class _Experts(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("up", _Weights), ("down", _Weights)]
 
 
 class _RowGroups(ctypes.Structure):
@@ -111,6 +117,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "twq_adapter_backward_workspace_bytes": ([I, I, I, I, I], S),
         "twq_adapter_backward": ([P, P, I, P, I, P, P, P, P, P, P, P, S, P], ctypes.c_int),
         "twq_adapter_backward_i8": ([P, P, P, P, I, P, P, P, P, P, P, P, S, P], ctypes.c_int),
+        "twq_fused_linear_a16": ([P, I, I, P, P, P, P], ctypes.c_int),
+        "twq_moe_route": ([P, I, I, I, I, ctypes.c_int, P, P, P], ctypes.c_int),
+        "twq_moe_route_bf16": ([P, I, I, I, I, ctypes.c_int, P, P, P], ctypes.c_int),
+        "twq_moe_workspace_bytes": ([I, I, P], S),
+        "twq_moe_experts": ([P, I, I, P, P, I, P, P, P, P, S, P], ctypes.c_int),
+        "twq_moe_layer": ([P, I, I, P, I, I, ctypes.c_int, P, P, P, P, P, P, S, P], ctypes.c_int),
+        "twq_moe_layer_bf16": ([P, I, I, P, I, I, ctypes.c_int, P, P, P, P, P, P, S, P],
+                               ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -742,6 +756,192 @@ def adapter_backward_i8(dy, xq8, sx, h, ad: Adapters, groups: RowGroups, dx_base
     return _adapter_backward("twq_adapter_backward_i8", dy,
                              _codes(xq8, sx, _adapter_sizes(ad, groups), ad), h, ad, groups,
                              dx_base, dx, da, db, workspace, stream)
+
+
+def _rows(t, name, dtype, b, m, device, where):
+    """A b x m tensor on `device` whose rows may be strided -> its address and row stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError("%s must be a 2-D torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device (the library has no CPU path)" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape[0] != b or t.shape[1] != m or t.device != device:
+        raise ValueError("%s must be (%d, %d) on %s" % (name, b, m, where))
+    if t.stride(1) != 1 and m != 1:
+        raise ValueError("%s must have unit stride along its rows" % name)
+    return t.data_ptr(), (t.stride(0) if b > 1 else m)
+
+
+def fused_linear_a16(x: torch.Tensor, w: Weights, y=None, h=None, stream=None):
+    """The layer on BF16 X (b x m, b <= 64, rows may be strided), which is not quantized:
+    y = x D(R) + bf16(x D(L1)) L2 with D() the weights' codes times scales. h: buffer of
+    x D(L1) (b x r BF16), left in it. autograd does not record the call."""
+    lib = load()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a 2-D torch tensor")
+    b, dev, bf = x.shape[0], w.rq.device, torch.bfloat16
+    px, ldx = _rows(x, "x", bf, b, w.m, dev, "the weights' device")
+    if y is None:
+        y = _empty((b, w.n), bf, dev, stream)
+    if h is None and w.r:
+        h = _empty((b, w.r), bf, dev, stream)
+    py = _mat(y, "y", bf, b, w.n, dev)
+    ph = _mat(h, "h", bf, b, w.r, dev) if w.r else None
+    st, back = _on(dev, stream)
+    status = lib.twq_fused_linear_a16(px, ldx, b, ctypes.byref(w.c_struct()), ph, py, st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, "twq_fused_linear_a16")
+    return y
+
+
+class Experts:
+    """The experts of one block: packed weights `up` (m x 2f, the gate's columns first) and `down`
+    (f x m), each a Weights whose tensors have a leading dimension of `count` experts,
+    contiguous on one CUDA device. Experts.empty and pack fill it from BF16 weights."""
+
+    def __init__(self, up: Weights, down: Weights):
+        load()
+        self.count, self.m, self.f = up.rq.shape[0], up.m, down.m
+        self.device = up.rq.device
+        if down.n != up.m or up.n != 2 * down.m:
+            raise ValueError("up must be (m, 2f) and down (f, m)")
+        for w, name in ((up, "up"), (down, "down")):
+            for t, field, dtype, shape in (
+                    (w.rq, "rq", torch.uint8, (w.n, w.m // 2)),
+                    (w.sr, "sr", torch.float32, (w.m // 128, w.n)),
+                    (w.l1q, "l1q", torch.uint8, (w.r, w.m // 2)),
+                    (w.sl1, "sl1", torch.float32, (w.m // 128, w.r)),
+                    (w.l2t, "l2t", torch.bfloat16, (w.n, w.r))):
+                _dev(t, "%s.%s" % (name, field), dtype)
+                if tuple(t.shape) != (self.count, *shape) or t.device != self.device:
+                    raise ValueError("%s.%s must be %s on one device" % (name, field, (self.count, *shape)))
+        self.up, self.down = up, down
+        self._c = _Experts(self.count, up.c_struct(), down.c_struct())
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def empty(count: int, m: int, f: int, r: int, device, r_down: int | None = None) -> "Experts":
+        def stacked(m, n, r):
+            one = Weights.empty(m, n, r, "meta")
+            return Weights(m, n, r, *(torch.empty((count, *t.shape), dtype=t.dtype, device=device)
+                                      for t in (one.rq, one.sr, one.l1q, one.sl1, one.l2t)))
+        return Experts(stacked(m, 2 * f, r), stacked(f, m, r if r_down is None else r_down))
+
+    def pack(self, e: int, R_up, L1_up, L2_up, R_down, L1_down, L2_down, stream=None) -> None:
+        """pack_weights of expert e's BF16 factors (L1, L2: None with rank 0)."""
+        if not 0 <= e < self.count:
+            raise IndexError("expert %d of %d" % (e, self.count))
+        for w, factors in ((self.up, (R_up, L1_up, L2_up)), (self.down, (R_down, L1_down, L2_down))):
+            R, L1, L2 = factors
+            want = (w.m, w.n), (w.m, w.r), (w.r, w.n)
+            got = tuple(R.shape), tuple(L1.shape) if w.r else want[1], tuple(L2.shape) if w.r else want[2]
+            if got != want:
+                raise ValueError("expert factors must be %s, got %s" % (want, got))
+            pack_weights(R, L1 if w.r else None, L2 if w.r else None,
+                         Weights(w.m, w.n, w.r, w.rq[e], w.sr[e], w.l1q[e], w.sl1[e], w.l2t[e]), stream)
+
+
+_ROUTE = {torch.float32: ("twq_moe_route", "twq_moe_layer"),
+          torch.bfloat16: ("twq_moe_route_bf16", "twq_moe_layer_bf16")}
+
+
+def _choices(ids, weights, b, k, device, stream):
+    if ids is None:
+        ids = _empty((b, k), torch.int32, device, stream)
+    if weights is None:
+        weights = _empty((b, k), torch.float32, device, stream)
+    return ids, weights, _mat(ids, "ids", torch.int32, b, k, device), _mat(
+        weights, "weights", torch.float32, b, k, device)
+
+
+def _logits_entry(logits, which):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D torch tensor")
+    if logits.dtype not in _ROUTE:
+        raise TypeError("logits must be torch.float32 or torch.bfloat16, got %s" % logits.dtype)
+    return _ROUTE[logits.dtype][which]
+
+
+def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, ids=None, weights=None,
+              stream=None):
+    """The k largest logits of each row (b x count, fp32 or BF16, rows may be strided) and their
+    softmax weights, over the chosen ones (renormalize) or over the row: ids (b x k int32) and
+    weights (b x k fp32). Ties go to the lowest index; where fewer than k logits are above -inf,
+    the last ids are -1 and their weights 0."""
+    lib = load()
+    fn = _logits_entry(logits, 0)
+    b, count = logits.shape
+    dev = logits.device
+    pl, ld = _rows(logits, "logits", logits.dtype, b, count, dev, "one device")
+    ids, weights, pi, pw = _choices(ids, weights, b, k, dev, stream)
+    st, back = _on(dev, stream)
+    status = getattr(lib, fn)(pl, ld, b, count, k, int(renormalize), pi, pw, st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, fn)
+    return ids, weights
+
+
+def moe_workspace_bytes(b: int, k: int, experts: Experts) -> int:
+    return int(load().twq_moe_workspace_bytes(b, k, experts._ref))
+
+
+def _moe_buffers(x, k, ex, base, y, workspace, stream):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a 2-D torch tensor")
+    b, dev, bf = x.shape[0], ex.device, torch.bfloat16
+    px, ldx = _rows(x, "x", bf, b, ex.m, dev, "the experts' device")
+    pb = None if base is None else _mat(base, "base", bf, b, ex.m, dev)
+    if y is None:
+        y = _empty((b, ex.m), bf, dev, stream)
+    if workspace is None:
+        workspace = _empty(max(moe_workspace_bytes(b, k, ex), 16), torch.uint8, dev, stream)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the experts' device")
+    _dev(workspace, "workspace", torch.uint8)
+    return b, px, ldx, pb, y, _mat(y, "y", bf, b, ex.m, dev), workspace
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, experts: Experts,
+                base=None, y=None, workspace=None, stream=None):
+    """y = base + sum over each token's k slots of weight * expert(x), the experts' gated products
+    (silu(gate) * up, then down) on BF16 X (b x m, b <= 64, rows may be strided): y (b x m BF16).
+    ids (b x k int32) and weights (b x k fp32) from moe_route or the caller; an id outside
+    [0, count) adds nothing. base: b x m BF16 (may be y itself) or None (0). autograd does not
+    record the call."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be a 2-D torch tensor")
+    k = ids.shape[1]
+    b, px, ldx, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
+    _, _, pi, pw = _choices(ids, weights, b, k, experts.device, stream)
+    st, back = _on(experts.device, stream)
+    status = _lib.twq_moe_experts(px, ldx, b, pi, pw, k, experts._ref, pb, py,
+                                  workspace.data_ptr(), workspace.numel(), st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, "twq_moe_experts")
+    return y
+
+
+def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, experts: Experts,
+              renormalize: bool = True, base=None, y=None, ids=None, weights=None, workspace=None,
+              stream=None):
+    """moe_route on the router's logits (b x count) and moe_experts on its choice, in one call:
+    (y, ids, weights)."""
+    fn = _logits_entry(logits, 1)
+    b, px, ldx, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
+    pl, ld = _rows(logits, "logits", logits.dtype, b, experts.count, experts.device,
+                   "the experts' device")
+    ids, weights, pi, pw = _choices(ids, weights, b, k, experts.device, stream)
+    st, back = _on(experts.device, stream)
+    status = getattr(_lib, fn)(px, ldx, b, pl, ld, k, int(renormalize), experts._ref, pb, pi, pw,
+                               py, workspace.data_ptr(), workspace.numel(), st)
+    if back is not None:
+        torch.cuda.set_device(back)
+    _check(status, fn)
+    return y, ids, weights
 
 
 def selftest_adapter_stall(wait_limit_ns: int) -> None:
