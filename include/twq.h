@@ -568,14 +568,14 @@ typedef struct {
  *   y          b x m BF16 (output, every row is written)
  *   workspace  device buffer of twq_moe_workspace_bytes(b, k, e) bytes, 16-byte aligned; calls
  *              that overlap on the GPU need one each
- * Sums are held in fp32. a is kept as two BF16 terms (16 bits), g and u are not rounded. Each
- * expert's weights are read once for all its tokens (beyond 32 of them again for every 32, beyond
- * 16 for down). The sum over slots follows the experts' order; equal calls give equal bits.
+ * Sums are held in fp32. a is kept as two BF16 terms (16 bits), g, u and y_e are not rounded. An
+ * expert's weights are read for 8, 16 or 32 of its tokens at a time (those of down for half as
+ * many). The sum over the slots is in their order; equal calls give equal bits.
  * Limits: b <= 64 (b == 0 is a no-op), k <= 16, count <= 1024, m and f multiples of 128, m and 2f
  * <= 2^20, ranks as twq_weights (up's and down's may differ).
  * Errors: TWQ_ERR_INVALID_ARG on a null pointer, a bad shape (down.n != up.m, up.n != 2 down.m) or
  * a short workspace; TWQ_ERR_UNSUPPORTED beyond the limits.
- * Two launches, and one more for each of the ranks that is not 0.
+ * Three launches, and one more for each of the ranks that is not 0.
  */
 TWQ_API size_t twq_moe_workspace_bytes(int64_t b, int64_t k, const twq_experts* e);
 TWQ_API twq_status twq_moe_experts(const uint16_t* x, int64_t ldx, int64_t b, const int32_t* ids,
@@ -628,6 +628,10 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
  * 0 (the initial state) sets it back. Launches nothing itself.
  */
 TWQ_API twq_status twq_selftest_adapter_stall(int64_t wait_limit_ns);
+
+/* The same for the calls on BF16 activations (twq_fused_linear_a16, twq_moe_experts and
+ * twq_moe_layer; site codes 71..74, 75: a copy in flight did not land). */
+TWQ_API twq_status twq_selftest_a16_stall(int64_t wait_limit_ns);
 
 /*
  * Drops the library's host-side caches: the encoded TMA tensor maps of the

@@ -51,4 +51,9 @@ struct MoeCall {
 cudaError_t launch_moe_experts(const MoeCall& c, cudaStream_t st);
 size_t moe_workspace(int64_t pairs, const twq_experts* e);
 
+// Self-test: while not 0, the calling thread's launches have a loading warp that stops early and
+// this limit of their waits.
+void set_a16_stall(int64_t wait_limit_ns);
+cudaError_t read_and_clear_a16_status(int* code);
+
 }  // namespace twq

@@ -6,71 +6,119 @@
 // exactly and sums in fp32, and the group's fp32 scale multiplies that sum once.
 //
 // Few rows make this a stream of weights: what bounds it is HBM, or latency where the weights are
-// few. So every warp has a ring of its own in shared memory that it fills with cp.async, no
-// thread waits for another one's copies, and the reduction is split as far as it takes to have all
-// SMs load: over warps, and over the blocks of a cluster, which add up over distributed shared
-// memory in a fixed order. The weights are the M side of the products, 32 columns of them to a
-// warp, rows of activations the N side, 8 to a tile.
+// few. A block takes 256 weight columns (the M side of the products; rows of activations are the N
+// side, 8 to a tile) and walks the reduction in steps of two groups through a ring in shared memory:
+//   TMA warp   the step's codes, 256 columns x 128 bytes in the 128-byte swizzle, and scales
+//   X warps    the step's activations, gathered, in the order in which the products take them
+//   8 warps    products, 32 columns each
+// A cluster of blocks splits the reduction where there are few columns, and adds up over distributed
+// shared memory in a fixed order.
 //
-// A unit of a warp's work is 32 weight columns x one group of 128: 16 bytes (32 codes) per lane and
-// column, as they lie in memory. The order in which a lane's 32 codes go through the products is
-// free as long as the activations follow it: codes i and i + 4 of a word become one BF16 pair by one
-// logic operation (0x4300 | (code ^ 8) is 136 + code) and one exact subtraction. The low-rank
-// factor L2 comes last, as units of 32 columns x 32 ranks.
+// 16 bytes (32 codes) of a column go to one lane. The order in which a lane's codes go through the
+// products is free as long as the activations follow it: codes i and i + 4 of a word become one BF16
+// pair by one logic operation (0x4300 | (code ^ 8) is 136 + code) and one exact subtraction. That
+// conversion, 11 instructions for 8 codes, is most of a warp's some 240 instructions for 32 columns
+// x one group; at the rate of HBM a quarter of an SM has 370 cycles for it. The low-rank factor L2
+// comes last, in steps of 64 ranks.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "sm100_ptx.cuh"
 #include "twq_a16.h"
 #include "twq_adapter.h"
+#include "twq_internal.h"
 
 namespace twq {
+
+__device__ int g_a16_status;
+
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 4;
-constexpr int kRows = 32;                 // weight columns of a unit (rows of the packed codes)
-constexpr int kStageBytes = kRows * 64 + kRows * 4;
-constexpr int kYStride = 40;              // floats between the rows of a warp's sums
+constexpr int kBox = 128;                 // weight columns of a copy, at most
+constexpr int kYStride = 36;              // floats between the rows of a warp's sums
 constexpr int kSms = 148;
+constexpr int kMaxSlots = 4;
+constexpr int kMaxSmem = 226 * 1024;      // dynamic
 
 enum Mode : int {
   kModeH = 0,    // h = bf16(x D(L1))
   kModeAct = 1,  // a = silu(g) u, in two BF16 terms
-  kModeY = 2,    // y = base + sum of weight * (x D(R) + h L2)
+  kModeY = 2,    // y = x D(R) + h L2
+  kModePart = 3, // the same in fp32, not rounded
 };
 
+// Site codes of the bounded waits.
+enum : int { kSiteEmpty = 71, kSiteXEmpty, kSiteWFull, kSiteXFull, kSiteSums, kSiteLand };
+
 struct A16Args {
-  const uint8_t* q;     // codes: n x K/2 per expert
-  const float* s;       // scales: K/128 x n per expert
-  const uint16_t* l2t;  // n x r per expert (kModeH: none)
-  int64_t q_expert, s_expert, l2_expert;  // elements from one expert to the next
-  int K, n, r;          // r: ranks of l2t read here
-  int f;                // kModeAct: gate columns (n = 2 f)
-  const uint16_t* x;    // token rows (row stride ldx), or the pairs' activations
-  const uint16_t* x_lo; // kParts == 2: the activations' second terms
+  CUtensorMap wq, ws, wl;  // codes, scales, L2: the experts' rows one after another
+  const uint8_t* q;        // what the maps are of (host)
+  const float* s;
+  const uint16_t* l2t;
+  int K, n, r;             // r: ranks of L2 read here
+  int f;                   // kModeAct: gate columns (n = 2 f)
+  int width;               // columns of a box: 128, or fewer (kModeH). kModeAct: gates in one box, what they multiply in the other
+  const uint16_t* x;       // token rows (row stride ldx), or the pairs' activations
+  const uint16_t* x_lo;    // kParts == 2: the activations' second terms
   int64_t ldx;
-  const uint16_t* h;    // low-rank input, tokens or pairs x r
-  const int32_t* ids;   // b x k
-  const float* weights; // b x k
+  const uint16_t* h;       // low-rank input, tokens or pairs x r
+  const int32_t* ids;      // b x k
   int b, k, count;
-  const uint16_t* base; // kModeY
-  uint16_t* out;
-  uint16_t* out_lo;     // kModeAct
-  int tiles;            // column tiles of a chunk
-  int split;            // blocks of a cluster
-  bool ids_ready, x_ready;  // complete before this kernel starts, whatever it waits for
+  uint16_t* out;           // kModePart: fp32
+  uint16_t* out_lo;        // kModeAct
+  int blocks;              // blocks of columns
+  int split_log;           // log2 of the blocks of a cluster
+  int slots;               // of the ring
+  int parts;               // room for other blocks' parts of a job
+  bool ids_ready, x_ready; // complete before this kernel starts, whatever it waits for
+  uint64_t wait_ns;
+  int stall;               // self-test: the X warps stop early
 };
+
+struct WaitState {  // a block's, in shared memory
+  int gave_up;
+  uint64_t ns;  // limit of a wait
+};
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (w->gave_up) return false;
+    if (global_timer_ns() - t0 > w->ns) {
+      atomicCAS(&g_a16_status, 0, site);
+      w->gave_up = 1;
+      return false;
+    }
+  }
+}
+// Bounded wait of a warp: one answer for all of its lanes; false once the block is giving up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, wait_slow(bar, parity, w, site));
+}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Activations may come from the kernel that this one overlaps: plain loads, kept in order.
@@ -87,35 +135,11 @@ __device__ __forceinline__ uint32_t ld4(const void* p) {
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
+__device__ __forceinline__ uint2 ld8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ float lds_f(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld_peer(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-// 16 bytes into shared memory; zeros where `in` is false (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -133,460 +157,827 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// What of a block's shared memory is where, in bytes. pairs: b x k.
+// What of a block's shared memory is where, in bytes from a 1024-byte boundary.
 struct Layout {
-  int ring, sums, part, chunks, order, cnt, total;
+  int sums, recv, chunks, order, cnt, total;
 };
-template <int NT, int kMode, int kParts, bool kRouted>
-__host__ __device__ inline Layout layout(int b, int k, int count, int split) {
-  constexpr int cap = 8 * NT / kParts;
-  const int pairs = kRouted ? b * k : b;
-  const int rows = kMode == kModeY ? b : cap;
-  const int buffers = kMode == kModeY ? 1 : 2;
-  const int groups = pairs < count ? pairs : count;
-  const int chunks = kRouted ? (groups + pairs / cap < pairs ? groups + pairs / cap : pairs) : 0;
-  Layout l;
-  l.ring = 0;
-  l.sums = l.ring + kWarps * kStages * kStageBytes;
-  l.part = l.sums + buffers * kWarps * rows * kYStride * 4;
-  l.chunks = l.part + (split > 1 ? buffers * rows * kRows * 4 : 0);
-  l.order = l.chunks + chunks * 8;
-  l.cnt = l.order + (kRouted ? 2 * ((pairs * 2 + 7) / 8 * 8) : 0);
-  l.total = l.cnt + (kRouted ? count * 4 : 0);
-  l.total = (l.total + 15) / 16 * 16;
-  return l;
+
+// kWarps: that multiply, 32 weight columns each.
+template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
+struct Kernel {
+  static constexpr int kMulThreads = kWarps * 32, kCols = kWarps * 32;
+  // Copies of a step: of 128 columns, or of the block's (kModeAct: of half, gates and what they multiply).
+  static constexpr int kBoxCols = kMode == kModeAct ? kCols / 2 : kCols < kBox ? kCols : kBox;
+  static constexpr int kWBytes = kCols * 128, kSBytes = kCols * 8 < 1024 ? 1024 : kCols * 8;
+  static constexpr int kCap = 8 * NT / kParts;                 // rows of activations in a chunk
+  static constexpr int kXWarps = NT == 1 ? 2 : 3;
+  static constexpr int kThreads = kMulThreads + 32 + 32 * kXWarps;
+  static constexpr int kBlocksPerSm = kWarps == 8 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;
+  static constexpr int kSlot = kWBytes + kSBytes + 4096 * NT;
+
+  static __host__ __device__ int max_chunks(int pairs, int count) {
+    const int groups = pairs < count ? pairs : count;
+    return groups + pairs / kCap < pairs ? groups + pairs / kCap : pairs;
+  }
+  // parts: other blocks' parts of a job that there is room for.
+  static __host__ __device__ Layout layout(int b, int k, int count, int slots, int parts) {
+    const int pairs = kRouted ? b * k : b;
+    Layout l;
+    l.sums = slots * kSlot;
+    l.recv = l.sums + kWarps * kCap * kYStride * 4;
+    l.chunks = l.recv + parts * kCap * kCols * 4;
+    l.order = l.chunks + (kRouted ? max_chunks(pairs, count) * 8 : 0);
+    l.cnt = l.order + (kRouted ? 3 * ((pairs * 2 + 7) / 8 * 8) : 0);
+    l.total = (l.cnt + (kRouted ? count * 4 : 0) + 15) / 16 * 16;
+    return l;
+  }
+};
+
+// Chunks of at most `cap` rows that share an expert, experts ascending, rows of an expert in the
+// order of their pairs: {expert, first place in `order` | rows << 16}. Returns their number.
+__device__ __noinline__ int make_chunks(const int32_t* ids, int pairs, int count, int cap, uint2* chunk,
+                                        uint16_t* order, int* cnt, int* number) {
+  if (pairs <= 32) {  // in one warp's registers
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      const unsigned before = (1u << lane) - 1u, all = 0xFFFFFFFFu;
+      int id = lane < pairs ? static_cast<int>(ld4(ids + lane)) : -1;
+      if (id < 0 || id >= count) id = -1;
+      const unsigned same = __match_any_sync(all, id);
+      const bool leads = id >= 0 && !(same & before);
+      int place = 0, at = 0;  // of the leader's expert: rows and chunks of the experts before it
+      for (unsigned todo = __ballot_sync(all, leads); todo; todo &= todo - 1) {
+        const int l = __ffs(todo) - 1;
+        const int e = __shfl_sync(all, id, l), n = __popc(__shfl_sync(all, same, l));
+        if (e < id) place += n, at += (n + cap - 1) / cap;
+      }
+      if (leads)
+        for (int i = 0, n = __popc(same); i < n; i += cap)
+          chunk[at + i / cap] = make_uint2(id, (place + i) | (min(cap, n - i) << 16));
+      if (id >= 0) order[place + __popc(same & before)] = static_cast<uint16_t>(lane);
+      const int chunks = __reduce_add_sync(all, leads ? (__popc(same) + cap - 1) / cap : 0);
+      if (lane == 0) *number = chunks;
+    }
+    __syncthreads();
+    return *number;
+  }
+  const int pad = (pairs * 2 + 7) / 8 * 4;
+  uint16_t* const rank = order + pad;
+  uint16_t* const id_of = rank + pad;  // 0xFFFF: none
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
+  for (int p = tid; p < pairs; p += threads) {
+    const int id = static_cast<int>(ld4(ids + p));
+    id_of[p] = static_cast<uint16_t>(id < 0 || id >= count ? 0xFFFF : id);
+  }
+  for (int i = tid; i < count; i += threads) cnt[i] = 0;
+  __syncthreads();
+  if (tid < 32) {
+    for (int p0 = 0; p0 < pairs; p0 += 32) {
+      const int p = p0 + lane;
+      const int id = p < pairs ? id_of[p] : 0xFFFF;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+      const int at = id != 0xFFFF ? cnt[id] : 0;
+      __syncwarp();
+      if (id != 0xFFFF) {
+        rank[p] = static_cast<uint16_t>(at + __popc(same & ((1u << lane) - 1u)));
+        if (lane == __ffs(same) - 1) cnt[id] = at + __popc(same);
+      }
+      __syncwarp();
+    }
+    int rows = 0, chunks = 0;
+    for (int e0 = 0; e0 < count; e0 += 32) {
+      const int e = e0 + lane;
+      const int c = e < count ? cnt[e] : 0;
+      if (!__any_sync(0xFFFFFFFFu, c)) continue;
+      const int n = (c + cap - 1) / cap;
+      int both = c | n << 16;  // up to 1024 of each
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, both, d);
+        if (lane >= d) both += o;
+      }
+      const int first = rows + (both & 0xFFFF) - c, at = chunks + (both >> 16) - n;
+      if (c) cnt[e] = first;
+      for (int i = 0; i < n; ++i)
+        chunk[at + i] = make_uint2(e, (first + i * cap) | (min(cap, c - i * cap) << 16));
+      both = __shfl_sync(0xFFFFFFFFu, both, 31);
+      rows += both & 0xFFFF;
+      chunks += both >> 16;
+    }
+    if (lane == 0) *number = chunks;
+  }
+  __syncthreads();
+  for (int p = tid; p < pairs; p += threads) {
+    const int id = id_of[p];
+    if (id == 0xFFFF) continue;
+    order[cnt[id] + rank[p]] = static_cast<uint16_t>(p);
+  }
+  __syncthreads();
+  return *number;
 }
 
-template <int NT, int kMode, int kParts, bool kRouted>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) a16_kernel(const __grid_constant__ A16Args a) {
-  constexpr int kCap = 8 * NT / kParts;  // rows of activations in a chunk
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_chunks, s_twice;
-  const Layout lay = layout<NT, kMode, kParts, kRouted>(a.b, a.k, a.count, a.split);
+template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
+__global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kThreads,
+                                  Kernel<kWarps, NT, kMode, kParts, kRouted>::kBlocksPerSm)
+    a16_kernel(const __grid_constant__ A16Args a) {
+  using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
+  constexpr int kCap = K::kCap, kSlot = K::kSlot, kCols = K::kCols, kMulThreads = K::kMulThreads;
+  constexpr int kWBytes = K::kWBytes, kSBytes = K::kSBytes, kBoxCols = K::kBoxCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  __shared__ uint64_t s_wfull[kMaxSlots], s_xfull[kMaxSlots], s_empty[kMaxSlots];
+  __shared__ uint64_t s_recv;
+  __shared__ WaitState s_wait;
+  __shared__ int s_chunks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rank = blockIdx.x % a.split, cluster = blockIdx.x / a.split;
-  const int clusters = gridDim.x / a.split;
-  uint2* s_chunk = reinterpret_cast<uint2*>(smem + lay.chunks);
-  uint16_t* s_order = reinterpret_cast<uint16_t*>(smem + lay.order);
-  const int pairs = kRouted ? a.b * a.k : a.b;
+  const int split = 1 << a.split_log;
+  const int rank = blockIdx.x & (split - 1), cluster = blockIdx.x >> a.split_log;
+  const Layout lay = K::layout(a.b, a.k, a.count, a.slots, a.parts);
+  uint2* const s_chunk = reinterpret_cast<uint2*>(smem + lay.chunks);
+  uint16_t* const s_order = reinterpret_cast<uint16_t*>(smem + lay.order);
 
-  bool waited = false;
-  auto wait_all = [&] {
-    if (!waited) pdl_wait();
-    waited = true;
-  };
+  if (tid == 0) {
+    for (int i = 0; i < a.slots; ++i) {
+      mbar_init(&s_wfull[i], 1);
+      mbar_init(&s_xfull[i], 1);
+      mbar_init(&s_empty[i], kWarps);
+    }
+    mbar_init(&s_recv, 1);
+    fence_barrier_init();
+    s_wait.gave_up = 0;
+    s_wait.ns = a.wait_ns;
+  }
   if (!a.ids_ready) {
-    wait_all();
+    pdl_wait();
     pdl_launch_dependents();
   }
-
-  // Chunks of at most kCap rows that share an expert, experts ascending, rows of an expert in the
-  // order of their pairs: {expert, first place in s_order | rows << 16}.
+  int chunks = 1;
   if constexpr (kRouted) {
-    int* s_cnt = reinterpret_cast<int*>(smem + lay.cnt);
-    uint16_t* s_rank = s_order + (pairs * 2 + 7) / 8 * 4;
-    for (int i = tid; i < a.count; i += kThreads) s_cnt[i] = 0;
-    if (tid == 0) s_twice = 0;
-    __syncthreads();
-    if (warp == 0) {
-      for (int p0 = 0; p0 < pairs; p0 += 32) {
-        const int p = p0 + lane;
-        int id = p < pairs ? static_cast<int>(ld4(a.ids + p)) : -1;
-        if (id < 0 || id >= a.count) id = -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-        const int at = id >= 0 ? s_cnt[id] : 0;
-        __syncwarp();
-        if (id >= 0) {
-          s_rank[p] = static_cast<uint16_t>(at + __popc(same & ((1u << lane) - 1u)));
-          if (lane == __ffs(same) - 1) s_cnt[id] = at + __popc(same);
-        }
-        __syncwarp();
-      }
-      int rows = 0, chunks = 0;
-      for (int e0 = 0; e0 < a.count; e0 += 32) {
-        const int e = e0 + lane;
-        const int c = e < a.count ? s_cnt[e] : 0;
-        const int n = (c + kCap - 1) / kCap;
-        int rs = c, cs = n;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const int r2 = __shfl_up_sync(0xFFFFFFFFu, rs, d), c2 = __shfl_up_sync(0xFFFFFFFFu, cs, d);
-          if (lane >= d) rs += r2, cs += c2;
-        }
-        const int first = rows + rs - c;
-        if (e < a.count) s_cnt[e] = first;
-        for (int i = 0; i < n; ++i)
-          s_chunk[chunks + cs - n + i] =
-              make_uint2(e, (first + i * kCap) | (min(kCap, c - i * kCap) << 16));
-        rows += __shfl_sync(0xFFFFFFFFu, rs, 31);
-        chunks += __shfl_sync(0xFFFFFFFFu, cs, 31);
-      }
-      if (lane == 0) s_chunks = chunks;
-    }
-    __syncthreads();
-    for (int p = tid; p < pairs; p += kThreads) {
-      const int id = static_cast<int>(ld4(a.ids + p));
-      if (id < 0 || id >= a.count) continue;
-      s_order[s_cnt[id] + s_rank[p]] = static_cast<uint16_t>(p);
-      // an expert twice among one token's
-      for (int o = p - p % a.k; o < p; ++o)
-        if (static_cast<int>(ld4(a.ids + o)) == id) s_twice = 1;
-    }
+    chunks = make_chunks(a.ids, a.b * a.k, a.count, kCap, s_chunk, s_order, reinterpret_cast<int*>(smem + lay.cnt),
+                         &s_chunks);
+  } else {
+    chunks = (a.b + kCap - 1) / kCap;
     __syncthreads();
   }
-  const int chunks = kRouted ? s_chunks : (a.b + kCap - 1) / kCap;
+  if (split > 1) cluster_arrive_relaxed();  // this block's barriers exist
   auto chunk_expert = [&](int c) { return kRouted ? static_cast<int>(s_chunk[c].x) : 0; };
   auto chunk_first = [&](int c) { return kRouted ? static_cast<int>(s_chunk[c].y & 0xFFFFu) : c * kCap; };
   auto chunk_rows = [&](int c) {
     return kRouted ? static_cast<int>(s_chunk[c].y >> 16) : min(kCap, a.b - c * kCap);
   };
+  auto pair_of = [&](int first, int i) { return kRouted ? static_cast<int>(s_order[first + i]) : first + i; };
 
-  // The warp's share of the units. kModeY: of all chunks' units of one column tile; else of every
-  // job's, a job being a chunk and a column tile.
-  const int groups = a.K >> 7, per = groups + (a.r + 31) / 32;
-  const int team = rank * kWarps + warp, teams = a.split * kWarps;
-  const int total = kMode == kModeY ? chunks * per : per;
-  const int lo = static_cast<int>(static_cast<int64_t>(total) * team / teams);
-  const int hi = static_cast<int>(static_cast<int64_t>(total) * (team + 1) / teams);
-  const int jobs = kMode == kModeY ? a.tiles : chunks * a.tiles;
-
-  // Column (row of the codes) that lane quad g loads for 8-row part i of tile `tile`, or -1.
-  const uint32_t ring = smem_u32(smem + lay.ring) + warp * kStages * kStageBytes;
-  const int64_t half = a.K >> 1;
-  auto column = [&](int tile, int i) {
-    if constexpr (kMode == kModeAct) return (i >> 1) * a.f + tile * 16 + (i & 1) * 8 + g;
-    const int c = tile * kRows + i * 8 + g;
-    return c < a.n ? c : -1;
+  // The work. A job is a chunk and a block of columns (chunks of one block next to one another where
+  // they share the weights). A cluster has the jobs [job0, job1), and each of its blocks an equal share
+  // [lo, hi) of their steps, one job after the other: so a block may end a job that the one before it
+  // began. All roles walk the same steps.
+  const int groups = a.K >> 7, code_steps = (groups + 1) / 2, per = code_steps + (a.r + 63) / 64;
+  const int jobs = chunks * a.blocks, clusters = gridDim.x >> a.split_log;
+  const int each = jobs / clusters, more = jobs - each * clusters;  // `more` clusters have one more
+  const int job0 = each * cluster + min(cluster, more), job1 = job0 + each + (cluster < more);
+  const int total = (job1 - job0) * per;
+  auto begin_of = [&](int r) { return total * r >> a.split_log; };
+  const int lo = begin_of(rank), hi = begin_of(rank + 1);
+  struct Walk {
+    int job, block, chunk, u;  // step u of the job
+  };
+  auto enter_job = [&](Walk& k) {
+    if constexpr (kRouted)
+      k.chunk = k.job / a.blocks, k.block = k.job - k.chunk * a.blocks;
+    else
+      k.block = k.job / chunks, k.chunk = k.job - k.block * chunks;
+  };
+  Walk at0 = {job0, 0, 0, 0};
+  if (lo < hi) {
+    const int skip = lo / per;
+    at0.job += skip, at0.u = lo - skip * per;
+    enter_job(at0);
+  }
+  // The next step; true where it is of another job.
+  auto advance = [&](Walk& k) {
+    if (++k.u < per) return false;
+    ++k.job, k.u = 0;
+    if (k.job < job1) enter_job(k);
+    return true;
+  };
+  struct Turn {
+    int slot = 0;
+    uint32_t phase = 0;
+  };
+  auto next_slot = [&](Turn& s) {
+    if (++s.slot == a.slots) s.slot = 0, s.phase ^= 1;
   };
 
-  // Copies, kStages - 1 units ahead.
-  struct {
-    int job, chunk, tile, u, left;
-  } p = {cluster, 0, 0, 0, 0};
-  auto start_job = [&] {
-    p.left = p.job < jobs ? hi - lo : 0;
-    if (p.left <= 0) return;
-    if constexpr (kMode == kModeY) {
-      p.tile = p.job, p.chunk = lo / per, p.u = lo % per;
-    } else {
-      p.chunk = p.job / a.tiles, p.tile = p.job - p.chunk * a.tiles, p.u = lo;
-    }
-  };
-  start_job();
-  auto request = [&](int stage) {
-    if (p.left > 0) {
-      const uint32_t dst = ring + stage * kStageBytes;
-      const int64_t e = chunk_expert(p.chunk);
-      if (p.u < groups) {
-        const uint8_t* q = a.q + e * a.q_expert + p.u * 64 + t * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = column(p.tile, i);
-          copy16(dst + i * 512 + lane * 16, c >= 0 ? q + c * half : q, c >= 0);
-        }
-        if (lane < 8) {  // four scales each
-          int c = kMode == kModeAct ? (lane >> 2) * a.f + p.tile * 16 + (lane & 3) * 4 : p.tile * kRows + lane * 4;
-          const bool in = c < a.n;
-          if (!in) c = 0;
-          copy16(dst + kRows * 64 + lane * 16, a.s + e * a.s_expert + static_cast<int64_t>(p.u) * a.n + c, in);
-        }
-      } else {
-        const int at = (p.u - groups) * 32 + t * 8;
-        const uint16_t* l2 = a.l2t + e * a.l2_expert;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = column(p.tile, i);
-          const bool in = c >= 0 && at < a.r;
-          copy16(dst + i * 512 + lane * 16, in ? l2 + static_cast<int64_t>(c) * a.r + at : l2, in);
+  if (warp == kWarps) {  // TMA
+    Turn s;
+    Walk k = at0;
+    int issued = 0;
+    for (int v = lo; v < hi; ++v) {
+      if (issued >= a.slots && !wait(&s_empty[s.slot], s.phase ^ 1, &s_wait, kSiteEmpty)) break;
+      if (lane == 0) {
+        const int col = k.block * (kMode == kModeAct ? kCols / 2 : kCols);
+        const int boxes = kMode == kModeAct ? 2 : min(kCols / kBoxCols, (a.n - col + kBoxCols - 1) / kBoxCols);
+        const int next = kMode == kModeAct ? a.f : kBoxCols;  // from one box to the other
+        uint8_t* const dst = smem + s.slot * kSlot;
+        const int e = chunk_expert(k.chunk), row = e * a.n + col;
+        if (k.u < code_steps) {
+          mbar_arrive_expect_tx(&s_wfull[s.slot], boxes * a.width * (128 + 8));
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i) {
+            tma_load_2d(dst + i * kBoxCols * 128, &a.wq, &s_wfull[s.slot], k.u * 128, row + i * next);
+            tma_load_2d(dst + kWBytes + i * kBoxCols * 8, &a.ws, &s_wfull[s.slot], col + i * next,
+                        e * groups + 2 * k.u);
+          }
+        } else {
+          mbar_arrive_expect_tx(&s_wfull[s.slot], boxes * a.width * 128);
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(dst + i * kBoxCols * 128, &a.wl, &s_wfull[s.slot], (k.u - code_steps) * 64, row + i * next);
         }
       }
-      --p.left;
-      if (++p.u == per) p.u = 0, ++p.chunk;
-      if (p.left == 0) {
-        p.job += clusters;
-        start_job();
-      }
-    }
-    copy_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) request(i);
-
-  if (!a.x_ready) wait_all();
-  if (a.ids_ready) pdl_launch_dependents();
-
-  int stage = 0;
-  float* const sums = reinterpret_cast<float*>(smem + lay.sums);
-  constexpr int kBuffers = kMode == kModeY ? 1 : 2;
-  const int srows = kMode == kModeY ? a.b : kCap;
-  float* const part = reinterpret_cast<float*>(smem + lay.part);
-  int buffer = 0;
-  for (int job = cluster; job < jobs; job += clusters) {
-    float* const mine = sums + (buffer * kWarps + warp) * srows * kYStride;
-    int chunk, u;
-    const int tile = kMode == kModeY ? job : job % a.tiles;
-    if constexpr (kMode == kModeY) {
-      chunk = lo / per, u = lo % per;
-      for (int i = lane; i < srows * kYStride; i += 32) mine[i] = 0.0f;
       __syncwarp();
-    } else {
-      chunk = job / a.tiles, u = lo;
+      ++issued;
+      next_slot(s);
+      advance(k);
     }
-    float acc[2][NT][4];
-    const uint16_t* row[NT];
-    auto enter_chunk = [&] {
-      const int first = chunk_first(chunk), rows = chunk_rows(chunk);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int col = nt * 8 + g, i = kParts == 2 ? col >> 1 : col;
-        row[nt] = nullptr;
-        if (i < rows) {
-          const int pr = kRouted ? s_order[first + i] : first + i;
-          const int64_t at = kRouted && kParts == 1 ? pr / a.k : pr;
-          row[nt] = (kParts == 2 && (col & 1) ? a.x_lo : a.x) + at * a.ldx;
+    // No copy is in flight when the block leaves, whether it was used or the block gave up.
+    if (lane == 0) {
+      for (int i = max(0, issued - a.slots); i < issued; ++i) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(&s_wfull[i % a.slots], (i / a.slots) & 1)) {
+          if (global_timer_ns() - t0 > 2000000000ull) {
+            atomicExch(&g_a16_status, kSiteLand);
+            break;
+          }
         }
+      }
+    }
+    __syncwarp();
+  } else if (warp > kWarps) {
+    // Activations, each warp a step in turn, its next one's on their way meanwhile. No more warps than
+    // slots: one that does not wait at the steps of the others must not get two turns of the ring ahead.
+    const int turns = min(K::kXWarps, a.slots), turn = warp - kWarps - 1;
+    if (!a.x_ready) pdl_wait();
+    if (a.ids_ready) pdl_launch_dependents();
+    constexpr int kN = NT < 2 ? 1 : 2;  // tiles whose loads are in flight together
+    bool waited = !a.x_ready;
+    Turn s;
+    Walk k = at0;
+    int v = lo, rows = 0, first = 0, known = -1;
+    const uint16_t* row[NT];  // of the lane's column of each tile
+    uint4 x[kN][2][4];
+    // Loads of tiles n0 and, if there is one, n0 + 1 of the step.
+    auto load = [&](int n0) {
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2)
+      for (int nt = 0; nt < kN; ++nt) {
+        if (nt > 0 && (n0 + nt) * 8 >= rows * kParts) break;
+        const uint16_t* const from = row[NT <= 2 ? nt : n0 + nt] + k.u * 256;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i2][nt][j] = 0.0f;
+        for (int w = 0; w < 2; ++w)
+          if (w == 0 || 2 * k.u + 1 < groups) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[nt][w][j] = ld16(from + w * 128 + j * 8);
+          }
       }
     };
-    // Adds (kModeY) or stores the chunk's sums to the warp's own rows.
-    auto leave_chunk = [&] {
-      const int first = chunk_first(chunk), rows = chunk_rows(chunk);
+    auto begin = [&] {  // the step's chunk, and its first loads
+      if (v >= hi) return;
+      if (known != k.chunk) {
+        known = k.chunk;
+        first = chunk_first(k.chunk), rows = chunk_rows(k.chunk);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int c = nt * 8 + g, i = kParts == 2 ? c >> 1 : c;
+          // columns beyond the rows: the first row's, into sums that no one reads
+          const int pr = pair_of(first, i < rows ? i : 0);
+          const int64_t at = kRouted && kParts == 1 ? pr / a.k : pr;
+          row[nt] = (kParts == 2 && (c & 1) ? a.x_lo : a.x) + at * a.ldx + t * 32;
+        }
+      }
+      if (k.u < code_steps) load(0);
+    };
+    auto skip = [&](int by) {
+#pragma unroll 1
+      for (int i = 0; i < by && v < hi; ++i) {
+        ++v;
+        next_slot(s);
+        advance(k);
+      }
+    };
+    if (turn >= turns) v = hi;
+    skip(turn);
+    begin();
+    while (v < hi) {
+      if (a.stall && v - lo >= K::kXWarps) break;
+      uint8_t* const dst = smem + s.slot * kSlot + kWBytes + kSBytes + lane * 16;
+      if (k.u >= code_steps) {
+        if (!waited) pdl_wait();
+        waited = true;
+      }
+      if (v - lo >= a.slots && !wait(&s_empty[s.slot], s.phase ^ 1, &s_wait, kSiteXEmpty)) break;
+      if (k.u < code_steps) {
+#pragma unroll
+        for (int n0 = 0; n0 < NT; n0 += kN) {
+          if (n0 > 0) {
+            if (n0 * 8 >= rows * kParts) break;
+            load(n0);
+          }
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt) {
+            if (nt > 0 && (n0 + nt) * 8 >= rows * kParts) break;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint4 v4 = x[nt][w][j];
+                *reinterpret_cast<uint4*>(dst + (w * NT + n0 + nt) * 2048 + j * 512) =
+                    make_uint4(__byte_perm(v4.x, v4.z, 0x5410), __byte_perm(v4.x, v4.z, 0x7632),
+                               __byte_perm(v4.y, v4.w, 0x5410), __byte_perm(v4.y, v4.w, 0x7632));
+              }
+          }
+        }
+      } else {  // h: ranks as they lie, zeros beyond them
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int c = nt * 8 + g, i = kParts == 2 ? c >> 1 : c;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int at = (k.u - code_steps) * 64 + w * 32 + t * 8;
+            uint4 v4 = make_uint4(0, 0, 0, 0);
+            if (i < rows && !(kParts == 2 && (c & 1)) && at < a.r)
+              v4 = ld16(a.h + static_cast<int64_t>(pair_of(first, i)) * a.r + at);
+            *reinterpret_cast<uint4*>(dst + (w * NT + nt) * 512) = v4;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_xfull[s.slot]);
+      skip(turns);
+      begin();
+    }
+  } else {  // products
+    float* const sums = reinterpret_cast<float*>(smem + lay.sums);
+    float* const mine = sums + warp * kCap * kYStride;
+    // The lane's columns: sigma + 8 i of its warp's 32, i < 4 (kModeAct: of its 16 gates for i < 2, else
+    // of what they multiply). sigma orders them so that 8 lanes read 128 bytes without conflict.
+    const int sigma = (g & 1) * 4 + (g >> 1);
+    const int line = kMode == kModeAct ? warp * 16 + sigma : warp * 32 + sigma;
+    auto line_of = [&](int i) { return kMode == kModeAct ? (i & 1) * 8 + (i >> 1) * kBoxCols : i * 8; };
+    const uint8_t* const w_at[2] = {smem + line * 128 + ((t ^ sigma) << 4),
+                                    smem + line * 128 + (((4 + t) ^ sigma) << 4)};
+    const uint8_t* const s_at = smem + kWBytes + line / kBoxCols * kBoxCols * 8 + line % kBoxCols * 4;
+    const int s_next = a.width * 4;
+    const uint8_t* const x_at = smem + kWBytes + kSBytes + lane * 16;
+    auto lds16 = [](const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); };
+    auto barrier = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kMulThreads) : "memory"); };
+
+    // Outputs are made in items of four neighbours (kModeAct: of four gates and what they multiply,
+    // 16 columns on) of one row.
+    constexpr int kItems = kMode == kModeAct ? kCols / 8 : kCols / 4, kQuads = kMode == kModeAct ? 2 : 1;
+    auto sum_of = [&](int item, int q) {  // this block's
+      const int c = item % kItems, col = kMode == kModeAct ? (c >> 2) * 32 + (c & 3) * 4 + 16 * q : c * 4;
+      return *reinterpret_cast<const float4*>(sums + ((col >> 5) * kCap + item / kItems) * kYStride + (col & 31));
+    };
+    auto put_item = [&](int block, int first, int item, const float4 (&v)[kQuads]) {
+      const int row = item / kItems, c = item % kItems;
+      const int64_t line = pair_of(first, row);
+      if constexpr (kMode == kModeAct) {
+        const float4 gate = v[0], up = v[1];
+        const float act[4] = {gate.x / (1.0f + expf(-gate.x)) * up.x, gate.y / (1.0f + expf(-gate.y)) * up.y,
+                              gate.z / (1.0f + expf(-gate.z)) * up.z, gate.w / (1.0f + expf(-gate.w)) * up.w};
+        float left[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float o = __bfloat162float(__float2bfloat16_rn(act[e]));
+          left[e] = isfinite(o) ? act[e] - o : 0.0f;
+        }
+        const int64_t at = line * a.f + block * (kCols / 2) + c * 4;
+        *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack2(act[0], act[1]), pack2(act[2], act[3]));
+        *reinterpret_cast<uint2*>(a.out_lo + at) = make_uint2(pack2(left[0], left[1]), pack2(left[2], left[3]));
+      } else {
+        const int col = block * kCols + c * 4;
+        if (col >= a.n) return;
+        const float4 o = v[0];
+        const int64_t at = line * a.n + col;
+        if constexpr (kMode == kModePart)
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = o;
+        else
+          *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+      }
+    };
+    auto add4 = [](float4& o, const float4& p) { o.x += p.x, o.y += p.y, o.z += p.z, o.w += p.w; };
+
+    float acc[2][NT][4];
+    auto clear = [&] {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
+    };
+    // Stores the sums to the warp's own rows.
+    auto leave = [&](int rows) {
       auto put = [&](int i, float v0, float v1, float v2, float v3) {
         if (i >= rows) return;
-        int at = i;
-        float f = 1.0f;
-        if constexpr (kMode == kModeY) {
-          const int pr = kRouted ? s_order[first + i] : first + i;
-          at = kRouted ? pr / a.k : pr;
-          if (kRouted) f = a.weights[pr];
-        }
-        float* y = mine + at * kYStride + g;
-        const float v[4] = {v0, v1, v2, v3};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j * 8] = kMode == kModeY ? fmaf(f, v[j], y[j * 8]) : v[j];
+        float* const y = mine + i * kYStride + sigma;
+        y[0] = v0, y[8] = v1, y[16] = v2, y[24] = v3;
       };
-      auto put_all = [&] {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (kParts == 2) {
-            put(nt * 4 + t, acc[0][nt][0] + acc[0][nt][1], acc[0][nt][2] + acc[0][nt][3],
-                acc[1][nt][0] + acc[1][nt][1], acc[1][nt][2] + acc[1][nt][3]);
-          } else {
-            put(nt * 8 + 2 * t, acc[0][nt][0], acc[0][nt][2], acc[1][nt][0], acc[1][nt][2]);
-            put(nt * 8 + 2 * t + 1, acc[0][nt][1], acc[0][nt][3], acc[1][nt][1], acc[1][nt][3]);
-          }
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (kParts == 2) {
+          put(nt * 4 + t, acc[0][nt][0] + acc[0][nt][1], acc[0][nt][2] + acc[0][nt][3],
+              acc[1][nt][0] + acc[1][nt][1], acc[1][nt][2] + acc[1][nt][3]);
+        } else {
+          put(nt * 8 + 2 * t, acc[0][nt][0], acc[0][nt][2], acc[1][nt][0], acc[1][nt][2]);
+          put(nt * 8 + 2 * t + 1, acc[0][nt][1], acc[0][nt][3], acc[1][nt][1], acc[1][nt][3]);
         }
-      };
-      if (kMode == kModeY && kRouted && s_twice) {  // two pairs of a chunk may be one token's
-        for (int o = 0; o < 4; ++o) {
-          if (t == o) put_all();
-          __syncwarp();
-        }
-      } else {
-        put_all();
-        __syncwarp();
       }
+      clear();
     };
-    if (lo < hi) enter_chunk();
-    for (int v = lo; v < hi; ++v) {
-      copy_wait<kStages - 2>();
+
+    // A block's part of a job that another one began goes to that one, as its (rank - owner - 1)-th part.
+    const int rest = lo < hi ? hi % per : 0;  // steps of the last job, if it goes on
+    float4* const recv = reinterpret_cast<float4*>(smem + lay.recv);
+    constexpr int kPart = kCap * kItems * kQuads;  // of one block, in quads
+    auto send_part = [&](int rows) {
+      int owner = rank - 1;
+      while (begin_of(owner) > lo - at0.u) --owner;
+      cluster_wait_acquire();  // the owner's barrier exists
+      const uint32_t to = map_peer(smem_u32(recv + (rank - owner - 1) * kPart), owner);
+      const uint32_t bar = map_peer(smem_u32(&s_recv), owner);
+#pragma unroll 1
+      for (int i = tid; i < rows * kItems; i += kMulThreads)
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+          const float4 o = sum_of(i, q);
+          st_async_peer_v4(to + (i * kQuads + q) * 16, o.x, o.y, o.z, o.w, bar);
+        }
+    };
+    // What peers store into this block lands before it leaves, whether it gave up or not.
+    auto wait_parts = [&] {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&s_recv, 0)) {
+        if (global_timer_ns() - t0 > 2000000000ull) {
+          atomicCAS(&g_a16_status, 0, kSiteSums);
+          break;
+        }
+      }
       __syncwarp();
-      request(stage == 0 ? kStages - 1 : stage - 1);
-      const uint32_t src = ring + stage * kStageBytes;
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      uint4 w[4];
+    };
+
+    Turn s;
+    Walk k = at0;
+    bool ok = true;
+    int from = at0.u;  // of the job's steps, the first of this block's
+    clear();
+    for (int v = lo; v < hi; ++v) {
+      const int chunk = k.chunk, block = k.block, u = k.u;
+      const int tiles = (chunk_rows(chunk) * kParts + 7) >> 3;  // tiles of rows in use
+      const bool codes = u < code_steps;
+      // columns that are not there: nothing to do
+      const int units = kMode != kModeAct && block * kCols + warp * 32 >= a.n
+                            ? 0
+                            : min(2, codes ? groups - 2 * u : (a.r - (u - code_steps) * 64 + 31) >> 5);
+      // A block that gives up walks on, so that all its warps meet at the barriers below.
+      ok = ok && wait(&s_wfull[s.slot], s.phase, &s_wait, kSiteWFull) &&
+           wait(&s_xfull[s.slot], s.phase, &s_wait, kSiteXFull);
+      const uint32_t at = s.slot * kSlot;
+#pragma unroll 1
+      for (int wk = 0; ok && wk < units; ++wk) {
+        uint4 w[4];
+        const uint8_t* const wp = (wk ? w_at[1] : w_at[0]) + at;
+        const uint8_t* const xp = x_at + at + wk * (codes ? NT * 2048 : NT * 512);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = lds16(src + i * 512 + lane * 16);
-      if (u < groups) {
-        float s[4], d[2][NT][4];
+        for (int i = 0; i < 4; ++i) w[i] = lds16(wp + line_of(i) * 128);
+        if (codes) {
+          float sc[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = lds_f(src + kRows * 64 + (i * 8 + g) * 4);
+          for (int i = 0; i < 4; ++i)
+            sc[i] = *reinterpret_cast<const float*>(
+                s_at + at + wk * s_next + (kMode == kModeAct ? (i & 1) * 32 + (i >> 1) * kBoxCols * 8 : i * 32));
+          float d[2][NT][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[i][nt][j] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 x[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            x[nt] = row[nt] ? ld16(row[nt] + u * 128 + t * 32 + j * 8) : make_uint4(0, 0, 0, 0);
-          uint32_t c[2][2][4];  // tile, code i & 3, {rows g: i, i + 4 ...}
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 w0 = w[2 * i], w1 = w[2 * i + 1];
-            const uint32_t a0 = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
-            const uint32_t a1 = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              c[i][k][0] = codes2(a0 >> (8 * k)), c[i][k][1] = codes2(a1 >> (8 * k));
-              c[i][k][2] = codes2(a0 >> (8 * k + 4)), c[i][k][3] = codes2(a1 >> (8 * k + 4));
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t b0 = __byte_perm(x[nt].x, x[nt].z, 0x5410), b1 = __byte_perm(x[nt].x, x[nt].z, 0x7632);
-            const uint32_t b2 = __byte_perm(x[nt].y, x[nt].w, 0x5410), b3 = __byte_perm(x[nt].y, x[nt].w, 0x7632);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t c[2][2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              mma16816(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], b0, b1);
-              mma16816(d[i][nt], c[i][1][0], c[i][1][1], c[i][1][2], c[i][1][3], b2, b3);
+              const uint4 w0 = w[2 * i], w1 = w[2 * i + 1];
+              const uint32_t a0 = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
+              const uint32_t a1 = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                c[i][h][0] = codes2(a0 >> (8 * h)), c[i][h][1] = codes2(a1 >> (8 * h));
+                c[i][h][2] = codes2(a0 >> (8 * h + 4)), c[i][h][3] = codes2(a1 >> (8 * h + 4));
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (nt > 0 && nt >= tiles) break;
+              const uint4 x = lds16(xp + nt * 2048 + j * 512);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (j == 0)
+                  mma16816_first(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], x.x, x.y);
+                else
+                  mma16816(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], x.x, x.y);
+                mma16816(d[i][nt], c[i][1][0], c[i][1][1], c[i][1][2], c[i][1][3], x.z, x.w);
+              }
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (nt > 0 && nt >= tiles) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              acc[i][nt][0] = fmaf(sc[2 * i], d[i][nt][0], acc[i][nt][0]);
+              acc[i][nt][1] = fmaf(sc[2 * i], d[i][nt][1], acc[i][nt][1]);
+              acc[i][nt][2] = fmaf(sc[2 * i + 1], d[i][nt][2], acc[i][nt][2]);
+              acc[i][nt][3] = fmaf(sc[2 * i + 1], d[i][nt][3], acc[i][nt][3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint4 x = lds16(xp + nt * 512);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              mma16816(acc[i][nt], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, x.x, x.y);
+              mma16816(acc[i][nt], w[2 * i].z, w[2 * i + 1].z, w[2 * i].w, w[2 * i + 1].w, x.z, x.w);
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            acc[i][nt][0] = fmaf(s[2 * i], d[i][nt][0], acc[i][nt][0]);
-            acc[i][nt][1] = fmaf(s[2 * i], d[i][nt][1], acc[i][nt][1]);
-            acc[i][nt][2] = fmaf(s[2 * i + 1], d[i][nt][2], acc[i][nt][2]);
-            acc[i][nt][3] = fmaf(s[2 * i + 1], d[i][nt][3], acc[i][nt][3]);
-          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[s.slot]);
+      next_slot(s);
+      const bool over = advance(k);
+      if (!over && v + 1 < hi) continue;
+      const int first = chunk_first(chunk), rows = chunk_rows(chunk);
+      leave(rows);
+      barrier();
+      if (from > 0) {
+        send_part(rows);
       } else {
-        wait_all();
-        const int at = (u - groups) * 32 + t * 8, first = chunk_first(chunk), rows = chunk_rows(chunk);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int col = nt * 8 + g, i = kParts == 2 ? col >> 1 : col;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (i < rows && !(kParts == 2 && (col & 1)) && at < a.r) {
-            const int64_t pr = kRouted ? s_order[first + i] : first + i;
-            x = ld16(a.h + pr * a.r + at);
+        pdl_wait();
+        int parts = 0;  // of other blocks
+        if (!over) {    // this block began the job, others end it
+          uint32_t bytes = 0;
+          for (int r = rank + 1; r < split && begin_of(r) < hi - rest + per; ++r) {
+            ++parts;
+            if (begin_of(r) < begin_of(r + 1)) bytes += rows * kItems * kQuads * 16;
           }
+          if (tid == 0) mbar_arrive_expect_tx(&s_recv, bytes);
+          __syncwarp();
+          wait_parts();
+        }
+#pragma unroll 1
+        for (int i = tid; i < rows * kItems; i += kMulThreads) {
+          float4 o[kQuads];
 #pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            mma16816(acc[i2][nt], w[2 * i2].x, w[2 * i2 + 1].x, w[2 * i2].y, w[2 * i2 + 1].y, x.x, x.y);
-            mma16816(acc[i2][nt], w[2 * i2].z, w[2 * i2 + 1].z, w[2 * i2].w, w[2 * i2 + 1].w, x.z, x.w);
-          }
+          for (int q = 0; q < kQuads; ++q) o[q] = sum_of(i, q);
+#pragma unroll 1
+          for (int r = 0; r < parts; ++r)
+            if (begin_of(rank + 1 + r) < begin_of(rank + 2 + r)) {
+#pragma unroll
+              for (int q = 0; q < kQuads; ++q) add4(o[q], recv[r * kPart + i * kQuads + q]);
+            }
+          put_item(block, first, i, o);
         }
       }
-      if (++u == per || v + 1 == hi) {
-        leave_chunk();
-        u = 0, ++chunk;
-        if (v + 1 < hi) enter_chunk();
-      }
+      from = 0;
+      if (v + 1 < hi) barrier();  // the sums are read
     }
-    if constexpr (kMode != kModeY) {
-      if (lo >= hi)
-        for (int i = lane; i < srows * kYStride; i += 32) mine[i] = 0.0f;
-    }
-    __syncthreads();
-
-    // The block's sum of its warps, then the cluster's of its blocks, each in order.
-    const int job_chunk = kMode == kModeY ? 0 : job / a.tiles;
-    const int first = kMode == kModeY ? 0 : chunk_first(job_chunk);
-    const int rows = kMode == kModeY ? a.b : chunk_rows(job_chunk);
-    const float* all = sums + buffer * kWarps * srows * kYStride;
-    float* const own = part + buffer * srows * kRows;
-    auto block_sum = [&](int r2, int c) {
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += all[(w * srows + r2) * kYStride + c];
-      return v;
-    };
-    if (a.split > 1) {
-      for (int i = tid; i < rows * kRows; i += kThreads) own[i] = block_sum(i >> 5, i & 31);
-      cluster_sync_startup();
-    }
-    auto sum = [&](int r2, int c) {
-      if (a.split == 1) return block_sum(r2, c);
-      const uint32_t at = smem_u32(own + r2 * kRows + c);
-      float v = 0.0f;
-      for (int s = 0; s < a.split; ++s) v += ld_peer(map_peer(at, s));
-      return v;
-    };
-    // Two neighbouring values per thread; the blocks of a cluster share the pairs out.
-    constexpr int kWide = kMode == kModeAct ? 8 : 16;
-    for (int i = rank * kThreads + tid; i < rows * kWide; i += a.split * kThreads) {
-      const int r2 = i / kWide, c = 2 * (i % kWide);
-      if constexpr (kMode == kModeAct) {
-        const int64_t at = static_cast<int64_t>(kRouted ? s_order[first + r2] : first + r2) * a.f + tile * 16 + c;
-        float v[2], hi2[2], lo2[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float gate = sum(r2, c + e), up = sum(r2, 16 + c + e);
-          v[e] = gate / (1.0f + expf(-gate)) * up;
-          hi2[e] = __bfloat162float(__float2bfloat16_rn(v[e]));
-          lo2[e] = isfinite(hi2[e]) ? v[e] - hi2[e] : 0.0f;
-        }
-        *reinterpret_cast<uint32_t*>(a.out + at) = pack2(hi2[0], hi2[1]);
-        *reinterpret_cast<uint32_t*>(a.out_lo + at) = pack2(lo2[0], lo2[1]);
-      } else {
-        const int col = tile * kRows + c;
-        if (col >= a.n) continue;
-        float v0 = sum(r2, c), v1 = sum(r2, c + 1);
-        const int64_t pr = kMode == kModeY ? r2 : kRouted ? s_order[first + r2] : first + r2;
-        const int64_t at = pr * a.n + col;
-        if (kMode == kModeY && a.base) {
-          const uint32_t bv = ld4(a.base + at);
-          v0 += lo_f(bv), v1 += hi_f(bv);
-        }
-        *reinterpret_cast<uint32_t*>(a.out + at) = pack2(v0, v1);
-      }
-    }
-    if (kBuffers == 2) buffer ^= 1;
   }
-  wait_all();  // this grid completes only after the one in front
-  if (a.split > 1) cluster_sync_startup();  // peers may still be reading this block's sums
+  pdl_wait();  // this grid completes only after the one in front
 }
 
-template <int NT, int kMode, int kParts, bool kRouted>
-cudaError_t launch(A16Args a, int64_t jobs, cudaStream_t st) {
-  auto kernel = a16_kernel<NT, kMode, kParts, kRouted>;
-  // Blocks of a cluster: as many as it takes for two blocks on every SM, while each of their warps
-  // has a unit still.
-  const int64_t units = a.K / 128 + (a.r + 31) / 32;
-  a.split = 1;
-  while (a.split < 8 && jobs * a.split * 2 <= 2 * kSms && units >= 2 * a.split * kWarps) a.split *= 2;
-  const Layout l = layout<NT, kMode, kParts, kRouted>(a.b, a.k, a.count, a.split);
-  const cudaError_t e = allow_smem(kernel, 227 * 1024 - 1024);
+// y = base + the sum of weight * part over a token's slots, in their order; four columns per thread.
+constexpr int kCombineThreads = 128;
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_kernel(const float* parts, const int32_t* ids, const float* weights, int k, int count, int n,
+                   const uint16_t* base, uint16_t* y) {
+  const int col = (blockIdx.x * kCombineThreads + threadIdx.x) * 4;
+  const int64_t token = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (col >= n) return;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (base) {
+    const uint2 b = ld8(base + token * n + col);
+    o = make_float4(lo_f(b.x), hi_f(b.x), lo_f(b.y), hi_f(b.y));
+  }
+  constexpr int kAhead = 4;  // slots whose loads are in flight together
+  for (int s0 = 0; s0 < k; s0 += kAhead) {
+    float4 p[kAhead];
+    float f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t pair = token * k + s0 + i;
+      const int id = s0 + i < k ? static_cast<int>(ld4(ids + pair)) : -1;
+      f[i] = 0.0f;
+      p[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (id >= 0 && id < count) {
+        f[i] = __uint_as_float(ld4(weights + pair));
+        const uint4 v = ld16(reinterpret_cast<const uint16_t*>(parts + pair * n + col));
+        p[i] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      o.x = fmaf(f[i], p[i].x, o.x), o.y = fmaf(f[i], p[i].y, o.y), o.z = fmaf(f[i], p[i].z, o.z),
+      o.w = fmaf(f[i], p[i].w, o.w);
+  }
+  *reinterpret_cast<uint2*>(y + token * n + col) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+}
+
+// How a launch divides its jobs (at most `jobs`, of `steps` each): clusters, log2 of their blocks, and
+// how many blocks' parts of a job a block may get.
+struct Plan {
+  int64_t clusters, cost;
+  int split_log, parts;
+};
+// The split that the busiest SM is done with first, of at most 2^most blocks; room: clusters of 1, 2, 4 and
+// 8 blocks that run at once. An SM's time for a group of 32 columns goes with
+// the warps that multiply there: 410 cycles with 16 of them, 555 with 8 (8 rows, 37888 columns of 4096).
+Plan plan(int64_t jobs, int64_t steps, const int* room, int per_sm, int warps, bool all_there, int most) {
+  Plan best = {0, 0, 0, 0};
+  for (int s = 0; s <= most; ++s) {
+    if (s > 0 && steps * jobs < 2 << s) break;
+    const int64_t clusters = std::min<int64_t>(jobs, room[s]);
+    const int64_t mine = ((jobs + clusters - 1) / clusters * steps + (1 << s) - 1) >> s;
+    const int64_t at_once = std::min<int64_t>(((clusters << s) + kSms - 1) / kSms, per_sm) * warps;
+    const int64_t cost = mine * at_once * (265 + 2320 / at_once);
+    if (best.clusters && cost >= best.cost) continue;
+    // Blocks that a job may reach over: all where they may have no step each (which jobs there are may be
+    // known on the GPU alone).
+    const int64_t least = all_there ? (jobs / clusters * steps) >> s : 0;
+    const int64_t others = least ? std::min<int64_t>((1 << s) - 1, (steps + least - 2) / least) : (1 << s) - 1;
+    best = {clusters, cost, s, static_cast<int>(others)};
+  }
+  return best;
+}
+
+// How many clusters of 1, 2, 4 and 8 blocks run at once, with per_sm blocks' shared memory on an SM. Asked
+// once for each kernel and device (a cluster keeps within a GPC, and GPCs differ); only answers are kept.
+cudaError_t clusters_at_once(const void* kernel, int threads, int per_sm, const int** room) {
+  struct Known {
+    const void* kernel;
+    int dev, per_sm, room[4];
+  };
+  constexpr int kKnown = 256;
+  static Known known[kKnown];
+  static std::atomic<int> count{0};
+  static std::mutex mutex;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  auto find = [&](int n) {
+    for (int i = 0; i < n; ++i)
+      if (known[i].kernel == kernel && known[i].dev == dev && known[i].per_sm == per_sm) return known[i].room;
+    return static_cast<int*>(nullptr);
+  };
+  if ((*room = find(count.load(std::memory_order_acquire)))) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(mutex);
+  const int n = count.load(std::memory_order_relaxed);
+  if ((*room = find(n))) return cudaSuccess;
+  e = allow_smem(kernel, kMaxSmem);
+  if (e != cudaSuccess) return e;
+  Known k = {kernel, dev, per_sm, {}};
+  for (int s = 0; s < 4; ++s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((8 * kSms) << s);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = std::min(kMaxSmem, 227 * 1024 / per_sm - 1536);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1 << s;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&k.room[s], kernel, &cfg);
+    if (e != cudaSuccess) {
+      cudaGetLastError();  // returned here; not a later launch's error
+      return e;
+    }
+    k.room[s] = std::max(k.room[s], 1);
+  }
+  if (n < kKnown) {
+    known[n] = k;
+    count.store(n + 1, std::memory_order_release);
+    *room = known[n].room;
+  } else {  // more devices than there is room for: as if every SM took its blocks
+    static const int plain[4] = {kSms, kSms / 2, kSms / 4, kSms / 8};
+    *room = plain;
+  }
+  return cudaSuccess;
+}
+
+template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
+cudaError_t plan_of(const A16Args& a, int* blocks, Plan* out, int most = 3, int per_sm = 0) {
+  using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
+  if (per_sm == 0) per_sm = K::kBlocksPerSm;
+  const int* room;
+  const cudaError_t e = clusters_at_once(reinterpret_cast<const void*>(a16_kernel<kWarps, NT, kMode, kParts, kRouted>),
+                                         K::kThreads, per_sm, &room);
+  if (e != cudaSuccess) return e;
+  const int64_t chunks = kRouted ? K::max_chunks(a.b * a.k, a.count) : (a.b + K::kCap - 1) / K::kCap;
+  const int width = kMode == kModeAct ? K::kCols / 2 : K::kCols;
+  *blocks = ((kMode == kModeAct ? a.f : a.n) + width - 1) / width;
+  const int64_t steps = (a.K / 128 + 1) / 2 + (a.r + 63) / 64;
+  *out = plan(chunks * *blocks, steps, room, per_sm, kWarps, !kRouted, most);
+  return cudaSuccess;
+}
+
+template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
+cudaError_t launch_warps(A16Args a, cudaStream_t st) {
+  using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
+  auto kernel = a16_kernel<kWarps, NT, kMode, kParts, kRouted>;
+  // Slots of the ring: what is left beside the sums and parts; a block less on an SM, or a smaller
+  // cluster, rather than one slot.
+  Plan p;
+  Layout l;
+  int per_sm = K::kBlocksPerSm;
+  for (int most = 3;;) {
+    cudaError_t e = plan_of<kWarps, NT, kMode, kParts, kRouted>(a, &a.blocks, &p, most, per_sm);
+    if (e != cudaSuccess) return e;
+    l = K::layout(a.b, a.k, a.count, 0, p.parts);
+    a.slots = std::min(kMaxSlots, (227 * 1024 / per_sm - 1024 - 1536 - l.total) / K::kSlot);
+    if (a.slots >= 2) break;
+    if (per_sm > 1)
+      --per_sm;
+    else if (most-- == 0)
+      return cudaErrorInvalidValue;
+  }
+  a.split_log = p.split_log, a.parts = p.parts;
+  const int split = 1 << p.split_log;
+  l = K::layout(a.b, a.k, a.count, a.slots, a.parts);
+  a.width = std::min(K::kBoxCols, a.n);
+  bool ok = encode_map_2d(&a.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, int64_t(a.count) * a.n, a.K / 2, 128,
+                          a.width, CU_TENSOR_MAP_SWIZZLE_128B) &&
+            encode_map_2d(&a.ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.s, a.n, int64_t(a.count) * (a.K / 128),
+                          int64_t(a.n) * 4, a.width, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (ok && a.r > 0)
+    ok = encode_map_2d(&a.wl, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.l2t, a.r, int64_t(a.count) * a.n, a.r * 2, 64,
+                       a.width, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem(kernel, kMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int64_t most = kMode == kModeY ? jobs : std::min<int64_t>(jobs, 4 * kSms / a.split);
-  cfg.gridDim = dim3(static_cast<unsigned>(most * a.split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = l.total;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.clusters * split));
+  cfg.blockDim = dim3(K::kThreads);
+  cfg.dynamicSmemBytes = l.total + 1024;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = a.split;
+  at[1].val.clusterDim.x = split;
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Rows of activations that a chunk has to hold: 8, 16 or 32.
-template <int kMode, int kParts, bool kRouted>
-cudaError_t launch_rows(const A16Args& a, int rows, int64_t jobs_of_pairs, cudaStream_t st) {
-  const int64_t tiles = a.tiles;
-  auto jobs = [&](int cap) {
-    if (kMode == kModeY) return tiles;
-    const int64_t pairs = jobs_of_pairs;
-    const int64_t groups = kRouted ? std::min<int64_t>(pairs, a.count) : 1;
-    return tiles * (kRouted ? std::min(pairs, groups + pairs / cap) : (pairs + cap - 1) / cap);
-  };
-  if (rows * kParts <= 8) return launch<1, kMode, kParts, kRouted>(a, jobs(8 / kParts), st);
-  if (rows * kParts <= 16) return launch<2, kMode, kParts, kRouted>(a, jobs(16 / kParts), st);
-  return launch<4, kMode, kParts, kRouted>(a, jobs(32 / kParts), st);
+// Blocks of 256 columns, or of 128 where that leaves the busiest SM less.
+template <int NT, int kMode, int kParts, bool kRouted>
+cudaError_t launch(const A16Args& a, cudaStream_t st) {
+  if constexpr (kMode == kModeH) {
+    return launch_warps<2, NT, kMode, kParts, kRouted>(a, st);
+  } else {
+    int blocks;
+    Plan wide, narrow;
+    cudaError_t e = plan_of<8, NT, kMode, kParts, kRouted>(a, &blocks, &wide);
+    if (e == cudaSuccess) e = plan_of<4, NT, kMode, kParts, kRouted>(a, &blocks, &narrow);
+    if (e != cudaSuccess) return e;
+    return wide.cost <= narrow.cost ? launch_warps<8, NT, kMode, kParts, kRouted>(a, st)
+                                        : launch_warps<4, NT, kMode, kParts, kRouted>(a, st);
+  }
 }
 
-A16Args product(const uint8_t* q, const float* s, const uint16_t* l2t, int64_t K, int64_t n, int64_t r) {
+// Tiles of a chunk: for as many rows as there are, or as an expert has on average twice over (then
+// most experts' weights are read once).
+template <int kMode, int kParts, bool kRouted>
+cudaError_t launch_rows(const A16Args& a, cudaStream_t st) {
+  const int rows = kRouted ? std::min(a.b, std::max(1, 2 * a.b * a.k / a.count)) : a.b;
+  if (rows * kParts <= 8) return launch<1, kMode, kParts, kRouted>(a, st);
+  if (rows * kParts <= 16) return launch<2, kMode, kParts, kRouted>(a, st);
+  return launch<4, kMode, kParts, kRouted>(a, st);
+}
+
+thread_local uint64_t t_stall_ns = 0;  // self-test: the calling thread's limit of the waits, or 0
+
+// One product of `count` experts' weights.
+A16Args product(const uint8_t* q, const float* s, const uint16_t* l2t, int64_t K, int64_t n, int64_t r,
+                int64_t count) {
   A16Args a = {};
   a.q = q, a.s = s, a.l2t = l2t;
   a.K = static_cast<int>(K), a.n = static_cast<int>(n), a.r = static_cast<int>(r);
-  a.q_expert = n * (K / 2), a.s_expert = n * (K / 128), a.l2_expert = n * r;
-  a.tiles = static_cast<int>((n + kRows - 1) / kRows);
-  a.k = 1, a.count = 1;
+  a.k = 1, a.count = static_cast<int>(count);
+  a.wait_ns = t_stall_ns ? t_stall_ns : 2000000000ull;
+  a.stall = t_stall_ns != 0;
   return a;
 }
 
@@ -597,20 +988,21 @@ size_t up16(size_t v) { return (v + 15) & ~size_t(15); }
 cudaError_t launch_a16_linear(const A16LinearCall& c, cudaStream_t st) {
   const twq_weights& w = *c.w;
   if (w.r > 0) {
-    A16Args a = product(w.l1q, w.sl1, nullptr, w.m, w.r, 0);
+    A16Args a = product(w.l1q, w.sl1, nullptr, w.m, w.r, 0, 1);
     a.x = c.x, a.ldx = c.ldx, a.b = c.b, a.out = c.h;
     a.ids_ready = true;
-    const cudaError_t e = launch_rows<kModeH, 1, false>(a, c.b, c.b, st);
+    const cudaError_t e = launch_rows<kModeH, 1, false>(a, st);
     if (e != cudaSuccess) return e;
   }
-  A16Args a = product(w.rq, w.sr, w.l2t, w.m, w.n, w.r);
+  A16Args a = product(w.rq, w.sr, w.l2t, w.m, w.n, w.r, 1);
   a.x = c.x, a.ldx = c.ldx, a.b = c.b, a.h = c.h, a.out = c.y;
   a.ids_ready = true, a.x_ready = w.r > 0;
-  return launch_rows<kModeY, 1, false>(a, c.b, c.b, st);
+  return launch_rows<kModeY, 1, false>(a, st);
 }
 
 size_t moe_workspace(int64_t pairs, const twq_experts* e) {
-  return 2 * up16(2 * pairs * e->down.m) + up16(2 * pairs * e->up.r) + up16(2 * pairs * e->down.r);
+  return 2 * up16(2 * pairs * e->down.m) + up16(2 * pairs * e->up.r) + up16(2 * pairs * e->down.r) +
+         4 * pairs * e->down.n;
 }
 
 cudaError_t launch_moe_experts(const MoeCall& c, cudaStream_t st) {
@@ -621,36 +1013,58 @@ cudaError_t launch_moe_experts(const MoeCall& c, cudaStream_t st) {
   uint16_t* act_lo = reinterpret_cast<uint16_t*>(ws + up16(2 * pairs * f));
   uint16_t* h1 = reinterpret_cast<uint16_t*>(ws + 2 * up16(2 * pairs * f));
   uint16_t* h2 = reinterpret_cast<uint16_t*>(ws + 2 * up16(2 * pairs * f) + up16(2 * pairs * u.r));
-  auto routed = [&](A16Args a) {
-    a.ids = c.ids, a.weights = c.weights, a.b = c.b, a.k = c.k, a.count = static_cast<int>(c.e->count);
+  float* parts = reinterpret_cast<float*>(ws + 2 * up16(2 * pairs * f) + up16(2 * pairs * u.r) + up16(2 * pairs * d.r));
+  // The weights `w`'s product; l1: x D(L1).
+  auto routed = [&](const twq_weights& w, bool l1) {
+    A16Args a = l1 ? product(w.l1q, w.sl1, nullptr, w.m, w.r, 0, c.e->count)
+                   : product(w.rq, w.sr, w.l2t, w.m, w.n, w.r, c.e->count);
+    a.ids = c.ids, a.b = c.b, a.k = c.k;
     return a;
   };
   cudaError_t e = cudaSuccess;
   if (u.r > 0) {
-    A16Args a = routed(product(u.l1q, u.sl1, nullptr, u.m, u.r, 0));
+    A16Args a = routed(u, true);
     a.x = c.x, a.ldx = c.ldx, a.out = h1;
-    e = launch_rows<kModeH, 1, true>(a, c.b, pairs, st);
-    if (e != cudaSuccess) return e;
+    if ((e = launch_rows<kModeH, 1, true>(a, st)) != cudaSuccess) return e;
   }
   {
-    A16Args a = routed(product(u.rq, u.sr, u.l2t, u.m, u.n, u.r));
+    A16Args a = routed(u, false);
     a.x = c.x, a.ldx = c.ldx, a.h = h1, a.f = static_cast<int>(f), a.out = act, a.out_lo = act_lo;
-    a.tiles = static_cast<int>(f / 16);
     a.ids_ready = a.x_ready = u.r > 0;
-    e = launch_rows<kModeAct, 1, true>(a, c.b, pairs, st);
-    if (e != cudaSuccess) return e;
+    if ((e = launch_rows<kModeAct, 1, true>(a, st)) != cudaSuccess) return e;
   }
   if (d.r > 0) {
-    A16Args a = routed(product(d.l1q, d.sl1, nullptr, d.m, d.r, 0));
+    A16Args a = routed(d, true);
     a.x = act, a.x_lo = act_lo, a.ldx = f, a.out = h2;
     a.ids_ready = true;
-    e = launch_rows<kModeH, 2, true>(a, c.b, pairs, st);
-    if (e != cudaSuccess) return e;
+    if ((e = launch_rows<kModeH, 2, true>(a, st)) != cudaSuccess) return e;
   }
-  A16Args a = routed(product(d.rq, d.sr, d.l2t, d.m, d.n, d.r));
-  a.x = act, a.x_lo = act_lo, a.ldx = f, a.h = h2, a.base = c.base, a.out = c.y;
-  a.ids_ready = true, a.x_ready = d.r > 0;
-  return launch_rows<kModeY, 2, true>(a, c.b, pairs, st);
+  {
+    A16Args a = routed(d, false);
+    a.x = act, a.x_lo = act_lo, a.ldx = f, a.h = h2, a.out = reinterpret_cast<uint16_t*>(parts);
+    a.ids_ready = true, a.x_ready = d.r > 0;
+    if ((e = launch_rows<kModePart, 2, true>(a, st)) != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((d.n / 4 + kCombineThreads - 1) / kCombineThreads), c.b);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel, parts, c.ids, c.weights, c.k, static_cast<int>(c.e->count),
+                            static_cast<int>(d.n), c.base, c.y);
+}
+
+void set_a16_stall(int64_t wait_limit_ns) { t_stall_ns = static_cast<uint64_t>(wait_limit_ns); }
+
+cudaError_t read_and_clear_a16_status(int* code) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_a16_status, sizeof(int));
+  if (e != cudaSuccess || *code == 0) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_a16_status, &zero, sizeof(int));
 }
 
 }  // namespace twq

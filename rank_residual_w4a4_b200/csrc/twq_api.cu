@@ -678,13 +678,14 @@ twq_status twq_device_status(int* code) {
   if (!code) return TWQ_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return TWQ_ERR_CUDA;
-  int c1 = 0, c2 = 0, c3 = 0, c4 = 0;
+  int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0;
   e = twq::read_and_clear_device_status(&c1);
   if (e == cudaSuccess) e = twq::read_and_clear_decode_status(&c2);
   if (e == cudaSuccess) e = twq::read_and_clear_pair_status(&c3);
   if (e == cudaSuccess) e = twq::read_and_clear_adapter_status(&c4);
+  if (e == cudaSuccess) e = twq::read_and_clear_a16_status(&c5);
   if (e != cudaSuccess) return TWQ_ERR_CUDA;
-  *code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : c4));
+  *code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : (c4 ? c4 : c5)));
   return *code ? TWQ_ERR_DEVICE : TWQ_OK;
 }
 
@@ -703,6 +704,12 @@ twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx, int64_t
 twq_status twq_selftest_adapter_stall(int64_t wait_limit_ns) {
   if (wait_limit_ns != 0 && (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)) return TWQ_ERR_INVALID_ARG;
   t_stall_ns = wait_limit_ns;
+  return TWQ_OK;
+}
+
+twq_status twq_selftest_a16_stall(int64_t wait_limit_ns) {
+  if (wait_limit_ns != 0 && (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)) return TWQ_ERR_INVALID_ARG;
+  twq::set_a16_stall(wait_limit_ns);
   return TWQ_OK;
 }
 
@@ -732,8 +739,8 @@ int twq_launches_per_call(const char* ep) {
   if (!strcmp(ep, "twq_adapter_backward") || !strcmp(ep, "twq_adapter_backward_i8")) return 5;
   if (!strcmp(ep, "twq_fused_linear_a16")) return 2;
   if (!strcmp(ep, "twq_moe_route") || !strcmp(ep, "twq_moe_route_bf16")) return 1;
-  if (!strcmp(ep, "twq_moe_experts")) return 4;
-  if (!strcmp(ep, "twq_moe_layer") || !strcmp(ep, "twq_moe_layer_bf16")) return 5;
+  if (!strcmp(ep, "twq_moe_experts")) return 5;
+  if (!strcmp(ep, "twq_moe_layer") || !strcmp(ep, "twq_moe_layer_bf16")) return 6;
   return -1;
 }
 

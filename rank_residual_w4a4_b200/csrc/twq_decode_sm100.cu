@@ -1017,6 +1017,12 @@ cudaError_t launch_decode_mode(const GemmCall& c, cudaStream_t st) {
 
 }  // namespace
 
+bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
+                   uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapSwizzle sw) {
+  return d_encode(map, dt, base, inner, outer, row_bytes, box_inner, box_outer, sw);
+}
+
 bool decode_eligible(const GemmCall& c) {
   const twq_weights* w = c.w;
   if (c.mode == kModeFusedS2Q) return !c.x && !c.a8 && c.b >= 1 && c.b <= kNT && w->r == 128 &&

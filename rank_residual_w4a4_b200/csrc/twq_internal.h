@@ -1,6 +1,7 @@
 // Internal interface between the C-ABI layer (twq_api.cu) and the kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -64,6 +65,11 @@ cudaError_t read_and_clear_pair_status(int* code);
 // Decode-shape kernel (b <= 16, split K over a 4- or 8-CTA cluster).
 bool decode_eligible(const GemmCall& call);
 cudaError_t launch_decode(const GemmCall& call, cudaStream_t stream);
+
+// A 2D tensor map (row pitch and sizes in elements of `dt` but the pitch, in bytes), from a cache.
+bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
+                   uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapSwizzle sw);
 
 // twq_release_cache: drop the decode path's cached tensor maps, and the
 // allocation-free entry point's resolved scratch addresses.

@@ -37,7 +37,7 @@ EXPORTS = ("twq_version", "twq_status_string", "twq_weights_sizes", "twq_act_siz
            "twq_adapter_backward_workspace_bytes", "twq_adapter_backward",
            "twq_adapter_backward_i8", "twq_selftest_adapter_stall", "twq_fused_linear_a16",
            "twq_moe_route", "twq_moe_route_bf16", "twq_moe_workspace_bytes", "twq_moe_experts",
-           "twq_moe_layer", "twq_moe_layer_bf16")
+           "twq_moe_layer", "twq_moe_layer_bf16", "twq_selftest_a16_stall")
 
 
 class TwqError(RuntimeError):
@@ -110,6 +110,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "twq_quantize_act_i8": ([P, I, I, I, P, P, P], ctypes.c_int),
         "twq_fused_linear_i8": ([P, P, I, P, P, P], ctypes.c_int),
         "twq_selftest_adapter_stall": ([I], ctypes.c_int),
+        "twq_selftest_a16_stall": ([I], ctypes.c_int),
         "twq_row_groups_sizes": ([I, I, P], ctypes.c_int),
         "twq_group_rows": ([P, P, P], ctypes.c_int),
         "twq_adapter_linear": ([P, I, I, P, P, P, P, P, P], ctypes.c_int),
@@ -948,6 +949,11 @@ def selftest_adapter_stall(wait_limit_ns: int) -> None:
     """Until called with 0: this thread's adapter calls of more than one launch run into their
     kernels' bounded waits (see twq_selftest_adapter_stall). Read device_status() after them."""
     _check(load().twq_selftest_adapter_stall(int(wait_limit_ns)), "twq_selftest_adapter_stall")
+
+
+def selftest_a16_stall(wait_limit_ns: int) -> None:
+    """The same for the calls on BF16 activations (see twq_selftest_a16_stall)."""
+    _check(load().twq_selftest_a16_stall(int(wait_limit_ns)), "twq_selftest_a16_stall")
 
 
 def device_status() -> int:

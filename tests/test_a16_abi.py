@@ -95,8 +95,8 @@ def test_workspace_of_a_refused_shape_is_zero(lib, args):
 
 def test_launch_accounting(lib):
     assert twq.launches_per_call("twq_fused_linear_a16") == 2
-    assert twq.launches_per_call("twq_moe_route") == 1 and twq.launches_per_call("twq_moe_experts") == 4
-    assert twq.launches_per_call("twq_moe_layer") == 5 and twq.launches_per_call("twq_moe_layer_bf16") == 5
+    assert twq.launches_per_call("twq_moe_route") == 1 and twq.launches_per_call("twq_moe_experts") == 5
+    assert twq.launches_per_call("twq_moe_layer") == 6 and twq.launches_per_call("twq_moe_layer_bf16") == 6
 
 
 def test_binding_refuses_the_host(lib):
