@@ -97,6 +97,21 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
     }
   }
 }
+// The same on an address.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // Bounded wait of a warp: one answer for all of its lanes; false once the block is giving up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
@@ -159,7 +174,7 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 
 // What of a block's shared memory is where, in bytes from a 1024-byte boundary.
 struct Layout {
-  int sums, recv, chunks, order, cnt, total;
+  int sums, recv, chunks, order, cnt, before, total;
 };
 
 // kWarps: that multiply, 32 weight columns each.
@@ -172,7 +187,7 @@ struct Kernel {
   static constexpr int kCap = 8 * NT / kParts;                 // rows of activations in a chunk
   static constexpr int kXWarps = NT == 1 ? 2 : 3;
   static constexpr int kThreads = kMulThreads + 32 + 32 * kXWarps;
-  static constexpr int kBlocksPerSm = kWarps == 8 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;
+  static constexpr int kBlocksPerSm = kWarps == 16 ? 1 : kWarps == 8 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;
   static constexpr int kSlot = kWBytes + kSBytes + 4096 * NT;
 
   static __host__ __device__ int max_chunks(int pairs, int count) {
@@ -187,8 +202,12 @@ struct Kernel {
     l.recv = l.sums + kWarps * kCap * kYStride * 4;
     l.chunks = l.recv + parts * kCap * kCols * 4;
     l.order = l.chunks + (kRouted ? max_chunks(pairs, count) * 8 : 0);
-    l.cnt = l.order + (kRouted ? 3 * ((pairs * 2 + 7) / 8 * 8) : 0);
+    l.cnt = l.order + (kRouted ? (pairs * 2 + 7) / 8 * 8 : 0);
     l.total = (l.cnt + (kRouted ? count * 4 : 0) + 15) / 16 * 16;
+    // Of many pairs: beside the rest where it does not fit into the ring, which is used after it.
+    const int ranks = kRouted && pairs > 32 ? (pairs + 31) / 32 * count * 2 : 0;
+    l.before = ranks <= slots * kSlot && slots > 0 ? 0 : l.total;
+    l.total += l.before ? (ranks + 15) / 16 * 16 : 0;
     return l;
   }
 };
@@ -196,15 +215,15 @@ struct Kernel {
 // Chunks of at most `cap` rows that share an expert, experts ascending, rows of an expert in the
 // order of their pairs: {expert, first place in `order` | rows << 16}. Returns their number.
 __device__ __noinline__ int make_chunks(const int32_t* ids, int pairs, int count, int cap, uint2* chunk,
-                                        uint16_t* order, int* cnt, int* number) {
+                                        uint16_t* order, int* cnt, uint16_t* before, int* number) {
   if (pairs <= 32) {  // in one warp's registers
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
-      const unsigned before = (1u << lane) - 1u, all = 0xFFFFFFFFu;
+      const unsigned lower = (1u << lane) - 1u, all = 0xFFFFFFFFu;
       int id = lane < pairs ? static_cast<int>(ld4(ids + lane)) : -1;
       if (id < 0 || id >= count) id = -1;
       const unsigned same = __match_any_sync(all, id);
-      const bool leads = id >= 0 && !(same & before);
+      const bool leads = id >= 0 && !(same & lower);
       int place = 0, at = 0;  // of the leader's expert: rows and chunks of the experts before it
       for (unsigned todo = __ballot_sync(all, leads); todo; todo &= todo - 1) {
         const int l = __ffs(todo) - 1;
@@ -214,36 +233,47 @@ __device__ __noinline__ int make_chunks(const int32_t* ids, int pairs, int count
       if (leads)
         for (int i = 0, n = __popc(same); i < n; i += cap)
           chunk[at + i / cap] = make_uint2(id, (place + i) | (min(cap, n - i) << 16));
-      if (id >= 0) order[place + __popc(same & before)] = static_cast<uint16_t>(lane);
+      if (id >= 0) order[place + __popc(same & lower)] = static_cast<uint16_t>(lane);
       const int chunks = __reduce_add_sync(all, leads ? (__popc(same) + cap - 1) / cap : 0);
       if (lane == 0) *number = chunks;
     }
     __syncthreads();
     return *number;
   }
-  const int pad = (pairs * 2 + 7) / 8 * 4;
-  uint16_t* const rank = order + pad;
-  uint16_t* const id_of = rank + pad;  // 0xFFFF: none
-  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
-  for (int p = tid; p < pairs; p += threads) {
-    const int id = static_cast<int>(ld4(ids + p));
-    id_of[p] = static_cast<uint16_t>(id < 0 || id >= count ? 0xFFFF : id);
+  // More: each warp ranks the pairs of some segments of 32 among themselves; `before`, segments x count,
+  // then has how many pairs of an expert the segments before one hold.
+  constexpr int kMine = (kA16MaxRows * kMoeMaxChoices / 32 + 4) / 5;  // segments of a warp, of 5 warps or more
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int segments = (pairs + 31) >> 5;
+  int id[kMine], rank[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int at = (warp + j * warps) * 32 + lane;
+    id[j] = at < pairs ? static_cast<int>(ld4(ids + at)) : -1;
+    if (id[j] >= count) id[j] = -1;
   }
-  for (int i = tid; i < count; i += threads) cnt[i] = 0;
+  for (int i = tid; i < segments * count; i += blockDim.x) before[i] = 0;
   __syncthreads();
-  if (tid < 32) {
-    for (int p0 = 0; p0 < pairs; p0 += 32) {
-      const int p = p0 + lane;
-      const int id = p < pairs ? id_of[p] : 0xFFFF;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-      const int at = id != 0xFFFF ? cnt[id] : 0;
-      __syncwarp();
-      if (id != 0xFFFF) {
-        rank[p] = static_cast<uint16_t>(at + __popc(same & ((1u << lane) - 1u)));
-        if (lane == __ffs(same) - 1) cnt[id] = at + __popc(same);
-      }
-      __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int at = warp + j * warps;
+    if (at >= segments) break;
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, id[j] < 0 ? -1 : id[j]);
+    rank[j] = __popc(same & ((1u << lane) - 1u));
+    if (id[j] >= 0 && rank[j] == 0) before[at * count + id[j]] = static_cast<uint16_t>(__popc(same));
+  }
+  __syncthreads();
+  for (int e = tid; e < count; e += blockDim.x) {
+    int n = 0;
+    for (int i = 0; i < segments; ++i) {
+      const int here = before[i * count + e];
+      before[i * count + e] = static_cast<uint16_t>(n);
+      n += here;
     }
+    cnt[e] = n;
+  }
+  __syncthreads();
+  if (warp == 0) {
     int rows = 0, chunks = 0;
     for (int e0 = 0; e0 < count; e0 += 32) {
       const int e = e0 + lane;
@@ -267,11 +297,13 @@ __device__ __noinline__ int make_chunks(const int32_t* ids, int pairs, int count
     if (lane == 0) *number = chunks;
   }
   __syncthreads();
-  for (int p = tid; p < pairs; p += threads) {
-    const int id = id_of[p];
-    if (id == 0xFFFF) continue;
-    order[cnt[id] + rank[p]] = static_cast<uint16_t>(p);
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int at = warp + j * warps;
+    if (at < segments && id[j] >= 0)
+      order[cnt[id[j]] + before[at * count + id[j]] + rank[j]] = static_cast<uint16_t>(at * 32 + lane);
   }
+  fence_proxy_async_smem();  // `before` may be the ring's
   __syncthreads();
   return *number;
 }
@@ -314,7 +346,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
   int chunks = 1;
   if constexpr (kRouted) {
     chunks = make_chunks(a.ids, a.b * a.k, a.count, kCap, s_chunk, s_order, reinterpret_cast<int*>(smem + lay.cnt),
-                         &s_chunks);
+                         reinterpret_cast<uint16_t*>(smem + lay.before), &s_chunks);
   } else {
     chunks = (a.b + kCap - 1) / kCap;
     __syncthreads();
@@ -523,12 +555,12 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     const int sigma = (g & 1) * 4 + (g >> 1);
     const int line = kMode == kModeAct ? warp * 16 + sigma : warp * 32 + sigma;
     auto line_of = [&](int i) { return kMode == kModeAct ? (i & 1) * 8 + (i >> 1) * kBoxCols : i * 8; };
-    const uint8_t* const w_at[2] = {smem + line * 128 + ((t ^ sigma) << 4),
-                                    smem + line * 128 + (((4 + t) ^ sigma) << 4)};
-    const uint8_t* const s_at = smem + kWBytes + line / kBoxCols * kBoxCols * 8 + line % kBoxCols * 4;
-    const int s_next = a.width * 4;
-    const uint8_t* const x_at = smem + kWBytes + kSBytes + lane * 16;
-    auto lds16 = [](const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); };
+    // Offsets into a slot, of 32 bits.
+    const uint32_t base = static_cast<uint32_t>(smem - smem_raw);
+    const uint32_t w_at[2] = {line * 128u + ((t ^ sigma) << 4), line * 128u + (((4 + t) ^ sigma) << 4)};
+    const uint32_t s_at = kWBytes + line / kBoxCols * kBoxCols * 8 + line % kBoxCols * 4, s_next = a.width * 4;
+    const uint32_t x_at = kWBytes + kSBytes + lane * 16;
+    auto lds16 = [&](uint32_t at) { return *reinterpret_cast<const uint4*>(smem_raw + at); };
     auto barrier = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kMulThreads) : "memory"); };
 
     // Outputs are made in items of four neighbours (kModeAct: of four gates and what they multiply,
@@ -542,6 +574,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
       const int row = item / kItems, c = item % kItems;
       const int64_t line = pair_of(first, row);
       if constexpr (kMode == kModeAct) {
+        if (block * (kCols / 2) + c * 4 >= a.f) return;
         const float4 gate = v[0], up = v[1];
         const float act[4] = {gate.x / (1.0f + expf(-gate.x)) * up.x, gate.y / (1.0f + expf(-gate.y)) * up.y,
                               gate.z / (1.0f + expf(-gate.z)) * up.z, gate.w / (1.0f + expf(-gate.w)) * up.w};
@@ -626,94 +659,125 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
       __syncwarp();
     };
 
-    Turn s;
-    Walk k = at0;
-    bool ok = true;
-    int from = at0.u;  // of the job's steps, the first of this block's
-    clear();
-    for (int v = lo; v < hi; ++v) {
-      const int chunk = k.chunk, block = k.block, u = k.u;
-      const int tiles = (chunk_rows(chunk) * kParts + 7) >> 3;  // tiles of rows in use
-      const bool codes = u < code_steps;
-      // columns that are not there: nothing to do
-      const int units = kMode != kModeAct && block * kCols + warp * 32 >= a.n
-                            ? 0
-                            : min(2, codes ? groups - 2 * u : (a.r - (u - code_steps) * 64 + 31) >> 5);
-      // A block that gives up walks on, so that all its warps meet at the barriers below.
-      ok = ok && wait(&s_wfull[s.slot], s.phase, &s_wait, kSiteWFull) &&
-           wait(&s_xfull[s.slot], s.phase, &s_wait, kSiteXFull);
-      const uint32_t at = s.slot * kSlot;
-#pragma unroll 1
-      for (int wk = 0; ok && wk < units; ++wk) {
-        uint4 w[4];
-        const uint8_t* const wp = (wk ? w_at[1] : w_at[0]) + at;
-        const uint8_t* const xp = x_at + at + wk * (codes ? NT * 2048 : NT * 512);
+    // One group of 32 columns; one 32 ranks of their low-rank factors.
+    int tiles = 1;  // of rows in use
+    auto code_unit = [&](uint32_t at, int wk) {
+      uint4 w[4];
+      float sc[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = lds16(wp + line_of(i) * 128);
-        if (codes) {
-          float sc[4];
+      for (int i = 0; i < 4; ++i) w[i] = lds16(at + (wk ? w_at[1] : w_at[0]) + line_of(i) * 128);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sc[i] = *reinterpret_cast<const float*>(
-                s_at + at + wk * s_next + (kMode == kModeAct ? (i & 1) * 32 + (i >> 1) * kBoxCols * 8 : i * 32));
-          float d[2][NT][4];
+      for (int i = 0; i < 4; ++i)
+        sc[i] = *reinterpret_cast<const float*>(
+            smem_raw + (at + s_at + wk * s_next + (kMode == kModeAct ? (i & 1) * 32 + (i >> 1) * kBoxCols * 8 : i * 32)));
+      float d[2][NT][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t c[2][2][4];
+      for (int j = 0; j < 4; ++j) {
+        uint32_t c[2][2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 w0 = w[2 * i], w1 = w[2 * i + 1];
-              const uint32_t a0 = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
-              const uint32_t a1 = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
+        for (int i = 0; i < 2; ++i) {
+          const uint4 w0 = w[2 * i], w1 = w[2 * i + 1];
+          const uint32_t a0 = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
+          const uint32_t a1 = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                c[i][h][0] = codes2(a0 >> (8 * h)), c[i][h][1] = codes2(a1 >> (8 * h));
-                c[i][h][2] = codes2(a0 >> (8 * h + 4)), c[i][h][3] = codes2(a1 >> (8 * h + 4));
-              }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (nt > 0 && nt >= tiles) break;
-              const uint4 x = lds16(xp + nt * 2048 + j * 512);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (j == 0)
-                  mma16816_first(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], x.x, x.y);
-                else
-                  mma16816(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], x.x, x.y);
-                mma16816(d[i][nt], c[i][1][0], c[i][1][1], c[i][1][2], c[i][1][3], x.z, x.w);
-              }
-            }
+          for (int h = 0; h < 2; ++h) {
+            c[i][h][0] = codes2(a0 >> (8 * h)), c[i][h][1] = codes2(a1 >> (8 * h));
+            c[i][h][2] = codes2(a0 >> (8 * h + 4)), c[i][h][3] = codes2(a1 >> (8 * h + 4));
           }
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (nt > 0 && nt >= tiles) break;
+        for (int nt = 0; nt < NT; ++nt) {
+          if (nt > 0 && nt >= tiles) break;
+          const uint4 x = lds16(at + x_at + (wk * NT + nt) * 2048 + j * 512);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              acc[i][nt][0] = fmaf(sc[2 * i], d[i][nt][0], acc[i][nt][0]);
-              acc[i][nt][1] = fmaf(sc[2 * i], d[i][nt][1], acc[i][nt][1]);
-              acc[i][nt][2] = fmaf(sc[2 * i + 1], d[i][nt][2], acc[i][nt][2]);
-              acc[i][nt][3] = fmaf(sc[2 * i + 1], d[i][nt][3], acc[i][nt][3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 x = lds16(xp + nt * 512);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              mma16816(acc[i][nt], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, x.x, x.y);
-              mma16816(acc[i][nt], w[2 * i].z, w[2 * i + 1].z, w[2 * i].w, w[2 * i + 1].w, x.z, x.w);
-            }
+          for (int i = 0; i < 2; ++i) {
+            if (j == 0)
+              mma16816_first(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], x.x, x.y);
+            else
+              mma16816(d[i][nt], c[i][0][0], c[i][0][1], c[i][0][2], c[i][0][3], x.x, x.y);
+            mma16816(d[i][nt], c[i][1][0], c[i][1][1], c[i][1][2], c[i][1][3], x.z, x.w);
           }
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0 && nt >= tiles) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc[i][nt][0] = fmaf(sc[2 * i], d[i][nt][0], acc[i][nt][0]);
+          acc[i][nt][1] = fmaf(sc[2 * i], d[i][nt][1], acc[i][nt][1]);
+          acc[i][nt][2] = fmaf(sc[2 * i + 1], d[i][nt][2], acc[i][nt][2]);
+          acc[i][nt][3] = fmaf(sc[2 * i + 1], d[i][nt][3], acc[i][nt][3]);
+        }
+      }
+    };
+    auto rank_unit = [&](uint32_t at, int wk) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = lds16(at + (wk ? w_at[1] : w_at[0]) + line_of(i) * 128);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 x = lds16(at + x_at + (wk * NT + nt) * 512);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma16816(acc[i][nt], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, x.x, x.y);
+          mma16816(acc[i][nt], w[2 * i].z, w[2 * i + 1].z, w[2 * i].w, w[2 * i + 1].w, x.z, x.w);
+        }
+      }
+    };
+    const uint32_t empty0 = smem_u32(s_empty), wfull0 = smem_u32(s_wfull), xfull0 = smem_u32(s_xfull);
+    uint32_t slot = 0, phase = 0;
+    bool ok = true;
+    // A block that gives up walks on, so that all its warps meet at the barriers below.
+    auto step_begin = [&] {
+      if (!__all_sync(0xFFFFFFFFu, try_wait(wfull0 + slot * 8, phase) && try_wait(xfull0 + slot * 8, phase)))
+        ok = ok && wait(&s_wfull[slot], phase, &s_wait, kSiteWFull) && wait(&s_xfull[slot], phase, &s_wait, kSiteXFull);
+      return base + slot * kSlot;
+    };
+    auto step_end = [&] {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[s.slot]);
-      next_slot(s);
-      const bool over = advance(k);
-      if (!over && v + 1 < hi) continue;
+      if (lane == 0) arrive(empty0 + slot * 8);
+      if (++slot == a.slots) slot = 0, phase ^= 1;
+    };
+
+    Walk k = at0;
+    int from = at0.u;  // of the job's steps, the first of this block's
+    clear();
+    for (int v = lo; v < hi;) {
+      const int chunk = k.chunk, block = k.block, to = min(per, from + hi - v);
       const int first = chunk_first(chunk), rows = chunk_rows(chunk);
+      tiles = (rows * kParts + 7) >> 3;
+      // columns that are not there: nothing to do
+      const bool any = kMode == kModeAct ? block * (kCols / 2) + warp * 16 < a.f : block * kCols + warp * 32 < a.n;
+      int u = from;
+#pragma unroll 1
+      for (; u < min(to, code_steps); ++u) {
+        const uint32_t at = step_begin();
+        if (ok && any) {
+          if constexpr (NT <= 2) {
+            code_unit(at, 0);
+            if (2 * u + 1 < groups) code_unit(at, 1);
+          } else {  // twice the registers: not both at once
+#pragma unroll 1
+            for (int wk = 0; wk < min(2, groups - 2 * u); ++wk) code_unit(at, wk);
+          }
+        }
+        step_end();
+      }
+#pragma unroll 1
+      for (; u < to; ++u) {
+        const uint32_t at = step_begin();
+#pragma unroll 1
+        for (int wk = 0; wk < 2; ++wk)
+          if (ok && any && (u - code_steps) * 64 + wk * 32 < a.r) rank_unit(at, wk);
+        step_end();
+      }
+      v += to - from;
+      const bool over = to == per;
+      if (over) {
+        ++k.job;
+        if (k.job < job1) enter_job(k);
+      }
       leave(rows);
       barrier();
       if (from > 0) {
@@ -746,7 +810,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
         }
       }
       from = 0;
-      if (v + 1 < hi) barrier();  // the sums are read
+      if (v < hi) barrier();  // the sums are read
     }
   }
   pdl_wait();  // this grid completes only after the one in front
@@ -952,6 +1016,12 @@ cudaError_t launch(const A16Args& a, cudaStream_t st) {
     cudaError_t e = plan_of<8, NT, kMode, kParts, kRouted>(a, &blocks, &wide);
     if (e == cudaSuccess) e = plan_of<4, NT, kMode, kParts, kRouted>(a, &blocks, &narrow);
     if (e != cudaSuccess) return e;
+    if constexpr (NT <= 2) {
+      Plan widest;
+      e = plan_of<16, NT, kMode, kParts, kRouted>(a, &blocks, &widest);
+      if (e != cudaSuccess) return e;
+      if (getenv("A16W16") && widest.cost <= 1.1 * std::min(wide.cost, narrow.cost)) return launch_warps<16, NT, kMode, kParts, kRouted>(a, st);
+    }
     return wide.cost <= narrow.cost ? launch_warps<8, NT, kMode, kParts, kRouted>(a, st)
                                         : launch_warps<4, NT, kMode, kParts, kRouted>(a, st);
   }
