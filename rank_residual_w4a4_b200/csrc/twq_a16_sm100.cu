@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "sm100_ptx.cuh"
@@ -76,7 +77,7 @@ struct A16Args {
   int parts;               // room for other blocks' parts of a job
   bool ids_ready, x_ready; // complete before this kernel starts, whatever it waits for
   uint64_t wait_ns;
-  int stall;               // self-test: the X warps stop early
+  int stall;               // self-test: a block's last step gets no activations
 };
 
 struct WaitState {  // a block's, in shared memory
@@ -177,17 +178,19 @@ struct Layout {
   int sums, recv, chunks, order, cnt, before, total;
 };
 
-// kWarps: that multiply, 32 weight columns each.
+// kWarps: that multiply, 32 weight columns each. kModeH, whose columns are few: two warps have the same
+// columns and one group of a step each.
 template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
 struct Kernel {
-  static constexpr int kMulThreads = kWarps * 32, kCols = kWarps * 32;
+  static constexpr int kShare = kMode == kModeH ? 2 : 1;
+  static constexpr int kMulThreads = kWarps * 32, kCols = kWarps / kShare * 32;
   // Copies of a step: of 128 columns, or of the block's (kModeAct: of half, gates and what they multiply).
   static constexpr int kBoxCols = kMode == kModeAct ? kCols / 2 : kCols < kBox ? kCols : kBox;
   static constexpr int kWBytes = kCols * 128, kSBytes = kCols * 8 < 1024 ? 1024 : kCols * 8;
   static constexpr int kCap = 8 * NT / kParts;                 // rows of activations in a chunk
   static constexpr int kXWarps = NT == 1 ? 2 : 3;
   static constexpr int kThreads = kMulThreads + 32 + 32 * kXWarps;
-  static constexpr int kBlocksPerSm = kWarps == 16 ? 1 : kWarps == 8 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;
+  static constexpr int kBlocksPerSm = (kWarps == 8 ? 1 : 2) + (NT == 1);
   static constexpr int kSlot = kWBytes + kSBytes + 4096 * NT;
 
   static __host__ __device__ int max_chunks(int pairs, int count) {
@@ -405,7 +408,10 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     Walk k = at0;
     int issued = 0;
     for (int v = lo; v < hi; ++v) {
-      if (issued >= a.slots && !wait(&s_empty[s.slot], s.phase ^ 1, &s_wait, kSiteEmpty)) break;
+      // The slot is free, and what was loaded into it is there (products that gave up do not wait for that).
+      if (issued >= a.slots && !(wait(&s_empty[s.slot], s.phase ^ 1, &s_wait, kSiteEmpty) &&
+                                 wait(&s_wfull[s.slot], s.phase ^ 1, &s_wait, kSiteWFull)))
+        break;
       if (lane == 0) {
         const int col = k.block * (kMode == kModeAct ? kCols / 2 : kCols);
         const int boxes = kMode == kModeAct ? 2 : min(kCols / kBoxCols, (a.n - col + kBoxCols - 1) / kBoxCols);
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     skip(turn);
     begin();
     while (v < hi) {
-      if (a.stall && v - lo >= K::kXWarps) break;
+      if (a.stall && v + 1 == hi) break;
       uint8_t* const dst = smem + s.slot * kSlot + kWBytes + kSBytes + lane * 16;
       if (k.u >= code_steps) {
         if (!waited) pdl_wait();
@@ -553,7 +559,8 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     // The lane's columns: sigma + 8 i of its warp's 32, i < 4 (kModeAct: of its 16 gates for i < 2, else
     // of what they multiply). sigma orders them so that 8 lanes read 128 bytes without conflict.
     const int sigma = (g & 1) * 4 + (g >> 1);
-    const int line = kMode == kModeAct ? warp * 16 + sigma : warp * 32 + sigma;
+    const int wr = warp % (kWarps / K::kShare), wk0 = warp / (kWarps / K::kShare);  // columns, group of a step
+    const int line = kMode == kModeAct ? wr * 16 + sigma : wr * 32 + sigma;
     auto line_of = [&](int i) { return kMode == kModeAct ? (i & 1) * 8 + (i >> 1) * kBoxCols : i * 8; };
     // Offsets into a slot, of 32 bits.
     const uint32_t base = static_cast<uint32_t>(smem - smem_raw);
@@ -563,12 +570,17 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     auto lds16 = [&](uint32_t at) { return *reinterpret_cast<const uint4*>(smem_raw + at); };
     auto barrier = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kMulThreads) : "memory"); };
 
+    auto add4 = [](float4& o, const float4& p) { o.x += p.x, o.y += p.y, o.z += p.z, o.w += p.w; };
+
     // Outputs are made in items of four neighbours (kModeAct: of four gates and what they multiply,
     // 16 columns on) of one row.
     constexpr int kItems = kMode == kModeAct ? kCols / 8 : kCols / 4, kQuads = kMode == kModeAct ? 2 : 1;
     auto sum_of = [&](int item, int q) {  // this block's
       const int c = item % kItems, col = kMode == kModeAct ? (c >> 2) * 32 + (c & 3) * 4 + 16 * q : c * 4;
-      return *reinterpret_cast<const float4*>(sums + ((col >> 5) * kCap + item / kItems) * kYStride + (col & 31));
+      const float* const at = sums + ((col >> 5) * kCap + item / kItems) * kYStride + (col & 31);
+      float4 o = *reinterpret_cast<const float4*>(at);
+      if constexpr (K::kShare == 2) add4(o, *reinterpret_cast<const float4*>(at + kWarps / 2 * kCap * kYStride));
+      return o;
     };
     auto put_item = [&](int block, int first, int item, const float4 (&v)[kQuads]) {
       const int row = item / kItems, c = item % kItems;
@@ -598,8 +610,6 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
           *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
       }
     };
-    auto add4 = [](float4& o, const float4& p) { o.x += p.x, o.y += p.y, o.z += p.z, o.w += p.w; };
-
     float acc[2][NT][4];
     auto clear = [&] {
 #pragma unroll
@@ -748,13 +758,15 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
       const int first = chunk_first(chunk), rows = chunk_rows(chunk);
       tiles = (rows * kParts + 7) >> 3;
       // columns that are not there: nothing to do
-      const bool any = kMode == kModeAct ? block * (kCols / 2) + warp * 16 < a.f : block * kCols + warp * 32 < a.n;
+      const bool any = kMode == kModeAct ? block * (kCols / 2) + wr * 16 < a.f : block * kCols + wr * 32 < a.n;
       int u = from;
 #pragma unroll 1
       for (; u < min(to, code_steps); ++u) {
         const uint32_t at = step_begin();
         if (ok && any) {
-          if constexpr (NT <= 2) {
+          if constexpr (K::kShare == 2) {
+            if (2 * u + wk0 < groups) code_unit(at, wk0);
+          } else if constexpr (NT <= 2) {
             code_unit(at, 0);
             if (2 * u + 1 < groups) code_unit(at, 1);
           } else {  // twice the registers: not both at once
@@ -855,29 +867,34 @@ __global__ void __launch_bounds__(kCombineThreads)
   *reinterpret_cast<uint2*>(y + token * n + col) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
 }
 
-// How a launch divides its jobs (at most `jobs`, of `steps` each): clusters, log2 of their blocks, and
+// How a launch divides its jobs (about `jobs`, of `steps` each): clusters, log2 of their blocks, and
 // how many blocks' parts of a job a block may get.
 struct Plan {
-  int64_t clusters, cost;
+  int64_t clusters, cost, mine;  // mine: steps of a block, at most
   int split_log, parts;
 };
 // The split that the busiest SM is done with first, of at most 2^most blocks; room: clusters of 1, 2, 4 and
 // 8 blocks that run at once. An SM's time for a group of 32 columns goes with
 // the warps that multiply there: 410 cycles with 16 of them, 555 with 8 (8 rows, 37888 columns of 4096).
+// Among equal splits of a long run of choices' jobs the finer one: how many jobs there are, the GPU alone knows,
+// and a cluster with one job more than another costs less (24 tokens, a quarter of 8 choices each among 32 local
+// experts of 4096 x 1024: 73 us instead of 77). For a short run joining the parts costs more (one token, 8 of
+// 128 experts of 2048 x 768: 18.6 us, 22.0 with the finer split).
+constexpr int kShortRun = 8, kLongRun = 16;
 Plan plan(int64_t jobs, int64_t steps, const int* room, int per_sm, int warps, bool all_there, int most) {
-  Plan best = {0, 0, 0, 0};
+  Plan best = {0, 0, 0, 0, 0};
   for (int s = 0; s <= most; ++s) {
     if (s > 0 && steps * jobs < 2 << s) break;
     const int64_t clusters = std::min<int64_t>(jobs, room[s]);
     const int64_t mine = ((jobs + clusters - 1) / clusters * steps + (1 << s) - 1) >> s;
     const int64_t at_once = std::min<int64_t>(((clusters << s) + kSms - 1) / kSms, per_sm) * warps;
     const int64_t cost = mine * at_once * (265 + 2320 / at_once);
-    if (best.clusters && cost >= best.cost) continue;
+    if (best.clusters && cost >= best.cost + (!all_there && mine >= kLongRun)) continue;
     // Blocks that a job may reach over: all where they may have no step each (which jobs there are may be
     // known on the GPU alone).
     const int64_t least = all_there ? (jobs / clusters * steps) >> s : 0;
     const int64_t others = least ? std::min<int64_t>((1 << s) - 1, (steps + least - 2) / least) : (1 << s) - 1;
-    best = {clusters, cost, s, static_cast<int>(others)};
+    best = {clusters, cost, mine, s, static_cast<int>(others)};
   }
   return best;
 }
@@ -938,45 +955,54 @@ cudaError_t clusters_at_once(const void* kernel, int threads, int per_sm, const 
   return cudaSuccess;
 }
 
+// A launch as it fits: of the blocks on an SM and the clusters that leave a ring of two slots or more beside
+// the sums and the parts, those with the least work on the busiest SM. Many experts' lists may leave a block
+// of more columns no room.
+constexpr int64_t kNoFit = int64_t(1) << 56;
+struct Choice {
+  Plan p;
+  int blocks, slots;
+};
+
 template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
-cudaError_t plan_of(const A16Args& a, int* blocks, Plan* out, int most = 3, int per_sm = 0) {
+cudaError_t choose(const A16Args& a, Choice* out) {
   using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
-  if (per_sm == 0) per_sm = K::kBlocksPerSm;
-  const int* room;
-  const cudaError_t e = clusters_at_once(reinterpret_cast<const void*>(a16_kernel<kWarps, NT, kMode, kParts, kRouted>),
-                                         K::kThreads, per_sm, &room);
-  if (e != cudaSuccess) return e;
-  const int64_t chunks = kRouted ? K::max_chunks(a.b * a.k, a.count) : (a.b + K::kCap - 1) / K::kCap;
+  int64_t chunks = (a.b + K::kCap - 1) / K::kCap;
+  if (kRouted) {  // as many different experts as so many choices among them leave on average
+    const double pairs = a.b * a.k, used = a.count * (1.0 - std::pow(1.0 - 1.0 / a.count, pairs));
+    chunks = std::min<int64_t>(K::max_chunks(a.b * a.k, a.count), std::ceil(std::max(used, pairs / K::kCap)));
+  }
   const int width = kMode == kModeAct ? K::kCols / 2 : K::kCols;
-  *blocks = ((kMode == kModeAct ? a.f : a.n) + width - 1) / width;
+  const int blocks = ((kMode == kModeAct ? a.f : a.n) + width - 1) / width;
   const int64_t steps = (a.K / 128 + 1) / 2 + (a.r + 63) / 64;
-  *out = plan(chunks * *blocks, steps, room, per_sm, kWarps, !kRouted, most);
+  *out = {};
+  out->p.cost = kNoFit;
+  for (int per_sm = K::kBlocksPerSm; per_sm > 0; --per_sm) {
+    const int* room;
+    const cudaError_t e = clusters_at_once(
+        reinterpret_cast<const void*>(a16_kernel<kWarps, NT, kMode, kParts, kRouted>), K::kThreads, per_sm, &room);
+    if (e != cudaSuccess) return e;
+    for (int most = 3; most >= 0; --most) {
+      const Plan p = plan(chunks * blocks, steps, room, per_sm, kWarps, !kRouted, most);
+      const int left = 227 * 1024 / per_sm - 1024 - 1536 - K::layout(a.b, a.k, a.count, 0, p.parts).total;
+      if (left < 2 * K::kSlot) continue;
+      if (p.cost < out->p.cost) *out = {p, blocks, std::min(kMaxSlots, left / K::kSlot)};
+      break;
+    }
+  }
   return cudaSuccess;
 }
 
 template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
-cudaError_t launch_warps(A16Args a, cudaStream_t st) {
+cudaError_t launch_warps(A16Args a, const Choice& c, cudaStream_t st) {
   using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
   auto kernel = a16_kernel<kWarps, NT, kMode, kParts, kRouted>;
-  // Slots of the ring: what is left beside the sums and parts; a block less on an SM, or a smaller
-  // cluster, rather than one slot.
-  Plan p;
-  Layout l;
-  int per_sm = K::kBlocksPerSm;
-  for (int most = 3;;) {
-    cudaError_t e = plan_of<kWarps, NT, kMode, kParts, kRouted>(a, &a.blocks, &p, most, per_sm);
-    if (e != cudaSuccess) return e;
-    l = K::layout(a.b, a.k, a.count, 0, p.parts);
-    a.slots = std::min(kMaxSlots, (227 * 1024 / per_sm - 1024 - 1536 - l.total) / K::kSlot);
-    if (a.slots >= 2) break;
-    if (per_sm > 1)
-      --per_sm;
-    else if (most-- == 0)
-      return cudaErrorInvalidValue;
-  }
+  const Plan& p = c.p;
+  if (p.cost >= kNoFit) return cudaErrorInvalidValue;
+  a.blocks = c.blocks, a.slots = c.slots;
   a.split_log = p.split_log, a.parts = p.parts;
   const int split = 1 << p.split_log;
-  l = K::layout(a.b, a.k, a.count, a.slots, a.parts);
+  const Layout l = K::layout(a.b, a.k, a.count, a.slots, a.parts);
   a.width = std::min(K::kBoxCols, a.n);
   bool ok = encode_map_2d(&a.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, int64_t(a.count) * a.n, a.K / 2, 128,
                           a.width, CU_TENSOR_MAP_SWIZZLE_128B) &&
@@ -1005,26 +1031,23 @@ cudaError_t launch_warps(A16Args a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Blocks of 256 columns, or of 128 where that leaves the busiest SM less.
+// Blocks of 256 columns, or of 128 where that leaves the busiest SM less. At the same work, blocks of 128
+// where a run is short: they are done sooner after their last step (one row, 4096 -> 4096 with rank 128: 7.4
+// us, 8.4 with 256), and of 256 where it is longer: they stage the activations half as often (61 rows, 5120 ->
+// 25600 with rank 64: 73.5 us, 82.1 with 128; 32 rows, 5120 -> 18944: 28.6, 30.6).
 template <int NT, int kMode, int kParts, bool kRouted>
 cudaError_t launch(const A16Args& a, cudaStream_t st) {
-  if constexpr (kMode == kModeH) {
-    return launch_warps<2, NT, kMode, kParts, kRouted>(a, st);
-  } else {
-    int blocks;
-    Plan wide, narrow;
-    cudaError_t e = plan_of<8, NT, kMode, kParts, kRouted>(a, &blocks, &wide);
-    if (e == cudaSuccess) e = plan_of<4, NT, kMode, kParts, kRouted>(a, &blocks, &narrow);
+  Choice narrow;
+  cudaError_t e = choose<4, NT, kMode, kParts, kRouted>(a, &narrow);
+  if (e != cudaSuccess) return e;
+  if constexpr (kMode != kModeH) {
+    Choice wide;
+    e = choose<8, NT, kMode, kParts, kRouted>(a, &wide);
     if (e != cudaSuccess) return e;
-    if constexpr (NT <= 2) {
-      Plan widest;
-      e = plan_of<16, NT, kMode, kParts, kRouted>(a, &blocks, &widest);
-      if (e != cudaSuccess) return e;
-      if (getenv("A16W16") && widest.cost <= 1.1 * std::min(wide.cost, narrow.cost)) return launch_warps<16, NT, kMode, kParts, kRouted>(a, st);
-    }
-    return wide.cost <= narrow.cost ? launch_warps<8, NT, kMode, kParts, kRouted>(a, st)
-                                        : launch_warps<4, NT, kMode, kParts, kRouted>(a, st);
+    if (wide.p.cost < narrow.p.cost || (wide.p.cost == narrow.p.cost && wide.p.mine >= kShortRun))
+      return launch_warps<8, NT, kMode, kParts, kRouted>(a, wide, st);
   }
+  return launch_warps<4, NT, kMode, kParts, kRouted>(a, narrow, st);
 }
 
 // Tiles of a chunk: for as many rows as there are, or as an expert has on average twice over (then

@@ -1992,7 +1992,7 @@ BackwardPlan backward_plan(int64_t b, int64_t m, int64_t n, int64_t r, int64_t c
 }
 
 // By device; a kernel's pointer where its limit is set. More places than the adapters have kernels.
-constexpr int kKnownDevices = 64, kKnownKernels = 64;
+constexpr int kKnownDevices = 64, kKnownKernels = 96;
 std::atomic<const void*> g_allowed[kKnownDevices][kKnownKernels];
 
 }  // namespace

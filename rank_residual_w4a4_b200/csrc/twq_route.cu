@@ -3,7 +3,8 @@
 // A warp takes a row and keeps all of it in registers as keys: the bits of a float, mapped so that
 // unsigned order is the order of the numbers (a NaN above all, -0 equal to +0, -inf above nothing).
 // Each of the k rounds is the lane's own largest key, one reduction of the warp for the key and one
-// for the lowest index that has it, so equal logits leave in the order of their indices.
+// for the lowest index that has it, so equal logits leave in the order of their indices. A BF16 logit's
+// key has 16 bits and leaves room for the index below it: then one reduction does.
 //
 // Reads 4 (BF16: 2) bytes per logit and writes 8 per choice; what bounds it is latency for a decode
 // batch and the rounds' instructions for a large one.
@@ -35,46 +36,64 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   pdl_wait();
   pdl_launch_dependents();
   if (row >= c.b) return;
+  // BF16: the upper half of the key, and 0xFFFF - index.
+  constexpr uint32_t kNone = kBf16 ? kMinusInf | 0xFFFFu : kMinusInf;  // no key of a choice is as small
+  auto number_of = [](uint32_t k) {  // (~ keeps a negative number's lower half out of the way)
+    return kBf16 ? value_of(k & 0x80000000u || k == 0 ? k & 0xFFFF0000u : k | 0xFFFFu) : value_of(k);
+  };
   uint32_t key[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
     const int at = i * 32 + lane;
     key[i] = 0;
     if (at < c.count) {
-      if constexpr (kBf16)
-        key[i] = key_of(__bfloat162float(static_cast<const __nv_bfloat16*>(c.logits)[row * c.ld + at]));
-      else
+      if constexpr (kBf16) {
+        const uint32_t k = key_of(__bfloat162float(static_cast<const __nv_bfloat16*>(c.logits)[row * c.ld + at]));
+        key[i] = (k & 0xFFFF0000u) | (0xFFFFu - at);
+      } else {
         key[i] = key_of(static_cast<const float*>(c.logits)[row * c.ld + at]);
+      }
     }
   }
   float top = 0.0f, sum = 0.0f;
   uint32_t mine = 0;  // the lane-th choice
   int mine_at = -1;
   for (int s = 0; s < c.k; ++s) {
-    uint32_t best = key[0];
-    int at = 0;
+    uint32_t best = key[0], index;
+    [[maybe_unused]] int at = 0;
 #pragma unroll
-    for (int i = 1; i < kV; ++i)
-      if (key[i] > best) best = key[i], at = i;
+    for (int i = 1; i < kV; ++i) {
+      if constexpr (kBf16)
+        best = max(best, key[i]);
+      else if (key[i] > best)
+        best = key[i], at = i;
+    }
     const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t index = __reduce_min_sync(0xFFFFFFFFu, best == most ? at * 32u + lane : 0xFFFFFFFFu);
+    if constexpr (kBf16)
+      index = 0xFFFFu - (most & 0xFFFFu);
+    else
+      index = __reduce_min_sync(0xFFFFFFFFu, best == most ? at * 32u + lane : 0xFFFFFFFFu);
     if (s == 0) {
-      top = value_of(most);
+      top = number_of(most);
       if (!c.renormalize) {
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-          const float v = value_of(key[i]);
-          if (key[i] > kMinusInf) sum += v == top ? 1.0f : expf(v - top);
+          const float v = number_of(key[i]);
+          if (key[i] > kNone) sum += v == top ? 1.0f : expf(v - top);
         }
       }
     }
-    if (most <= kMinusInf) break;
+    if (most <= kNone) break;
     if (lane == s) mine = most, mine_at = static_cast<int>(index);
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
-      if (index == i * 32u + lane) key[i] = 0;
+    for (int i = 0; i < kV; ++i) {
+      if constexpr (kBf16)
+        key[i] = key[i] == most ? 0 : key[i];
+      else if (index == i * 32u + lane)
+        key[i] = 0;
+    }
   }
-  const float v = value_of(mine);
+  const float v = number_of(mine);
   const float e = mine_at < 0 ? 0.0f : v == top ? 1.0f : expf(v - top);
   if (c.renormalize) sum = e;
 #pragma unroll

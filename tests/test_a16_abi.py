@@ -93,6 +93,12 @@ def test_workspace_of_a_refused_shape_is_zero(lib, args):
     assert lib.twq_moe_workspace_bytes(b, k, ctypes.byref(experts(**e))) == 0
 
 
+def test_stall_selftest_validation(lib):
+    f = lib.twq_selftest_a16_stall
+    assert f(-1) == 1 and f(999) == 1 and f(1000000001) == 1
+    assert f(1000) == 0 and f(1000000000) == 0 and f(0) == 0
+
+
 def test_launch_accounting(lib):
     assert twq.launches_per_call("twq_fused_linear_a16") == 2
     assert twq.launches_per_call("twq_moe_route") == 1 and twq.launches_per_call("twq_moe_experts") == 5

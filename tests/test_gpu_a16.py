@@ -338,6 +338,57 @@ def test_two_streams(twq, device):
         assert all(torch.equal(v, w) for v in o)
 
 
+def test_two_graphs_share_a_workspace(twq, device):
+    """Two captured calls with one workspace and one output, replayed one after the other."""
+    gen = torch.Generator().manual_seed(15)
+    ex = make_experts(twq, gen, 8, 512, 256, 16, 16, device)
+    ws = torch.empty(twq.moe_workspace_bytes(20, 3, ex), dtype=torch.uint8, device=device)
+    y = torch.empty((20, 512), dtype=BF, device=device)
+    graphs, want = [], []
+    for b in (20, 2):
+        x, logits = make_x(gen, b, 512).to(device), normal(gen, b, 8).to(device)
+        want.append(twq.moe_layer(x, logits, 3, ex)[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = twq.moe_layer(x, logits, 3, ex, y=y[:b], workspace=ws)
+        graphs.append((graph, b, held, x, logits))
+    for _ in range(3):
+        for (graph, b, *_), w in zip(graphs, want):
+            y.fill_(7.0)
+            graph.replay()
+            assert torch.equal(y[:b], w) and (y[b:] == 7.0).all()  # rows behind the last: as they were
+
+
+@pytest.mark.parametrize("call", ["linear", "experts"])
+@pytest.mark.parametrize("b", [1, 12, 64])
+def test_waits_that_run_out(twq, device, b, call):
+    """The blocks' last steps get no activations: the waits on them run out after 0.2 ms, the
+    copies under way land, the kernels leave, the status tells, and the next calls are right."""
+    import time
+
+    gen = torch.Generator().manual_seed(16)
+    if call == "linear":
+        x, w = make_x(gen, b, 8192).to(device), make_layer(twq, gen, 8192, 12800, 64, device)
+        f = lambda: twq.fused_linear_a16(x, w)
+    else:
+        x, ex = make_x(gen, b, 2048).to(device), make_experts(twq, gen, 4, 2048, 1024, 16, 16, device)
+        logits = normal(gen, b, 4).to(device)
+        f = lambda: twq.moe_layer(x, logits, 2, ex)[0]
+    want = f()
+    assert twq.device_status() == 0
+    twq.selftest_a16_stall(200000)
+    try:
+        t0 = time.perf_counter()
+        f()
+        code = twq.device_status()
+        spent = time.perf_counter() - t0
+    finally:
+        twq.selftest_a16_stall(0)
+    assert 71 <= code <= 76 and spent < 1.0, (code, spent)
+    assert twq.device_status() == 0
+    assert torch.equal(f(), want) and twq.device_status() == 0
+
+
 def test_experts_beyond_two_gigabytes(twq, device):
     """Codes of the last experts lie beyond 2^31 bytes."""
     count, m, f = 640, 2048, 2048
