@@ -584,7 +584,7 @@ TWQ_API twq_status twq_moe_experts(const uint16_t* x, int64_t ldx, int64_t b, co
                                    size_t workspace_bytes, twq_stream_t stream);
 
 /* twq_moe_route (logits over e->count experts) and twq_moe_experts on its ids and weights (both
- * are outputs). */
+ * are outputs; every buffer as there, and the limits of both): one launch more than the latter. */
 TWQ_API twq_status twq_moe_layer(const uint16_t* x, int64_t ldx, int64_t b, const float* logits,
                                  int64_t ld, int64_t k, int renormalize, const twq_experts* e,
                                  const uint16_t* base, int32_t* ids, float* weights, uint16_t* y,
@@ -630,7 +630,8 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
 TWQ_API twq_status twq_selftest_adapter_stall(int64_t wait_limit_ns);
 
 /* The same for the calls on BF16 activations (twq_fused_linear_a16, twq_moe_experts and
- * twq_moe_layer; site codes 71..74, 75: a copy in flight did not land). */
+ * twq_moe_layer): while it is set, no block gets the activations of its last step. Site codes
+ * 71..75; 76: a copy in flight did not land. */
 TWQ_API twq_status twq_selftest_a16_stall(int64_t wait_limit_ns);
 
 /*

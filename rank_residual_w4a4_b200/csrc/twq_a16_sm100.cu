@@ -5,12 +5,11 @@
 // operand is BF16: codes are small integers, which BF16 holds, so mma.sync m16n8k16 multiplies them
 // exactly and sums in fp32, and the group's fp32 scale multiplies that sum once.
 //
-// Few rows make this a stream of weights: what bounds it is HBM, or latency where the weights are
-// few. A block takes 256 weight columns (the M side of the products; rows of activations are the N
+// A block takes 256 or 128 weight columns (the M side of the products; rows of activations are the N
 // side, 8 to a tile) and walks the reduction in steps of two groups through a ring in shared memory:
-//   TMA warp   the step's codes, 256 columns x 128 bytes in the 128-byte swizzle, and scales
+//   TMA warp   the step's codes, 128 bytes of each column in the 128-byte swizzle, and scales
 //   X warps    the step's activations, gathered, in the order in which the products take them
-//   8 warps    products, 32 columns each
+//   8, 4 warps products, 32 columns each
 // A cluster of blocks splits the reduction where there are few columns, and adds up over distributed
 // shared memory in a fixed order.
 //
@@ -20,6 +19,13 @@
 // conversion, 11 instructions for 8 codes, is most of a warp's some 240 instructions for 32 columns
 // x one group; at the rate of HBM a quarter of an SM has 370 cycles for it. The low-rank factor L2
 // comes last, in steps of 64 ranks.
+//
+// What bounds it. The copies alone, with nothing multiplied, take 15 us for 4096 x 37888 (5.5 TB/s).
+// Up to 8 rows it is the issue of the conversion and products, 323 cycles a group with 4 warps on a
+// quarter of an SM, 380 with 2: 18.5 us there with 8 rows (82 MB, 4.5 TB/s), 10.0 us for 4096 x 14336
+// with 4. Beyond 16 rows it is mma.sync (8 cycles each on a quarter of an SM) and the registers, which
+// leave 2 warps a quarter: 707 cycles a group of 32 rows, 28.7 us for 5120 x 18944. Small layers are
+// bound by two launches, first copies and joining: 7.4 us for one row of 4096 x 4096 with rank 128.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -828,7 +834,10 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
   pdl_wait();  // this grid completes only after the one in front
 }
 
-// y = base + the sum of weight * part over a token's slots, in their order; four columns per thread.
+// y = base + the sum of weight * part over a token's slots, in their order; four columns per thread. A kernel
+// of its own, since a token's slots are different clusters' work: atomics would add in any order, and a product
+// that goes token by token has too few rows a weight. Latency of one load after the other bounds it (4.6 us
+// alone and cold for 4 tokens of 4096, less behind the products, whose end its start overlaps).
 constexpr int kCombineThreads = 128;
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const float* parts, const int32_t* ids, const float* weights, int k, int count, int n,

@@ -7,7 +7,8 @@
 // key has 16 bits and leaves room for the index below it: then one reduction does.
 //
 // Reads 4 (BF16: 2) bytes per logit and writes 8 per choice; what bounds it is latency for a decode
-// batch and the rounds' instructions for a large one.
+// batch (2.2 us for one row of 128 fp32 logits, mostly launch) and the rounds' instructions for a large
+// one (9.4 us for 8192 rows of 256 BF16 logits, 8 choices; issue active 61% of the time).
 #include <cuda_bf16.h>
 
 #include "sm100_ptx.cuh"
