@@ -763,15 +763,17 @@ def _rows(t, name, dtype, b, m, device, where):
     """A b x m tensor on `device` whose rows may be strided -> its address and row stride."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError("%s must be a 2-D torch tensor" % name)
+    ld, unit = t.stride()
+    if (t.shape == (b, m) and t.dtype == dtype and t.device == device and t.is_cuda
+            and (unit == 1 or m == 1)):
+        return t.data_ptr(), (ld if b > 1 else m)
     if not t.is_cuda:
         raise ValueError("%s must be on a CUDA device (the library has no CPU path)" % name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape[0] != b or t.shape[1] != m or t.device != device:
+    if t.shape != (b, m) or t.device != device:
         raise ValueError("%s must be (%d, %d) on %s" % (name, b, m, where))
-    if t.stride(1) != 1 and m != 1:
-        raise ValueError("%s must have unit stride along its rows" % name)
-    return t.data_ptr(), (t.stride(0) if b > 1 else m)
+    raise ValueError("%s must have unit stride along its rows" % name)
 
 
 def fused_linear_a16(x: torch.Tensor, w: Weights, y=None, h=None, stream=None):
@@ -819,8 +821,16 @@ class Experts:
                 if tuple(t.shape) != (self.count, *shape) or t.device != self.device:
                     raise ValueError("%s.%s must be %s on one device" % (name, field, (self.count, *shape)))
         self.up, self.down = up, down
-        self._c = _Experts(self.count, up.c_struct(), down.c_struct())
+        self._views = up.c_struct(), down.c_struct()
+        self._c = _Experts(self.count, *self._views)
         self._ref = ctypes.byref(self._c)
+
+    def _struct(self):
+        """The C-ABI view; checked and built anew after a field of up or down changed."""
+        up, down = self._views
+        if self.up.c_struct() is not up or self.down.c_struct() is not down:
+            self.__init__(self.up, self.down)
+        return self._ref
 
     @staticmethod
     def empty(count: int, m: int, f: int, r: int, device, r_down: int | None = None) -> "Experts":
@@ -886,12 +896,13 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, ids=None, 
 
 
 def moe_workspace_bytes(b: int, k: int, experts: Experts) -> int:
-    return int(load().twq_moe_workspace_bytes(b, k, experts._ref))
+    return int(load().twq_moe_workspace_bytes(b, k, experts._struct()))
 
 
 def _moe_buffers(x, k, ex, base, y, workspace, stream):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a 2-D torch tensor")
+    ref = ex._struct()
     b, dev, bf = x.shape[0], ex.device, torch.bfloat16
     px, ldx = _rows(x, "x", bf, b, ex.m, dev, "the experts' device")
     pb = None if base is None else _mat(base, "base", bf, b, ex.m, dev)
@@ -902,7 +913,7 @@ def _moe_buffers(x, k, ex, base, y, workspace, stream):
     elif workspace.device != dev:
         raise ValueError("workspace must be on the experts' device")
     _dev(workspace, "workspace", torch.uint8)
-    return b, px, ldx, pb, y, _mat(y, "y", bf, b, ex.m, dev), workspace
+    return b, px, ldx, ref, pb, y, _mat(y, "y", bf, b, ex.m, dev), workspace
 
 
 def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, experts: Experts,
@@ -915,10 +926,10 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, exper
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise TypeError("ids must be a 2-D torch tensor")
     k = ids.shape[1]
-    b, px, ldx, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
+    b, px, ldx, pe, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
     _, _, pi, pw = _choices(ids, weights, b, k, experts.device, stream)
     st, back = _on(experts.device, stream)
-    status = _lib.twq_moe_experts(px, ldx, b, pi, pw, k, experts._ref, pb, py,
+    status = _lib.twq_moe_experts(px, ldx, b, pi, pw, k, pe, pb, py,
                                   workspace.data_ptr(), workspace.numel(), st)
     if back is not None:
         torch.cuda.set_device(back)
@@ -932,12 +943,12 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, experts: Experts,
     """moe_route on the router's logits (b x count) and moe_experts on its choice, in one call:
     (y, ids, weights)."""
     fn = _logits_entry(logits, 1)
-    b, px, ldx, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
+    b, px, ldx, pe, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
     pl, ld = _rows(logits, "logits", logits.dtype, b, experts.count, experts.device,
                    "the experts' device")
     ids, weights, pi, pw = _choices(ids, weights, b, k, experts.device, stream)
     st, back = _on(experts.device, stream)
-    status = getattr(_lib, fn)(px, ldx, b, pl, ld, k, int(renormalize), experts._ref, pb, pi, pw,
+    status = getattr(_lib, fn)(px, ldx, b, pl, ld, k, int(renormalize), pe, pb, pi, pw,
                                py, workspace.data_ptr(), workspace.numel(), st)
     if back is not None:
         torch.cuda.set_device(back)

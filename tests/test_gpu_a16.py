@@ -338,6 +338,22 @@ def test_two_streams(twq, device):
         assert all(torch.equal(v, w) for v in o)
 
 
+def test_experts_follow_their_weights(twq, device):
+    """A field of up or down that is set anew is what the next call reads; one that does not fit is refused."""
+    gen = torch.Generator().manual_seed(17)
+    one, two = (make_experts(twq, gen, 3, 256, 128, 0, 0, device) for _ in range(2))
+    x, ids = make_x(gen, 4, 256).to(device), make_ids(gen, 4, 2, 3, "mixed").to(device)
+    w = torch.rand((4, 2), generator=gen).to(device)
+    want = twq.moe_experts(x, ids, w, two)
+    assert not torch.equal(twq.moe_experts(x, ids, w, one), want)
+    one.up.rq, one.up.sr = two.up.rq.clone(), two.up.sr.clone()
+    one.down = two.down
+    assert torch.equal(twq.moe_experts(x, ids, w, one), want)
+    one.up.rq = two.up.rq[:2].clone()
+    with pytest.raises(ValueError):
+        twq.moe_experts(x, ids, w, one)
+
+
 def test_two_graphs_share_a_workspace(twq, device):
     """Two captured calls with one workspace and one output, replayed one after the other."""
     gen = torch.Generator().manual_seed(15)
