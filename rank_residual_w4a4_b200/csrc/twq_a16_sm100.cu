@@ -68,7 +68,7 @@ struct A16Args {
   const uint16_t* l2t;
   int K, n, r;             // r: ranks of L2 read here
   int f;                   // kModeAct: gate columns (n = 2 f)
-  int width;               // columns of a box: 128, or fewer (kModeH). kModeAct: gates in one box, what they multiply in the other
+  int width;               // columns of a box (kModeAct: gates in one, what they multiply in the other)
   const uint16_t* x;       // token rows (row stride ldx), or the pairs' activations
   const uint16_t* x_lo;    // kParts == 2: the activations' second terms
   int64_t ldx;
@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     // A block that gives up walks on, so that all its warps meet at the barriers below.
     auto step_begin = [&] {
       if (!__all_sync(0xFFFFFFFFu, try_wait(wfull0 + slot * 8, phase) && try_wait(xfull0 + slot * 8, phase)))
-        ok = ok && wait(&s_wfull[slot], phase, &s_wait, kSiteWFull) && wait(&s_xfull[slot], phase, &s_wait, kSiteXFull);
+        ok = ok && wait(&s_wfull[slot], phase, &s_wait, kSiteWFull) &&
+             wait(&s_xfull[slot], phase, &s_wait, kSiteXFull);
       return base + slot * kSlot;
     };
     auto step_end = [&] {
@@ -885,10 +886,10 @@ struct Plan {
 // The split that the busiest SM is done with first, of at most 2^most blocks; room: clusters of 1, 2, 4 and
 // 8 blocks that run at once. An SM's time for a group of 32 columns goes with
 // the warps that multiply there: 410 cycles with 16 of them, 555 with 8 (8 rows, 37888 columns of 4096).
-// Among equal splits of a long run of choices' jobs the finer one: how many jobs there are, the GPU alone knows,
-// and a cluster with one job more than another costs less (24 tokens, a quarter of 8 choices each among 32 local
-// experts of 4096 x 1024: 73 us instead of 77). For a short run joining the parts costs more (one token, 8 of
-// 128 experts of 2048 x 768: 18.6 us, 22.0 with the finer split).
+// Among equal splits of a long run of choices' jobs the finer one: how many jobs there are, the GPU alone
+// knows, and a cluster with one job more than another costs less (24 tokens, a quarter of 8 choices each among
+// 32 local experts of 4096 x 1024: 73 us instead of 77). For a short run joining the parts costs more (one
+// token, 8 of 128 experts of 2048 x 768: 18.6 us, 22.0 with the finer split).
 constexpr int kShortRun = 8, kLongRun = 16;
 Plan plan(int64_t jobs, int64_t steps, const int* room, int per_sm, int warps, bool all_there, int most) {
   Plan best = {0, 0, 0, 0, 0};
@@ -977,7 +978,9 @@ template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
 cudaError_t choose(const A16Args& a, Choice* out) {
   using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
   int64_t chunks = (a.b + K::kCap - 1) / K::kCap;
-  if (kRouted) {  // as many different experts as so many choices among them leave on average
+  // As many different experts as so many choices among them leave on average (13 tokens, 8 each of 128 experts of
+  // 2048 x 768: 68 us, 75 if planned for as many as there may be). Other numbers of them run as well.
+  if (kRouted) {
     const double pairs = a.b * a.k, used = a.count * (1.0 - std::pow(1.0 - 1.0 / a.count, pairs));
     chunks = std::min<int64_t>(K::max_chunks(a.b * a.k, a.count), std::ceil(std::max(used, pairs / K::kCap)));
   }
