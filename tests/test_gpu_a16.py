@@ -354,6 +354,31 @@ def test_experts_follow_their_weights(twq, device):
         twq.moe_experts(x, ids, w, one)
 
 
+def test_threads(twq, device):
+    """Calls from several threads at once, each on a stream of its own."""
+    import threading
+
+    gen = torch.Generator().manual_seed(18)
+    w, ex = make_layer(twq, gen, 1024, 512, 32, device), make_experts(twq, gen, 5, 512, 256, 16, 16, device)
+    x, x2, logits = (t.to(device) for t in (make_x(gen, 7, 1024), make_x(gen, 7, 512), normal(gen, 7, 5)))
+    calls = lambda: (twq.fused_linear_a16(x, w), twq.moe_layer(x2, logits, 2, ex)[0])
+    want, wrong = calls(), []
+    torch.cuda.synchronize()
+
+    def run():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                if not all(torch.equal(a, c) for a, c in zip(calls(), want)):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=run) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and twq.device_status() == 0
+
+
 def test_two_graphs_share_a_workspace(twq, device):
     """Two captured calls with one workspace and one output, replayed one after the other."""
     gen = torch.Generator().manual_seed(15)
