@@ -630,8 +630,9 @@ TWQ_API twq_status twq_selftest_wait_timeout(const uint8_t* xq, const float* sx,
 TWQ_API twq_status twq_selftest_adapter_stall(int64_t wait_limit_ns);
 
 /* The same for the calls on BF16 activations (twq_fused_linear_a16, twq_moe_experts and
- * twq_moe_layer): while it is set, no block gets the activations of its last step. Site codes
- * 71..75; 76: a copy in flight did not land. */
+ * twq_moe_layer): while it is set, no block gets the activations of its last step, and the r-th
+ * block of a cluster waits r + 1 times the limit, so that blocks outlast those that wait for their
+ * parts. Site codes 71..75; 76: a copy in flight did not land. */
 TWQ_API twq_status twq_selftest_a16_stall(int64_t wait_limit_ns);
 
 /*
