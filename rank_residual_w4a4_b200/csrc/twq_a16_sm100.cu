@@ -667,10 +667,10 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     // themselves may begin that later than this block, so no limit of time here is one of theirs too: past it,
     // the block waits for every block of the cluster to have sent what it sends, at the barrier of the cluster.
     // That comes to an end, since each of their waits does and a block that gave up walks on and sends; then
-    // the stores are under way.
+    // the stores are under way. They are other blocks': an acquire at the cluster's scope orders them.
     auto parts_there = [&](uint64_t ns) {
       const uint64_t t0 = global_timer_ns();
-      while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&s_recv, 0)))
+      while (!__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(&s_recv, 0)))
         if (__any_sync(0xFFFFFFFFu, global_timer_ns() - t0 > ns)) return false;
       return true;
     };

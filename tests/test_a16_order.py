@@ -40,3 +40,12 @@ def test_no_block_leaves_before_its_peers_have_sent():
     first = kernel.index("if (split > 1) cluster_wait_acquire();")
     assert products < first < kernel.index("for (int v = lo; v < hi;)", products)
     assert "cluster_wait" not in body(kernel, r"auto send_part = \[&\]\(int rows\)")
+
+
+def test_parts_of_peers_are_acquired_at_the_clusters_scope():
+    """Peers' stores complete on this block's barrier with a release at the cluster's scope; a wait
+    whose acquire is the block's own would not be ordered behind them."""
+    text = source()
+    waits = re.findall(r"(\w+)\(&s_recv, 0\)", text)
+    assert waits and set(waits) == {"mbar_try_wait_cluster"}
+    assert "acquire.cluster" in body(source("sm100_ptx.cuh"), r"bool mbar_try_wait_cluster\(")
