@@ -157,6 +157,22 @@ __device__ __forceinline__ uint32_t ld4(const void* p) {
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// What may be read before this kernel's own wait: written by a kernel further in front, for whose end the one
+// in front has waited before it let this one start (ids_ready, x_ready). It lies in L2 then, but nothing has
+// told this SM's L1 so: strong loads, which L1 does not serve.
+__device__ __forceinline__ uint4 ld16_early(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld4_early(const void* p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint2 ld8(const void* p) {
   uint2 v;
   asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
@@ -229,7 +245,7 @@ __device__ __noinline__ int make_chunks(const int32_t* ids, int pairs, int count
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
       const unsigned lower = (1u << lane) - 1u, all = 0xFFFFFFFFu;
-      int id = lane < pairs ? static_cast<int>(ld4(ids + lane)) : -1;
+      int id = lane < pairs ? static_cast<int>(ld4_early(ids + lane)) : -1;
       if (id < 0 || id >= count) id = -1;
       const unsigned same = __match_any_sync(all, id);
       const bool leads = id >= 0 && !(same & lower);
@@ -258,7 +274,7 @@ __device__ __noinline__ int make_chunks(const int32_t* ids, int pairs, int count
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     const int at = (warp + j * warps) * 32 + lane;
-    id[j] = at < pairs ? static_cast<int>(ld4(ids + at)) : -1;
+    id[j] = at < pairs ? static_cast<int>(ld4_early(ids + at)) : -1;
     if (id[j] >= count) id[j] = -1;
   }
   for (int i = tid; i < segments * count; i += blockDim.x) before[i] = 0;
@@ -481,7 +497,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
         for (int w = 0; w < 2; ++w)
           if (w == 0 || 2 * k.u + 1 < groups) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[nt][w][j] = ld16(from + w * 128 + j * 8);
+            for (int j = 0; j < 4; ++j) x[nt][w][j] = ld16_early(from + w * 128 + j * 8);
           }
       }
     };
