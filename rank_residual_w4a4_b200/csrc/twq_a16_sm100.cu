@@ -90,6 +90,15 @@ struct WaitState {  // a block's, in shared memory
   int gave_up;
   uint64_t ns;  // limit of a wait
 };
+// That limit, for block `rank` of a cluster. In the self-test each outlasts those in front of it.
+__host__ __device__ inline uint64_t wait_limit(uint64_t ns, bool stall, int rank) { return stall ? ns * (rank + 1) : ns; }
+// The limit for peers' parts, of a block with `steps` steps. A peer may store into a block only while that is
+// there, so it is longer than any peer takes to send: one has a step more at most, and in each waits at most
+// twice, for weights and for activations, up to its own limit, at most the last block's. (Once a wait has run out it
+// waits no more, but walks on and sends.) The rest of a step, under 1 us, is counted at 0.1 ms, and 2 s are added.
+__host__ __device__ inline uint64_t parts_limit(uint64_t ns, bool stall, int split, int steps) {
+  return (2 * wait_limit(ns, stall, split - 1) + 100000) * (steps + 1) + 2000000000ull;
+}
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile WaitState* w, int site) {
   const uint64_t t0 = global_timer_ns();
   for (;;) {
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     mbar_init(&s_recv, 1);
     fence_barrier_init();
     s_wait.gave_up = 0;
-    s_wait.ns = a.stall ? a.wait_ns * (rank + 1) : a.wait_ns;  // self-test: later blocks of a cluster outlast earlier ones
+    s_wait.ns = wait_limit(a.wait_ns, a.stall, rank);
   }
   if (!a.ids_ready) {
     pdl_wait();
@@ -376,8 +385,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     chunks = (a.b + kCap - 1) / kCap;
     __syncthreads();
   }
-  // The cluster's barrier, first round: this block's barriers exist. Second: this thread sends nothing more.
-  if (split > 1) cluster_arrive_relaxed();
+  if (split > 1) cluster_arrive_relaxed();  // this block's barriers exist
   auto chunk_expert = [&](int c) { return kRouted ? static_cast<int>(s_chunk[c].x) : 0; };
   auto chunk_first = [&](int c) { return kRouted ? static_cast<int>(s_chunk[c].y & 0xFFFFu) : c * kCap; };
   auto chunk_rows = [&](int c) {
@@ -669,6 +677,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     auto send_part = [&](int rows) {
       int owner = rank - 1;
       while (begin_of(owner) > lo - at0.u) --owner;
+      cluster_wait_acquire();  // the owner's barrier exists
       const uint32_t to = map_peer(smem_u32(recv + (rank - owner - 1) * kPart), owner);
       const uint32_t bar = map_peer(smem_u32(&s_recv), owner);
 #pragma unroll 1
@@ -679,22 +688,17 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
           st_async_peer_v4(to + (i * kQuads + q) * 16, o.x, o.y, o.z, o.w, bar);
         }
     };
-    // What peers store into this block lands before it leaves, whether it or they gave up. Peers that wait
-    // themselves may begin that later than this block, so no limit of time here is one of theirs too: past it,
-    // the block waits for every block of the cluster to have sent what it sends, at the barrier of the cluster.
-    // That comes to an end, since each of their waits does and a block that gave up walks on and sends; then
-    // the stores are under way. They are other blocks': an acquire at the cluster's scope orders them.
-    auto parts_there = [&](uint64_t ns) {
-      const uint64_t t0 = global_timer_ns();
-      while (!__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(&s_recv, 0)))
-        if (__any_sync(0xFFFFFFFFu, global_timer_ns() - t0 > ns)) return false;
-      return true;
-    };
+    // What peers store into this block lands before it leaves, whether it or they gave up: the limit is longer
+    // than a peer takes to send. The stores are other blocks': an acquire at the cluster's scope orders them.
     auto wait_parts = [&] {
-      if (parts_there(a.stall ? a.wait_ns / 2 : a.wait_ns)) return;
-      cluster_arrive_relaxed();
-      cluster_wait_acquire();
-      if (!parts_there(2000000000ull) && lane == 0) atomicCAS(&g_a16_status, 0, kSiteSums);
+      const uint64_t t0 = global_timer_ns(), ns = parts_limit(a.wait_ns, a.stall, split, hi - lo);
+      while (!mbar_try_wait_cluster(&s_recv, 0)) {
+        if (global_timer_ns() - t0 > ns) {
+          atomicCAS(&g_a16_status, 0, kSiteSums);
+          break;
+        }
+      }
+      __syncwarp();
     };
 
     // One group of 32 columns; one 32 ranks of their low-rank factors.
@@ -779,7 +783,6 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
       if (++slot == a.slots) slot = 0, phase ^= 1;
     };
 
-    if (split > 1) cluster_wait_acquire();  // peers' barriers exist (they do before the first copies land)
     Walk k = at0;
     int from = at0.u;  // of the job's steps, the first of this block's
     clear();
@@ -854,11 +857,6 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
       from = 0;
       if (v < hi) barrier();  // the sums are read
     }
-  }
-  __syncwarp();
-  if (split > 1) {
-    if (warp >= kWarps) cluster_wait_acquire();
-    cluster_arrive_relaxed();
   }
   pdl_wait();  // this grid completes only after the one in front
 }

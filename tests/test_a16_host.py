@@ -1,0 +1,64 @@
+"""What the host computes for launches on BF16 activations, from the kernel's own translation unit."""
+import ctypes
+import hashlib
+import os
+import random
+import subprocess
+
+import pytest
+
+from test_a16_plan import CSRC, DEPS, ROOT, _nvcc
+
+HARNESS = os.path.join(ROOT, "tests", "a16_host_harness.cu")
+
+
+@pytest.fixture(scope="module")
+def harness():
+    h = hashlib.sha256()
+    for d in [HARNESS] + DEPS[1:]:
+        with open(d, "rb") as fh:
+            h.update(fh.read())
+    out_dir = os.path.join(ROOT, "tests", "_build")
+    os.makedirs(out_dir, exist_ok=True)
+    path = os.path.join(out_dir, "liba16host_%s.so" % h.hexdigest()[:16])
+    if not os.path.exists(path):
+        # PTX only for the device side: the harness runs host code alone. What launches call in other
+        # files may stay unresolved.
+        tmp = path + ".tmp%d" % os.getpid()
+        cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=compute_100a", "-std=c++17", "-O1",
+               "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+               HARNESS, "-o", tmp]
+        try:
+            subprocess.run(cmd, check=True, capture_output=True, timeout=900)
+        except FileNotFoundError:
+            pytest.skip("nvcc is not available")
+        os.replace(tmp, path)
+    return ctypes.CDLL(path, mode=os.RTLD_LAZY)
+
+
+@pytest.mark.parametrize("ns,stall", [(2000000000, 0), (1000, 1), (200000, 1), (1000000000, 1)])
+def test_a_block_outwaits_every_peer_that_sends_to_it(harness, ns, stall):
+    """A block that began a job waits for the parts of the blocks that go on with it, from the end of its
+    own steps. Whenever theirs run into their limits, in any step and in as many as there are before
+    one runs out, they have sent before its limit is over: a store may not meet a block that left."""
+    wait, parts = harness.twq_test_a16_wait_limit, harness.twq_test_a16_parts_limit
+    wait.restype = parts.restype = ctypes.c_uint64
+    wait.argtypes = [ctypes.c_uint64, ctypes.c_int, ctypes.c_int]
+    parts.argtypes = [ctypes.c_uint64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+    step_ns = 2000  # what is not waiting: 240 to 707 cycles a group of 32 columns, two groups a step, twofold
+    rng = random.Random(ns)
+    for _ in range(2000):
+        split_log = rng.choice([1, 2, 3])
+        split, steps, jobs = 1 << split_log, rng.randint(1, 200), rng.randint(1, 4)
+        total = steps * jobs
+        begin = [total * r >> split_log for r in range(split + 1)]
+        for r in range(split):
+            lo, hi = begin[r], begin[r + 1]
+            if lo == hi or hi % steps == 0:
+                continue
+            for q in range(r + 1, split):
+                mine = begin[q + 1] - begin[q]
+                if begin[q] >= hi - hi % steps + steps or not mine:
+                    continue
+                longest = 2 * mine * wait(ns, stall, q) + mine * step_ns
+                assert parts(ns, stall, split, hi - lo) > longest

@@ -23,25 +23,6 @@ def body(text, head):
     raise AssertionError("unbalanced braces")
 
 
-def test_no_block_leaves_before_its_peers_have_sent():
-    """A peer's own waits may end later than any limit of the block that gets its part. So past the
-    limit the block meets all others at the cluster's barrier, at which each arrives after its
-    sending, and only then gives up."""
-    text = source()
-    wait = body(text, r"auto wait_parts = \[&\]")
-    arrive, meet = wait.index("cluster_arrive_relaxed"), wait.index("cluster_wait_acquire")
-    assert arrive < meet < wait.index("g_a16_status")
-    # one arrival of every thread where the cluster starts, one after the roles, each round waited for
-    # before the next: by the products ahead of their steps, by the others at the end
-    kernel = body(text, r"a16_kernel\(const __grid_constant__ A16Args a\)")
-    end = kernel[kernel.rindex("if (split > 1)"):]
-    assert re.search(r"if \(warp >= kWarps\) cluster_wait_acquire\(\);\s*cluster_arrive_relaxed\(\);", end)
-    products = kernel.index("float acc[2][NT][4]")
-    first = kernel.index("if (split > 1) cluster_wait_acquire();")
-    assert products < first < kernel.index("for (int v = lo; v < hi;)", products)
-    assert "cluster_wait" not in body(kernel, r"auto send_part = \[&\]\(int rows\)")
-
-
 def test_parts_of_peers_are_acquired_at_the_clusters_scope():
     """Peers' stores complete on this block's barrier with a release at the cluster's scope; a wait
     whose acquire is the block's own would not be ordered behind them."""

@@ -40,3 +40,21 @@ def test_blocks_that_outlast_one_another(twq, device, b, call):
         assert 71 <= code <= 76 and spent < 1.0, (code, spent)
         assert twq.device_status() == 0
         assert torch.equal(f(), want) and twq.device_status() == 0
+
+
+def test_a_block_outwaits_its_peers(twq, device):
+    """The last blocks of a cluster of eight give up after 2.8 s, the first, which gets their parts,
+    after 0.35 s: it is there when they come."""
+    gen = torch.Generator().manual_seed(23)
+    x, w = make_x(gen, 1, 8192).to(device), make_layer(twq, gen, 8192, 256, 0, device)
+    want = twq.fused_linear_a16(x, w)
+    twq.selftest_a16_stall(350000000)
+    try:
+        t0 = time.perf_counter()
+        twq.fused_linear_a16(x, w)
+        code = twq.device_status()
+        spent = time.perf_counter() - t0
+    finally:
+        twq.selftest_a16_stall(0)
+    assert code == 74 and 0.35 <= spent < 4.0, (code, spent)  # 74: activations that did not come
+    assert twq.device_status() == 0 and torch.equal(twq.fused_linear_a16(x, w), want)
