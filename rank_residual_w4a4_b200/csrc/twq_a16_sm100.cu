@@ -168,14 +168,12 @@ __device__ __forceinline__ uint32_t ld4(const void* p) {
 }
 // What may be read before this kernel's own wait: written by a kernel further in front, for whose end the one
 // in front has waited before it let this one start (ids_ready, x_ready). It lies in L2 then, but nothing has
-// told this SM's L1 so: strong loads, which L1 does not serve.
-__device__ __forceinline__ uint4 ld16_early(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
+// told this SM's L1 so. Single words are read by loads that are strong at the GPU's scope, which L1 does not
+// serve; rows of activations by plain ones behind an acquire at that scope, from which on L1 holds nothing from
+// before. (Strong loads of rows fetch each 32-byte sector twice: 32 rows of 5120 x 18944 took 31.7 us, not 28.8.)
+__device__ __forceinline__ void acquire_early(const uint16_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
 }
 __device__ __forceinline__ uint32_t ld4_early(const void* p) {
   uint32_t v;
@@ -486,7 +484,10 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     // Activations, each warp a step in turn, its next one's on their way meanwhile. No more warps than
     // slots: one that does not wait at the steps of the others must not get two turns of the ring ahead.
     const int turns = min(K::kXWarps, a.slots), turn = warp - kWarps - 1;
-    if (!a.x_ready) pdl_wait();
+    if (a.x_ready)
+      acquire_early(a.x);
+    else
+      pdl_wait();
     if (a.ids_ready) pdl_launch_dependents();
     constexpr int kN = NT < 2 ? 1 : 2;  // tiles whose loads are in flight together
     bool waited = !a.x_ready;
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
         for (int w = 0; w < 2; ++w)
           if (w == 0 || 2 * k.u + 1 < groups) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[nt][w][j] = ld16_early(from + w * 128 + j * 8);
+            for (int j = 0; j < 4; ++j) x[nt][w][j] = ld16(from + w * 128 + j * 8);
           }
       }
     };

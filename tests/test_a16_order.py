@@ -35,16 +35,16 @@ def test_parts_of_peers_are_acquired_at_the_clusters_scope():
 def test_early_reads_do_not_come_from_l1():
     """ids and activations may be read before the kernel's own wait, on the ground that the kernel in
     front has waited for their writer. Visibility is promised at the wait alone; loads that are strong at
-    the GPU's scope do not find an older line in an SM's L1."""
+    the GPU's scope, and loads behind an acquire there, do not find an older line in an SM's L1."""
     text = source()
-    for name in ("ld16_early", "ld4_early"):
-        assert "ld.relaxed.gpu.global" in body(text, r"%s\(const \w+\* p\)" % name)
+    assert "ld.relaxed.gpu.global" in body(text, r"ld4_early\(const void\* p\)")
+    assert "ld.acquire.gpu.global" in body(text, r"acquire_early\(const uint16_t\* p\)")
     loads = re.findall(r"(\w+)\(ids \+", body(text, r"int make_chunks\("))
     assert loads and set(loads) == {"ld4_early"}
     kernel = body(text, r"a16_kernel\(const __grid_constant__ A16Args a\)")
-    load = body(kernel, r"auto load = \[&\]\(int n0\)")
-    assert set(re.findall(r"\bld\d+\w*", load)) == {"ld16_early"}
-    # h alone is read by plain loads, behind the wait
-    rest = re.findall(r"\bld\d+\w*\(([^)]*)\)", kernel.replace(load, "").replace("ld16_early", "early"))
-    assert rest and all("a.h" in r for r in rest)
+    # the warps that load activations: wait or acquire, before the first load and on every way to it
+    ready = re.search(r"if \(a\.x_ready\)\s*acquire_early\(a\.x\);\s*else\s*pdl_wait\(\);", kernel)
+    assert ready and ready.end() < re.search(r"\bld16\(", kernel).start()
+    # h, which the kernel in front writes, behind the wait
     assert kernel.index("if (!waited) pdl_wait();") < kernel.index("ld16(a.h")
+    assert len(re.findall(r"\bld\d+\(", kernel)) == 2
