@@ -925,6 +925,8 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, exper
     record the call."""
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise TypeError("ids must be a 2-D torch tensor")
+    if not isinstance(weights, torch.Tensor):
+        raise TypeError("weights must be a torch tensor")
     k = ids.shape[1]
     b, px, ldx, pe, pb, y, py, workspace = _moe_buffers(x, k, experts, base, y, workspace, stream)
     _, _, pi, pw = _choices(ids, weights, b, k, experts.device, stream)
