@@ -641,7 +641,7 @@ def _mat(t, name, dtype, rows, cols, device) -> int:
     if t.shape != (rows, cols):
         raise ValueError("%s must be (%d, %d)" % (name, rows, cols))
     if t.device != device:
-        raise ValueError("%s must be on the adapters' device" % name)
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
     return p
 
 

@@ -22,3 +22,10 @@ def test_experts_need_their_weights(monkeypatch):
             twq.moe_experts(torch.zeros((2, 128), dtype=torch.bfloat16), torch.zeros((2, 1), dtype=torch.int32),
                             weights, None)
     assert not made
+
+
+def test_a_matrix_elsewhere_is_named_with_both_devices(monkeypatch):
+    """Adapters, layers and experts share the check of their matrices; its message is none of theirs."""
+    monkeypatch.setattr(twq, "_dev", lambda t, name, dtype: 16)
+    with pytest.raises(ValueError, match="^ids must be on cuda:1, got cpu$"):
+        twq._mat(torch.zeros((2, 3), dtype=torch.int32), "ids", torch.int32, 2, 3, torch.device("cuda", 1))
