@@ -32,7 +32,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <mutex>
 
 #include "sm100_ptx.cuh"
 #include "twq_a16.h"
@@ -936,59 +935,44 @@ Plan plan(int64_t jobs, int64_t steps, const int* room, int per_sm, int warps, b
   return best;
 }
 
-// How many clusters of 1, 2, 4 and 8 blocks run at once, with per_sm blocks' shared memory on an SM. Asked
-// once for each kernel and device (a cluster keeps within a GPC, and GPCs differ); only answers are kept.
-cudaError_t clusters_at_once(const void* kernel, int threads, int per_sm, const int** room) {
-  struct Known {
-    const void* kernel;
-    int dev, per_sm, room[4];
-  };
-  constexpr int kKnown = 256;
-  static Known known[kKnown];
-  static std::atomic<int> count{0};
-  static std::mutex mutex;
+// How many clusters of 1, 2, 4 and 8 blocks run at once, with per_sm blocks' shared memory on an SM (a cluster
+// keeps within a GPC, and GPCs differ). Asked once for each kernel, device and per_sm; only answers are kept, the
+// four in one word (0: not asked yet), so that calls from several threads at once need no lock. On devices beyond
+// kDevices it is asked at every launch.
+constexpr int kDevices = 64, kMostPerSm = 3;
+using Rooms = std::atomic<uint64_t>[kDevices][kMostPerSm];
+cudaError_t clusters_at_once(const void* kernel, int threads, int per_sm, Rooms& rooms, int (&room)[4]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto find = [&](int n) {
-    for (int i = 0; i < n; ++i)
-      if (known[i].kernel == kernel && known[i].dev == dev && known[i].per_sm == per_sm) return known[i].room;
-    return static_cast<int*>(nullptr);
-  };
-  if ((*room = find(count.load(std::memory_order_acquire)))) return cudaSuccess;
-  std::lock_guard<std::mutex> lock(mutex);
-  const int n = count.load(std::memory_order_relaxed);
-  if ((*room = find(n))) return cudaSuccess;
-  e = allow_smem(kernel, kMaxSmem);
-  if (e != cudaSuccess) return e;
-  Known k = {kernel, dev, per_sm, {}};
-  for (int s = 0; s < 4; ++s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((8 * kSms) << s);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = std::min(kMaxSmem, 227 * 1024 / per_sm - 1536);
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1 << s;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&k.room[s], kernel, &cfg);
-    if (e != cudaSuccess) {
-      cudaGetLastError();  // returned here; not a later launch's error
-      return e;
+  std::atomic<uint64_t>* const known = dev < kDevices ? &rooms[dev][per_sm - 1] : nullptr;
+  uint64_t all = known ? known->load(std::memory_order_relaxed) : 0;
+  if (!all) {
+    e = allow_smem(kernel, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    for (int s = 0; s < 4; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((8 * kSms) << s);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = std::min(kMaxSmem, 227 * 1024 / per_sm - 1536);
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 1 << s;
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) {
+        cudaGetLastError();  // returned here; not a later launch's error
+        return e;
+      }
+      all |= static_cast<uint64_t>(std::min(std::max(n, 1), 0xFFFF)) << (16 * s);
     }
-    k.room[s] = std::max(k.room[s], 1);
+    if (known) known->store(all, std::memory_order_relaxed);
   }
-  if (n < kKnown) {
-    known[n] = k;
-    count.store(n + 1, std::memory_order_release);
-    *room = known[n].room;
-  } else {  // more devices than there is room for: as if every SM took its blocks
-    static const int plain[4] = {kSms, kSms / 2, kSms / 4, kSms / 8};
-    *room = plain;
-  }
+  for (int s = 0; s < 4; ++s) room[s] = static_cast<int>(all >> (16 * s) & 0xFFFF);
   return cudaSuccess;
 }
 
@@ -1004,6 +988,8 @@ struct Choice {
 template <int kWarps, int NT, int kMode, int kParts, bool kRouted>
 cudaError_t choose(const A16Args& a, Choice* out) {
   using K = Kernel<kWarps, NT, kMode, kParts, kRouted>;
+  static_assert(K::kBlocksPerSm <= kMostPerSm, "places of the answers");
+  static Rooms rooms;
   int64_t chunks = (a.b + K::kCap - 1) / K::kCap;
   // As many different experts as so many choices among them leave on average (13 tokens, 8 each of 128 experts of
   // 2048 x 768: 68 us, 75 if planned for as many as there may be). Other numbers of them run as well.
@@ -1017,9 +1003,10 @@ cudaError_t choose(const A16Args& a, Choice* out) {
   *out = {};
   out->p.cost = kNoFit;
   for (int per_sm = K::kBlocksPerSm; per_sm > 0; --per_sm) {
-    const int* room;
-    const cudaError_t e = clusters_at_once(
-        reinterpret_cast<const void*>(a16_kernel<kWarps, NT, kMode, kParts, kRouted>), K::kThreads, per_sm, &room);
+    int room[4];
+    const cudaError_t e =
+        clusters_at_once(reinterpret_cast<const void*>(a16_kernel<kWarps, NT, kMode, kParts, kRouted>), K::kThreads,
+                         per_sm, rooms, room);
     if (e != cudaSuccess) return e;
     for (int most = 3; most >= 0; --most) {
       const Plan p = plan(chunks * blocks, steps, room, per_sm, kWarps, !kRouted, most);

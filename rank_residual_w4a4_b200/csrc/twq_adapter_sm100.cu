@@ -1991,7 +1991,8 @@ BackwardPlan backward_plan(int64_t b, int64_t m, int64_t n, int64_t r, int64_t c
   return s;
 }
 
-// By device; a kernel's pointer where its limit is set. More places than the adapters have kernels.
+// By device; a kernel's pointer where its limit is set. More places than there are such kernels: the
+// adapters', and 27 of the products on BF16 activations.
 constexpr int kKnownDevices = 64, kKnownKernels = 96;
 std::atomic<const void*> g_allowed[kKnownDevices][kKnownKernels];
 

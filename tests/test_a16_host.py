@@ -62,3 +62,23 @@ def test_a_block_outwaits_every_peer_that_sends_to_it(harness, ns, stall):
                     continue
                 longest = 2 * mine * wait(ns, stall, q) + mine * step_ns
                 assert parts(ns, stall, split, hi - lo) > longest
+
+
+def test_every_device_is_asked_once(harness):
+    """How many clusters run at once is asked once for each kernel, device and number of blocks on an SM,
+    on as many devices as a machine has and in any order; the answers are each device's own."""
+    out = (ctypes.c_int64 * 2)()
+
+    def plans(dev):
+        harness.twq_test_a16_plans(ctypes.c_int(dev), out)
+        return out[0], out[1]
+
+    first = [plans(d) for d in range(16)]
+    assert len({asked for asked, _ in first}) == 1 and first[0][0] % 4 == 0
+    assert first[0][0] // 4 <= 27 * 3
+    assert len({s for _, s in first}) > 1  # other devices, other plans
+    for d in reversed(range(16)):
+        assert plans(d) == (0, first[d][1])
+    # a device beyond the places for answers is asked again, and gets its own plan all the same
+    far = plans(1000)
+    assert far[0] > 0 and plans(1000) == far and far[1] != first[0][1]
