@@ -6,6 +6,7 @@ import time
 import pytest
 import torch
 
+import a16_norm as norm
 import a16_ref as ref
 from test_gpu_a16 import BF, make_experts, make_layer, make_x, normal, twq  # noqa: F401 (fixture)
 
@@ -58,3 +59,99 @@ def test_a_block_outwaits_its_peers(twq, device):
         twq.selftest_a16_stall(0)
     assert code == 74 and 0.35 <= spent < 4.0, (code, spent)  # 74: activations that did not come
     assert twq.device_status() == 0 and torch.equal(twq.fused_linear_a16(x, w), want)
+
+
+def on_gpu(twq, ex, device):
+    def weights(w):
+        return twq.Weights(w.m, w.n, w.r, *(t.to(device) for t in (w.rq, w.sr, w.l1q, w.sl1, w.l2t)))
+    return twq.Experts(weights(ex.up), weights(ex.down))
+
+
+@pytest.mark.parametrize("case", norm.CASES, ids=str)
+def test_precision_of_experts(twq, device, case):
+    """y's own rounding is nearly all of the error: a in two BF16 terms, g, u and y_e not rounded
+    (test_a16_norm.py has what this check rejects)."""
+    x, ids, weights, ex = norm.make(case)
+    y = twq.moe_experts(x.to(device), ids.to(device), weights.to(device), on_gpu(twq, ex, device))
+    norm.check_norm(y.cpu(), norm.experts(x, ids, weights, ex), "y")
+
+
+@pytest.mark.parametrize("b", [4, 8, 24])
+def test_precision_of_the_down_products_h(twq, device, b):
+    """y is h2, and that of both terms of a: few of its elements round the other way."""
+    x, ids, weights, ex = norm.make_low_rank(b)
+    y = twq.moe_experts(x.to(device), ids.to(device), weights.to(device), on_gpu(twq, ex, device))
+    assert norm.changed(y.cpu(), norm.experts(x, ids, weights, ex)) <= 0.05
+
+
+@pytest.mark.parametrize("share", [1.0, 0.5])
+@pytest.mark.parametrize("b,m,f,r,rd,count,k", [(64, 256, 256, 16, 16, 128, 8), (64, 384, 128, 0, 0, 128, 1),
+                                                (37, 256, 384, 0, 32, 64, 2), (64, 128, 128, 16, 0, 1024, 16)])
+def test_one_expert_takes_the_tokens(twq, device, b, m, f, r, rd, count, k, share):
+    """One of many experts is in the first slot of all tokens, or of half of them: many chunks of one
+    expert where the launch is planned for few rows of each."""
+    gen = torch.Generator().manual_seed(b + m + f + count + k)
+    few = make_experts(twq, gen, 5, m, f, r, rd, device)
+    at = torch.arange(count, device=device) % 5
+    ex = twq.Experts(*(twq.Weights(w.m, w.n, w.r, *(t[at].contiguous() for t in (w.rq, w.sr, w.l1q, w.sl1, w.l2t)))
+                       for w in (few.up, few.down)))
+    x, base = make_x(gen, b, m).to(device), normal(gen, b, m).to(device)
+    ids = torch.rand((b, count), generator=gen).argsort(dim=1)[:, :k].to(torch.int32)
+    ids[:int(b * share), 0] = count - 2
+    ids, weights = ids.contiguous().to(device), torch.rand((b, k), generator=gen).to(device)
+    y = twq.moe_experts(x, ids, weights, ex, base=base)
+    y64, ye = ref.experts(x, ids, weights, ex, base)
+    ref.check(y, y64, ye, "y")
+    assert torch.equal(y, twq.moe_experts(x, ids, weights, ex, base=base)) and twq.device_status() == 0
+
+
+def large_factors(gen, m, n, r, device):
+    def matrix(a, c, std):
+        return (torch.randn((a, c), generator=gen, device=device) * std).to(BF)
+    return matrix(m, n, m ** -0.5), matrix(m, r, m ** -0.5), matrix(r, n, 0.4 * r ** -0.5)
+
+
+@pytest.mark.parametrize("b,m,n", [(3, 2 ** 20, 128), (3, 128, 2 ** 20), (33, 2 ** 20, 128)])
+def test_linear_at_its_limits(twq, device, b, m, n):
+    gen = torch.Generator(device=device).manual_seed(24)
+    w = twq.pack_weights(*large_factors(gen, m, n, 16, device))
+    x = make_x(torch.Generator().manual_seed(b), b, m).to(device)
+    h = torch.empty((b, 16), dtype=BF, device=device)
+    y = twq.fused_linear_a16(x, w, h=h)
+    (y64, h64), (ye, he) = ref.linear(x, w)
+    ref.check(y, y64, ye, "y")
+    ref.check(h, h64, he, "h")
+    assert twq.device_status() == 0
+
+
+@pytest.mark.parametrize("m,f", [(128, 2 ** 19), (2 ** 20, 128)])
+def test_experts_at_their_limits(twq, device, m, f):
+    gen = torch.Generator(device=device).manual_seed(25)
+    ex = twq.Experts.empty(2, m, f, 16, device)
+    for e in range(2):
+        ex.pack(e, *large_factors(gen, m, 2 * f, 16, device), *large_factors(gen, f, m, 16, device))
+    host = torch.Generator().manual_seed(26)
+    x, weights = make_x(host, 3, m).to(device), torch.rand((3, 2), generator=host).to(device)
+    ids = torch.tensor([[0, 1], [1, -1], [1, 1]], dtype=torch.int32, device=device)
+    y = twq.moe_experts(x, ids, weights, ex)
+    y64, ye = ref.experts(x, ids, weights, ex, None)
+    ref.check(y, y64, ye, "y")
+    assert twq.device_status() == 0
+
+
+def test_rows_beyond_two_to_the_32(twq, device):
+    """Strides that put the last rows of X and of the logits more than 2^32 elements on."""
+    gen = torch.Generator().manual_seed(27)
+    w, x = make_layer(twq, gen, 256, 128, 16, device), make_x(gen, 64, 256).to(device)
+    far = torch.empty(2 ** 32 + 2 ** 27, dtype=BF, device=device)
+    wide = far.as_strided((64, 256), (2 ** 26 + 2 ** 20, 1))
+    wide.copy_(x)
+    assert torch.equal(twq.fused_linear_a16(wide, w), twq.fused_linear_a16(x, w))
+    logits = far.as_strided((2 ** 24, 8), (257, 1))
+    logits.copy_(torch.randn((2 ** 24, 8), generator=torch.Generator(device=device).manual_seed(28), device=device))
+    ids, weights = twq.moe_route(logits, 2)
+    want = logits.float().sort(dim=1, descending=True, stable=True)
+    assert torch.equal(ids, want.indices[:, :2].to(torch.int32))
+    soft = want.values[:, :2].double().softmax(dim=1)
+    assert bool(((weights.double() - soft).abs() <= (40 + 2 * 33) * 2.0 ** -24 * soft).all())  # as in test_route
+    assert twq.device_status() == 0
