@@ -171,8 +171,7 @@ __device__ __forceinline__ uint32_t ld4(const void* p) {
 // serve; rows of activations by plain ones behind an acquire at that scope, from which on L1 holds nothing from
 // before. (Strong loads of rows fetch each 32-byte sector twice: 32 rows of 5120 x 18944 took 31.7 us, not 28.8.)
 __device__ __forceinline__ void acquire_early(const uint16_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("{\n\t.reg .b32 v;\n\tld.acquire.gpu.global.b32 v, [%0];\n\t}" ::"l"(p) : "memory");
 }
 __device__ __forceinline__ uint32_t ld4_early(const void* p) {
   uint32_t v;
@@ -200,6 +199,31 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
       __hsub2(*reinterpret_cast<__nv_bfloat162*>(&t), *reinterpret_cast<const __nv_bfloat162*>(&off));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
+
+// The jobs [job0, job1) of a cluster, `per` steps each, and its blocks' shares of their steps, counted from job0's
+// first.
+struct Shares {
+  int job0, job1, total;
+  const int& split_log;
+  __host__ __device__ Shares(int jobs, int clusters, int cluster, int per, const int& log) : split_log(log) {
+    const int each = jobs / clusters, more = jobs - each * clusters;  // `more` clusters have one more
+    job0 = each * cluster + (cluster < more ? cluster : more), job1 = job0 + each + (cluster < more);
+    total = (job1 - job0) * per;
+  }
+  __host__ __device__ int begin(int rank) const { return total * rank >> split_log; }
+  __host__ __device__ bool any(int rank) const { return begin(rank) < begin(rank + 1); }
+  // The block that began the job whose first step is `first`, of which `rank` has a later one as its own first.
+  __host__ __device__ int owner(int rank, int first) const {
+    int o = rank - 1;
+    while (begin(o) > first) --o;
+    return o;
+  }
+  // f(whether it has steps) for each block behind `rank` up to the last that goes on with a job that ends at `end`.
+  template <typename F>
+  __host__ __device__ void others(int rank, int end, F f) const {
+    for (int r = rank + 1; r < 1 << split_log && begin(r) < end; ++r) f(any(r));
+  }
+};
 
 // What of a block's shared memory is where, in bytes from a 1024-byte boundary.
 struct Layout {
@@ -396,11 +420,8 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
   // began. All roles walk the same steps.
   const int groups = a.K >> 7, code_steps = (groups + 1) / 2, per = code_steps + (a.r + 63) / 64;
   const int jobs = chunks * a.blocks, clusters = gridDim.x >> a.split_log;
-  const int each = jobs / clusters, more = jobs - each * clusters;  // `more` clusters have one more
-  const int job0 = each * cluster + min(cluster, more), job1 = job0 + each + (cluster < more);
-  const int total = (job1 - job0) * per;
-  auto begin_of = [&](int r) { return total * r >> a.split_log; };
-  const int lo = begin_of(rank), hi = begin_of(rank + 1);
+  const Shares shares(jobs, clusters, cluster, per, a.split_log);
+  const int job1 = shares.job1, lo = shares.begin(rank), hi = shares.begin(rank + 1);
   struct Walk {
     int job, block, chunk, u;  // step u of the job
   };
@@ -410,7 +431,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     else
       k.block = k.job / chunks, k.chunk = k.job - k.block * chunks;
   };
-  Walk at0 = {job0, 0, 0, 0};
+  Walk at0 = {shares.job0, 0, 0, 0};
   if (lo < hi) {
     const int skip = lo / per;
     at0.job += skip, at0.u = lo - skip * per;
@@ -675,8 +696,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
     float4* const recv = reinterpret_cast<float4*>(smem + lay.recv);
     constexpr int kPart = kCap * kItems * kQuads;  // of one block, in quads
     auto send_part = [&](int rows) {
-      int owner = rank - 1;
-      while (begin_of(owner) > lo - at0.u) --owner;
+      const int owner = shares.owner(rank, lo - at0.u);
       cluster_wait_acquire();  // the owner's barrier exists
       const uint32_t to = map_peer(smem_u32(recv + (rank - owner - 1) * kPart), owner);
       const uint32_t bar = map_peer(smem_u32(&s_recv), owner);
@@ -832,10 +852,10 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
         int parts = 0;  // of other blocks
         if (!over) {    // this block began the job, others end it
           uint32_t bytes = 0;
-          for (int r = rank + 1; r < split && begin_of(r) < hi - rest + per; ++r) {
+          shares.others(rank, hi - rest + per, [&](bool any) {
             ++parts;
-            if (begin_of(r) < begin_of(r + 1)) bytes += rows * kItems * kQuads * 16;
-          }
+            if (any) bytes += rows * kItems * kQuads * 16;
+          });
           if (tid == 0) mbar_arrive_expect_tx(&s_recv, bytes);
           __syncwarp();
           wait_parts();
@@ -847,7 +867,7 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
           for (int q = 0; q < kQuads; ++q) o[q] = sum_of(i, q);
 #pragma unroll 1
           for (int r = 0; r < parts; ++r)
-            if (begin_of(rank + 1 + r) < begin_of(rank + 2 + r)) {
+            if (shares.any(rank + 1 + r)) {
 #pragma unroll
               for (int q = 0; q < kQuads; ++q) add4(o[q], recv[r * kPart + i * kQuads + q]);
             }

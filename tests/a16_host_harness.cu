@@ -57,3 +57,24 @@ TWQ_TEST void twq_test_a16_plans(int dev, int64_t* out) {
   out[1] = plan_rows<1>() + 29 * plan_rows<2>() + 31 * plan_rows<4>();
   out[0] = g_asked;
 }
+
+// One cluster's jobs and its blocks' shares, as the kernel computes them. begin: 2^log + 1 places; of each block
+// (2^log places): owner, the block that gets its first job's part, or -1; others, how many blocks may send it
+// parts of its last job. Returns the first job | the one behind the last << 32.
+TWQ_TEST int64_t twq_test_a16_shares(int jobs, int clusters, int cluster, int per, int log, int* begin, int* owner,
+                                     int* others) {
+  const twq::Shares s(jobs, clusters, cluster, per, log);
+  for (int r = 0; r <= 1 << log; ++r) begin[r] = s.begin(r);
+  for (int r = 0; r < 1 << log; ++r) {
+    const int lo = s.begin(r), hi = s.begin(r + 1);
+    owner[r] = s.any(r) && lo % per ? s.owner(r, lo - lo % per) : -1;
+    others[r] = 0;
+    if (s.any(r) && hi % per && hi - hi % per >= lo) s.others(r, hi - hi % per + per, [&](bool) { ++others[r]; });
+  }
+  return s.job0 | static_cast<int64_t>(s.job1) << 32;
+}
+TWQ_TEST void twq_test_a16_plan(int64_t jobs, int64_t steps, const int* room, int per_sm, int warps, int all_there,
+                                int64_t* out) {
+  const twq::Plan p = twq::plan(jobs, steps, room, per_sm, warps, all_there != 0, 3);
+  out[0] = p.clusters, out[1] = p.split_log, out[2] = p.parts;
+}

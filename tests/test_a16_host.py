@@ -82,3 +82,40 @@ def test_every_device_is_asked_once(harness):
     # a device beyond the places for answers is asked again, and gets its own plan all the same
     far = plans(1000)
     assert far[0] > 0 and plans(1000) == far and far[1] != first[0][1]
+
+
+@pytest.mark.parametrize("all_there", [True, False])
+def test_the_kernels_shares_fit_together(harness, all_there):
+    """The kernel's own walk: each step of each job is one block's; a block that goes on with a job sends its
+    part to the block that began it, to a place that is there; and that one waits for exactly those."""
+    shares = harness.twq_test_a16_shares
+    shares.restype = ctypes.c_int64
+    out = (ctypes.c_int64 * 3)()
+    begin, owner, others = (ctypes.c_int * 9)(), (ctypes.c_int * 8)(), (ctypes.c_int * 8)()
+    rng = random.Random(7 + all_there)
+    for _ in range(600):
+        jobs, per = int(rng.choice([1, 2, 5, 40, 150, 700]) * rng.uniform(1, 2)), rng.choice([1, 2, 3, rng.randint(1, 60)])
+        room, per_sm = rng.choice([((148, 74, 36, 15), 1), ((296, 148, 71, 33), 2), ((444, 222, 107, 48), 3)])
+        harness.twq_test_a16_plan(ctypes.c_int64(jobs), ctypes.c_int64(per), (ctypes.c_int * 4)(*room), per_sm,
+                                  rng.choice([4, 8]), int(all_there), out)
+        clusters, log, room_for = out
+        blocks = 1 << log
+        there = jobs if all_there else rng.choice([0, 1, rng.randint(0, jobs), jobs, 2 * jobs])
+        done = 0
+        for c in range(clusters):
+            both = shares(there, clusters, c, per, log, begin, owner, others)
+            first, last = both & 0xFFFFFFFF, both >> 32
+            assert first == done and begin[0] == 0 and begin[blocks] == (last - first) * per
+            done = last
+            sends = {r: [] for r in range(blocks)}
+            for r in range(blocks):
+                assert begin[r] <= begin[r + 1]
+                if owner[r] >= 0:
+                    o = owner[r]
+                    job = begin[r] // per * per
+                    assert begin[o] <= job < begin[o + 1] and 0 <= r - o - 1 < room_for
+                    sends[o].append(r)
+            for r in range(blocks):
+                waits = [q for q in range(r + 1, r + 1 + others[r]) if begin[q] < begin[q + 1]]
+                assert waits == sends[r]
+        assert done == there
