@@ -17,15 +17,22 @@
 // products is free as long as the activations follow it: codes i and i + 4 of a word become one BF16
 // pair by one logic operation (0x4300 | (code ^ 8) is 136 + code) and one exact subtraction. That
 // conversion, 11 instructions for 8 codes, is most of a warp's some 240 instructions for 32 columns
-// x one group; at the rate of HBM a quarter of an SM has 370 cycles for it. The low-rank factor L2
-// comes last, in steps of 64 ranks.
+// x one group; at the measured copy rate (6.55 TB/s) a quarter of an SM has 386 cycles for them. The
+// low-rank factor L2 comes last, in steps of 64 ranks.
 //
-// What bounds it. The copies alone, with nothing multiplied, take 15 us for 4096 x 37888 (5.5 TB/s).
-// Up to 8 rows it is the issue of the conversion and products, 323 cycles a group with 4 warps on a
-// quarter of an SM, 380 with 2: 18.5 us there with 8 rows (82 MB, 4.5 TB/s), 10.0 us for 4096 x 14336
-// with 4. Beyond 16 rows it is mma.sync (8 cycles each on a quarter of an SM) and the registers, which
-// leave 2 warps a quarter: 707 cycles a group of 32 rows, 28.7 us for 5120 x 18944. Small layers are
-// bound by two launches, first copies and joining: 7.4 us for one row of 4096 x 4096 with rank 128.
+// What bounds it, in cycles (1965 MHz) that a quarter of an SM takes for 32 columns x one group, from the
+// difference of 4096 x 151552 and 4096 x 75776, so without start and end:
+//     rows                                                    8     16     32
+//     as it runs, blocks and warps as planned               472    620   1108   (64: twice 32)
+//     the same with nothing multiplied                      435    407    599
+//     products alone, 4 | 2 | 1 warps, operands there   323 | 355 | 412
+// Up to 8 rows it is the copies as they are made (5.8 TB/s with nothing multiplied; two slots in the ring,
+// since two blocks and their parts share an SM), and the products add 8% to them: 5.4 TB/s. Start, first
+// copies, joining and end are 3.7 us more: 18.5 us for 4096 x 37888 (82 MB), 10.1 for 4096 x 14336 with 4 rows.
+// From 9 rows on it is the products: two tiles of 8 rows, and with 32 rows 64 mma.sync of 8 cycles each, while
+// the sums of so many rows leave 2 warps a quarter, and X is staged by every block (599 above): 28.9 us for 32
+// rows of 5120 x 18944. Small layers are bound by two launches, first copies and joining: 7.4 us for one row
+// of 4096 x 4096 with rank 128.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -642,6 +649,10 @@ __global__ void __launch_bounds__(Kernel<kWarps, NT, kMode, kParts, kRouted>::kT
         const float4 gate = v[0], up = v[1];
         const float act[4] = {gate.x / (1.0f + expf(-gate.x)) * up.x, gate.y / (1.0f + expf(-gate.y)) * up.y,
                               gate.z / (1.0f + expf(-gate.z)) * up.z, gate.w / (1.0f + expf(-gate.w)) * up.w};
+        // a in two BF16 terms, 2^-17 of a off at most, since mma.sync takes BF16 beside the codes: each is a column
+        // of the down product, 4 rows to a tile. A third term would leave 2 rows to a tile, for an error that y's
+        // own rounding (2^-8) hides as it is: against 64 bits y's error is that of the exact y, rounded (0.0016 to
+        // 0.0017), and 1 to 4 of a thousand elements of y are the neighbour of that.
         float left[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -930,8 +941,11 @@ struct Plan {
   int split_log, parts;
 };
 // The split that the busiest SM is done with first, of at most 2^most blocks; room: clusters of 1, 2, 4 and
-// 8 blocks that run at once. An SM's time for a group of 32 columns goes with
-// the warps that multiply there: 410 cycles with 16 of them, 555 with 8 (8 rows, 37888 columns of 4096).
+// 8 blocks that run at once. An SM's time for a group of 32 columns goes with the warps that multiply there: the
+// constants, fitted to 8 rows of 4096 x 37888, start and end included, say 410 cycles with 16 warps and 555 with 8.
+// They stand for all numbers of rows, whose own curves differ (without start and end 472 and 517 for 8 rows). What
+// they choose at 4096 x 37888, and one block on an SM instead: 8 rows 18.5 us, 20.4; 32 rows 40.5, 42.5; 64 rows 77.0
+// either way; 16 rows 25.2, 24.3: there they choose the worse by 4%.
 // Among equal splits of a long run of choices' jobs the finer one: how many jobs there are, the GPU alone
 // knows, and a cluster with one job more than another costs less (24 tokens, a quarter of 8 choices each among
 // 32 local experts of 4096 x 1024: 73 us instead of 77). For a short run joining the parts costs more (one
